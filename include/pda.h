@@ -69,7 +69,10 @@ enum {
     PDA_ERRW_BAD_CONTEXT_LEN = 1,   /* context_lens[b] < 0 or > max_blocks_per_seq*kv_block_size */
     PDA_ERRW_BAD_BLOCK_ID = 2,      /* a block-table entry used by the context is outside [0, NB) */
     PDA_ERRW_PIPELINE_TIMEOUT = 4,  /* a bounded wait inside the kernel gave up */
-    PDA_ERRW_BAD_POSITION = 8       /* pda_append_kv: a position >= max_blocks_per_seq*kv_block_size */
+    PDA_ERRW_BAD_POSITION = 8,      /* pda_append_kv: a position >= max_blocks_per_seq*kv_block_size;
+                                       pda_fork_sequences: a row that would grow past it, or by < 0 */
+    PDA_ERRW_BAD_SEQUENCE = 16,     /* pda_fork_sequences: parents[i] >= num_seqs */
+    PDA_ERRW_OUT_OF_BLOCKS = 32     /* pda_fork_sequences: fewer free blocks than the rows need */
 };
 
 /*
@@ -285,6 +288,143 @@ PDA_API int pda_decode_step_noalloc(const pda_plan_t* plan, const void* query, c
  * pages.
  */
 PDA_API int pda_kernel_variant(const pda_plan_t* plan);
+
+/* ---------------------------------------------------------------- pages of the cache
+ * A pool of num_cache_blocks blocks is shared by the sequences of a batch.  refcounts[id] is the
+ * number of block-table entries that hold block id (entries of any batch the caller keeps, of
+ * prefixes and so on); a block with count 0 is free.  Sequence b holds the first
+ * ceil(context_lens[b] / kv_block_size) entries of its table row.  The plan gives the block size
+ * in bytes (any kv_dtype), num_seqs, max_blocks_per_seq and kv_block_size.
+ *
+ * pda_copy_blocks: block pairs[2i] of src_cache to block pairs[2i+1] of dst_cache, whole
+ * (data and metadata region), for i < num_pairs.
+ *   src_cache, dst_cache   device memory, or pinned host memory that the device can address (a
+ *                          block swapped out or in); the same pool, or two that do not overlap
+ *   pairs                  device, int32 [num_pairs][2]; a pair with a negative id is skipped
+ * A source may be named any number of times.  A destination that is also another pair's source or
+ * destination races with it (no order is kept).  An id past its pool sets PDA_ERRW_BAD_BLOCK_ID and
+ * its pair is skipped.
+ */
+PDA_API int pda_copy_blocks(const pda_plan_t* plan, const void* src_cache, long long src_blocks, void* dst_cache,
+                            long long dst_blocks, const int* pairs, long long num_pairs, int* err_word, void* stream);
+
+/* Bytes of the workspace (16-byte aligned device memory) of pda_fork_sequences with num_rows new rows
+ * and of pda_compact_blocks (num_rows = 0); -1 for an invalid plan or size. */
+PDA_API long long pda_page_workspace_size(const pda_plan_t* plan, int num_rows, long long num_cache_blocks);
+
+/*
+ * pda_fork_sequences -- a batch laid out anew: row i of the new batch is sequence parents[i] of the
+ * old one, grown by new_tokens[i] positions.  One call forks (a parent named by several rows),
+ * reorders, keeps, grows and frees (a sequence that no row names): the step of a beam search, of
+ * parallel sampling, or of continuous batching between two decode steps.
+ *   - Full blocks of the parent are shared.  Its partial last block stays with the first row that
+ *     names it when nothing else holds that block (count 1); every other row gets a copy of it in a
+ *     fresh block, so that rows may append independently.
+ *   - Positions past the last block get fresh blocks.  Fresh blocks are the free blocks of
+ *     `refcounts`, lowest id first, in row order (a row's copy before its new blocks).
+ *   - out_refcounts = refcounts - the entries the old sequences hold + those the new rows hold.
+ *   parents        device, int32 [num_rows], negative: an empty row
+ *   new_tokens     device, int32 [num_rows], or NULL (no growth)
+ *   out_table      device, int32 [num_rows][max_blocks_per_seq]; entries a row does not hold are -1
+ *   out_lens       device, int32 [num_rows]
+ *   out_refcounts  device, int32 [num_cache_blocks]
+ * block_table, context_lens and refcounts are not changed and must not overlap their outputs, and
+ * blocks are copied only into blocks that were free: until the caller drops it the old batch stays
+ * valid, so a call that set an error bit can be repeated with other rows.
+ * Data errors: a parent >= num_seqs (PDA_ERRW_BAD_SEQUENCE), a length past max_blocks_per_seq *
+ * kv_block_size or a negative growth (PDA_ERRW_BAD_POSITION), and a row whose fresh blocks lie past
+ * the last free one (PDA_ERRW_OUT_OF_BLOCKS; the rows before it have theirs) give an empty row (length
+ * 0).  A context length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN).  A held id outside the
+ * pool is carried along and counted nowhere (PDA_ERRW_BAD_BLOCK_ID).
+ */
+PDA_API int pda_fork_sequences(const pda_plan_t* plan, void* kv_cache, long long num_cache_blocks,
+                               const int* block_table, const int* context_lens, const int* refcounts, int num_rows,
+                               const int* parents, const int* new_tokens, int* out_table, int* out_lens,
+                               int* out_refcounts, void* workspace, long long workspace_bytes, int* err_word,
+                               void* stream);
+
+/*
+ * pda_compact_blocks -- moves the blocks in use (count > 0) to ids 0 .. U-1, U their number, so that
+ * the rest of the pool can be given back.  Blocks below U stay; the k-th block in use at or above U
+ * moves to the k-th free id below U.
+ *   out_table      device, int32 [num_seqs][max_blocks_per_seq]: the table with the new ids; entries a
+ *                  sequence does not hold are -1
+ *   out_refcounts  device, int32 [num_cache_blocks]
+ *   remap          device, int32 [num_cache_blocks]: the new id of each block, -1 for a free one (for
+ *                  tables the caller keeps elsewhere)
+ *   num_used       device, int32 [1]: U
+ * The inputs are not changed, must not overlap their outputs, and stay valid until a block at or past
+ * U is overwritten.  A held id that is outside the pool or free becomes -1 (PDA_ERRW_BAD_BLOCK_ID).
+ */
+PDA_API int pda_compact_blocks(const pda_plan_t* plan, void* kv_cache, long long num_cache_blocks,
+                               const int* block_table, const int* context_lens, const int* refcounts, int* out_table,
+                               int* out_refcounts, int* remap, int* num_used, void* workspace,
+                               long long workspace_bytes, int* err_word, void* stream);
+
+/* ---------------------------------------------------------------- attention over selected blocks
+ * For long contexts: keep a summary of every block, score the blocks of a sequence against the step's
+ * query, select some of them per (sequence, KV head), attend to those.
+ *
+ * A summary holds, per KV head, the largest and the smallest value of each key dimension over the
+ * block's tokens: bf16 [num_cache_blocks][num_kv_heads][2: max, min][128], rounded outwards (bf16
+ * keys exactly), pda_summary_size bytes, 16-byte aligned.  Keys must be finite.
+ */
+PDA_API long long pda_summary_size(const pda_plan_t* plan, long long num_cache_blocks);
+
+/*
+ * pda_summarize_blocks -- writes the summaries of the blocks that hold tokens since[b] ..
+ * context_lens[b]-1 of each sequence, each over all its tokens below context_lens[b] (call it after
+ * pda_append_kv with the position appended, or with since NULL for whole contexts).
+ *   since      device, int32 [num_seqs] or NULL
+ *   centroids  device, fp32 [16] for a TQ4 plan, else NULL
+ * A block id outside the pool is skipped (PDA_ERRW_BAD_BLOCK_ID).  Sequences that share a block must
+ * give it the same tokens, or race.
+ */
+PDA_API int pda_summarize_blocks(const pda_plan_t* plan, const void* kv_cache, long long num_cache_blocks,
+                                 const int* block_table, const int* context_lens, const int* since,
+                                 const float* centroids, void* summaries, int* err_word, void* stream);
+
+/*
+ * pda_score_blocks -- scores[b][h][j] = softmax_scale * max over the query rows r of KV head h of
+ *   sum_d max(q_rd, 0) * kmax_d + min(q_rd, 0) * kmin_d,
+ * an upper bound of every logit of block j.  scores: device, fp32 [num_seqs][num_kv_heads]
+ * [max_blocks_per_seq]; entries past the context are left as they are.  A block id outside the pool
+ * scores -inf (PDA_ERRW_BAD_BLOCK_ID).  query as for pda_decode, in device memory.
+ */
+PDA_API int pda_score_blocks(const pda_plan_t* plan, const void* query, const void* summaries,
+                             long long num_cache_blocks, const int* block_table, const int* context_lens,
+                             float* scores, int* err_word, void* stream);
+
+/*
+ * pda_select_blocks -- per (sequence, KV head): the first num_first blocks, the last num_last, and of
+ * the others those with the highest scores (of equal scores the first; NaN lowest), num_select blocks
+ * in all, or every block where there are no more.
+ *   sel_table   device, int32 [num_seqs][num_kv_heads][num_select]: their block ids in the sequence's
+ *               order, then -1
+ *   sel_lens    device, int32 [num_seqs][num_kv_heads]: their tokens
+ *   sel_blocks  device, int32 like sel_table, or NULL: their indices in the sequence
+ * num_first + num_last <= num_select.  With num_last >= 1 the newest block, the only one that may be
+ * partly filled, is always among them.
+ */
+PDA_API int pda_select_blocks(const pda_plan_t* plan, const float* scores, const int* block_table,
+                              const int* context_lens, int num_select, int num_first, int num_last, int* sel_table,
+                              int* sel_lens, int* sel_blocks, int* err_word, void* stream);
+
+/*
+ * pda_decode_selected -- a decode step over selected blocks: the partition pass and the reduce, with one
+ * table row and one length per (sequence, KV head).
+ *   plan        as for pda_decode, with max_blocks_per_seq = num_select (kernel_variant automatic or
+ *               head warps, else PDA_ERR_UNSUPPORTED)
+ *   centroids   device, fp32 [16] for a TQ4 plan, else NULL
+ *   sel_table   device, int32 [num_seqs][num_kv_heads][max_blocks_per_seq]
+ *   sel_lens    device, int32 [num_seqs][num_kv_heads]: tokens; all blocks but the last are full
+ *   partials, out, out_dtype and the data errors as for pda_decode and pda_reduce
+ * query may be pinned host memory as for pda_decode, and out as for pda_reduce.
+ */
+PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* kv_cache,
+                                long long num_cache_blocks, const float* centroids, const int* sel_table,
+                                const int* sel_lens, float* partial_out, float* exp_sums, float* max_logits, void* out,
+                                int out_dtype, int* err_word, void* stream);
 
 /* Human-readable name of a pda_status value (static string; never NULL). */
 PDA_API const char* pda_status_string(int status);

@@ -31,6 +31,8 @@ ERRW_BAD_CONTEXT_LEN = 1
 ERRW_BAD_BLOCK_ID = 2
 ERRW_PIPELINE_TIMEOUT = 4
 ERRW_BAD_POSITION = 8
+ERRW_BAD_SEQUENCE = 16
+ERRW_OUT_OF_BLOCKS = 32
 HEAD_DIM = 128
 VARIANT_AUTO = 0
 VARIANT_HEAD_WARPS = 1
@@ -98,6 +100,22 @@ def lib():
             L.pda_decode_step_noalloc.argtypes = [P, _VP, _VP, ctypes.c_longlong, _VP, _VP, _VP, ctypes.c_int, _VP,
                                                   _VP]
             L.pda_decode_step_noalloc.restype = ctypes.c_int
+            CLL, CI = ctypes.c_longlong, ctypes.c_int
+            L.pda_copy_blocks.argtypes = [P, _VP, CLL, _VP, CLL, _VP, CLL, _VP, _VP]
+            L.pda_page_workspace_size.argtypes = [P, CI, CLL]
+            L.pda_page_workspace_size.restype = CLL
+            L.pda_fork_sequences.argtypes = [P, _VP, CLL, _VP, _VP, _VP, CI, _VP, _VP, _VP, _VP, _VP, _VP, CLL, _VP,
+                                             _VP]
+            L.pda_compact_blocks.argtypes = [P, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, CLL, _VP, _VP]
+            L.pda_summary_size.argtypes = [P, CLL]
+            L.pda_summary_size.restype = CLL
+            L.pda_summarize_blocks.argtypes = [P, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
+            L.pda_score_blocks.argtypes = [P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP]
+            L.pda_select_blocks.argtypes = [P, _VP, _VP, _VP, CI, CI, CI, _VP, _VP, _VP, _VP, _VP]
+            L.pda_decode_selected.argtypes = [P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, _VP, CI, _VP, _VP]
+            for f in (L.pda_copy_blocks, L.pda_fork_sequences, L.pda_compact_blocks, L.pda_summarize_blocks,
+                      L.pda_score_blocks, L.pda_select_blocks, L.pda_decode_selected):
+                f.restype = CI
             L.pda_kernel_variant.argtypes = [P]
             L.pda_kernel_variant.restype = ctypes.c_int
             L.pda_plan_struct_size.argtypes = []
@@ -321,3 +339,180 @@ def decode_step_noalloc(p: Plan, query, kv_cache, num_cache_blocks: int, block_t
     rc = lib().pda_decode_step_noalloc(ctypes.byref(p), *args)
     if rc != 0:
         raise PdaError(rc, "pda_decode_step_noalloc")
+
+
+# ------------------------------------------------------------------------------------------------
+# Pages of the cache, and attention over selected blocks.  Every tensor of a call lies on one GPU,
+# which the call makes current; `stream` defaults to that GPU's current stream.
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_I32 = torch.int32
+
+
+class _Call:
+    """Checks the tensors of one call: on the device of the first, contiguous, large enough."""
+
+    def __init__(self, t: torch.Tensor, name: str):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        self.index = t.get_device()
+
+    def ptr(self, t, name: str, dtype, nbytes: int, host_ok: bool = False):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != self.index and not (host_ok and t.device.type == "cpu" and t.is_pinned()):
+            raise ValueError(f"{name} must be on cuda:{self.index}" + (" or pinned host memory" if host_ok else ""))
+        if dtype is not None and t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+            raise ValueError(f"{name} has dtype {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.nbytes < nbytes:
+            raise ValueError(f"{name} is too small ({t.nbytes} < {nbytes} bytes)")
+        return t.data_ptr()
+
+    def opt(self, t, name: str, dtype, nbytes: int):
+        return None if t is None else self.ptr(t, name, dtype, nbytes)
+
+    def run(self, what: str, fn, p: Plan, args: tuple, err_word, stream) -> None:
+        err = None if err_word is None else self.ptr(err_word, "err_word", _I32, 4)
+        if torch.cuda.current_device() == self.index:
+            rc = fn(p, *args, err, self._stream(stream))
+        else:
+            with torch.cuda.device(self.index):
+                rc = fn(p, *args, err, self._stream(stream))
+        if rc != 0:
+            raise PdaError(rc, what)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.index).cuda_stream
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _scratch(ws: dict, stream) -> dict:
+    """A workspace of the call's own, not handed out again before `stream` has passed the call."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in ws.values():
+            t.record_stream(s)
+    return ws
+
+
+def copy_blocks(p: Plan, src_cache, src_blocks: int, dst_cache, dst_blocks: int, pairs, err_word=None,
+                stream=None) -> None:
+    """pda_copy_blocks: block pairs[i, 0] of src_cache to block pairs[i, 1] of dst_cache (see
+    include/pda.h).  pairs: int32 [n][2].  Either cache may be pinned host memory."""
+    c = _Call(pairs, "pairs")
+    n = pairs.numel() // 2
+    cbb = p.cache_block_bytes
+    args = (c.ptr(src_cache, "src_cache", None, src_blocks * cbb, host_ok=True), src_blocks,
+            c.ptr(dst_cache, "dst_cache", None, dst_blocks * cbb, host_ok=True), dst_blocks,
+            c.ptr(pairs, "pairs", _I32, n * 8), n)
+    c.run("pda_copy_blocks", lib().pda_copy_blocks, p, args, err_word, stream)
+
+
+def page_workspace(p: Plan, num_rows: int, num_cache_blocks: int, device):
+    """The workspace of fork_sequences with up to num_rows rows, and of compact_blocks."""
+    n = lib().pda_page_workspace_size(p, num_rows, num_cache_blocks)
+    if n < 0:
+        raise PdaError(-1, "pda_page_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fork_sequences(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, refcounts, parents, out_table,
+                   out_lens, out_refcounts, workspace, new_tokens=None, err_word=None, stream=None) -> None:
+    """pda_fork_sequences: row i of the new batch is old sequence parents[i] grown by new_tokens[i]
+    positions; sequences that no row names are freed (see include/pda.h).  parents: int32 [R];
+    out_table: int32 [R][max_blocks_per_seq]; workspace: page_workspace(p, R, ...) or larger."""
+    c = _Call(kv_cache, "kv_cache")
+    B, MB, NB, R = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks, parents.numel()
+    args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,
+            c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
+            c.ptr(refcounts, "refcounts", _I32, NB * 4), R, c.ptr(parents, "parents", _I32, R * 4),
+            c.opt(new_tokens, "new_tokens", _I32, R * 4), c.ptr(out_table, "out_table", _I32, R * MB * 4),
+            c.ptr(out_lens, "out_lens", _I32, R * 4), c.ptr(out_refcounts, "out_refcounts", _I32, NB * 4),
+            c.ptr(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    c.run("pda_fork_sequences", lib().pda_fork_sequences, p, args, err_word, stream)
+
+
+def compact_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, refcounts, out_table,
+                   out_refcounts, remap, num_used, workspace, err_word=None, stream=None) -> None:
+    """pda_compact_blocks: moves the blocks in use to the low end of the pool (see include/pda.h)."""
+    c = _Call(kv_cache, "kv_cache")
+    B, MB, NB = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks
+    args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,
+            c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
+            c.ptr(refcounts, "refcounts", _I32, NB * 4), c.ptr(out_table, "out_table", _I32, B * MB * 4),
+            c.ptr(out_refcounts, "out_refcounts", _I32, NB * 4), c.ptr(remap, "remap", _I32, NB * 4),
+            c.ptr(num_used, "num_used", _I32, 4), c.ptr(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    c.run("pda_compact_blocks", lib().pda_compact_blocks, p, args, err_word, stream)
+
+
+def block_summaries(p: Plan, num_cache_blocks: int, device):
+    """Summaries of every block: bf16 [num_cache_blocks][num_kv_heads][2: max, min][128]."""
+    return torch.empty((num_cache_blocks, p.num_kv_heads, 2, p.head_dim), dtype=torch.bfloat16, device=device)
+
+
+def summarize_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, summaries, since=None,
+                     centroids=None, err_word=None, stream=None) -> None:
+    """pda_summarize_blocks: renews the summaries of the blocks with tokens since[b] and later (all
+    blocks without `since`; see include/pda.h).  centroids: fp32 [16], for a TQ4 plan."""
+    c = _Call(kv_cache, "kv_cache")
+    B, MB, NB = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks
+    args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,
+            c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
+            c.opt(since, "since", _I32, B * 4), c.opt(centroids, "centroids", torch.float32, 64),
+            c.ptr(summaries, "summaries", _BF16, NB * p.num_kv_heads * 512))
+    c.run("pda_summarize_blocks", lib().pda_summarize_blocks, p, args, err_word, stream)
+
+
+def score_blocks(p: Plan, query, summaries, num_cache_blocks: int, block_table, context_lens, scores, err_word=None,
+                 stream=None) -> None:
+    """pda_score_blocks: an upper bound of every block's logits, fp32 [B][Hk][max_blocks_per_seq]
+    (see include/pda.h)."""
+    c = _Call(summaries, "summaries")
+    B, Hk, MB, NB = p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq, num_cache_blocks
+    args = (c.ptr(query, "query", _BF16, B * Hk * p.query_group_size * p.head_dim * 2),
+            c.ptr(summaries, "summaries", _BF16, NB * Hk * 512), NB,
+            c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
+            c.ptr(scores, "scores", torch.float32, B * Hk * MB * 4))
+    c.run("pda_score_blocks", lib().pda_score_blocks, p, args, err_word, stream)
+
+
+def select_blocks(p: Plan, scores, block_table, context_lens, num_select: int, num_first: int, num_last: int,
+                  sel_table, sel_lens, sel_blocks=None, err_word=None, stream=None) -> None:
+    """pda_select_blocks: the blocks each (sequence, KV head) attends to (see include/pda.h).
+    sel_table, sel_blocks: int32 [B][Hk][num_select]; sel_lens: int32 [B][Hk]."""
+    c = _Call(scores, "scores")
+    B, Hk, MB = p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq
+    need = B * Hk * max(num_select, 0) * 4
+    args = (c.ptr(scores, "scores", torch.float32, B * Hk * MB * 4),
+            c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
+            num_select, num_first, num_last, c.ptr(sel_table, "sel_table", _I32, need),
+            c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4), c.opt(sel_blocks, "sel_blocks", _I32, need))
+    c.run("pda_select_blocks", lib().pda_select_blocks, p, args, err_word, stream)
+
+
+def decode_selected(p: Plan, query, kv_cache, num_cache_blocks: int, sel_table, sel_lens, ws: dict | None = None,
+                    out=None, out_dtype=torch.bfloat16, centroids=None, err_word=None, stream=None):
+    """pda_decode_selected: a decode step over the blocks in sel_table [B][Hk][max_blocks_per_seq],
+    sel_lens [B][Hk] tokens (see include/pda.h); returns out [B][Hk*QG][D]."""
+    c = _Call(kv_cache, "kv_cache")
+    B, Hk, QG, D, P = p.num_seqs, p.num_kv_heads, p.query_group_size, p.head_dim, p.num_partitions
+    if ws is None:
+        ws = _scratch(workspace(p, kv_cache.device), stream)
+    if out is None:
+        out = torch.empty((B, Hk * QG, D), dtype=out_dtype, device=kv_cache.device)
+    rows = B * Hk * QG
+    f32 = out.dtype is torch.float32
+    args = (c.ptr(query, "query", _BF16, rows * D * 2, host_ok=True),
+            c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.opt(centroids, "centroids", torch.float32, 64),
+            c.ptr(sel_table, "sel_table", _I32, B * Hk * p.max_blocks_per_seq * 4),
+            c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4),
+            c.ptr(ws["partial_out"], "partial_out", torch.float32, rows * P * D * 4),
+            c.ptr(ws["exp_sums"], "exp_sums", torch.float32, rows * P * 4),
+            c.ptr(ws["max_logits"], "max_logits", torch.float32, rows * P * 4),
+            c.ptr(out, "out", (torch.float32, torch.bfloat16), rows * D * (4 if f32 else 2), host_ok=True),
+            OUT_F32 if f32 else OUT_BF16)
+    c.run("pda_decode_selected", lib().pda_decode_selected, p, args, err_word, stream)
+    return out

@@ -303,6 +303,7 @@ static int decode_launch(const pda_plan_t* plan, const void* query, const void* 
 
     a.HG = 1;
     a.sched = nullptr;
+    a.sel_heads = 0;
     CUtensorMap kv_map, sc_map;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (plan->kv_dtype == PDA_KV_FP8_E4M3 && use_head_groups(plan)) {
@@ -371,6 +372,74 @@ int pda_reduce(const pda_plan_t* plan, const int* context_lens, const float* par
     r.W = plan->partition_tokens;
     r.out_f32 = out_dtype == PDA_OUT_F32;
     return launch_reduce(r, static_cast<cudaStream_t>(stream));
+}
+
+int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+                        const float* centroids, const int* sel_table, const int* sel_lens, float* partial_out,
+                        float* exp_sums, float* max_logits, void* out, int out_dtype, int* err_word, void* stream) {
+    if (!plan || !plan_matches(plan)) return PDA_ERR_INVALID_ARG;
+    const bool tq = plan->kv_dtype == PDA_KV_TQ4;
+    if (tq != (centroids != nullptr) || (out_dtype != PDA_OUT_BF16 && out_dtype != PDA_OUT_F32))
+        return PDA_ERR_INVALID_ARG;
+    // the other layouts share a block's copy between heads or take their units per sequence
+    if (plan->kernel_variant > PDA_VARIANT_HEAD_WARPS) return PDA_ERR_UNSUPPORTED;
+    if (plan->num_seqs == 0) return PDA_OK;
+    if (!query || !kv_cache || !sel_table || !sel_lens || !partial_out || !exp_sums || !max_logits || !out)
+        return PDA_ERR_INVALID_ARG;
+    if (num_cache_blocks < 1 || num_cache_blocks > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
+    if (!aligned16(query) || !aligned16(kv_cache) || !aligned16(partial_out)) return PDA_ERR_INVALID_ARG;
+    if (((uintptr_t)exp_sums & 3u) || ((uintptr_t)max_logits & 3u) || ((uintptr_t)sel_table & 3u) ||
+        ((uintptr_t)sel_lens & 3u) || ((uintptr_t)err_word & 3u) || ((uintptr_t)centroids & 3u) ||
+        ((uintptr_t)out & (out_dtype == PDA_OUT_F32 ? 15u : 7u)))
+        return PDA_ERR_INVALID_ARG;
+    // B * Hk sequences of one KV head each: query rows, partials and output have the same layout
+    DecodeArgs a = {};
+    a.query = static_cast<const uint16_t*>(query);
+    a.block_table = sel_table;
+    a.context_lens = sel_lens;
+    a.centroids = centroids;
+    a.partial_out = partial_out;
+    a.exp_sums = exp_sums;
+    a.max_logits = max_logits;
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.B = plan->num_seqs * plan->num_kv_heads;
+    a.Hk = 1;
+    a.QG = plan->query_group_size;
+    a.MB = plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.P = plan->num_partitions;
+    a.W = plan->partition_tokens;
+    a.bs_shift = plan->kv_block_size == 32 ? 5 : 4;
+    a.HG = 1;
+    a.qk_scale_log2 = plan->resolved_softmax_scale * 1.4426950408889634f;
+    a.timeout_ns = plan->wait_timeout_ns > 0 ? (unsigned long long)plan->wait_timeout_ns : kDefaultTimeoutNs;
+    a.sel_heads = plan->num_kv_heads;
+    CUtensorMap kv_map, sc_map;
+    if (!encode_kv_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+    if (plan->kv_dtype == PDA_KV_BF16)
+        sc_map = kv_map;
+    else if (!encode_scale_map(&sc_map, kv_cache, plan, num_cache_blocks))
+        return PDA_ERR_LAUNCH;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rc = launch_decode_selected(plan->kv_dtype, a, kv_map, sc_map, s);
+    if (rc != PDA_OK) return rc;
+    ReduceArgs r;
+    r.context_lens = sel_lens;
+    r.partial_out = partial_out;
+    r.exp_sums = exp_sums;
+    r.max_logits = max_logits;
+    r.out = out;
+    r.err_word = err_word;
+    r.B = a.B;
+    r.Hk = 1;
+    r.QG = a.QG;
+    r.MB = a.MB;
+    r.BS = a.BS;
+    r.P = a.P;
+    r.W = a.W;
+    r.out_f32 = out_dtype == PDA_OUT_F32;
+    return launch_reduce(r, s);
 }
 
 const char* pda_status_string(int status) {

@@ -34,6 +34,7 @@ struct DecodeArgs {
     int* counters;             // [B][Hk], zero
     void* out;                 // [B][Hk*QG][D] bf16 or fp32
     int out_f32;
+    int sel_heads;             // selected blocks: KV heads of the cache (B counts (sequence, head) pairs, Hk is 1)
 };
 
 struct ReduceArgs {
@@ -60,6 +61,9 @@ int launch_decode_fp8_groups(const DecodeArgs& a, const CUtensorMap& kv_map, con
                              bool fused, cudaStream_t stream);
 // KV heads per CTA of the head-group kernel for Hk heads: the largest divisor of Hk not above 4.
 int group_heads(int Hk);
+// Head warps with one table per (sequence, KV head); a.B, a.Hk and a.sel_heads as stated there.
+int launch_decode_selected(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                           cudaStream_t stream);
 int launch_decode_tq4(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, cudaStream_t stream);
 int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 
