@@ -49,7 +49,7 @@ L2_BYTES = 129e6        # GB300 L2: a step whose KV reads exceed it gets no reus
 # the files that make up the partition kernel (its ncu counters go stale when one changes)
 PARTITION_KERNEL_SOURCES = ("pda_decode.cuh", "pda_group.cuh", "pda_rows.cuh", "pda_merge.cuh", "pda_ptx.cuh", "pda_launch.cuh",
                             "pda_internal.h", "pda_decode_bf16.cu", "pda_decode_fp8.cu", "pda_decode_tq4.cu",
-                            "pda_api.cu")
+                            "pda_decode_selected.cu", "pda_api.cu")
 
 
 def parse():
