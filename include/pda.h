@@ -72,7 +72,8 @@ enum {
     PDA_ERRW_BAD_POSITION = 8,      /* pda_append_kv: a position >= max_blocks_per_seq*kv_block_size;
                                        pda_fork_sequences: a row that would grow past it, or by < 0 */
     PDA_ERRW_BAD_SEQUENCE = 16,     /* pda_fork_sequences: parents[i] >= num_seqs */
-    PDA_ERRW_OUT_OF_BLOCKS = 32     /* pda_fork_sequences: fewer free blocks than the rows need */
+    PDA_ERRW_OUT_OF_BLOCKS = 32,    /* pda_fork_sequences: fewer free blocks than the rows need */
+    PDA_ERRW_BAD_GROUP = 64         /* pda_decode_shared: group_starts not ascending within [0, num_seqs] */
 };
 
 /*
@@ -425,6 +426,39 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
                                 long long num_cache_blocks, const float* centroids, const int* sel_table,
                                 const int* sel_lens, float* partial_out, float* exp_sums, float* max_logits, void* out,
                                 int out_dtype, int* err_word, void* stream);
+
+/* ---------------------------------------------------------------- sequences that share a prefix
+ * pda_decode_shared -- a decode step for a batch whose sequences share prefixes in groups: sequences
+ * group_starts[g] .. group_starts[g+1]-1 attend over the first prefix_lens[g] tokens of group g's blocks and then
+ * over the context_lens[b] tokens of their own.  The prefix is read once for all of a group's query rows
+ * (tensor-core products over 256 rows at a time) instead of once per sequence; out equals a decode over
+ * the concatenation.
+ *   prefix_plan    num_seqs = groups (>= 1), max_blocks_per_seq = row length of prefix_table, and
+ *                  tile_groups_per_partition (pda_shared_tile_groups gives a good one): a prefix is cut into at
+ *                  most num_partitions + 1 pieces.  kernel_variant is not looked at.
+ *   plan           num_seqs = sequences; as for pda_decode over the sequences' own tokens
+ *                  (heads, group size, block size, kv_dtype and softmax_scale equal in both plans;
+ *                  bf16 and fp8: a TQ4 plan is PDA_ERR_UNSUPPORTED)
+ *   group_starts   device, int32 [groups + 1], ascending; sequences outside [group_starts[0],
+ *                  group_starts[groups]) have no prefix
+ *   prefix_table   device, int32 [groups][prefix_plan->max_blocks_per_seq]
+ *   prefix_lens    device, int32 [groups]; a prefix may end inside a block
+ *   block_table, context_lens   device, the sequences' own blocks and lengths (0: prefix only)
+ *   workspace      device, pda_shared_workspace_size bytes, 32-byte aligned
+ *   query, out, out_dtype as for pda_decode and pda_reduce (query and out may be pinned host memory)
+ * The weights of the prefix part are rounded to bf16 (bf16 KV) or f16 (fp8 KV) before their product with V, so
+ * an fp32 out carries that rounding (at most 2^-8 or 2^-11 of each weight).
+ * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN), a group that is not
+ * ascending or leaves [0, num_seqs] as empty (PDA_ERRW_BAD_GROUP; where other groups then overlap, their
+ * rows are undefined), block ids as for pda_decode.
+ */
+PDA_API int pda_shared_tile_groups(const pda_plan_t* plan, int num_groups, int prefix_blocks);
+PDA_API long long pda_shared_workspace_size(const pda_plan_t* prefix_plan, const pda_plan_t* plan);
+PDA_API int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, const void* query,
+                              const void* kv_cache, long long num_cache_blocks, const int* group_starts,
+                              const int* prefix_table, const int* prefix_lens, const int* block_table,
+                              const int* context_lens, void* workspace, long long workspace_bytes, void* out,
+                              int out_dtype, int* err_word, void* stream);
 
 /* Human-readable name of a pda_status value (static string; never NULL). */
 PDA_API const char* pda_status_string(int status);

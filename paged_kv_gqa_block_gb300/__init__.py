@@ -33,6 +33,7 @@ ERRW_PIPELINE_TIMEOUT = 4
 ERRW_BAD_POSITION = 8
 ERRW_BAD_SEQUENCE = 16
 ERRW_OUT_OF_BLOCKS = 32
+ERRW_BAD_GROUP = 64
 HEAD_DIM = 128
 VARIANT_AUTO = 0
 VARIANT_HEAD_WARPS = 1
@@ -113,6 +114,12 @@ def lib():
             L.pda_score_blocks.argtypes = [P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP]
             L.pda_select_blocks.argtypes = [P, _VP, _VP, _VP, CI, CI, CI, _VP, _VP, _VP, _VP, _VP]
             L.pda_decode_selected.argtypes = [P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, _VP, CI, _VP, _VP]
+            L.pda_shared_tile_groups.argtypes = [P, CI, CI]
+            L.pda_shared_tile_groups.restype = CI
+            L.pda_shared_workspace_size.argtypes = [P, P]
+            L.pda_shared_workspace_size.restype = CLL
+            L.pda_decode_shared.argtypes = [P, P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, CLL, _VP, CI, _VP, _VP]
+            L.pda_decode_shared.restype = CI
             for f in (L.pda_copy_blocks, L.pda_fork_sequences, L.pda_compact_blocks, L.pda_summarize_blocks,
                       L.pda_score_blocks, L.pda_select_blocks, L.pda_decode_selected):
                 f.restype = CI
@@ -342,7 +349,7 @@ def decode_step_noalloc(p: Plan, query, kv_cache, num_cache_blocks: int, block_t
 
 
 # ------------------------------------------------------------------------------------------------
-# Pages of the cache, and attention over selected blocks.  Every tensor of a call lies on one GPU,
+# Pages of the cache, attention over selected blocks, and shared prefixes.  Every tensor of a call lies on one GPU,
 # which the call makes current; `stream` defaults to that GPU's current stream.
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I32 = torch.int32
@@ -515,4 +522,54 @@ def decode_selected(p: Plan, query, kv_cache, num_cache_blocks: int, sel_table, 
             c.ptr(out, "out", (torch.float32, torch.bfloat16), rows * D * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_selected", lib().pda_decode_selected, p, args, err_word, stream)
+    return out
+
+
+def shared_plans(num_seqs: int, num_groups: int, num_kv_heads: int, query_group_size: int, kv_block_size: int,
+                 prefix_blocks: int, max_blocks_per_seq: int, kv_dtype: int = KV_BF16, softmax_scale: float = 0.0,
+                 tile_groups_per_partition: int = 1, prefix_tile_groups: int = 0, wait_timeout_ns: int = 0):
+    """The two plans of decode_shared: of the prefixes (num_groups tables of prefix_blocks entries) and of
+    the sequences' own tokens.  prefix_tile_groups 0 asks pda_shared_tile_groups."""
+    p = plan(num_seqs, num_kv_heads, query_group_size, kv_block_size, max_blocks_per_seq, tile_groups_per_partition,
+             kv_dtype=kv_dtype, softmax_scale=softmax_scale, wait_timeout_ns=wait_timeout_ns)
+    if prefix_tile_groups == 0:
+        prefix_tile_groups = lib().pda_shared_tile_groups(p, num_groups, prefix_blocks)
+        if prefix_tile_groups < 0:
+            raise PdaError(prefix_tile_groups, "pda_shared_tile_groups")
+    pp = plan(num_groups, num_kv_heads, query_group_size, kv_block_size, prefix_blocks, prefix_tile_groups,
+              kv_dtype=kv_dtype, softmax_scale=softmax_scale, wait_timeout_ns=wait_timeout_ns)
+    return pp, p
+
+
+def shared_workspace(prefix_plan: Plan, p: Plan, device):
+    """The workspace of decode_shared (torch memory is aligned far beyond what it needs)."""
+    n = lib().pda_shared_workspace_size(prefix_plan, p)
+    if n < 0:
+        raise PdaError(-1, "pda_shared_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def decode_shared(prefix_plan: Plan, p: Plan, query, kv_cache, num_cache_blocks: int, group_starts, prefix_table,
+                  prefix_lens, block_table, context_lens, ws=None, out=None, out_dtype=torch.bfloat16, err_word=None,
+                  stream=None):
+    """pda_decode_shared: a decode step over each group's shared prefix and each sequence's own tokens
+    (see include/pda.h); returns out [B][Hk*QG][D]."""
+    c = _Call(kv_cache, "kv_cache")
+    B, NG = p.num_seqs, prefix_plan.num_seqs
+    if ws is None:
+        ws = _scratch({"ws": shared_workspace(prefix_plan, p, kv_cache.device)}, stream)["ws"]
+    if out is None:
+        out = torch.empty((B, p.num_kv_heads * p.query_group_size, p.head_dim), dtype=out_dtype, device=kv_cache.device)
+    n = B * p.num_kv_heads * p.query_group_size * p.head_dim
+    f32 = out.dtype is torch.float32
+    args = (p, c.ptr(query, "query", _BF16, n * 2, host_ok=True),
+            c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.ptr(group_starts, "group_starts", _I32, (NG + 1) * 4),
+            c.ptr(prefix_table, "prefix_table", _I32, NG * prefix_plan.max_blocks_per_seq * 4),
+            c.ptr(prefix_lens, "prefix_lens", _I32, NG * 4),
+            c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
+            c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(ws, "ws", torch.uint8, 0), ws.nbytes,
+            c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
+            OUT_F32 if f32 else OUT_BF16)
+    c.run("pda_decode_shared", lib().pda_decode_shared, prefix_plan, args, err_word, stream)
     return out

@@ -160,6 +160,36 @@ static bool encode_scale_map(CUtensorMap* m, const void* cache, const pda_plan_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// K or V of one cache block and KV head, one 128-byte chunk of every token (pda_decode_shared): the same
+// dimensions, box {128, BS, 1, 1, 1}.
+bool encode_block_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long nb) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t thb = (cuuint64_t)token_head_bytes(p->kv_dtype);
+    cuuint64_t dims[5] = {128, (cuuint64_t)p->kv_block_size, thb / 128, (cuuint64_t)p->num_kv_heads, (cuuint64_t)nb};
+    cuuint64_t strides[4] = {(cuuint64_t)p->num_kv_heads * thb, 128, thb, (cuuint64_t)p->cache_block_bytes};
+    cuuint32_t box[5] = {128, (cuuint32_t)p->kv_block_size, 1, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(cache), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The K and V scales of one cache block and KV head (fp8): box {BS, 2, 1, 1}, as [field][token].
+bool encode_block_scale_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long nb) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const char* base = static_cast<const char*>(cache) + p->meta_offset_bytes;
+    const cuuint64_t bs = (cuuint64_t)p->kv_block_size;
+    cuuint64_t dims[4] = {bs, 2, (cuuint64_t)p->num_kv_heads, (cuuint64_t)nb};
+    cuuint64_t strides[3] = {bs * 4, bs * 8, (cuuint64_t)p->cache_block_bytes};
+    cuuint32_t box[4] = {(cuuint32_t)bs, 2, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<char*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------------------- plan
 static int compute_plan(const pda_plan_t* in, pda_plan_t* out) {
     *out = *in;

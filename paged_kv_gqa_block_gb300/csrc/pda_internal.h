@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "pda.h"
+
 namespace pda {
 
 constexpr int kHeadDim = 128;
@@ -70,6 +72,10 @@ int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 // The next slot of per-launch counters on the current device (zero; the launch's last CTA leaves
 // it zero).  Sets *status to a pda_status value.
 unsigned int* launch_counter_slot(int* status);
+
+// Tensor maps of pda_decode_shared: one (block, KV head) and 128-byte chunk, or its scales, per copy.
+bool encode_block_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);
+bool encode_block_scale_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();

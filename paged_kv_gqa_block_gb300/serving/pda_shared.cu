@@ -1,0 +1,1021 @@
+// pda_shared.cu -- pda_decode_shared: a decode step for sequences that share prefixes in groups.
+//
+// For query row r of sequence b in group g,
+//   out = softmax(scale [q.K_g ; q.K_b]) [V_g ; V_b],
+// with K_g, V_g the group's prefix and K_b, V_b the sequence's own tokens.  The two parts are
+// computed apart as (m, l, o), the running maximum, the sum of exponentials and the normalised
+// output, and joined: w = l e^(m - M), out = sum w o / sum w.  The own part is the library's
+// partition pass (pda_decode).  The prefix part is one matrix product per group and KV head for the
+// query rows of all its sequences, n_g * QG of them, and this file's first kernel.
+//
+// The prefix pass.  A CTA holds 256 query rows of one (group, KV head) in two tiles of 128 and walks
+// the prefix in steps of 128 tokens: S = Q K^T and O += P V by tcgen05.mma (M = N = 128), S, P and
+// O in tensor memory (two tiles x (128 + 128) columns = all 512; P, 16-bit, lies over the S it was
+// made of).  Warps take one role each:
+//   0-3, 4-7  softmax of tile 0, tile 1: one query row per thread, so a row's maximum and sum need
+//             no shuffles; S is read from TMEM, P written back
+//   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
+//   9         the matrix products (one thread issues)
+//   10-13     fp8 only: e4m3 codes to f16 (exact) between the copy and the product
+// The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
+// softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
+// row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
+// TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
+// P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11); m, l, S and O
+// are fp32.
+//
+// Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
+// row tile) are laid end to end and every CTA takes an equal run; a row tile that is cut leaves one
+// partial per piece.  Nothing depends on how lengths and groups fall.  Bound by the tensor cores
+// where a group has many rows (4 * 256 * D flops per token and pair of tiles), by HBM where it has few.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "pda.h"
+#include "pda_internal.h"
+#include "pda_ptx.cuh"
+#include "pda_tc.cuh"
+
+namespace pda {
+
+constexpr uint32_t kLanes = 0xFFFFFFFFu;
+constexpr int kStep = 128;                 // tokens per step
+constexpr int kTileRows = 128, kUnitRows = 256;
+constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bits
+constexpr int kRawBytes = 16384;           // the same in 8 bits
+constexpr int kScaleBytes = 1024;          // 128 tokens x {K scale, V scale}
+constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
+constexpr float kLazy = 8.f;
+
+struct SharedArgs {
+    const uint16_t* query;       // bf16 [B][Hk*QG][D]
+    const int* group_starts;     // [NG + 1]
+    const int* prefix_table;     // [NG][MP]
+    const int* prefix_lens;      // [NG]
+    float* part_o;               // [B][Hk][slots][QG][D]
+    float* part_l;               // [B][Hk][slots][QG]
+    float* part_m;
+    int* pieces;                 // [B][Hk][QG]: partials of a row
+    int* err_word;
+    long long num_cache_blocks;
+    int B, NG, Hk, QG, MP, BS, P, slots;
+    float qk_scale_log2;
+    unsigned long long timeout_ns;
+};
+
+template <int KV>
+struct SharedCfg {
+    static constexpr bool kF16 = KV != PDA_KV_BF16;              // f16 products, converter warps
+    static constexpr int kSlots = kF16 ? 4 : 5;
+    static constexpr int kThreads = kF16 ? 448 : 320;
+    static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
+    static constexpr int kOffSlots = 2 * kSlotBytes;
+    static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;          // 2 x 16 KB
+    static constexpr int kOffScales = kOffRaw + (kF16 ? 2 * kRawBytes : 0);  // 2 x 1 KB
+    static constexpr int kOffBars = kOffScales + (kF16 ? 2 * kScaleBytes : 0);
+    static constexpr int kSmem = kOffBars + 256;
+};
+// barriers and scalars after kOffBars
+enum {
+    kBarFull = 0,        // [5] a slot holds its tile
+    kBarEmpty = 40,      // [5] the products that read a slot are done
+    kBarQ = 80,          // [2] a tile's query rows are in shared memory
+    kBarS = 96,          // [2] S is in TMEM
+    kBarP = 112,         // [2] P is in TMEM
+    kBarO = 128,         // [2] the unit's last product of a tile is done
+    kBarRawFull = 144,   // [2]
+    kBarRawEmpty = 160,  // [2]
+    kBarScFull = 176,    // [2] scales and their largest are readable
+    kBarScEmpty = 192,   // [2]
+    kBarDrain = 208,
+    kTmemAt = 216,       // TMEM address
+    kAbortAt = 220,      // a wait gave up
+    kFmaxAt = 224        // [2] largest V scale of a step
+};
+
+// ------------------------------------------------------------------------- the split
+struct Split {
+    long long total;   // steps of all row tiles
+    int per;           // steps of a CTA's run
+    bool bad;
+};
+struct Unit {
+    int g, h, rt;          // group, KV head, row tile
+    int seq0, rows;        // first sequence and query rows of the group
+    int len;               // prefix length
+    int step0, steps;      // this piece
+    int slot, pieces;      // its number, and how many the row tile has
+};
+
+// A group's sequences, rows tiles and steps; an out-of-range length or range counts as empty.
+__device__ __forceinline__ void group_shape(const SharedArgs& a, int g, int& seq0, int& rows, int& len, int& tiles,
+                                            int& steps, int& bad) {
+    const int s0 = __ldg(a.group_starts + g), s1 = __ldg(a.group_starts + g + 1);
+    len = __ldg(a.prefix_lens + g);
+    bad = 0;
+    if (len < 0 || len > a.MP * a.BS) {
+        bad |= PDA_ERRW_BAD_CONTEXT_LEN;
+        len = 0;
+    }
+    seq0 = s0;
+    rows = 0;
+    if (s0 < 0 || s1 < s0 || s1 > a.B)
+        bad |= PDA_ERRW_BAD_GROUP;
+    else
+        rows = (s1 - s0) * a.QG;
+    tiles = (rows + kUnitRows - 1) / kUnitRows;
+    steps = (len + kStep - 1) / kStep;
+}
+
+// One warp.  `per` is an even share of the steps, and at least 1/P of the longest prefix, so that a row
+// tile is cut into at most P + 1 pieces (the workspace's slots).
+__device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool report) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    int longest = 0, bad = 0;
+    for (int g = lane; g < a.NG; g += 32) {
+        int s0, rows, len, tiles, steps, e;
+        group_shape(a, g, s0, rows, len, tiles, steps, e);
+        bad |= e;
+        total += (long long)tiles * a.Hk * steps;
+        if (tiles > 0) longest = max(longest, steps);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(kLanes, total, o);
+        longest = max(longest, __shfl_xor_sync(kLanes, longest, o));
+        bad |= __shfl_xor_sync(kLanes, bad, o);
+    }
+    if (report && bad && lane == 0 && a.err_word) atomicOr(a.err_word, bad);
+    Split s;
+    s.total = total;
+    const long long even = (total + ctas - 1) / ctas, least = (longest + a.P - 1) / a.P;
+    s.per = (int)max(max(even, least), 1ll);
+    s.bad = bad != 0;
+    return s;
+}
+
+// One warp: the piece that starts at step `at` of the run of all steps and ends with its row tile or at `end`.
+__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, long long at, long long end) {
+    const int lane = threadIdx.x & 31;
+    Unit u = {};
+    long long before = 0;
+    for (int g0 = 0; g0 < a.NG; g0 += 32) {
+        int seq0 = 0, rows = 0, len = 0, tiles = 0, steps = 0, e;
+        if (g0 + lane < a.NG) group_shape(a, g0 + lane, seq0, rows, len, tiles, steps, e);
+        const long long mine = (long long)tiles * a.Hk * steps;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(kLanes, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const long long lo = before + incl - mine;
+        const unsigned hit = __ballot_sync(kLanes, mine > 0 && lo <= at && at < lo + mine);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            u.g = g0 + src;
+            u.seq0 = __shfl_sync(kLanes, seq0, src);
+            u.rows = __shfl_sync(kLanes, rows, src);
+            u.len = __shfl_sync(kLanes, len, src);
+            const int nt = __shfl_sync(kLanes, tiles, src), ns = __shfl_sync(kLanes, steps, src);
+            const long long base = __shfl_sync(kLanes, lo, src);
+            const long long tile = (at - base) / ns;
+            u.step0 = (int)(at - base - tile * ns);
+            u.h = (int)(tile / nt);
+            u.rt = (int)(tile - (long long)u.h * nt);
+            u.steps = (int)min((long long)(ns - u.step0), end - at);
+            const long long first = base + tile * ns;   // the row tile's own first step
+            u.slot = (int)(at / s.per - first / s.per);
+            u.pieces = (int)((first + ns - 1) / s.per - first / s.per) + 1;
+            return u;
+        }
+        before += __shfl_sync(kLanes, incl, 31);
+    }
+    u.steps = 0;
+    return u;
+}
+
+// ------------------------------------------------------------------------- the prefix pass
+__device__ __forceinline__ void st_global_v8(float* p, const float (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(__float_as_uint(v[0])),
+                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+                 "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32v(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32v(uint32_t addr, uint32_t v) {
+    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+template <int KV>
+struct Prefix {
+    using Cfg = SharedCfg<KV>;
+    static constexpr bool F16 = Cfg::kF16;
+    static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
+
+    const SharedArgs& a;
+    const uint32_t sm;         // shared memory base
+    const uint32_t bars;
+    Split split;
+    long long at, end;         // this CTA's run
+
+    __device__ __forceinline__ Prefix(const SharedArgs& args, uint32_t smem)
+        : a(args), sm(smem), bars(smem + Cfg::kOffBars) {}
+
+    // A whole warp waits (bounded).  False once any wait of the CTA has given up.
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        bool ok = mbar_test_wait(bar, parity);
+        if (!__all_sync(kLanes, ok)) {
+            const uint64_t t0 = global_timer_ns();
+            const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
+            for (;;) {
+                ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+                if (__all_sync(kLanes, ok)) break;
+                const bool late = global_timer_ns() - t0 > a.timeout_ns;
+                if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
+                    sts32v(bars + kAbortAt, 1u);
+                    return false;
+                }
+            }
+        }
+        return true;
+    }
+
+    __device__ __forceinline__ bool next(Unit& u) {
+        if (at >= end) return false;
+        u = find_unit(a, split, at, end);
+        at += u.steps;
+        return u.steps > 0;
+    }
+    __device__ __forceinline__ static bool active(const Unit& u, int tile) {
+        return u.rt * kUnitRows + tile * kTileRows < u.rows;
+    }
+
+    // ---------------------------------------------------------------- copies
+    // Slot order K(0), V(0), K(1), V(1), ...  Each lane copies one (block, 64-dimension half): box
+    // {128 bytes, BS tokens}; the halves are 16 KB apart, so that a slot is the products' operand as
+    // it lands ([half][token][128 bytes], swizzled).  fp8 rows are one 128-byte piece, copied to the
+    // raw slots with the step's scales.
+    __device__ void copies(const CUtensorMap* kv_map, const CUtensorMap* sc_map) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? 2 : Cfg::kSlots;
+        constexpr uint32_t kFull0 = F16 ? kBarRawFull : kBarFull, kEmpty0 = F16 ? kBarRawEmpty : kBarEmpty;
+        constexpr int kBytes = F16 ? kRawBytes : kSlotBytes;
+        const uint32_t base = sm + (F16 ? Cfg::kOffRaw : Cfg::kOffSlots);
+        const int nblk = kStep / a.BS;
+        const int blk = lane / kHalves, half = lane % kHalves;
+        const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+        unsigned seq = 0, step = 0;
+        bool ok = true;
+        Unit u;
+        while (ok && next(u)) {
+            const uint64_t policy = u.rows > kUnitRows ? again : once;   // other row tiles read it too
+            const int* table = a.prefix_table + (long long)u.g * a.MP;
+            const int last = (u.len + a.BS - 1) / a.BS;   // blocks of the prefix
+            int id = 0;
+            if (blk < nblk && u.step0 * nblk + blk < last) id = __ldg(table + u.step0 * nblk + blk);
+            for (int j = 0; ok && j < u.steps; ++j, ++step) {
+                const int b0 = (u.step0 + j) * nblk;
+                const int n = min(nblk, last - b0);
+                const bool mine = blk < n;
+                int nid = 0;
+                if (j + 1 < u.steps && blk < nblk && b0 + nblk + blk < last) nid = __ldg(table + b0 + nblk + blk);
+                if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
+                    atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
+                if (F16 && step >= 2 && !wait(bars + kBarScEmpty + 8 * (step & 1), ((step >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v, ++seq) {   // K, then V
+                    const int s = seq % kNS;
+                    if (seq >= kNS && !wait(bars + kEmpty0 + 8 * s, (seq / kNS - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = bars + kFull0 + 8 * s;
+                    const uint32_t row_bytes = (uint32_t)n * a.BS * 128u * kHalves;
+                    const bool scales = F16 && v == 0;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, row_bytes + (scales ? (uint32_t)n * a.BS * 8u : 0u));
+                    __syncwarp();
+                    if (mine) {
+                        tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
+                                    v * kHalves + half, u.h, id, policy);
+                        if (scales)
+                            tma_load_4d(sm + Cfg::kOffScales + (step & 1) * kScaleBytes + blk * a.BS * 8, sc_map, bar, 0, 0,
+                                        u.h, id, policy);
+                    }
+                    __syncwarp();
+                }
+                id = nid;
+            }
+        }
+        // no copy may land in this CTA's memory after it leaves, whichever role gave up
+        for (int s = 0; s < kNS; ++s)
+            if (seq > (unsigned)s) {
+                const unsigned q = (seq - 1 - s) / kNS;   // the slot's last use
+                (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
+            }
+    }
+
+    // ---------------------------------------------------------------- conversion (fp8)
+    // Thread t turns token t's 128 codes into f16 (exact: every e4m3 value is an f16 value).  Rows past
+    // the prefix become zeros, since a weight of zero does not silence a NaN.
+    __device__ void convert() {
+        const int t = threadIdx.x - 320, lane = t & 31;
+        unsigned seq = 0, step = 0;
+        Unit u;
+        while (next(u)) {
+            for (int j = 0; j < u.steps; ++j, ++step) {
+                const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v, ++seq) {
+                    const int r = seq & 1, s = seq % Cfg::kSlots;
+                    if (!wait(bars + kBarRawFull + 8 * r, (seq >> 1) & 1)) return;
+                    if (v == 0 && t < 32) {   // the step's largest V scale
+                        const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
+                        float f = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = lane + 32 * i;
+                            if (tok < valid) f = fmaxf(f, fabsf(__uint_as_float(lds32v(scale_at(sc, tok, 1)))));
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
+                        if (lane == 0) {
+                            sts32v(bars + kFmaxAt + 4 * (step & 1), __float_as_uint(f));
+                            mbar_arrive(bars + kBarScFull + 8 * (step & 1));
+                        }
+                    }
+                    if (seq >= Cfg::kSlots && !wait(bars + kBarEmpty + 8 * s, (seq / Cfg::kSlots - 1) & 1)) return;
+                    const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + t * 128;
+                    const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + t * 128;
+                    const int x = t & 7;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t w[4], o[8];
+                        lds128(src + ((c ^ x) << 4), w[0], w[1], w[2], w[3]);
+                        if (t >= valid) w[0] = w[1] = w[2] = w[3] = 0u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
+                        const uint32_t d = dst + (c >> 2) * 16384;
+                        const int k = 2 * (c & 3);
+                        sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
+                        sts128(d + (((k + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bars + kBarFull + 8 * s);
+                        mbar_arrive(bars + kBarRawEmpty + 8 * r);
+                    }
+                }
+            }
+        }
+    }
+    // Address of token tok's K (field 0) or V (field 1) scale: [block][field][BS].
+    __device__ __forceinline__ uint32_t scale_at(uint32_t sc, int tok, int field) const {
+        const int b = a.BS == 32 ? tok >> 5 : tok >> 4;
+        return sc + (b * a.BS * 2 + field * a.BS + (tok - b * a.BS)) * 4;
+    }
+
+    // ---------------------------------------------------------------- products
+    __device__ __forceinline__ void qk(uint32_t tmem, int tile, uint32_t slot) const {
+        const uint64_t q = umma_desc(sm + Cfg::kOffQ + tile * kSlotBytes, 16, 1024);
+        const uint64_t k = umma_desc(sm + Cfg::kOffSlots + slot * kSlotBytes, 16, 1024);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t o = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            umma_ss(tmem + tile * 128, q + o, k + o, kIdescQK, i > 0);
+        }
+    }
+    __device__ __forceinline__ void pv(uint32_t tmem, int tile, uint32_t slot, bool accumulate) const {
+        const uint64_t v = umma_desc(sm + Cfg::kOffSlots + slot * kSlotBytes, 16384, 1024);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            umma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
+    }
+    __device__ void products(uint32_t tmem) {
+        const int lane = threadIdx.x & 31;
+        unsigned seq = 0, unit[2] = {0, 0}, np[2] = {0, 0};   // slots used; units and P tiles seen, per tile
+        bool ok = true;
+        Unit u;
+        constexpr int NS = Cfg::kSlots;
+        auto full = [&](unsigned q) { return wait(bars + kBarFull + 8 * (q % NS), (q / NS) & 1); };
+        while (ok && next(u)) {
+            const int tiles = active(u, 1) ? 2 : 1;
+            ok = full(seq);
+            for (int w = 0; ok && w < tiles; ++w) {
+                ok = wait(bars + kBarQ + 8 * w, unit[w]++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    qk(tmem, w, seq % NS);
+                    umma_commit(bars + kBarS + 8 * w);
+                    if (w == tiles - 1) umma_commit(bars + kBarEmpty + 8 * (seq % NS));
+                }
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < u.steps; ++j, seq += 2) {
+                const unsigned vs = seq + 1, ks = seq + 2;
+                const bool more = j + 1 < u.steps;
+                if (!(ok = full(vs))) break;
+                if constexpr (!F16) {
+                    // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
+                    const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+                    if (valid < kStep) {
+                        const uint32_t s = sm + Cfg::kOffSlots + (vs % NS) * kSlotBytes;
+                        for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
+                            sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                            sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                    }
+                }
+                if (more && !(ok = full(ks))) break;
+                for (int w = 0; w < tiles; ++w) {
+                    if (!(ok = wait(bars + kBarP + 8 * w, np[w]++ & 1))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        pv(tmem, w, vs % NS, j > 0);
+                        if (more) {
+                            qk(tmem, w, ks % NS);
+                            umma_commit(bars + kBarS + 8 * w);
+                        } else {
+                            umma_commit(bars + kBarO + 8 * w);
+                        }
+                        if (w == tiles - 1) {
+                            umma_commit(bars + kBarEmpty + 8 * (vs % NS));
+                            if (more) umma_commit(bars + kBarEmpty + 8 * (ks % NS));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        // products in flight read shared memory and TMEM: let them end, whichever role gave up
+        if (lane == 0) umma_commit(bars + kBarDrain);
+        __syncwarp();
+        (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
+    }
+
+    // ---------------------------------------------------------------- softmax
+    // Loads this thread's query row into its tile's operand; returns the factor from S to log2 units.
+    __device__ __forceinline__ float load_q(const Unit& u, int tile, int r, const uint16_t* src) const {
+        const uint32_t dst = sm + Cfg::kOffQ + tile * kSlotBytes + r * 128;
+        uint4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = src ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+        float c = a.qk_scale_log2;
+        if constexpr (F16) {
+            // a power of two that brings the row's largest |q| into [2^14, 2^15): f16 then keeps every bf16 bit
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+            }
+            int e = 0;
+            if (amax > 0.f) e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
+            e = max(-100, min(100, e));
+            const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
+            c *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i].x = pack_f16(bf16_lo(v[i].x) * pw, bf16_hi(v[i].x) * pw);
+                v[i].y = pack_f16(bf16_lo(v[i].y) * pw, bf16_hi(v[i].y) * pw);
+                v[i].z = pack_f16(bf16_lo(v[i].z) * pw, bf16_hi(v[i].z) * pw);
+                v[i].w = pack_f16(bf16_lo(v[i].w) * pw, bf16_hi(v[i].w) * pw);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        fence_proxy_async_shared();
+        return c;
+    }
+
+    // 32 columns of S as logits without the row's factor c: fp8 multiplies by the K scales; tokens
+    // at or past `valid` become -inf.
+    __device__ __forceinline__ void logits(float (&x)[32], const uint32_t (&s)[32], int col0, int valid, uint32_t sc) const {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(s[i]);
+        if constexpr (F16) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                uint32_t k0, k1, k2, k3;
+                lds128(scale_at(sc, col0 + i, 0), k0, k1, k2, k3);
+                x[i] *= __uint_as_float(k0);
+                x[i + 1] *= __uint_as_float(k1);
+                x[i + 2] *= __uint_as_float(k2);
+                x[i + 3] *= __uint_as_float(k3);
+            }
+        }
+        if (valid < kStep) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = col0 + i < valid ? x[i] : -INFINITY;
+        }
+    }
+
+    __device__ void softmax(uint32_t tmem_base, int tile) {
+        const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+        const uint32_t lanes = (uint32_t)(r & ~31) << 16;
+        const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
+        unsigned ns = 0, no = 0, step = 0;
+        Unit u;
+        while (next(u)) {
+            const bool on = active(u, tile);
+            const int row = u.rt * kUnitRows + tile * kTileRows + r;
+            const bool live = row < u.rows;
+            const int b = u.seq0 + row / a.QG, q = row % a.QG;
+            const long long head = (long long)b * a.Hk + u.h;
+            float c = 0.f;
+            if (on) {
+                c = load_q(u, tile, r, live ? a.query + (head * a.QG + q) * kHeadDim : nullptr);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + kBarQ + 8 * tile);
+            }
+            float m = 0.f, l = 0.f, F = 1.f, rF = 1.f;
+            for (int j = 0; j < u.steps; ++j, ++step) {
+                const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+                const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
+                if (F16 && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
+                if (on) {
+                    if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
+                    tc_fence_after();
+                    float top = -INFINITY;
+                    uint32_t s[32];
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_ld32(s, tS + 32 * k);
+                        tmem_wait_ld();
+                        logits(x, s, 32 * k, valid, sc);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+                    }
+                    top = fmaxf(top * c, -1e30f);
+                    float fm = 1.f;
+                    if constexpr (F16) {
+                        fm = __uint_as_float(lds32v(bars + kFmaxAt + 4 * (step & 1)));
+                        if (!(fm > 0.f)) fm = 1.f;
+                    }
+                    if (j == 0) {
+                        m = top;
+                        if constexpr (F16) {
+                            F = fm;
+                            rF = 1.f / fm;
+                        }
+                    } else {
+                        const bool up = top > m + kLazy, fs = F16 && (fm > F * 64.f || fm < F * 0.015625f);
+                        if (__any_sync(kLanes, up || fs)) {
+                            float f = 1.f;
+                            if (up) {
+                                f = ex2(m - top);
+                                m = top;
+                                l *= f;
+                            }
+                            if (fs) {
+                                f *= F / fm;
+                                F = fm;
+                                rF = 1.f / fm;
+                            }
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                tmem_ld32(s, tO + 32 * k);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
+                                tmem_st32(tO + 32 * k, s);
+                            }
+                        }
+                    }
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t p[16];
+                        tmem_ld32(s, tS + 32 * k);
+                        tmem_wait_ld();
+                        logits(x, s, 32 * k, valid, sc);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float p0 = ex2(fmaf(x[i], c, -m)), p1 = ex2(fmaf(x[i + 1], c, -m));
+                            l0 += p0;
+                            l1 += p1;
+                            x[i] = p0;
+                            x[i + 1] = p1;
+                        }
+                        if constexpr (F16) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                uint32_t v0, v1, v2, v3;
+                                lds128(scale_at(sc, 32 * k + i, 1), v0, v1, v2, v3);
+                                const uint32_t vv[4] = {v0, v1, v2, v3};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float w = __uint_as_float(vv[e]) * rF;
+                                    x[i + e] = valid < kStep && 32 * k + i + e >= valid ? 0.f : x[i + e] * w;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            p[i] = F16 ? pack_f16(x[2 * i], x[2 * i + 1]) : pack_bf16(x[2 * i], x[2 * i + 1]);
+                        tmem_st16(tS + 16 * k, p);   // over the columns of S already read
+                    }
+                    l += l0 + l1;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + kBarP + 8 * tile);
+                }
+                if (F16) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * (step & 1));
+                }
+            }
+            if (!on) continue;
+            if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
+            tc_fence_after();
+            const float inv = l > 0.f ? F / l : 0.f;
+            const long long at_row = (head * a.slots + u.slot) * a.QG + q;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t s[32];
+                tmem_ld32(s, tO + 32 * k);
+                tmem_wait_ld();
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(s[i + e]) * inv;
+                        st_global_v8(a.part_o + at_row * kHeadDim + 32 * k + i, v);
+                    }
+                }
+            }
+            if (live) {
+                a.part_l[at_row] = l;
+                a.part_m[at_row] = m * kLn2S;
+                if (u.slot == 0) a.pieces[head * a.QG + q] = u.pieces;
+            }
+            tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
+        }
+    }
+};
+
+template <int KV>
+__global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
+    pda_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
+                      const SharedArgs a) {
+    using Cfg = SharedCfg<KV>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sm = smem_addr(smem);
+    const uint32_t bars = sm + Cfg::kOffBars;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cfg::kSlots; ++i) {
+            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 ? 4 : 1);
+            mbar_init(bars + kBarEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + kBarQ + 8 * i, 4);
+            mbar_init(bars + kBarS + 8 * i, 1);
+            mbar_init(bars + kBarP + 8 * i, 4);
+            mbar_init(bars + kBarO + 8 * i, 1);
+            mbar_init(bars + kBarRawFull + 8 * i, 1);
+            mbar_init(bars + kBarRawEmpty + 8 * i, 4);
+            mbar_init(bars + kBarScFull + 8 * i, 1);
+            mbar_init(bars + kBarScEmpty + 8 * i, 8);
+        }
+        mbar_init(bars + kBarDrain, 1);
+        sts32v(bars + kAbortAt, (sm & 1023u) ? 1u : 0u);   // the operands' swizzle needs the alignment
+        fence_mbar_init();
+        prefetch_tensormap(&kv_map);
+        if (Cfg::kF16) prefetch_tensormap(&sc_map);
+    }
+    if (warp == 9) tmem_alloc(bars + kTmemAt, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds32v(bars + kTmemAt);
+    allow_dependent_launch();
+    grid_dependency_wait();
+    Prefix<KV> p(a, sm);
+    p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
+    p.at = (long long)blockIdx.x * p.split.per;
+    p.end = min(p.split.total, p.at + p.split.per);
+    if (lds32v(bars + kAbortAt) == 0u) {
+        if (warp < 8)
+            p.softmax(tmem, warp >> 2);
+        else if (warp == 8)
+            p.copies(&kv_map, &sc_map);
+        else if (warp == 9)
+            p.products(tmem);
+        else if constexpr (Cfg::kF16)
+            p.convert();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0 && lds32v(bars + kAbortAt) && a.err_word) atomicOr(a.err_word, PDA_ERRW_PIPELINE_TIMEOUT);
+    if (warp == 9) tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------------- the join
+struct JoinArgs {
+    const int* group_starts;
+    const int* prefix_lens;
+    const int* context_lens;
+    const float* part_o[2];   // prefix pieces [B][Hk][slots][QG][D]; own partitions [B][Hk][P][QG][D]
+    const float* part_l[2];
+    const float* part_m[2];
+    const int* pieces;
+    void* out;
+    int* err_word;
+    int B, NG, Hk, QG, MP, MB, BS, W, slots, P, out_f32;
+};
+
+// One CTA per (sequence, KV head), one warp per query row: lane i holds (m, l) of partials i, i + 32,
+// ... of both parts, prefix pieces first; each lane then sums four dimensions over the partials in
+// that order, eight loads in flight.  Bound by latency (a row's partials are a few KB, in L2).
+__global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) {
+    grid_dependency_wait();
+    const int b = blockIdx.x / a.Hk, lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const long long unit = blockIdx.x;
+    int np = 0;
+    for (int g0 = 0; g0 < a.NG; g0 += 32) {
+        bool in = false;
+        if (g0 + lane < a.NG) {
+            const int s0 = __ldg(a.group_starts + g0 + lane), s1 = __ldg(a.group_starts + g0 + lane + 1);
+            const int len = __ldg(a.prefix_lens + g0 + lane);
+            in = s0 >= 0 && s1 <= a.B && s0 <= b && b < s1 && len > 0 && len <= a.MP * a.BS;
+        }
+        if (__any_sync(kLanes, in)) np = 1;
+    }
+    if (np) np = max(0, min(a.slots, __ldg(a.pieces + unit * a.QG + q)));
+    int ctx = __ldg(a.context_lens + b);
+    if (ctx < 0 || ctx > a.MB * a.BS) ctx = 0;   // reported by the partition pass
+    const int total = np + (ctx + a.W - 1) / a.W;
+    const long long row0 = unit * a.slots * a.QG + q, row1 = unit * a.P * a.QG + q;
+    auto at = [&](int i, int& part) {   // index of partial i's row in its part
+        part = i >= np;
+        return part ? row1 + (long long)(i - np) * a.QG : row0 + (long long)i * a.QG;
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < total; i += 32) {
+        int part;
+        const long long k = at(i, part);
+        M = fmaxf(M, __ldcg((part ? a.part_m[1] : a.part_m[0]) + k));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kLanes, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int i0 = 0; i0 < total; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < total) {
+            int part;
+            const long long k = at(i0 + lane, part);
+            w = partition_weight(__ldcg((part ? a.part_l[1] : a.part_l[0]) + k),
+                                 __ldcg((part ? a.part_m[1] : a.part_m[0]) + k), M);
+        }
+        sum += w;
+        const int n = min(32, total - i0);
+        for (int j0 = 0; j0 < n; j0 += 8) {
+            float4 o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                int part;
+                const long long k = at(i0 + min(j0 + j, n - 1), part);
+                o[j] = __ldcg(reinterpret_cast<const float4*>((part ? a.part_o[1] : a.part_o[0]) + k * kHeadDim) + lane);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = __shfl_sync(kLanes, w, (j0 + j) & 31);
+                if (j0 + j < n) {
+                    acc.x = fmaf(f, o[j].x, acc.x);
+                    acc.y = fmaf(f, o[j].y, acc.y);
+                    acc.z = fmaf(f, o[j].z, acc.z);
+                    acc.w = fmaf(f, o[j].w, acc.w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kLanes, sum, o);
+    const float inv = total > 0 ? 1.f / sum : 0.f;
+    const long long orow = unit * a.QG + q;
+    if (a.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * kHeadDim + 4 * lane) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        uint2 v;
+        v.x = pack_bf16(acc.x * inv, acc.y * inv);
+        v.y = pack_bf16(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim + 4 * lane) = v;
+    }
+}
+
+// ------------------------------------------------------------------------- host side
+static long long up256(long long x) { return (x + 255) & ~255ll; }
+
+struct SharedLayout {
+    long long o0, l0, m0, pieces, o1, l1, m1, bytes;
+};
+static SharedLayout shared_layout(const pda_plan_t* pp, const pda_plan_t* p) {
+    const long long heads = (long long)p->num_seqs * p->num_kv_heads * p->query_group_size;
+    const long long r0 = heads * (pp->num_partitions + 1), r1 = heads * p->num_partitions;
+    SharedLayout s;
+    s.o0 = 0;
+    s.l0 = s.o0 + up256(r0 * kHeadDim * 4);
+    s.m0 = s.l0 + up256(r0 * 4);
+    s.pieces = s.m0 + up256(r0 * 4);
+    s.o1 = s.pieces + up256(heads * 4);
+    s.l1 = s.o1 + up256(r1 * kHeadDim * 4);
+    s.m1 = s.l1 + up256(r1 * 4);
+    s.bytes = s.m1 + up256(r1 * 4);
+    return s;
+}
+static bool plans_agree(const pda_plan_t* pp, const pda_plan_t* p) {
+    return pp && p && pda_workspace_size(pp) >= 0 && pda_workspace_size(p) >= 0 && pp->num_kv_heads == p->num_kv_heads &&
+           pp->query_group_size == p->query_group_size && pp->kv_block_size == p->kv_block_size &&
+           pp->kv_dtype == p->kv_dtype && pp->resolved_softmax_scale == p->resolved_softmax_scale;
+}
+static bool odd(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+template <int KV>
+static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int sms,
+                         cudaStream_t stream) {
+    using Cfg = SharedCfg<KV>;
+    static bool attr_set[64] = {false};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PDA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(pda_prefix_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
+                cudaSuccess)
+                return PDA_ERR_LAUNCH;
+            attr_set[dev] = true;
+        }
+    }
+    // no more CTAs than there can be steps
+    const long long tiles = ((long long)a.B * a.QG + kUnitRows - 1) / kUnitRows + a.NG;
+    const long long most = tiles * a.Hk * (((long long)a.MP * a.BS + kStep - 1) / kStep);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pda_prefix_kernel<KV>, kv_map, sc_map, a) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+}  // namespace pda
+
+using namespace pda;
+
+extern "C" {
+
+int pda_shared_tile_groups(const pda_plan_t* plan, int num_groups, int prefix_blocks) {
+    if (!plan || pda_workspace_size(plan) < 0 || num_groups < 1 || prefix_blocks < 1) return PDA_ERR_INVALID_ARG;
+    int sms = device_sm_count();
+    if (sms <= 0) sms = 152;   // planned without a GPU
+    // row tiles that work at the same time; with several groups the longest prefix may be twice the
+    // average, and is then cut into twice as many pieces
+    const long long rows = ((long long)plan->num_seqs * plan->query_group_size + kUnitRows - 1) / kUnitRows;
+    const long long tiles = (rows > num_groups ? rows : num_groups) * plan->num_kv_heads;
+    const long long pieces = (sms + tiles - 1) / tiles * (num_groups > 1 ? 2 : 1);
+    const long long tokens = (long long)prefix_blocks * plan->kv_block_size;
+    const long long G = (tokens + pieces * kTokensPerTileGroup - 1) / (pieces * kTokensPerTileGroup);
+    // a piece of fewer than 512 tokens would cost the join more than it saves
+    return (int)(G < 2 ? 2 : G > (1 << 22) ? (1 << 22) : G);
+}
+
+long long pda_shared_workspace_size(const pda_plan_t* prefix_plan, const pda_plan_t* plan) {
+    if (!plans_agree(prefix_plan, plan)) return -1;
+    return shared_layout(prefix_plan, plan).bytes;
+}
+
+int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, const void* query, const void* kv_cache,
+                      long long num_cache_blocks, const int* group_starts, const int* prefix_table,
+                      const int* prefix_lens, const int* block_table, const int* context_lens, void* workspace,
+                      long long workspace_bytes, void* out, int out_dtype, int* err_word, void* stream) {
+    if (!plans_agree(prefix_plan, plan) || (out_dtype != PDA_OUT_BF16 && out_dtype != PDA_OUT_F32))
+        return PDA_ERR_INVALID_ARG;
+    if (plan->kv_dtype == PDA_KV_TQ4) return PDA_ERR_UNSUPPORTED;
+    if (plan->num_seqs == 0) return PDA_OK;
+    if (prefix_plan->num_seqs == 0) return PDA_ERR_INVALID_ARG;   // no groups: that is pda_decode
+    if (!query || !kv_cache || !group_starts || !prefix_table || !prefix_lens || !block_table || !context_lens ||
+        !workspace || !out)
+        return PDA_ERR_INVALID_ARG;
+    if (num_cache_blocks < 1 || num_cache_blocks > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
+    if (odd(query, 16) || odd(kv_cache, 16) || odd(workspace, 32) || odd(group_starts, 4) || odd(prefix_table, 4) ||
+        odd(prefix_lens, 4) || odd(block_table, 4) || odd(context_lens, 4) || odd(err_word, 4) ||
+        odd(out, out_dtype == PDA_OUT_F32 ? 16 : 8))
+        return PDA_ERR_INVALID_ARG;
+    const SharedLayout w = shared_layout(prefix_plan, plan);
+    if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PDA_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto f32 = [&](long long at) { return reinterpret_cast<float*>(ws + at); };
+    SharedArgs a = {};
+    a.query = static_cast<const uint16_t*>(query);
+    a.group_starts = group_starts;
+    a.prefix_table = prefix_table;
+    a.prefix_lens = prefix_lens;
+    a.part_o = f32(w.o0);
+    a.part_l = f32(w.l0);
+    a.part_m = f32(w.m0);
+    a.pieces = reinterpret_cast<int*>(ws + w.pieces);
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.B = plan->num_seqs;
+    a.NG = prefix_plan->num_seqs;
+    a.Hk = plan->num_kv_heads;
+    a.QG = plan->query_group_size;
+    a.MP = prefix_plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.P = prefix_plan->num_partitions;
+    a.slots = a.P + 1;
+    a.qk_scale_log2 = plan->resolved_softmax_scale * kLog2eS;
+    a.timeout_ns = prefix_plan->wait_timeout_ns > 0 ? (unsigned long long)prefix_plan->wait_timeout_ns : kDefaultTimeoutNs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap kv_map, sc_map;
+    if (!encode_block_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+    int rc;
+    if (plan->kv_dtype == PDA_KV_BF16) {
+        rc = launch_prefix<PDA_KV_BF16>(a, kv_map, kv_map, sms, s);
+    } else {
+        if (!encode_block_scale_map(&sc_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+        rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, sms, s);
+    }
+    if (rc != PDA_OK) return rc;
+    rc = pda_decode(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
+                    err_word, stream);
+    if (rc != PDA_OK) return rc;
+    JoinArgs j = {};
+    j.group_starts = group_starts;
+    j.prefix_lens = prefix_lens;
+    j.context_lens = context_lens;
+    j.part_o[0] = f32(w.o0);
+    j.part_l[0] = f32(w.l0);
+    j.part_m[0] = f32(w.m0);
+    j.part_o[1] = f32(w.o1);
+    j.part_l[1] = f32(w.l1);
+    j.part_m[1] = f32(w.m1);
+    j.pieces = a.pieces;
+    j.out = out;
+    j.err_word = err_word;
+    j.B = a.B;
+    j.NG = a.NG;
+    j.Hk = a.Hk;
+    j.QG = a.QG;
+    j.MP = a.MP;
+    j.MB = plan->max_blocks_per_seq;
+    j.BS = a.BS;
+    j.W = plan->partition_tokens;
+    j.slots = a.slots;
+    j.P = plan->num_partitions;
+    j.out_f32 = out_dtype == PDA_OUT_F32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hk));
+    cfg.blockDim = dim3(a.QG * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pda_shared_join_kernel, j) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+}  // extern "C"
