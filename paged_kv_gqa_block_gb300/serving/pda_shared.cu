@@ -16,7 +16,9 @@
 //             no shuffles; S is read from TMEM, P written back
 //   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
 //   9         the matrix products (one thread issues)
-//   10-13     fp8 only: e4m3 codes to f16 (exact) between the copy and the product
+//   10, 11    fp8 only: e4m3 codes to f16 (exact) between the copy and the product
+// The softmax warps hold a whole row of S (128 registers) and take 200 registers each; the other four
+// give some up (104).
 // The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
 // softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
 // row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
@@ -43,6 +45,8 @@ namespace pda {
 
 constexpr uint32_t kLanes = 0xFFFFFFFFu;
 constexpr int kStep = 128;                 // tokens per step
+constexpr int kPrefixThreads = 384;        // three warpgroups
+constexpr int kConvertWarps = 2;
 constexpr int kTileRows = 128, kUnitRows = 256;
 constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bits
 constexpr int kRawBytes = 16384;           // the same in 8 bits
@@ -70,7 +74,6 @@ template <int KV>
 struct SharedCfg {
     static constexpr bool kF16 = KV != PDA_KV_BF16;              // f16 products, converter warps
     static constexpr int kSlots = kF16 ? 4 : 5;
-    static constexpr int kThreads = kF16 ? 448 : 320;
     static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
     static constexpr int kOffSlots = 2 * kSlotBytes;
     static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;          // 2 x 16 KB
@@ -93,7 +96,7 @@ enum {
     kBarDrain = 208,
     kTmemAt = 216,       // TMEM address
     kAbortAt = 220,      // a wait gave up
-    kFmaxAt = 224        // [2] largest V scale of a step
+    kFAt = 224           // [2] what a step's V scales are divided by
 };
 
 // ------------------------------------------------------------------------- the split
@@ -224,6 +227,26 @@ __device__ __forceinline__ void sts32v(uint32_t addr, uint32_t v) {
     asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// Two fp32 operations per instruction.
+__device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, uint32_t a, uint32_t b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "r"(a), "r"(b));
+}
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float c, float d) {   // x c + d
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float2& x, const float2& y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x.x), "+f"(x.y)
+        : "f"(y.x), "f"(y.y));
+}
+
 template <int KV>
 struct Prefix {
     using Cfg = SharedCfg<KV>;
@@ -336,11 +359,15 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- conversion (fp8)
-    // Thread t turns token t's 128 codes into f16 (exact: every e4m3 value is an f16 value).  Rows past
-    // the prefix become zeros, since a weight of zero does not silence a NaN.
+    // A thread turns the 128 codes of tokens t and t + 64 into f16 (exact: every e4m3 value is an f16
+    // value).  Rows past the prefix become zeros, since a weight of zero does not silence a NaN.
+    // The first warp also lays the step's scales out for the softmax as [128 K scales][128 V scales / F].
+    // F keeps P V-scale products in f16's range: it is the step's largest V scale, and stays as
+    // it is while the largest lies in [F/64, 64F] (the accumulator counts in units of F).
     __device__ void convert() {
         const int t = threadIdx.x - 320, lane = t & 31;
         unsigned seq = 0, step = 0;
+        float F = 1.f;
         Unit u;
         while (next(u)) {
             for (int j = 0; j < u.steps; ++j, ++step) {
@@ -349,36 +376,48 @@ struct Prefix {
                 for (int v = 0; v < 2; ++v, ++seq) {
                     const int r = seq & 1, s = seq % Cfg::kSlots;
                     if (!wait(bars + kBarRawFull + 8 * r, (seq >> 1) & 1)) return;
-                    if (v == 0 && t < 32) {   // the step's largest V scale
+                    if (v == 0 && t < 32) {
                         const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
-                        float f = 0.f;
+                        float ks[4], vs[4], f = 0.f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int tok = lane + 32 * i;
-                            if (tok < valid) f = fmaxf(f, fabsf(__uint_as_float(lds32v(scale_at(sc, tok, 1)))));
+                            ks[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 0))) : 0.f;
+                            vs[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 1))) : 0.f;
+                            f = fmaxf(f, fabsf(vs[i]));
                         }
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
-                        if (lane == 0) {
-                            sts32v(bars + kFmaxAt + 4 * (step & 1), __float_as_uint(f));
-                            mbar_arrive(bars + kBarScFull + 8 * (step & 1));
+                        if (!(f > 0.f)) f = 1.f;
+                        if (j == 0 || f > F * 64.f || f < F * 0.015625f) F = f;
+                        const float rF = 1.f / F;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {   // the shuffles above come after every lane's reads
+                            sts32v(sc + (lane + 32 * i) * 4, __float_as_uint(ks[i]));
+                            sts32v(sc + 512 + (lane + 32 * i) * 4, __float_as_uint(vs[i] * rF));
                         }
+                        if (lane == 0) sts32v(bars + kFAt + 4 * (step & 1), __float_as_uint(F));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * (step & 1));
                     }
                     if (seq >= Cfg::kSlots && !wait(bars + kBarEmpty + 8 * s, (seq / Cfg::kSlots - 1) & 1)) return;
-                    const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + t * 128;
-                    const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + t * 128;
                     const int x = t & 7;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t w[4], o[8];
-                        lds128(src + ((c ^ x) << 4), w[0], w[1], w[2], w[3]);
-                        if (t >= valid) w[0] = w[1] = w[2] = w[3] = 0u;
+                    for (int row = t; row < kStep; row += 32 * kConvertWarps) {
+                        const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + row * 128;
+                        const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + row * 128;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
-                        const uint32_t d = dst + (c >> 2) * 16384;
-                        const int k = 2 * (c & 3);
-                        sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
-                        sts128(d + (((k + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t w[4], o[8];
+                            lds128(src + ((c ^ x) << 4), w[0], w[1], w[2], w[3]);
+                            if (row >= valid) w[0] = w[1] = w[2] = w[3] = 0u;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
+                            const uint32_t d = dst + (c >> 2) * 16384;
+                            const int k = 2 * (c & 3);
+                            sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
+                            sts128(d + (((k + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
+                        }
                     }
                     fence_proxy_async_shared();
                     __syncwarp();
@@ -390,7 +429,7 @@ struct Prefix {
             }
         }
     }
-    // Address of token tok's K (field 0) or V (field 1) scale: [block][field][BS].
+    // Address of token tok's K (field 0) or V (field 1) scale as copied: [block][field][BS].
     __device__ __forceinline__ uint32_t scale_at(uint32_t sc, int tok, int field) const {
         const int b = a.BS == 32 ? tok >> 5 : tok >> 4;
         return sc + (b * a.BS * 2 + field * a.BS + (tok - b * a.BS)) * 4;
@@ -515,26 +554,27 @@ struct Prefix {
         return c;
     }
 
-    // 32 columns of S as logits without the row's factor c: fp8 multiplies by the K scales; tokens
-    // at or past `valid` become -inf.
-    __device__ __forceinline__ void logits(float (&x)[32], const uint32_t (&s)[32], int col0, int valid, uint32_t sc) const {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(s[i]);
-        if constexpr (F16) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                uint32_t k0, k1, k2, k3;
-                lds128(scale_at(sc, col0 + i, 0), k0, k1, k2, k3);
-                x[i] *= __uint_as_float(k0);
-                x[i + 1] *= __uint_as_float(k1);
-                x[i + 2] *= __uint_as_float(k2);
-                x[i + 3] *= __uint_as_float(k3);
-            }
+    // Query rows of one unit for this thread's tile.
+    struct Rows {
+        bool on, live;       // the tile has rows; this thread has one
+        long long head;      // (sequence, KV head)
+        int q;
+        float c;             // from S to log2 units
+    };
+    __device__ __forceinline__ Rows start_unit(const Unit& u, int tile, int r) const {
+        Rows w;
+        w.on = active(u, tile);
+        const int row = u.rt * kUnitRows + tile * kTileRows + r;
+        w.live = row < u.rows;
+        w.head = (long long)(u.seq0 + row / a.QG) * a.Hk + u.h;
+        w.q = row % a.QG;
+        w.c = 0.f;
+        if (w.on) {   // every product with the last unit's rows has ended: their S was read
+            w.c = load_q(u, tile, r, w.live ? a.query + (w.head * a.QG + w.q) * kHeadDim : nullptr);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarQ + 8 * tile);
         }
-        if (valid < kStep) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = col0 + i < valid ? x[i] : -INFINITY;
-        }
+        return w;
     }
 
     __device__ void softmax(uint32_t tmem_base, int tile) {
@@ -543,107 +583,100 @@ struct Prefix {
         const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
         unsigned ns = 0, no = 0, step = 0;
         Unit u;
-        while (next(u)) {
-            const bool on = active(u, tile);
-            const int row = u.rt * kUnitRows + tile * kTileRows + r;
-            const bool live = row < u.rows;
-            const int b = u.seq0 + row / a.QG, q = row % a.QG;
-            const long long head = (long long)b * a.Hk + u.h;
-            float c = 0.f;
-            if (on) {
-                c = load_q(u, tile, r, live ? a.query + (head * a.QG + q) * kHeadDim : nullptr);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars + kBarQ + 8 * tile);
-            }
-            float m = 0.f, l = 0.f, F = 1.f, rF = 1.f;
+        bool more = next(u);
+        Rows w;
+        if (more) w = start_unit(u, tile, r);
+        while (more) {
+            float m = 0.f, l = 0.f, F = 1.f;
             for (int j = 0; j < u.steps; ++j, ++step) {
                 const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
                 const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
                 if (F16 && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
-                if (on) {
+                if (w.on) {
                     if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
                     tc_fence_after();
-                    float top = -INFINITY;
-                    uint32_t s[32];
-                    float x[32];
+                    uint32_t s[4][32];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        tmem_ld32(s, tS + 32 * k);
-                        tmem_wait_ld();
-                        logits(x, s, 32 * k, valid, sc);
+                    for (int k = 0; k < 4; ++k) tmem_ld32(s[k], tS + 32 * k);
+                    tmem_wait_ld();
+                    if constexpr (F16) {   // the K scales
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                uint32_t f[4];
+                                lds128(sc + (32 * k + i) * 4, f[0], f[1], f[2], f[3]);
+                                mul2(s[k][i], s[k][i + 1], f[0], f[1]);
+                                mul2(s[k][i + 2], s[k][i + 3], f[2], f[3]);
+                            }
                     }
-                    top = fmaxf(top * c, -1e30f);
-                    float fm = 1.f;
-                    if constexpr (F16) {
-                        fm = __uint_as_float(lds32v(bars + kFmaxAt + 4 * (step & 1)));
-                        if (!(fm > 0.f)) fm = 1.f;
+                    if (valid < kStep) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * k + i >= valid) s[k][i] = 0xFF800000u;   // -inf
                     }
+                    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[0][i]), __uint_as_float(s[0][i + 1])));
+                        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[1][i]), __uint_as_float(s[1][i + 1])));
+                        t2 = fmaxf(t2, fmaxf(__uint_as_float(s[2][i]), __uint_as_float(s[2][i + 1])));
+                        t3 = fmaxf(t3, fmaxf(__uint_as_float(s[3][i]), __uint_as_float(s[3][i + 1])));
+                    }
+                    const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * w.c, -1e30f);
+                    float nF = 1.f;
+                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * (step & 1)));
                     if (j == 0) {
                         m = top;
-                        if constexpr (F16) {
-                            F = fm;
-                            rF = 1.f / fm;
-                        }
                     } else {
-                        const bool up = top > m + kLazy, fs = F16 && (fm > F * 64.f || fm < F * 0.015625f);
-                        if (__any_sync(kLanes, up || fs)) {
-                            float f = 1.f;
+                        const bool up = top > m + kLazy;
+                        if (__any_sync(kLanes, up || nF != F)) {
+                            float f = F / nF;
+                            if (nF == F) f = 1.f;
                             if (up) {
-                                f = ex2(m - top);
+                                const float e = ex2(m - top);
                                 m = top;
-                                l *= f;
+                                l *= e;
+                                f *= e;
                             }
-                            if (fs) {
-                                f *= F / fm;
-                                F = fm;
-                                rF = 1.f / fm;
-                            }
-#pragma unroll 1
-                            for (int k = 0; k < 4; ++k) {
-                                tmem_ld32(s, tO + 32 * k);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
-                                tmem_st32(tO + 32 * k, s);
-                            }
+                            rescale(tO, f);
                         }
                     }
-                    float l0 = 0.f, l1 = 0.f;
+                    F = nF;
+                    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t p[16];
-                        tmem_ld32(s, tS + 32 * k);
-                        tmem_wait_ld();
-                        logits(x, s, 32 * k, valid, sc);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float p0 = ex2(fmaf(x[i], c, -m)), p1 = ex2(fmaf(x[i + 1], c, -m));
-                            l0 += p0;
-                            l1 += p1;
-                            x[i] = p0;
-                            x[i + 1] = p1;
-                        }
-                        if constexpr (F16) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                uint32_t v0, v1, v2, v3;
-                                lds128(scale_at(sc, 32 * k + i, 1), v0, v1, v2, v3);
-                                const uint32_t vv[4] = {v0, v1, v2, v3};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float w = __uint_as_float(vv[e]) * rF;
-                                    x[i + e] = valid < kStep && 32 * k + i + e >= valid ? 0.f : x[i + e] * w;
-                                }
+                        for (int i = 0; i < 32; i += 4) {
+                            fma2(s[k][i], s[k][i + 1], w.c, -m);
+                            fma2(s[k][i + 2], s[k][i + 3], w.c, -m);
+                            float2 x, y;
+                            x.x = ex2(__uint_as_float(s[k][i]));
+                            x.y = ex2(__uint_as_float(s[k][i + 1]));
+                            y.x = ex2(__uint_as_float(s[k][i + 2]));
+                            y.y = ex2(__uint_as_float(s[k][i + 3]));
+                            add2(la, x);
+                            add2(lb, y);
+                            if constexpr (F16) {
+                                uint32_t f[4];
+                                lds128(sc + 512 + (32 * k + i) * 4, f[0], f[1], f[2], f[3]);
+                                uint32_t e[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                                                 __float_as_uint(y.y)};
+                                mul2(e[0], e[1], f[0], f[1]);
+                                mul2(e[2], e[3], f[2], f[3]);
+                                p[i / 2] = pack_f16(__uint_as_float(e[0]), __uint_as_float(e[1]));
+                                p[i / 2 + 1] = pack_f16(__uint_as_float(e[2]), __uint_as_float(e[3]));
+                            } else {
+                                p[i / 2] = pack_bf16(x.x, x.y);
+                                p[i / 2 + 1] = pack_bf16(y.x, y.y);
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            p[i] = F16 ? pack_f16(x[2 * i], x[2 * i + 1]) : pack_bf16(x[2 * i], x[2 * i + 1]);
-                        tmem_st16(tS + 16 * k, p);   // over the columns of S already read
+                        tmem_st16(tS + 16 * k, p);   // over S, which is in registers
                     }
-                    l += l0 + l1;
+                    l += (la.x + la.y) + (lb.x + lb.y);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -654,38 +687,53 @@ struct Prefix {
                     if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * (step & 1));
                 }
             }
-            if (!on) continue;
+            const Rows done = w;
+            const int slot = u.slot, pieces = u.pieces;
+            more = next(u);
+            if (more) w = start_unit(u, tile, r);   // the next unit's first products need not wait for this epilogue
+            if (!done.on) continue;
             if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
             tc_fence_after();
             const float inv = l > 0.f ? F / l : 0.f;
-            const long long at_row = (head * a.slots + u.slot) * a.QG + q;
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                uint32_t s[32];
-                tmem_ld32(s, tO + 32 * k);
-                tmem_wait_ld();
-                if (live) {
+            const long long at_row = (done.head * a.slots + slot) * a.QG + done.q;
+            uint32_t s[4][32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld32(s[k], tO + 32 * k);
+            tmem_wait_ld();
+            tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
+            if (done.live) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(s[i + e]) * inv;
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(s[k][i + e]) * inv;
                         st_global_v8(a.part_o + at_row * kHeadDim + 32 * k + i, v);
                     }
-                }
-            }
-            if (live) {
                 a.part_l[at_row] = l;
                 a.part_m[at_row] = m * kLn2S;
-                if (u.slot == 0) a.pieces[head * a.QG + q] = u.pieces;
+                if (slot == 0) a.pieces[done.head * a.QG + done.q] = pieces;
             }
-            tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
         }
+    }
+    // O *= f, one row per thread (rare; few registers, since S is held meanwhile).
+    static __device__ __forceinline__ void rescale(uint32_t tO, float f) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o, tO + 16 * k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(tO + 16 * k, o);
+        }
+        tmem_wait_st();
     }
 };
 
 template <int KV>
-__global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
+__global__ void __launch_bounds__(kPrefixThreads, 1)
     pda_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                       const SharedArgs a) {
     using Cfg = SharedCfg<KV>;
@@ -695,7 +743,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::kSlots; ++i) {
-            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 ? 4 : 1);
+            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 ? kConvertWarps : 1);
             mbar_init(bars + kBarEmpty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -704,7 +752,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
             mbar_init(bars + kBarP + 8 * i, 4);
             mbar_init(bars + kBarO + 8 * i, 1);
             mbar_init(bars + kBarRawFull + 8 * i, 1);
-            mbar_init(bars + kBarRawEmpty + 8 * i, 4);
+            mbar_init(bars + kBarRawEmpty + 8 * i, kConvertWarps);
             mbar_init(bars + kBarScFull + 8 * i, 1);
             mbar_init(bars + kBarScEmpty + 8 * i, 8);
         }
@@ -725,15 +773,21 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
     p.at = (long long)blockIdx.x * p.split.per;
     p.end = min(p.split.total, p.at + p.split.per);
-    if (lds32v(bars + kAbortAt) == 0u) {
-        if (warp < 8)
-            p.softmax(tmem, warp >> 2);
-        else if (warp == 8)
-            p.copies(&kv_map, &sc_map);
-        else if (warp == 9)
-            p.products(tmem);
-        else if constexpr (Cfg::kF16)
-            p.convert();
+    // 384 threads x 168 registers at launch = 64512 = 256 x 200 + 128 x 104
+    const bool fine = lds32v(bars + kAbortAt) == 0u;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if (fine) p.softmax(tmem, warp >> 2);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (fine) {
+            if (warp == 8)
+                p.copies(&kv_map, &sc_map);
+            else if (warp == 9)
+                p.products(tmem);
+            else if constexpr (Cfg::kF16)
+                p.convert();
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -887,7 +941,7 @@ static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const C
     const long long most = tiles * a.Hk * (((long long)a.MP * a.BS + kStep - 1) / kStep);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
-    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.blockDim = dim3(kPrefixThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
