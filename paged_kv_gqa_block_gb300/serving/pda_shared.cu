@@ -110,6 +110,7 @@ struct Unit {
     int seq0, rows;        // first sequence and query rows of the group
     int len;               // prefix length
     int step0, steps;      // this piece
+    int rot;               // the piece's steps are taken from step0 + rot on, then from step0
     int slot, pieces;      // its number, and how many the row tile has
 };
 
@@ -194,6 +195,11 @@ __device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, l
             const long long first = base + tile * ns;   // the row tile's own first step
             u.slot = (int)(at / s.per - first / s.per);
             u.pieces = (int)((first + ns - 1) / s.per - first / s.per) + 1;
+            // The row tiles of one (group, KV head) read the same tokens, but are cut at different places.
+            // Taking the steps of a piece from the first multiple of `per` on makes every CTA read, at
+            // time t, tokens of step t mod per of its tile: the copies of other row tiles then hit L2.
+            const int s0 = (u.step0 + s.per - 1) / s.per * s.per;
+            u.rot = s0 < u.step0 + u.steps ? s0 - u.step0 : 0;
             return u;
         }
         before += __shfl_sync(kLanes, incl, 31);
@@ -287,6 +293,14 @@ struct Prefix {
         at += u.steps;
         return u.steps > 0;
     }
+    // Step number of the piece's j-th step, and its tokens.
+    __device__ __forceinline__ static int step_of(const Unit& u, int j) {
+        const int i = j + u.rot;
+        return u.step0 + (i < u.steps ? i : i - u.steps);
+    }
+    __device__ __forceinline__ static int tokens_of(const Unit& u, int j) {
+        return min(kStep, u.len - step_of(u, j) * kStep);
+    }
     __device__ __forceinline__ static bool active(const Unit& u, int tile) {
         return u.rt * kUnitRows + tile * kTileRows < u.rows;
     }
@@ -313,13 +327,16 @@ struct Prefix {
             const int* table = a.prefix_table + (long long)u.g * a.MP;
             const int last = (u.len + a.BS - 1) / a.BS;   // blocks of the prefix
             int id = 0;
-            if (blk < nblk && u.step0 * nblk + blk < last) id = __ldg(table + u.step0 * nblk + blk);
+            int b0 = step_of(u, 0) * nblk;
+            if (blk < nblk && b0 + blk < last) id = __ldg(table + b0 + blk);
             for (int j = 0; ok && j < u.steps; ++j, ++step) {
-                const int b0 = (u.step0 + j) * nblk;
                 const int n = min(nblk, last - b0);
                 const bool mine = blk < n;
-                int nid = 0;
-                if (j + 1 < u.steps && blk < nblk && b0 + nblk + blk < last) nid = __ldg(table + b0 + nblk + blk);
+                int nid = 0, b1 = 0;
+                if (j + 1 < u.steps) {
+                    b1 = step_of(u, j + 1) * nblk;
+                    if (blk < nblk && b1 + blk < last) nid = __ldg(table + b1 + blk);
+                }
                 if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
                     atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
                 if (F16 && step >= 2 && !wait(bars + kBarScEmpty + 8 * (step & 1), ((step >> 1) - 1) & 1)) {
@@ -348,6 +365,7 @@ struct Prefix {
                     __syncwarp();
                 }
                 id = nid;
+                b0 = b1;
             }
         }
         // no copy may land in this CTA's memory after it leaves, whichever role gave up
@@ -371,7 +389,7 @@ struct Prefix {
         Unit u;
         while (next(u)) {
             for (int j = 0; j < u.steps; ++j, ++step) {
-                const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+                const int valid = tokens_of(u, j);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v, ++seq) {
                     const int r = seq & 1, s = seq % Cfg::kSlots;
@@ -478,7 +496,7 @@ struct Prefix {
                 if (!(ok = full(vs))) break;
                 if constexpr (!F16) {
                     // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
-                    const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+                    const int valid = tokens_of(u, j);
                     if (valid < kStep) {
                         const uint32_t s = sm + Cfg::kOffSlots + (vs % NS) * kSlotBytes;
                         for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
@@ -589,7 +607,7 @@ struct Prefix {
         while (more) {
             float m = 0.f, l = 0.f, F = 1.f;
             for (int j = 0; j < u.steps; ++j, ++step) {
-                const int valid = min(kStep, u.len - (u.step0 + j) * kStep);
+                const int valid = tokens_of(u, j);
                 const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
                 if (F16 && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
                 if (w.on) {
