@@ -270,21 +270,22 @@ struct Prefix {
 
     // A whole warp waits (bounded).  False once any wait of the CTA has given up.
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-        bool ok = mbar_test_wait(bar, parity);
-        if (!__all_sync(kLanes, ok)) {
-            const uint64_t t0 = global_timer_ns();
-            const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
-            for (;;) {
-                ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-                if (__all_sync(kLanes, ok)) break;
-                const bool late = global_timer_ns() - t0 > a.timeout_ns;
-                if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
-                    sts32v(bars + kAbortAt, 1u);
-                    return false;
-                }
+        const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
+        bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(kLanes, ok)) return true;
+        return wait_on(bar, parity, poll);
+    }
+    __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool poll) const {
+        const uint64_t t0 = global_timer_ns();
+        for (;;) {
+            const bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+            if (__all_sync(kLanes, ok)) return true;
+            const bool late = global_timer_ns() - t0 > a.timeout_ns;
+            if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
+                sts32v(bars + kAbortAt, 1u);
+                return false;
             }
         }
-        return true;
     }
 
     __device__ __forceinline__ bool next(Unit& u) {
@@ -454,51 +455,58 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- products
-    __device__ __forceinline__ void qk(uint32_t tmem, int tile, uint32_t slot) const {
-        const uint64_t q = umma_desc(sm + Cfg::kOffQ + tile * kSlotBytes, 16, 1024);
-        const uint64_t k = umma_desc(sm + Cfg::kOffSlots + slot * kSlotBytes, 16, 1024);
+    static constexpr uint32_t kSlot16 = kSlotBytes >> 4;   // descriptors count 16 bytes
+    static __device__ __forceinline__ void qk(uint32_t leader, uint32_t d, uint64_t q, uint64_t k) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t o = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-            umma_ss(tmem + tile * 128, q + o, k + o, kIdescQK, i > 0);
+            umma_ss(leader, d, q + o, k + o, kIdescQK, i > 0);
         }
     }
-    __device__ __forceinline__ void pv(uint32_t tmem, int tile, uint32_t slot, bool accumulate) const {
-        const uint64_t v = umma_desc(sm + Cfg::kOffSlots + slot * kSlotBytes, 16384, 1024);
+    static __device__ __forceinline__ void pv(uint32_t leader, uint32_t d, uint32_t p, uint64_t v, bool accumulate) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            umma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
+            umma_ts(leader, d, p + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
     }
-    __device__ void products(uint32_t tmem) {
+    __device__ void products(uint32_t tmem_base) {
         const int lane = threadIdx.x & 31;
-        unsigned seq = 0, unit[2] = {0, 0}, np[2] = {0, 0};   // slots used; units and P tiles seen, per tile
+        const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm);
+        const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024);
+        const uint64_t k0 = umma_desc(smu + Cfg::kOffSlots, 16, 1024), v0 = umma_desc(smu + Cfg::kOffSlots, 16384, 1024);
+        const uint32_t bar = uniform(bars);
+        constexpr uint32_t NS = Cfg::kSlots;
+        // the slot of the next tile in the ring and the parity of its full barrier
+        uint32_t slot = 0, ph = 0, unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
         bool ok = true;
         Unit u;
-        constexpr int NS = Cfg::kSlots;
-        auto full = [&](unsigned q) { return wait(bars + kBarFull + 8 * (q % NS), (q / NS) & 1); };
-        while (ok && next(u)) {
-            const int tiles = active(u, 1) ? 2 : 1;
-            ok = full(seq);
-            for (int w = 0; ok && w < tiles; ++w) {
-                ok = wait(bars + kBarQ + 8 * w, unit[w]++ & 1);
+        while (ok && uniform((int)next(u))) {
+            const int tiles = uniform(active(u, 1) ? 2 : 1), steps = uniform(u.steps);
+            ok = wait(bar + kBarFull + 8 * slot, ph);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!ok || w >= tiles) break;
+                uint32_t& n = w ? unit1 : unit0;
+                ok = wait(bar + kBarQ + 8 * w, n);
+                n ^= 1;
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    qk(tmem, w, seq % NS);
-                    umma_commit(bars + kBarS + 8 * w);
-                    if (w == tiles - 1) umma_commit(bars + kBarEmpty + 8 * (seq % NS));
-                }
-                __syncwarp();
+                qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + slot * kSlot16);
+                umma_commit(leader, bar + kBarS + 8 * w);
             }
-            for (int j = 0; ok && j < u.steps; ++j, seq += 2) {
-                const unsigned vs = seq + 1, ks = seq + 2;
-                const bool more = j + 1 < u.steps;
-                if (!(ok = full(vs))) break;
+            if (!ok) break;
+            umma_commit(leader, bar + kBarEmpty + 8 * slot);
+            for (int j = 0; j < steps; ++j) {
+                uint32_t vs = slot + 1, vph = ph;
+                if (vs == NS) vs = 0, vph ^= 1;
+                uint32_t ks = vs + 1, kph = vph;
+                if (ks == NS) ks = 0, kph ^= 1;
+                const bool more = j + 1 < steps;
+                if (!(ok = wait(bar + kBarFull + 8 * vs, vph))) break;
                 if constexpr (!F16) {
                     // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
-                    const int valid = tokens_of(u, j);
+                    const int valid = uniform(tokens_of(u, j));
                     if (valid < kStep) {
-                        const uint32_t s = sm + Cfg::kOffSlots + (vs % NS) * kSlotBytes;
+                        const uint32_t s = sm + Cfg::kOffSlots + vs * kSlotBytes;
                         for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
                             sts128(s + i * 16, 0u, 0u, 0u, 0u);
                             sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
@@ -507,29 +515,28 @@ struct Prefix {
                         __syncwarp();
                     }
                 }
-                if (more && !(ok = full(ks))) break;
-                for (int w = 0; w < tiles; ++w) {
-                    if (!(ok = wait(bars + kBarP + 8 * w, np[w]++ & 1))) break;
+                if (more && !(ok = wait(bar + kBarFull + 8 * ks, kph))) break;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= tiles) break;
+                    uint32_t& n = w ? p1 : p0;
+                    ok = wait(bar + kBarP + 8 * w, n);
+                    n ^= 1;
+                    if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        pv(tmem, w, vs % NS, j > 0);
-                        if (more) {
-                            qk(tmem, w, ks % NS);
-                            umma_commit(bars + kBarS + 8 * w);
-                        } else {
-                            umma_commit(bars + kBarO + 8 * w);
-                        }
-                        if (w == tiles - 1) {
-                            umma_commit(bars + kBarEmpty + 8 * (vs % NS));
-                            if (more) umma_commit(bars + kBarEmpty + 8 * (ks % NS));
-                        }
-                    }
-                    __syncwarp();
+                    pv(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + vs * kSlot16, j > 0);
+                    if (more) qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + ks * kSlot16);
+                    umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
                 }
+                if (!ok) break;
+                umma_commit(leader, bar + kBarEmpty + 8 * vs);
+                if (more) umma_commit(leader, bar + kBarEmpty + 8 * ks);
+                slot = ks;
+                ph = kph;
             }
         }
         // products in flight read shared memory and TMEM: let them end, whichever role gave up
-        if (lane == 0) umma_commit(bars + kBarDrain);
+        umma_commit(leader, bar + kBarDrain);
         __syncwarp();
         (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
     }
