@@ -475,64 +475,74 @@ struct Prefix {
         const uint64_t k0 = umma_desc(smu + Cfg::kOffSlots, 16, 1024), v0 = umma_desc(smu + Cfg::kOffSlots, 16384, 1024);
         const uint32_t bar = uniform(bars);
         constexpr uint32_t NS = Cfg::kSlots;
-        // the slot of the next tile in the ring and the parity of its full barrier
-        uint32_t slot = 0, ph = 0, unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
+        // Position in the ring: slot and parity of its full barrier.
+        struct Pos {
+            uint32_t slot, ph;
+            __device__ __forceinline__ Pos next() const {
+                return slot + 1 == NS ? Pos{0, ph ^ 1} : Pos{slot + 1, ph};
+            }
+        };
+        Pos pos = {0, 0};        // the next tile
+        uint32_t unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
         bool ok = true;
         Unit u;
+        auto full = [&](const Pos& x) { return wait(bar + kBarFull + 8 * x.slot, x.ph); };
         while (ok && uniform((int)next(u))) {
             const int tiles = uniform(active(u, 1) ? 2 : 1), steps = uniform(u.steps);
-            ok = wait(bar + kBarFull + 8 * slot, ph);
+            // the step that holds the prefix's last, partly filled tile (-1: none)
+            int ragged = -1;
+            if (!F16 && u.len % kStep) {
+                const int i = u.len / kStep - u.step0 - u.rot;
+                if (u.len / kStep < u.step0 + u.steps) ragged = i < 0 ? i + u.steps : i;
+            }
+            ragged = uniform(ragged);
+            if (!(ok = full(pos))) break;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                if (!ok || w >= tiles) break;
+                if (w >= tiles) break;
                 uint32_t& n = w ? unit1 : unit0;
-                ok = wait(bar + kBarQ + 8 * w, n);
+                if (!(ok = wait(bar + kBarQ + 8 * w, n))) break;
                 n ^= 1;
-                if (!ok) break;
                 tc_fence_after();
-                qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + slot * kSlot16);
+                qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + pos.slot * kSlot16);
                 umma_commit(leader, bar + kBarS + 8 * w);
             }
             if (!ok) break;
-            umma_commit(leader, bar + kBarEmpty + 8 * slot);
+            umma_commit(leader, bar + kBarEmpty + 8 * pos.slot);
+            if (!(ok = full(pos.next()))) break;
+            // Between one step's last product and the next step's first only the wait for P stands: K(j + 1) is
+            // waited for while PV(0, j) runs, V(j + 1) while QK(0, j + 1) does.
             for (int j = 0; j < steps; ++j) {
-                uint32_t vs = slot + 1, vph = ph;
-                if (vs == NS) vs = 0, vph ^= 1;
-                uint32_t ks = vs + 1, kph = vph;
-                if (ks == NS) ks = 0, kph ^= 1;
                 const bool more = j + 1 < steps;
-                if (!(ok = wait(bar + kBarFull + 8 * vs, vph))) break;
-                if constexpr (!F16) {
+                const Pos v = pos.next(), k = v.next();   // V(j), K(j + 1)
+                if (j == ragged) {
                     // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
-                    const int valid = uniform(tokens_of(u, j));
-                    if (valid < kStep) {
-                        const uint32_t s = sm + Cfg::kOffSlots + vs * kSlotBytes;
-                        for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
-                            sts128(s + i * 16, 0u, 0u, 0u, 0u);
-                            sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_shared();
-                        __syncwarp();
+                    const int valid = u.len % kStep;
+                    const uint32_t s = sm + Cfg::kOffSlots + v.slot * kSlotBytes;
+                    for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
+                        sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                        sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
                     }
+                    fence_proxy_async_shared();
+                    __syncwarp();
                 }
-                if (more && !(ok = wait(bar + kBarFull + 8 * ks, kph))) break;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (w >= tiles) break;
                     uint32_t& n = w ? p1 : p0;
-                    ok = wait(bar + kBarP + 8 * w, n);
+                    if (!(ok = wait(bar + kBarP + 8 * w, n))) break;
                     n ^= 1;
-                    if (!ok) break;
                     tc_fence_after();
-                    pv(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + vs * kSlot16, j > 0);
-                    if (more) qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + ks * kSlot16);
+                    pv(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, j > 0);
+                    if (w == 0 && more && !(ok = full(k))) break;
+                    if (more) qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + k.slot * kSlot16);
                     umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
+                    if (w == 0 && more && !(ok = full(k.next()))) break;
                 }
                 if (!ok) break;
-                umma_commit(leader, bar + kBarEmpty + 8 * vs);
-                if (more) umma_commit(leader, bar + kBarEmpty + 8 * ks);
-                slot = ks;
-                ph = kph;
+                umma_commit(leader, bar + kBarEmpty + 8 * v.slot);
+                if (more) umma_commit(leader, bar + kBarEmpty + 8 * k.slot);
+                pos = k;   // after the last step: the next unit's K(0)
             }
         }
         // products in flight read shared memory and TMEM: let them end, whichever role gave up
