@@ -100,11 +100,6 @@ enum {
 };
 
 // ------------------------------------------------------------------------- the split
-struct Split {
-    long long total;   // steps of all row tiles
-    int per;           // steps of a CTA's run
-    bool bad;
-};
 struct Unit {
     int g, h, rt;          // group, KV head, row tile
     int seq0, rows;        // first sequence and query rows of the group
@@ -114,108 +109,117 @@ struct Unit {
     int slot, pieces;      // its number, and how many the row tile has
 };
 
-// A group's sequences, rows tiles and steps; an out-of-range length or range counts as empty.
-__device__ __forceinline__ void group_shape(const SharedArgs& a, int g, int& seq0, int& rows, int& len, int& tiles,
-                                            int& steps, int& bad) {
+struct Group {
+    int seq0, rows, len;   // first sequence, query rows, prefix length
+    int tiles, steps;      // row tiles and steps of each; a group's steps: tiles * Hk * steps
+};
+// An out-of-range length or range counts as empty.
+__device__ __forceinline__ Group group_shape(const SharedArgs& a, int g, int& bad) {
+    Group x = {};
+    if (g >= a.NG) return x;
     const int s0 = __ldg(a.group_starts + g), s1 = __ldg(a.group_starts + g + 1);
-    len = __ldg(a.prefix_lens + g);
-    bad = 0;
-    if (len < 0 || len > a.MP * a.BS) {
+    x.len = __ldg(a.prefix_lens + g);
+    if (x.len < 0 || x.len > a.MP * a.BS) {
         bad |= PDA_ERRW_BAD_CONTEXT_LEN;
-        len = 0;
+        x.len = 0;
     }
-    seq0 = s0;
-    rows = 0;
+    x.seq0 = s0;
     if (s0 < 0 || s1 < s0 || s1 > a.B)
         bad |= PDA_ERRW_BAD_GROUP;
     else
-        rows = (s1 - s0) * a.QG;
-    tiles = (rows + kUnitRows - 1) / kUnitRows;
-    steps = (len + kStep - 1) / kStep;
+        x.rows = (s1 - s0) * a.QG;
+    x.tiles = (x.rows + kUnitRows - 1) / kUnitRows;
+    x.steps = (x.len + kStep - 1) / kStep;
+    return x;
 }
+// How one warp sees the split: lane i holds group i (and re-reads the others where there are more
+// than 32).  The host has made sure that the number of all steps fits an int.
+struct Split {
+    Group mine;
+    int before, total;     // steps of the groups before lane i's (of the first 32), and of all
+    int per;               // steps of a CTA's run
+};
 
-// One warp.  `per` is an even share of the steps, and at least 1/P of the longest prefix, so that a row
-// tile is cut into at most P + 1 pieces (the workspace's slots).
+// `per` is an even share of the steps, and at least 1/P of the longest prefix, so that a row tile is cut
+// into at most P + 1 pieces (the workspace's slots).
 __device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool report) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
-    int longest = 0, bad = 0;
-    for (int g = lane; g < a.NG; g += 32) {
-        int s0, rows, len, tiles, steps, e;
-        group_shape(a, g, s0, rows, len, tiles, steps, e);
-        bad |= e;
-        total += (long long)tiles * a.Hk * steps;
-        if (tiles > 0) longest = max(longest, steps);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(kLanes, total, o);
-        longest = max(longest, __shfl_xor_sync(kLanes, longest, o));
-        bad |= __shfl_xor_sync(kLanes, bad, o);
-    }
-    if (report && bad && lane == 0 && a.err_word) atomicOr(a.err_word, bad);
     Split s;
-    s.total = total;
-    const long long even = (total + ctas - 1) / ctas, least = (longest + a.P - 1) / a.P;
-    s.per = (int)max(max(even, least), 1ll);
-    s.bad = bad != 0;
+    int bad = 0;
+    s.mine = group_shape(a, lane, bad);
+    const int steps = s.mine.tiles * a.Hk * s.mine.steps;
+    int incl = steps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kLanes, incl, o);
+        if (lane >= o) incl += x;
+    }
+    s.before = incl - steps;
+    s.total = __shfl_sync(kLanes, incl, 31);
+    int longest = s.mine.tiles > 0 ? s.mine.steps : 0;
+    if (a.NG > 32) {
+        int more = 0;
+        for (int g = lane + 32; g < a.NG; g += 32) {
+            const Group x = group_shape(a, g, bad);
+            more += x.tiles * a.Hk * x.steps;
+            if (x.tiles > 0) longest = max(longest, x.steps);
+        }
+        s.total += __reduce_add_sync(kLanes, more);
+    }
+    longest = __reduce_max_sync(kLanes, longest);
+    if (report && bad && a.err_word) atomicOr(a.err_word, bad);
+    s.per = max(max((s.total + ctas - 1) / ctas, (longest + a.P - 1) / a.P), 1);
     return s;
 }
 
 // One warp: the piece that starts at step `at` of the run of all steps and ends with its row tile or at `end`.
-__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, long long at, long long end) {
+__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, int at, int end) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
-    long long before = 0;
-    for (int g0 = 0; g0 < a.NG; g0 += 32) {
-        int seq0 = 0, rows = 0, len = 0, tiles = 0, steps = 0, e;
-        if (g0 + lane < a.NG) group_shape(a, g0 + lane, seq0, rows, len, tiles, steps, e);
-        const long long mine = (long long)tiles * a.Hk * steps;
-        long long incl = mine;
+    Group x = s.mine;
+    int lo = s.before, g0 = 0;
+    unsigned hit;
+    for (;;) {
+        const int n = x.tiles * a.Hk * x.steps;
+        hit = __ballot_sync(kLanes, lo <= at && at < lo + n);
+        if (hit || (g0 += 32) >= a.NG) break;
+        const int next = __shfl_sync(kLanes, lo + n, 31);   // the next 32 groups
+        int bad = 0;
+        x = group_shape(a, g0 + lane, bad);
+        const int m = x.tiles * a.Hk * x.steps;
+        int incl = m;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(kLanes, incl, o);
-            if (lane >= o) incl += x;
+            const int y = __shfl_up_sync(kLanes, incl, o);
+            if (lane >= o) incl += y;
         }
-        const long long lo = before + incl - mine;
-        const unsigned hit = __ballot_sync(kLanes, mine > 0 && lo <= at && at < lo + mine);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            u.g = g0 + src;
-            u.seq0 = __shfl_sync(kLanes, seq0, src);
-            u.rows = __shfl_sync(kLanes, rows, src);
-            u.len = __shfl_sync(kLanes, len, src);
-            const int nt = __shfl_sync(kLanes, tiles, src), ns = __shfl_sync(kLanes, steps, src);
-            const long long base = __shfl_sync(kLanes, lo, src);
-            const long long tile = (at - base) / ns;
-            u.step0 = (int)(at - base - tile * ns);
-            u.h = (int)(tile / nt);
-            u.rt = (int)(tile - (long long)u.h * nt);
-            u.steps = (int)min((long long)(ns - u.step0), end - at);
-            const long long first = base + tile * ns;   // the row tile's own first step
-            u.slot = (int)(at / s.per - first / s.per);
-            u.pieces = (int)((first + ns - 1) / s.per - first / s.per) + 1;
-            // The row tiles of one (group, KV head) read the same tokens, but are cut at different places.
-            // Taking the steps of a piece from the first multiple of `per` on makes every CTA read, at
-            // time t, tokens of step t mod per of its tile: the copies of other row tiles then hit L2.
-            const int s0 = (u.step0 + s.per - 1) / s.per * s.per;
-            u.rot = s0 < u.step0 + u.steps ? s0 - u.step0 : 0;
-            return u;
-        }
-        before += __shfl_sync(kLanes, incl, 31);
+        lo = next + incl - m;
     }
-    u.steps = 0;
+    if (!hit) return u;
+    const int src = __ffs(hit) - 1;
+    u.g = g0 + src;
+    u.seq0 = __shfl_sync(kLanes, x.seq0, src);
+    u.rows = __shfl_sync(kLanes, x.rows, src);
+    u.len = __shfl_sync(kLanes, x.len, src);
+    const int nt = __shfl_sync(kLanes, x.tiles, src), ns = __shfl_sync(kLanes, x.steps, src);
+    const int base = __shfl_sync(kLanes, lo, src);
+    const int tile = (at - base) / ns, first = base + tile * ns;   // the row tile's own first step
+    u.step0 = at - first;
+    u.h = tile / nt;
+    u.rt = tile - u.h * nt;
+    u.steps = min(ns - u.step0, end - at);
+    const int c0 = first / s.per;
+    u.slot = at / s.per - c0;
+    u.pieces = (first + ns - 1) / s.per - c0 + 1;
+    // The row tiles of one (group, KV head) read the same tokens, but are cut at different places.
+    // Taking the steps of a piece from the first multiple of `per` on makes every CTA read, at
+    // time t, tokens of step t mod per of its tile: the copies of other row tiles then hit L2.
+    const int s0 = (u.step0 + s.per - 1) / s.per * s.per;
+    u.rot = s0 < u.step0 + u.steps ? s0 - u.step0 : 0;
     return u;
 }
 
 // ------------------------------------------------------------------------- the prefix pass
-__device__ __forceinline__ void st_global_v8(float* p, const float (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(__float_as_uint(v[0])),
-                 "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
-                 "r"(__float_as_uint(v[7]))
-                 : "memory");
-}
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
@@ -260,13 +264,14 @@ struct Prefix {
     static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
 
     const SharedArgs& a;
+    const uint8_t* const smem;
     const uint32_t sm;         // shared memory base
     const uint32_t bars;
     Split split;
-    long long at, end;         // this CTA's run
+    int at, end;               // this CTA's run
 
-    __device__ __forceinline__ Prefix(const SharedArgs& args, uint32_t smem)
-        : a(args), sm(smem), bars(smem + Cfg::kOffBars) {}
+    __device__ __forceinline__ Prefix(const SharedArgs& args, const uint8_t* base)
+        : a(args), smem(base), sm(smem_addr(base)), bars(sm + Cfg::kOffBars) {}
 
     // A whole warp waits (bounded).  False once any wait of the CTA has given up.
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
@@ -425,13 +430,15 @@ struct Prefix {
                     for (int row = t; row < kStep; row += 32 * kConvertWarps) {
                         const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + row * 128;
                         const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + row * 128;
+                        uint32_t w[8][4];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) lds128(src + ((c ^ x) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            uint32_t w[4], o[8];
-                            lds128(src + ((c ^ x) << 4), w[0], w[1], w[2], w[3]);
-                            if (row >= valid) w[0] = w[1] = w[2] = w[3] = 0u;
+                            uint32_t o[8];
+                            if (row >= valid) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[i], o[2 * i], o[2 * i + 1]);
+                            for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
                             const uint32_t d = dst + (c >> 2) * 16384;
                             const int k = 2 * (c & 3);
                             sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
@@ -552,39 +559,48 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- softmax
-    // Loads this thread's query row into its tile's operand; returns the factor from S to log2 units.
-    __device__ __forceinline__ float load_q(const Unit& u, int tile, int r, const uint16_t* src) const {
-        const uint32_t dst = sm + Cfg::kOffQ + tile * kSlotBytes + r * 128;
+    // The warp's 32 query rows into its tile's operand, two rows (16 lanes each) per load; returns the
+    // factor from S to log2 units of this lane's own row, 32 * (warp % 4) + lane.
+    __device__ __forceinline__ float load_q(const Unit& u, int tile) const {
+        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, half = lane >> 4, w = lane & 15;
+        const uint32_t dst = sm + Cfg::kOffQ + tile * kSlotBytes + (w >> 3) * 16384;
+        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
         uint4 v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            v[i] = src ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-        float c = a.qk_scale_log2;
-        if constexpr (F16) {
-            // a power of two that brings the row's largest |q| into [2^14, 2^15): f16 then keeps every bf16 bit
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
-            }
-            int e = 0;
-            if (amax > 0.f) e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
-            e = max(-100, min(100, e));
-            const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
-            c *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                v[i].x = pack_f16(bf16_lo(v[i].x) * pw, bf16_hi(v[i].x) * pw);
-                v[i].y = pack_f16(bf16_lo(v[i].y) * pw, bf16_hi(v[i].y) * pw);
-                v[i].z = pack_f16(bf16_lo(v[i].z) * pw, bf16_hi(v[i].z) * pw);
-                v[i].w = pack_f16(bf16_lo(v[i].w) * pw, bf16_hi(v[i].w) * pw);
+        for (int i = 0; i < 16; ++i) {
+            const int row = row0 + 2 * i + half;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < u.rows) {
+                const int seq = row / a.QG, q = row - seq * a.QG;
+                v[i] = __ldg(reinterpret_cast<const uint4*>(
+                                 a.query + (((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG + q) * kHeadDim) + w);
             }
         }
+        float c = a.qk_scale_log2;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (F16) {
+                // a power of two that brings the row's largest |q| into [2^14, 2^15): f16 then keeps every bf16 bit
+                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                float amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kLanes, amax, o));
+                int e = 0;
+                if (amax > 0.f) e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
+                e = max(-100, min(100, e));
+                const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
+                const float back = __shfl_sync(kLanes, __uint_as_float((uint32_t)(127 - e) << 23), (lane & 1) << 4);
+                if (lane >> 1 == i) c *= back;   // lane 2i + k owns row 2i + k
+                v[i].x = pack_f16(bf16_lo(x[0]) * pw, bf16_hi(x[0]) * pw);
+                v[i].y = pack_f16(bf16_lo(x[1]) * pw, bf16_hi(x[1]) * pw);
+                v[i].z = pack_f16(bf16_lo(x[2]) * pw, bf16_hi(x[2]) * pw);
+                v[i].w = pack_f16(bf16_lo(x[3]) * pw, bf16_hi(x[3]) * pw);
+            }
+            const int r = r0 + 2 * i + half;
+            sts128(dst + r * 128 + (((w & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        }
         fence_proxy_async_shared();
         return c;
     }
@@ -605,7 +621,7 @@ struct Prefix {
         w.q = row % a.QG;
         w.c = 0.f;
         if (w.on) {   // every product with the last unit's rows has ended: their S was read
-            w.c = load_q(u, tile, r, w.live ? a.query + (w.head * a.QG + w.q) * kHeadDim : nullptr);
+            w.c = load_q(u, tile);
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarQ + 8 * tile);
         }
@@ -618,14 +634,12 @@ struct Prefix {
         const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
         unsigned ns = 0, no = 0, step = 0;
         Unit u;
-        bool more = next(u);
-        Rows w;
-        if (more) w = start_unit(u, tile, r);
-        while (more) {
+        while (next(u)) {
+            const Rows w = start_unit(u, tile, r);
             float m = 0.f, l = 0.f, F = 1.f;
             for (int j = 0; j < u.steps; ++j, ++step) {
                 const int valid = tokens_of(u, j);
-                const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
+                const uint4* scales = reinterpret_cast<const uint4*>(smem + Cfg::kOffScales + (step & 1) * kScaleBytes);
                 if (F16 && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
                 if (w.on) {
                     if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
@@ -639,10 +653,9 @@ struct Prefix {
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
-                                uint32_t f[4];
-                                lds128(sc + (32 * k + i) * 4, f[0], f[1], f[2], f[3]);
-                                mul2(s[k][i], s[k][i + 1], f[0], f[1]);
-                                mul2(s[k][i + 2], s[k][i + 3], f[2], f[3]);
+                                const uint4 f = scales[8 * k + i / 4];
+                                mul2(s[k][i], s[k][i + 1], f.x, f.y);
+                                mul2(s[k][i + 2], s[k][i + 3], f.z, f.w);
                             }
                     }
                     if (valid < kStep) {
@@ -696,12 +709,11 @@ struct Prefix {
                             add2(la, x);
                             add2(lb, y);
                             if constexpr (F16) {
-                                uint32_t f[4];
-                                lds128(sc + 512 + (32 * k + i) * 4, f[0], f[1], f[2], f[3]);
+                                const uint4 f = scales[32 + 8 * k + i / 4];
                                 uint32_t e[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
                                                  __float_as_uint(y.y)};
-                                mul2(e[0], e[1], f[0], f[1]);
-                                mul2(e[2], e[3], f[2], f[3]);
+                                mul2(e[0], e[1], f.x, f.y);
+                                mul2(e[2], e[3], f.z, f.w);
                                 p[i / 2] = pack_f16(__uint_as_float(e[0]), __uint_as_float(e[1]));
                                 p[i / 2 + 1] = pack_f16(__uint_as_float(e[2]), __uint_as_float(e[3]));
                             } else {
@@ -722,35 +734,59 @@ struct Prefix {
                     if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * (step & 1));
                 }
             }
-            const Rows done = w;
-            const int slot = u.slot, pieces = u.pieces;
-            more = next(u);
-            if (more) w = start_unit(u, tile, r);   // the next unit's first products need not wait for this epilogue
-            if (!done.on) continue;
+            if (!w.on) continue;
             if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
             tc_fence_after();
-            const float inv = l > 0.f ? F / l : 0.f;
-            const long long at_row = (done.head * a.slots + slot) * a.QG + done.q;
-            uint32_t s[4][32];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_ld32(s[k], tO + 32 * k);
-            tmem_wait_ld();
+            store_partial(u, tile, tO, w, m, l, l > 0.f ? F / l : 0.f);
             tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
-            if (done.live) {
+        }
+    }
+
+    // The warp's 32 rows of O, times inv, to the partials.  A thread holds a row, and storing rows from
+    // there would touch 32 lines per instruction; each half (64 columns) goes through the warp's own rows of
+    // its tile's query operand, which no product reads any more, and out two rows per instruction.
+    __device__ __forceinline__ void store_partial(const Unit& u, int tile, uint32_t tO, const Rows& w, float m, float l,
+                                                  float inv) const {
+        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96;
+        const uint32_t stage = sm + Cfg::kOffQ + tile * kSlotBytes + r0 * 128;
+        auto at = [&](int r, int c) {   // 16 bytes c of the half row r
+            return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        };
+        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
+        const int rows = min(32, u.rows - row0);   // may be negative
+        const long long mine = (w.head * a.slots + u.slot) * a.QG + w.q;
+        if (w.live) {
+            a.part_l[mine] = l;
+            a.part_m[mine] = m * kLn2S;
+            if (u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
+        }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+        for (int half = 0; half < 2; ++half) {
+            uint32_t s[2][32];
+            tmem_ld32(s[0], tO + 64 * half);
+            tmem_ld32(s[1], tO + 64 * half + 32);
+            tmem_wait_ld();
+            __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(s[k][i + e]) * inv;
-                        st_global_v8(a.part_o + at_row * kHeadDim + 32 * k + i, v);
-                    }
-                a.part_l[at_row] = l;
-                a.part_m[at_row] = m * kLn2S;
-                if (slot == 0) a.pieces[done.head * a.QG + done.q] = pieces;
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t* x = &s[c >> 3][(c & 7) * 4];
+                sts128(at(lane, c), __float_as_uint(__uint_as_float(x[0]) * inv),
+                       __float_as_uint(__uint_as_float(x[1]) * inv), __float_as_uint(__uint_as_float(x[2]) * inv),
+                       __float_as_uint(__uint_as_float(x[3]) * inv));
+            }
+            __syncwarp();
+            const int c = lane & 15;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                const long long dst = __shfl_sync(kLanes, mine, r);
+                uint32_t v0, v1, v2, v3;
+                lds128(at(r, c), v0, v1, v2, v3);
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(a.part_o + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
             }
         }
+        __syncwarp();   // the next unit's query rows are written by other lanes
     }
     // O *= f, one row per thread (rare; few registers, since S is held meanwhile).
     static __device__ __forceinline__ void rescale(uint32_t tO, float f) {
@@ -804,10 +840,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t tmem = lds32v(bars + kTmemAt);
     allow_dependent_launch();
     grid_dependency_wait();
-    Prefix<KV> p(a, sm);
+    Prefix<KV> p(a, smem);
     p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
-    p.at = (long long)blockIdx.x * p.split.per;
-    p.end = min(p.split.total, p.at + p.split.per);
+    p.at = (int)min((long long)blockIdx.x * p.split.per, (long long)p.split.total);
+    p.end = p.at + min(p.split.per, p.split.total - p.at);
     // 384 threads x 168 registers at launch = 64512 = 256 x 200 + 128 x 104
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
@@ -952,10 +988,15 @@ static bool plans_agree(const pda_plan_t* pp, const pda_plan_t* p) {
            pp->query_group_size == p->query_group_size && pp->kv_block_size == p->kv_block_size &&
            pp->kv_dtype == p->kv_dtype && pp->resolved_softmax_scale == p->resolved_softmax_scale;
 }
+// The most steps that the groups can have.
+static long long most_steps(const pda_plan_t* pp, const pda_plan_t* p) {
+    const long long tiles = ((long long)p->num_seqs * p->query_group_size + kUnitRows - 1) / kUnitRows + pp->num_seqs;
+    return tiles * p->num_kv_heads * (((long long)pp->max_blocks_per_seq * pp->kv_block_size + kStep - 1) / kStep);
+}
 static bool odd(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
 template <int KV>
-static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int sms,
+static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int ctas,
                          cudaStream_t stream) {
     using Cfg = SharedCfg<KV>;
     static bool attr_set[64] = {false};
@@ -971,11 +1012,8 @@ static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const C
             attr_set[dev] = true;
         }
     }
-    // no more CTAs than there can be steps
-    const long long tiles = ((long long)a.B * a.QG + kUnitRows - 1) / kUnitRows + a.NG;
-    const long long most = tiles * a.Hk * (((long long)a.MP * a.BS + kStep - 1) / kStep);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kPrefixThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = stream;
@@ -1032,6 +1070,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
         return PDA_ERR_INVALID_ARG;
     const SharedLayout w = shared_layout(prefix_plan, plan);
     if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;
+    if (most_steps(prefix_plan, plan) > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;   // the split counts in ints
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1060,12 +1099,14 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap kv_map, sc_map;
     if (!encode_block_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+    const long long most = most_steps(prefix_plan, plan);   // no more CTAs than there can be steps
+    const int ctas = (int)(most < sms ? most : sms);
     int rc;
     if (plan->kv_dtype == PDA_KV_BF16) {
-        rc = launch_prefix<PDA_KV_BF16>(a, kv_map, kv_map, sms, s);
+        rc = launch_prefix<PDA_KV_BF16>(a, kv_map, kv_map, ctas, s);
     } else {
         if (!encode_block_scale_map(&sc_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
-        rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, sms, s);
+        rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, ctas, s);
     }
     if (rc != PDA_OK) return rc;
     rc = pda_decode(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
