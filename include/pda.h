@@ -446,8 +446,8 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  *   block_table, context_lens   device, the sequences' own blocks and lengths (0: prefix only)
  *   workspace      device, pda_shared_workspace_size bytes, 32-byte aligned
  *   query, out, out_dtype as for pda_decode and pda_reduce (query and out may be pinned host memory)
- * The weights of the prefix part are rounded to bf16 (bf16 KV) or f16 (fp8 KV) before their product with V, so
- * an fp32 out carries that rounding (at most 2^-8 or 2^-11 of each weight).
+ * The weights of the prefix part are rounded to bf16 (bf16 KV), or they and the scaled V to f16 (fp8 KV), before
+ * their product, so an fp32 out carries that rounding (at most 2^-8, or 3 * 2^-11, of each term).
  * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN), a group that is not
  * ascending or leaves [0, num_seqs] as empty (PDA_ERRW_BAD_GROUP; where other groups then overlap, their
  * rows are undefined), block ids as for pda_decode.

@@ -350,6 +350,48 @@ static int decode_launch(const pda_plan_t* plan, const void* query, const void* 
     if (tq) return launch_decode_tq4(a, kv_map, sc_map, s);
     return launch_decode_fp8(a, kv_map, sc_map, fused, s);
 }
+
+// The fields of the partition pass's arguments that a plan gives, for a call of its own kind.
+static DecodeArgs plan_args(const pda_plan_t* plan, const void* query, long long num_cache_blocks,
+                            const int* block_table, const int* context_lens, float* partial_out, float* exp_sums,
+                            float* max_logits, int* err_word) {
+    DecodeArgs a = {};
+    a.query = static_cast<const uint16_t*>(query);
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.partial_out = partial_out;
+    a.exp_sums = exp_sums;
+    a.max_logits = max_logits;
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.B = plan->num_seqs;
+    a.Hk = plan->num_kv_heads;
+    a.QG = plan->query_group_size;
+    a.MB = plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.P = plan->num_partitions;
+    a.W = plan->partition_tokens;
+    a.bs_shift = plan->kv_block_size == 32 ? 5 : 4;
+    a.HG = 1;
+    a.qk_scale_log2 = plan->resolved_softmax_scale * 1.4426950408889634f;
+    a.timeout_ns = plan->wait_timeout_ns > 0 ? (unsigned long long)plan->wait_timeout_ns : kDefaultTimeoutNs;
+    return a;
+}
+
+int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+               const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
+               int W, int P, int* err_word, cudaStream_t stream) {
+    DecodeArgs a = plan_args(plan, query, num_cache_blocks, block_table, context_lens, partial_out, exp_sums, max_logits,
+                             err_word);
+    a.W = W;
+    a.P = P;
+    CUtensorMap kv_map, sc_map;
+    if (!encode_kv_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+    sc_map = kv_map;
+    if (plan->kv_dtype != PDA_KV_BF16 && !encode_scale_map(&sc_map, kv_cache, plan, num_cache_blocks))
+        return PDA_ERR_LAUNCH;
+    return launch_decode_own(plan->kv_dtype, a, kv_map, sc_map, stream);
+}
 }  // namespace pda
 
 extern "C" {
@@ -423,27 +465,10 @@ int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* k
         ((uintptr_t)out & (out_dtype == PDA_OUT_F32 ? 15u : 7u)))
         return PDA_ERR_INVALID_ARG;
     // B * Hk sequences of one KV head each: query rows, partials and output have the same layout
-    DecodeArgs a = {};
-    a.query = static_cast<const uint16_t*>(query);
-    a.block_table = sel_table;
-    a.context_lens = sel_lens;
+    DecodeArgs a = plan_args(plan, query, num_cache_blocks, sel_table, sel_lens, partial_out, exp_sums, max_logits, err_word);
     a.centroids = centroids;
-    a.partial_out = partial_out;
-    a.exp_sums = exp_sums;
-    a.max_logits = max_logits;
-    a.err_word = err_word;
-    a.num_cache_blocks = num_cache_blocks;
     a.B = plan->num_seqs * plan->num_kv_heads;
     a.Hk = 1;
-    a.QG = plan->query_group_size;
-    a.MB = plan->max_blocks_per_seq;
-    a.BS = plan->kv_block_size;
-    a.P = plan->num_partitions;
-    a.W = plan->partition_tokens;
-    a.bs_shift = plan->kv_block_size == 32 ? 5 : 4;
-    a.HG = 1;
-    a.qk_scale_log2 = plan->resolved_softmax_scale * 1.4426950408889634f;
-    a.timeout_ns = plan->wait_timeout_ns > 0 ? (unsigned long long)plan->wait_timeout_ns : kDefaultTimeoutNs;
     a.sel_heads = plan->num_kv_heads;
     CUtensorMap kv_map, sc_map;
     if (!encode_kv_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;

@@ -66,6 +66,9 @@ int group_heads(int Hk);
 // Head warps with one table per (sequence, KV head); a.B, a.Hk and a.sel_heads as stated there.
 int launch_decode_selected(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                            cudaStream_t stream);
+// Head warps over the sequences' own tokens beside a shared prefix (bf16, fp8).
+int launch_decode_own(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                      cudaStream_t stream);
 int launch_decode_tq4(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, cudaStream_t stream);
 int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 
@@ -73,6 +76,11 @@ int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 // it zero).  Sets *status to a pda_status value.
 unsigned int* launch_counter_slot(int* status);
 
+// The partition pass of pda_decode_shared over the sequences' own tokens: partials of W tokens (a multiple of
+// 16), P of them per sequence and KV head.  The plan and the pointers have been checked.
+int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+               const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
+               int W, int P, int* err_word, cudaStream_t stream);
 // Tensor maps of pda_decode_shared: one (block, KV head) and 128-byte chunk, or its scales, per copy.
 bool encode_block_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);
 bool encode_block_scale_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);

@@ -23,7 +23,8 @@
 // softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
 // row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
 // TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
-// P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11); m, l, S and O
+// P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11; V carries two more such
+// roundings, see the conversion); m, l, S and O
 // are fp32.
 //
 // Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
@@ -228,6 +229,11 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// 16 bytes global -> shared, of which `bytes` (16 or 0) are read and the rest are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds32v(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -237,6 +243,10 @@ __device__ __forceinline__ void sts32v(uint32_t addr, uint32_t v) {
     asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 // Two fp32 operations per instruction.
 __device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, uint32_t a, uint32_t b) {
     asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
@@ -293,7 +303,18 @@ struct Prefix {
         }
     }
 
+    // The CTA's first unit, looked up by all warps at once (one fetch of this code), and the ones after it.
+    Unit first_unit;
+    __device__ __forceinline__ void look_up() {
+        first_unit = find_unit(a, split, at, end);
+        at += first_unit.steps;
+    }
     __device__ __forceinline__ bool next(Unit& u) {
+        if (first_unit.steps > 0) {
+            u = first_unit;
+            first_unit.steps = 0;
+            return true;
+        }
         if (at >= end) return false;
         u = find_unit(a, split, at, end);
         at += u.steps;
@@ -383,11 +404,12 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- conversion (fp8)
-    // A thread turns the 128 codes of tokens t and t + 64 into f16 (exact: every e4m3 value is an f16
-    // value).  Rows past the prefix become zeros, since a weight of zero does not silence a NaN.
-    // The first warp also lays the step's scales out for the softmax as [128 K scales][128 V scales / F].
-    // F keeps P V-scale products in f16's range: it is the step's largest V scale, and stays as
-    // it is while the largest lies in [F/64, 64F] (the accumulator counts in units of F).
+    // A thread turns the 128 codes of tokens t and t + 64 into f16: K as it is (exact: every e4m3 value is
+    // an f16 value), V times its token's scale over F (two roundings to f16, 2^-11 each, beside P's one; it spares
+    // the softmax a product per weight).  Rows past the prefix become zeros, since a weight of zero does
+    // not silence a NaN.  The first warp also lays the step's scales out as [128 K scales][128 V scales / F]: the K
+    // scales for the softmax.  F keeps V in f16's range: it is the step's largest V scale, and stays
+    // as it is while the largest lies in [F/64, 64F] (the accumulator counts in units of F).
     __device__ void convert() {
         const int t = threadIdx.x - 320, lane = t & 31;
         unsigned seq = 0, step = 0;
@@ -426,10 +448,13 @@ struct Prefix {
                     }
                     if (seq >= Cfg::kSlots && !wait(bars + kBarEmpty + 8 * s, (seq / Cfg::kSlots - 1) & 1)) return;
                     const int x = t & 7;
+                    if (v && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
 #pragma unroll
                     for (int row = t; row < kStep; row += 32 * kConvertWarps) {
                         const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + row * 128;
                         const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + row * 128;
+                        const float vs = v ? __uint_as_float(lds32v(sm + Cfg::kOffScales + (step & 1) * kScaleBytes + 512 + row * 4)) : 1.f;
+                        const uint32_t vs2 = pack_f16(vs, vs);
                         uint32_t w[8][4];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) lds128(src + ((c ^ x) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
@@ -439,6 +464,10 @@ struct Prefix {
                             if (row >= valid) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
+                            if (v) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
+                            }
                             const uint32_t d = dst + (c >> 2) * 16384;
                             const int k = 2 * (c & 3);
                             sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
@@ -559,47 +588,60 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- softmax
-    // The warp's 32 query rows into its tile's operand, two rows (16 lanes each) per load; returns the
-    // factor from S to log2 units of this lane's own row, 32 * (warp % 4) + lane.
+    // The warp's 32 query rows into its tile's operand, two rows (16 lanes each) per asynchronous copy; returns
+    // the factor from S to log2 units of this lane's own row, 32 * (warp % 4) + lane.  The loops stay
+    // rolled: a short prefix waits for this code's first fetch longer than for its execution.
     __device__ __forceinline__ float load_q(const Unit& u, int tile) const {
         const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, half = lane >> 4, w = lane & 15;
-        const uint32_t dst = sm + Cfg::kOffQ + tile * kSlotBytes + (w >> 3) * 16384;
-        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
-        uint4 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = row0 + 2 * i + half;
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < u.rows) {
-                const int seq = row / a.QG, q = row - seq * a.QG;
-                v[i] = __ldg(reinterpret_cast<const uint4*>(
-                                 a.query + (((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG + q) * kHeadDim) + w);
+        const uint32_t base = sm + Cfg::kOffQ + tile * kSlotBytes;
+        {
+            const uint32_t dst = base + (w >> 3) * 16384;
+            const int row0 = u.rt * kUnitRows + tile * kTileRows + r0 + half;
+            int seq = row0 / a.QG, q = row0 - seq * a.QG;
+            const uint16_t* src = a.query + ((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG * kHeadDim + 8 * w;
+            const long long skip = (long long)a.Hk * a.QG * kHeadDim;
+#pragma unroll 2
+            for (int i = 0; i < 16; ++i) {
+                const int r = r0 + 2 * i + half;
+                const bool live = row0 + 2 * i < u.rows;   // else: zeros, and no read
+                cp_async16(dst + r * 128 + (((w & 7) ^ (r & 7)) << 4), live ? src + q * kHeadDim : a.query, live ? 16u : 0u);
+                q += 2;
+                if (q >= a.QG) {   // the group size is above 2
+                    q -= a.QG;
+                    src += skip;
+                }
             }
+            cp_async_wait_all();
+            __syncwarp();
         }
         float c = a.qk_scale_log2;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if constexpr (F16) {
-                // a power of two that brings the row's largest |q| into [2^14, 2^15): f16 then keeps every bf16 bit
-                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                float amax = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kLanes, amax, o));
-                int e = 0;
-                if (amax > 0.f) e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
-                e = max(-100, min(100, e));
-                const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
-                const float back = __shfl_sync(kLanes, __uint_as_float((uint32_t)(127 - e) << 23), (lane & 1) << 4);
-                if (lane >> 1 == i) c *= back;   // lane 2i + k owns row 2i + k
-                v[i].x = pack_f16(bf16_lo(x[0]) * pw, bf16_hi(x[0]) * pw);
-                v[i].y = pack_f16(bf16_lo(x[1]) * pw, bf16_hi(x[1]) * pw);
-                v[i].z = pack_f16(bf16_lo(x[2]) * pw, bf16_hi(x[2]) * pw);
-                v[i].w = pack_f16(bf16_lo(x[3]) * pw, bf16_hi(x[3]) * pw);
+        if constexpr (F16) {
+            // This lane's row times a power of two that brings its largest |q| into [2^14, 2^15): f16 then
+            // keeps every bf16 bit.  The magnitudes of bf16 values order like their bits.
+            const uint32_t row = base + (r0 + lane) * 128;
+            const int x = lane & 7;
+            uint32_t mx = 0;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                uint32_t v[4];
+                lds128(row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4), v[0], v[1], v[2], v[3]);
+                mx = __vmaxs2(mx, __vmaxs2(__vmaxs2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu),
+                                           __vmaxs2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu)));
             }
-            const int r = r0 + 2 * i + half;
-            sts128(dst + r * 128 + (((w & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+            const int top = max(mx & 0xFFFFu, mx >> 16);   // bf16 bits
+            int e = top ? 14 - ((top >> 7) - 127) : 0;
+            e = max(-100, min(100, e));
+            const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
+            c *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t at = row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4);
+                uint32_t v[4];
+                lds128(at, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = pack_f16(bf16_lo(v[k]) * pw, bf16_hi(v[k]) * pw);
+                sts128(at, v[0], v[1], v[2], v[3]);
+            }
         }
         fence_proxy_async_shared();
         return c;
@@ -708,18 +750,8 @@ struct Prefix {
                             y.y = ex2(__uint_as_float(s[k][i + 3]));
                             add2(la, x);
                             add2(lb, y);
-                            if constexpr (F16) {
-                                const uint4 f = scales[32 + 8 * k + i / 4];
-                                uint32_t e[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
-                                                 __float_as_uint(y.y)};
-                                mul2(e[0], e[1], f.x, f.y);
-                                mul2(e[2], e[3], f.z, f.w);
-                                p[i / 2] = pack_f16(__uint_as_float(e[0]), __uint_as_float(e[1]));
-                                p[i / 2 + 1] = pack_f16(__uint_as_float(e[2]), __uint_as_float(e[3]));
-                            } else {
-                                p[i / 2] = pack_bf16(x.x, x.y);
-                                p[i / 2 + 1] = pack_bf16(y.x, y.y);
-                            }
+                            p[i / 2] = F16 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                            p[i / 2 + 1] = F16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
                         }
                         tmem_st16(tS + 16 * k, p);   // over S, which is in registers
                     }
@@ -760,7 +792,7 @@ struct Prefix {
             a.part_m[mine] = m * kLn2S;
             if (u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
         }
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             uint32_t s[2][32];
             tmem_ld32(s[0], tO + 64 * half);
@@ -839,11 +871,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tc_fence_after();
     const uint32_t tmem = lds32v(bars + kTmemAt);
     allow_dependent_launch();
-    grid_dependency_wait();
+    // No wait for the previous grid here: it is this call's pass over the sequences' own tokens, which lets
+    // this one start only after everything before it has ended, and of which nothing is read.
     Prefix<KV> p(a, smem);
     p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
     p.at = (int)min((long long)blockIdx.x * p.split.per, (long long)p.split.total);
     p.end = p.at + min(p.split.per, p.split.total - p.at);
+    p.look_up();
     // 384 threads x 168 registers at launch = 64512 = 256 x 200 + 128 x 104
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
@@ -866,6 +900,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tc_fence_after();
     if (threadIdx.x == 0 && lds32v(bars + kAbortAt) && a.err_word) atomicOr(a.err_word, PDA_ERRW_PIPELINE_TIMEOUT);
     if (warp == 9) tmem_free(tmem, 512);
+    grid_dependency_wait();   // this grid ends after the own pass: the join waits for this one alone
 }
 
 // ------------------------------------------------------------------------- the join
@@ -966,13 +1001,25 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
 // ------------------------------------------------------------------------- host side
 static long long up256(long long x) { return (x + 255) & ~255ll; }
 
+// Tokens of a partial of the sequences' own part.  A warp takes 0.6 us per 16 tokens, so short partials end
+// sooner; they are worth their join while there are few of them.
+static int own_tokens(const pda_plan_t* p) {
+    const long long units = (long long)p->num_seqs * p->num_kv_heads, most = (long long)p->max_blocks_per_seq * p->kv_block_size;
+    for (int W = 64; W < p->partition_tokens; W *= 2)
+        if (units * ((most + W - 1) / W) <= 8192) return W;
+    return p->partition_tokens;
+}
+
 struct SharedLayout {
     long long o0, l0, m0, pieces, o1, l1, m1, bytes;
+    int W, P;   // the own part's partials
 };
 static SharedLayout shared_layout(const pda_plan_t* pp, const pda_plan_t* p) {
     const long long heads = (long long)p->num_seqs * p->num_kv_heads * p->query_group_size;
-    const long long r0 = heads * (pp->num_partitions + 1), r1 = heads * p->num_partitions;
     SharedLayout s;
+    s.W = own_tokens(p);
+    s.P = (int)(((long long)p->max_blocks_per_seq * p->kv_block_size + s.W - 1) / s.W);
+    const long long r0 = heads * (pp->num_partitions + 1), r1 = heads * s.P;
     s.o0 = 0;
     s.l0 = s.o0 + up256(r0 * kHeadDim * 4);
     s.m0 = s.l0 + up256(r0 * 4);
@@ -1099,18 +1146,19 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap kv_map, sc_map;
     if (!encode_block_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
+    // The sequences' own tokens first: the prefix pass, which takes whole SMs, starts on each SM as that
+    // one's short work ends.
+    int rc = decode_own(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
+                        w.W, w.P, err_word, s);
+    if (rc != PDA_OK) return rc;
     const long long most = most_steps(prefix_plan, plan);   // no more CTAs than there can be steps
     const int ctas = (int)(most < sms ? most : sms);
-    int rc;
     if (plan->kv_dtype == PDA_KV_BF16) {
         rc = launch_prefix<PDA_KV_BF16>(a, kv_map, kv_map, ctas, s);
     } else {
         if (!encode_block_scale_map(&sc_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
         rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, ctas, s);
     }
-    if (rc != PDA_OK) return rc;
-    rc = pda_decode(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
-                    err_word, stream);
     if (rc != PDA_OK) return rc;
     JoinArgs j = {};
     j.group_starts = group_starts;
@@ -1132,9 +1180,9 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     j.MP = a.MP;
     j.MB = plan->max_blocks_per_seq;
     j.BS = a.BS;
-    j.W = plan->partition_tokens;
+    j.W = w.W;
     j.slots = a.slots;
-    j.P = plan->num_partitions;
+    j.P = w.P;
     j.out_f32 = out_dtype == PDA_OUT_F32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hk));

@@ -63,14 +63,14 @@ class Case:
         return pda.shared_plans(self.B, len(self.plens), self.Hk, self.QG, self.BS, self.MP, self.MB, kv_dtype=self.kv, **kw)
 
     def reference(self, scale=128 ** -0.5):
-        """(out, bound) in 64 bits.  The bound: a prefix weight rounded to bf16 is off by at most 2^-8, to f16 by 2^-11;
-        a logit's 128 products are summed in fp32, each addition off by at most a step (2^-23), which moves its
+        """(out, bound) in 64 bits.  The bound: a prefix weight rounded to bf16 is off by at most 2^-8; with fp8 KV the weight, V's
+        scale and the scaled V are each rounded to f16, 2^-11 each, 3 * 2^-11 per term; a logit's 128 products are summed in fp32, each addition off by at most a step (2^-23), which moves its
         weight by as much in absolute terms; ex2, the scales and the sums over T tokens each add steps of 2^-23
         per term.  The own part is the library's partition pass (P in 16 bits: 2^-16 bf16, 2^-11 fp8)."""
         K, V = pp.block_values(self.w, self.cache)
         q = wl.bf16_bits_to_f32(self.q).astype(np.float64)
         out, bound = np.zeros((self.B, self.Hk * self.QG, 128)), np.zeros((self.B, self.Hk * self.QG, 128))
-        half = 2.0 ** -8 if self.kv == BF16 else 2.0 ** -11
+        half = 2.0 ** -8 if self.kv == BF16 else 3 * 2.0 ** -11 * (1 + 2.0 ** -10)
         for b in range(self.B):
             for h in range(self.Hk):
                 k, v = [], []
