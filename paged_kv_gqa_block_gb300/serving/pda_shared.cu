@@ -16,9 +16,8 @@
 //             no shuffles; S is read from TMEM, P written back
 //   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
 //   9         the matrix products (one thread issues)
-//   10, 11    fp8 only: e4m3 codes to f16 (exact) between the copy and the product
-// The softmax warps hold a whole row of S (128 registers) and take 200 registers each; the other four
-// give some up (104).
+//   12-15     fp8 only: e4m3 codes to f16 between the copy and the product
+// The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
 // The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
 // softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
 // row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
@@ -46,8 +45,7 @@ namespace pda {
 
 constexpr uint32_t kLanes = 0xFFFFFFFFu;
 constexpr int kStep = 128;                 // tokens per step
-constexpr int kPrefixThreads = 384;        // three warpgroups
-constexpr int kConvertWarps = 2;
+constexpr int kConvertWarps = 4;
 constexpr int kTileRows = 128, kUnitRows = 256;
 constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bits
 constexpr int kRawBytes = 16384;           // the same in 8 bits
@@ -74,13 +72,15 @@ struct SharedArgs {
 template <int KV>
 struct SharedCfg {
     static constexpr bool kF16 = KV != PDA_KV_BF16;              // f16 products, converter warps
-    static constexpr int kSlots = kF16 ? 4 : 5;
+    static constexpr int kSlots = kF16 ? 3 : 5;
+    static constexpr int kRaw = 3, kScales = 3;                  // fp8: raw slots, scale stages
+    static constexpr int kThreads = kF16 ? 512 : 384;
     static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
     static constexpr int kOffSlots = 2 * kSlotBytes;
-    static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;          // 2 x 16 KB
-    static constexpr int kOffScales = kOffRaw + (kF16 ? 2 * kRawBytes : 0);  // 2 x 1 KB
-    static constexpr int kOffBars = kOffScales + (kF16 ? 2 * kScaleBytes : 0);
-    static constexpr int kSmem = kOffBars + 256;
+    static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;
+    static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
+    static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
+    static constexpr int kSmem = kOffBars + 320;
 };
 // barriers and scalars after kOffBars
 enum {
@@ -90,14 +90,14 @@ enum {
     kBarS = 96,          // [2] S is in TMEM
     kBarP = 112,         // [2] P is in TMEM
     kBarO = 128,         // [2] the unit's last product of a tile is done
-    kBarRawFull = 144,   // [2]
-    kBarRawEmpty = 160,  // [2]
-    kBarScFull = 176,    // [2] scales and their largest are readable
-    kBarScEmpty = 192,   // [2]
-    kBarDrain = 208,
-    kTmemAt = 216,       // TMEM address
-    kAbortAt = 220,      // a wait gave up
-    kFAt = 224           // [2] what a step's V scales are divided by
+    kBarRawFull = 144,   // [3]
+    kBarRawEmpty = 168,  // [3]
+    kBarScFull = 192,    // [3] scales are laid out
+    kBarScEmpty = 216,   // [3]
+    kBarDrain = 240,
+    kTmemAt = 248,       // TMEM address
+    kAbortAt = 252,      // a wait gave up
+    kFAt = 256           // [3] what a step's V scales are divided by
 };
 
 // ------------------------------------------------------------------------- the split
@@ -274,14 +274,13 @@ struct Prefix {
     static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
 
     const SharedArgs& a;
-    const uint8_t* const smem;
     const uint32_t sm;         // shared memory base
     const uint32_t bars;
     Split split;
     int at, end;               // this CTA's run
 
-    __device__ __forceinline__ Prefix(const SharedArgs& args, const uint8_t* base)
-        : a(args), smem(base), sm(smem_addr(base)), bars(sm + Cfg::kOffBars) {}
+    __device__ __forceinline__ Prefix(const SharedArgs& args, uint32_t base)
+        : a(args), sm(base), bars(base + Cfg::kOffBars) {}
 
     // A whole warp waits (bounded).  False once any wait of the CTA has given up.
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
@@ -339,7 +338,7 @@ struct Prefix {
     // raw slots with the step's scales.
     __device__ void copies(const CUtensorMap* kv_map, const CUtensorMap* sc_map) {
         const int lane = threadIdx.x & 31;
-        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? 2 : Cfg::kSlots;
+        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? Cfg::kRaw : Cfg::kSlots;
         constexpr uint32_t kFull0 = F16 ? kBarRawFull : kBarFull, kEmpty0 = F16 ? kBarRawEmpty : kBarEmpty;
         constexpr int kBytes = F16 ? kRawBytes : kSlotBytes;
         const uint32_t base = sm + (F16 ? Cfg::kOffRaw : Cfg::kOffSlots);
@@ -366,7 +365,8 @@ struct Prefix {
                 }
                 if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
                     atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
-                if (F16 && step >= 2 && !wait(bars + kBarScEmpty + 8 * (step & 1), ((step >> 1) - 1) & 1)) {
+                const unsigned st = step % Cfg::kScales;
+                if (F16 && step >= Cfg::kScales && !wait(bars + kBarScEmpty + 8 * st, (step / Cfg::kScales - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -386,7 +386,7 @@ struct Prefix {
                         tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
                                     v * kHalves + half, u.h, id, policy);
                         if (scales)
-                            tma_load_4d(sm + Cfg::kOffScales + (step & 1) * kScaleBytes + blk * a.BS * 8, sc_map, bar, 0, 0,
+                            tma_load_4d(sm + Cfg::kOffScales + st * kScaleBytes + blk * a.BS * 8, sc_map, bar, 0, 0,
                                         u.h, id, policy);
                     }
                     __syncwarp();
@@ -404,14 +404,14 @@ struct Prefix {
     }
 
     // ---------------------------------------------------------------- conversion (fp8)
-    // A thread turns the 128 codes of tokens t and t + 64 into f16: K as it is (exact: every e4m3 value is
+    // Thread t turns token t's 128 codes into f16: K as it is (exact: every e4m3 value is
     // an f16 value), V times its token's scale over F (two roundings to f16, 2^-11 each, beside P's one; it spares
     // the softmax a product per weight).  Rows past the prefix become zeros, since a weight of zero does
     // not silence a NaN.  The first warp also lays the step's scales out as [128 K scales][128 V scales / F]: the K
     // scales for the softmax.  F keeps V in f16's range: it is the step's largest V scale, and stays
     // as it is while the largest lies in [F/64, 64F] (the accumulator counts in units of F).
     __device__ void convert() {
-        const int t = threadIdx.x - 320, lane = t & 31;
+        const int t = threadIdx.x - 384, lane = t & 31;
         unsigned seq = 0, step = 0;
         float F = 1.f;
         Unit u;
@@ -420,10 +420,11 @@ struct Prefix {
                 const int valid = tokens_of(u, j);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v, ++seq) {
-                    const int r = seq & 1, s = seq % Cfg::kSlots;
-                    if (!wait(bars + kBarRawFull + 8 * r, (seq >> 1) & 1)) return;
+                    const int r = seq % Cfg::kRaw, s = seq % Cfg::kSlots;
+                    const unsigned st = step % Cfg::kScales, st_ph = step / Cfg::kScales & 1;
+                    if (!wait(bars + kBarRawFull + 8 * r, seq / Cfg::kRaw & 1)) return;
                     if (v == 0 && t < 32) {
-                        const uint32_t sc = sm + Cfg::kOffScales + (step & 1) * kScaleBytes;
+                        const uint32_t sc = sm + Cfg::kOffScales + st * kScaleBytes;
                         float ks[4], vs[4], f = 0.f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -442,18 +443,18 @@ struct Prefix {
                             sts32v(sc + (lane + 32 * i) * 4, __float_as_uint(ks[i]));
                             sts32v(sc + 512 + (lane + 32 * i) * 4, __float_as_uint(vs[i] * rF));
                         }
-                        if (lane == 0) sts32v(bars + kFAt + 4 * (step & 1), __float_as_uint(F));
+                        if (lane == 0) sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * (step & 1));
+                        if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * st);
                     }
                     if (seq >= Cfg::kSlots && !wait(bars + kBarEmpty + 8 * s, (seq / Cfg::kSlots - 1) & 1)) return;
                     const int x = t & 7;
-                    if (v && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
+                    if (v && !wait(bars + kBarScFull + 8 * st, st_ph)) return;
 #pragma unroll
                     for (int row = t; row < kStep; row += 32 * kConvertWarps) {
                         const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + row * 128;
                         const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + row * 128;
-                        const float vs = v ? __uint_as_float(lds32v(sm + Cfg::kOffScales + (step & 1) * kScaleBytes + 512 + row * 4)) : 1.f;
+                        const float vs = v ? __uint_as_float(lds32v(sm + Cfg::kOffScales + st * kScaleBytes + 512 + row * 4)) : 1.f;
                         const uint32_t vs2 = pack_f16(vs, vs);
                         uint32_t w[8][4];
 #pragma unroll
@@ -621,7 +622,7 @@ struct Prefix {
             const uint32_t row = base + (r0 + lane) * 128;
             const int x = lane & 7;
             uint32_t mx = 0;
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < 16; ++i) {
                 uint32_t v[4];
                 lds128(row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4), v[0], v[1], v[2], v[3]);
@@ -633,7 +634,7 @@ struct Prefix {
             e = max(-100, min(100, e));
             const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
             c *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < 16; ++i) {
                 const uint32_t at = row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4);
                 uint32_t v[4];
@@ -681,8 +682,8 @@ struct Prefix {
             float m = 0.f, l = 0.f, F = 1.f;
             for (int j = 0; j < u.steps; ++j, ++step) {
                 const int valid = tokens_of(u, j);
-                const uint4* scales = reinterpret_cast<const uint4*>(smem + Cfg::kOffScales + (step & 1) * kScaleBytes);
-                if (F16 && !wait(bars + kBarScFull + 8 * (step & 1), (step >> 1) & 1)) return;
+                const unsigned st = step % Cfg::kScales;
+                if (F16 && !wait(bars + kBarScFull + 8 * st, step / Cfg::kScales & 1)) return;
                 if (w.on) {
                     if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
                     tc_fence_after();
@@ -691,14 +692,18 @@ struct Prefix {
                     for (int k = 0; k < 4; ++k) tmem_ld32(s[k], tS + 32 * k);
                     tmem_wait_ld();
                     if constexpr (F16) {   // the K scales
+                        const uint32_t sc = sm + Cfg::kOffScales + st * kScaleBytes;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t f[16];
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const uint4 f = scales[8 * k + i / 4];
-                                mul2(s[k][i], s[k][i + 1], f.x, f.y);
-                                mul2(s[k][i + 2], s[k][i + 3], f.z, f.w);
+                            for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const int c = (k & 1) * 16 + i;
+                                mul2(s[k >> 1][c], s[k >> 1][c + 1], f[i], f[i + 1]);
                             }
+                        }
                     }
                     if (valid < kStep) {
 #pragma unroll
@@ -717,7 +722,7 @@ struct Prefix {
                     }
                     const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * w.c, -1e30f);
                     float nF = 1.f;
-                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * (step & 1)));
+                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
                     if (j == 0) {
                         m = top;
                     } else {
@@ -763,7 +768,7 @@ struct Prefix {
                 }
                 if (F16) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * (step & 1));
+                    if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * st);
                 }
             }
             if (!w.on) continue;
@@ -836,7 +841,7 @@ struct Prefix {
 };
 
 template <int KV>
-__global__ void __launch_bounds__(kPrefixThreads, 1)
+__global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     pda_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                       const SharedArgs a) {
     using Cfg = SharedCfg<KV>;
@@ -854,6 +859,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(bars + kBarS + 8 * i, 1);
             mbar_init(bars + kBarP + 8 * i, 4);
             mbar_init(bars + kBarO + 8 * i, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
             mbar_init(bars + kBarRawFull + 8 * i, 1);
             mbar_init(bars + kBarRawEmpty + 8 * i, kConvertWarps);
             mbar_init(bars + kBarScFull + 8 * i, 1);
@@ -873,24 +880,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     allow_dependent_launch();
     // No wait for the previous grid here: it is this call's pass over the sequences' own tokens, which lets
     // this one start only after everything before it has ended, and of which nothing is read.
-    Prefix<KV> p(a, smem);
+    Prefix<KV> p(a, sm);
     p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
     p.at = (int)min((long long)blockIdx.x * p.split.per, (long long)p.split.total);
     p.end = p.at + min(p.split.per, p.split.total - p.at);
     p.look_up();
-    // 384 threads x 168 registers at launch = 64512 = 256 x 200 + 128 x 104
+    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (Cfg::kF16)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         if (fine) p.softmax(tmem, warp >> 2);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if constexpr (Cfg::kF16)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (fine) {
             if (warp == 8)
                 p.copies(&kv_map, &sc_map);
             else if (warp == 9)
                 p.products(tmem);
-            else if constexpr (Cfg::kF16)
+            else if (Cfg::kF16 && warp >= 12)
                 p.convert();
         }
     }
@@ -924,7 +937,10 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
     grid_dependency_wait();
     const int b = blockIdx.x / a.Hk, lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     const long long unit = blockIdx.x;
-    int np = 0;
+    // asked for at once, whether or not the sequence has a prefix (the row's entry is then not used)
+    const int pieces = __ldg(a.pieces + unit * a.QG + q);
+    int ctx = __ldg(a.context_lens + b);
+    bool prefix = false;
     for (int g0 = 0; g0 < a.NG; g0 += 32) {
         bool in = false;
         if (g0 + lane < a.NG) {
@@ -932,10 +948,9 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
             const int len = __ldg(a.prefix_lens + g0 + lane);
             in = s0 >= 0 && s1 <= a.B && s0 <= b && b < s1 && len > 0 && len <= a.MP * a.BS;
         }
-        if (__any_sync(kLanes, in)) np = 1;
+        prefix |= __any_sync(kLanes, in) != 0;
     }
-    if (np) np = max(0, min(a.slots, __ldg(a.pieces + unit * a.QG + q)));
-    int ctx = __ldg(a.context_lens + b);
+    const int np = prefix ? max(0, min(a.slots, pieces)) : 0;
     if (ctx < 0 || ctx > a.MB * a.BS) ctx = 0;   // reported by the partition pass
     const int total = np + (ctx + a.W - 1) / a.W;
     const long long row0 = unit * a.slots * a.QG + q, row1 = unit * a.P * a.QG + q;
@@ -943,24 +958,31 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
         part = i >= np;
         return part ? row1 + (long long)(i - np) * a.QG : row0 + (long long)i * a.QG;
     };
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) {
-        int part;
-        const long long k = at(i, part);
-        M = fmaxf(M, __ldcg((part ? a.part_m[1] : a.part_m[0]) + k));
+    auto stats = [&](int i, float& m, float& l) {
+        m = -INFINITY;
+        l = 0.f;
+        if (i < total) {
+            int part;
+            const long long k = at(i, part);
+            m = __ldcg((part ? a.part_m[1] : a.part_m[0]) + k);
+            l = __ldcg((part ? a.part_l[1] : a.part_l[0]) + k);
+        }
+    };
+    float m0, l0;   // of the first 32 partials
+    stats(lane, m0, l0);
+    float M = m0;
+    for (int i = lane + 32; i < total; i += 32) {
+        float m, l;
+        stats(i, m, l);
+        M = fmaxf(M, m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kLanes, M, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     for (int i0 = 0; i0 < total; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < total) {
-            int part;
-            const long long k = at(i0 + lane, part);
-            w = partition_weight(__ldcg((part ? a.part_l[1] : a.part_l[0]) + k),
-                                 __ldcg((part ? a.part_m[1] : a.part_m[0]) + k), M);
-        }
+        if (i0 > 0) stats(i0 + lane, m0, l0);
+        const float w = i0 + lane < total ? partition_weight(l0, m0, M) : 0.f;
         sum += w;
         const int n = min(32, total - i0);
         for (int j0 = 0; j0 < n; j0 += 8) {
@@ -1061,7 +1083,7 @@ static int launch_prefix(const SharedArgs& a, const CUtensorMap& kv_map, const C
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kPrefixThreads);
+    cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

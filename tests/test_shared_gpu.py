@@ -321,3 +321,33 @@ def test_fork_then_shared_decode(pda):
                             out_dtype=torch.float32)
     # P in bf16 (2^-8 of each weight) against the step's 16 bits; |v| < 5
     assert (out - want).abs().max() <= 2.0 ** -8 * 5
+
+
+def test_every_e4m3_code_in_a_prefix(pda):
+    """All 256 codes through the fp8 conversion: a one-hot query reads single key codes as logits, and values are picked out one
+    token at a time (a query far along one key's direction)."""
+    c = Case(FP8, 1, 8, 16, [256], [1], [0], seed=20)
+    data, meta = wl.cache_views(c.w, c.cache)
+    codes = np.arange(256, dtype=np.uint8)
+    finite = (codes & 0x7F) != 0x7F
+    t = np.arange(256)
+    blk, slot = c.ptable[0][t // 16], t % 16
+    data[blk, slot, 0, 0, :] = 0
+    data[blk, slot, 0, 0, 0] = np.where(finite, codes, 0)
+    data[blk, slot, 0, 1, :] = np.where(finite, codes, 0)[:, None]
+    meta[blk, 0, 0, slot] = 0.25
+    meta[blk, 0, 1, slot] = 0.5
+    q = np.zeros((1, 8, 128), np.float32)
+    q[0, :, 0] = [0.0, 0.1, -0.1, 1.0, -1.0, 0.01, 3.0, -3.0]
+    c.q = wl.round_bf16(q)
+    check(pda, c)
+    for code in (0x7F, 0xFF):                                # a NaN code in V makes its dimension NaN, in K every row that weighs it
+        d = c.device()
+        keep = c.cache.copy()
+        data[c.ptable[0][5], 3, 0, 1, 70] = code
+        out = pda.decode_shared(*c.plans(pda), **c.device(), out_dtype=torch.float32).cpu().numpy()
+        assert np.isnan(out[0, :, 70]).all() and np.isfinite(np.delete(out, 70, axis=2)).all()
+        c.cache[:] = keep
+        data[c.ptable[0][5], 3, 0, 0, 1] = code
+        assert np.isnan(pda.decode_shared(*c.plans(pda), **c.device(), out_dtype=torch.float32).cpu().numpy()).all()
+        c.cache[:] = keep
