@@ -352,11 +352,15 @@ def decode_step_noalloc(p: Plan, query, kv_cache, num_cache_blocks: int, block_t
 # Pages of the cache, attention over selected blocks, and shared prefixes.  Every tensor of a call lies on one GPU,
 # which the call makes current; `stream` defaults to that GPU's current stream.
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
-_I32 = torch.int32
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
 
 
 class _Call:
     """Checks the tensors of one call: on the device of the first, contiguous, large enough."""
+
+    __slots__ = ("index",)
 
     def __init__(self, t: torch.Tensor, name: str):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -364,11 +368,15 @@ class _Call:
         self.index = t.get_device()
 
     def ptr(self, t, name: str, dtype, nbytes: int, host_ok: bool = False):
+        # the common case in one line: a step of many short kernels waits for this code
+        if (isinstance(t, torch.Tensor) and t.get_device() == self.index and (dtype is None or t.dtype in dtype)
+                and t.is_contiguous() and t.nbytes >= nbytes):
+            return t.data_ptr()
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.get_device() != self.index and not (host_ok and t.device.type == "cpu" and t.is_pinned()):
             raise ValueError(f"{name} must be on cuda:{self.index}" + (" or pinned host memory" if host_ok else ""))
-        if dtype is not None and t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+        if dtype is not None and t.dtype not in dtype:
             raise ValueError(f"{name} has dtype {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -391,7 +399,7 @@ class _Call:
 
     def _stream(self, stream):
         if stream is None:
-            return torch.cuda.current_stream(self.index).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(self.index)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -437,7 +445,7 @@ def fork_sequences(p: Plan, kv_cache, num_cache_blocks: int, block_table, contex
             c.ptr(refcounts, "refcounts", _I32, NB * 4), R, c.ptr(parents, "parents", _I32, R * 4),
             c.opt(new_tokens, "new_tokens", _I32, R * 4), c.ptr(out_table, "out_table", _I32, R * MB * 4),
             c.ptr(out_lens, "out_lens", _I32, R * 4), c.ptr(out_refcounts, "out_refcounts", _I32, NB * 4),
-            c.ptr(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+            c.ptr(workspace, "workspace", _U8, 0), workspace.nbytes)
     c.run("pda_fork_sequences", lib().pda_fork_sequences, p, args, err_word, stream)
 
 
@@ -450,7 +458,7 @@ def compact_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, contex
             c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
             c.ptr(refcounts, "refcounts", _I32, NB * 4), c.ptr(out_table, "out_table", _I32, B * MB * 4),
             c.ptr(out_refcounts, "out_refcounts", _I32, NB * 4), c.ptr(remap, "remap", _I32, NB * 4),
-            c.ptr(num_used, "num_used", _I32, 4), c.ptr(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+            c.ptr(num_used, "num_used", _I32, 4), c.ptr(workspace, "workspace", _U8, 0), workspace.nbytes)
     c.run("pda_compact_blocks", lib().pda_compact_blocks, p, args, err_word, stream)
 
 
@@ -467,7 +475,7 @@ def summarize_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, cont
     B, MB, NB = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks
     args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,
             c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
-            c.opt(since, "since", _I32, B * 4), c.opt(centroids, "centroids", torch.float32, 64),
+            c.opt(since, "since", _I32, B * 4), c.opt(centroids, "centroids", _F32, 64),
             c.ptr(summaries, "summaries", _BF16, NB * p.num_kv_heads * 512))
     c.run("pda_summarize_blocks", lib().pda_summarize_blocks, p, args, err_word, stream)
 
@@ -481,7 +489,7 @@ def score_blocks(p: Plan, query, summaries, num_cache_blocks: int, block_table, 
     args = (c.ptr(query, "query", _BF16, B * Hk * p.query_group_size * p.head_dim * 2),
             c.ptr(summaries, "summaries", _BF16, NB * Hk * 512), NB,
             c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
-            c.ptr(scores, "scores", torch.float32, B * Hk * MB * 4))
+            c.ptr(scores, "scores", _F32, B * Hk * MB * 4))
     c.run("pda_score_blocks", lib().pda_score_blocks, p, args, err_word, stream)
 
 
@@ -492,7 +500,7 @@ def select_blocks(p: Plan, scores, block_table, context_lens, num_select: int, n
     c = _Call(scores, "scores")
     B, Hk, MB = p.num_seqs, p.num_kv_heads, p.max_blocks_per_seq
     need = B * Hk * max(num_select, 0) * 4
-    args = (c.ptr(scores, "scores", torch.float32, B * Hk * MB * 4),
+    args = (c.ptr(scores, "scores", _F32, B * Hk * MB * 4),
             c.ptr(block_table, "block_table", _I32, B * MB * 4), c.ptr(context_lens, "context_lens", _I32, B * 4),
             num_select, num_first, num_last, c.ptr(sel_table, "sel_table", _I32, need),
             c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4), c.opt(sel_blocks, "sel_blocks", _I32, need))
@@ -513,12 +521,12 @@ def decode_selected(p: Plan, query, kv_cache, num_cache_blocks: int, sel_table, 
     f32 = out.dtype is torch.float32
     args = (c.ptr(query, "query", _BF16, rows * D * 2, host_ok=True),
             c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
-            c.opt(centroids, "centroids", torch.float32, 64),
+            c.opt(centroids, "centroids", _F32, 64),
             c.ptr(sel_table, "sel_table", _I32, B * Hk * p.max_blocks_per_seq * 4),
             c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4),
-            c.ptr(ws["partial_out"], "partial_out", torch.float32, rows * P * D * 4),
-            c.ptr(ws["exp_sums"], "exp_sums", torch.float32, rows * P * 4),
-            c.ptr(ws["max_logits"], "max_logits", torch.float32, rows * P * 4),
+            c.ptr(ws["partial_out"], "partial_out", _F32, rows * P * D * 4),
+            c.ptr(ws["exp_sums"], "exp_sums", _F32, rows * P * 4),
+            c.ptr(ws["max_logits"], "max_logits", _F32, rows * P * 4),
             c.ptr(out, "out", (torch.float32, torch.bfloat16), rows * D * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_selected", lib().pda_decode_selected, p, args, err_word, stream)
@@ -568,7 +576,7 @@ def decode_shared(prefix_plan: Plan, p: Plan, query, kv_cache, num_cache_blocks:
             c.ptr(prefix_table, "prefix_table", _I32, NG * prefix_plan.max_blocks_per_seq * 4),
             c.ptr(prefix_lens, "prefix_lens", _I32, NG * 4),
             c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
-            c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(ws, "ws", torch.uint8, 0), ws.nbytes,
+            c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(ws, "ws", _U8, 0), ws.nbytes,
             c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_shared", lib().pda_decode_shared, prefix_plan, args, err_word, stream)

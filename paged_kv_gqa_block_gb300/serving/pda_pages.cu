@@ -10,8 +10,8 @@
 // Both are two launches, the second a programmatic dependent of the first:
 //   1. a scan by one thread-block cluster (kScanCtas CTAs of 1024 threads; one CTA for a small
 //      pool): every CTA counts its slice of the counts, the totals are exchanged through
-//      distributed shared memory, and a second sweep over the slice (now in L1 or L2) gives each
-//      free block, or each block to move, its rank.  One launch in place of count / prefix / write;
+//      distributed shared memory, and a second sweep over the slice (now in L1) gives each free or
+//      used block its rank.  One launch in place of count / prefix / write;
 //   2. a grid over the table segments and the 4 KB chunks of the blocks to copy.
 // What bounds them: the copies HBM (read + write), everything else launch and load latency.
 #include <cooperative_groups.h>
@@ -30,7 +30,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kScanThreads = 1024;
 constexpr int kScanCtas = 8;              // the portable cluster size
-constexpr long long kScanOneCta = 8192;   // pools up to here are scanned by one CTA (two int4 per thread)
+constexpr int kScanTile = 4 * kScanThreads;
+constexpr long long kScanOneCta = kScanTile;   // pools up to here are scanned by one CTA, in one tile
 constexpr int kPageThreads = 256;
 constexpr int kRowInts = 8;
 
@@ -127,9 +128,9 @@ struct ScanArgs {
     int* rows;             // workspace [R][kRowInts]
     int B, R, MB, BS;
     // compaction
-    int* movers;           // workspace [NB]
+    int* used_ids;         // workspace [NB]: at r, the id of the used block of rank r, where it moves
     int* holes;            // workspace [NB]
-    int* num_moved;        // workspace [1]
+    int* scalars;          // workspace: {moved, used below U}
     int* remap;
     int* num_used;
 };
@@ -137,16 +138,29 @@ struct ScanArgs {
 // A new row's record: {parent, length, new length, its first place in free_ids}, {flags, last block's id}
 enum { kRowCopy = 1, kRowFirst = 2 };
 
-// Counts, over this CTA's slice, the entries for which `f` holds; returns the count before the slice
-// and the cluster's total.
+// The slice of the pool that this CTA of the cluster scans.
+__device__ __forceinline__ void slice_of(const cg::cluster_group& cl, long long NB, long long& lo, long long& hi) {
+    const long long per = (NB + cl.num_blocks() - 1) / cl.num_blocks();
+    lo = min(NB, per * cl.block_rank());
+    hi = min(NB, lo + per);
+}
+
+// Counts the entries of this CTA's slice for which `f` holds; returns how many there are before the
+// slice, and their number in the pool.
 template <class F>
-__device__ __forceinline__ int count_before(const ScanArgs& a, long long lo, long long hi, int* tmp, int* share,
-                                            int& total, F f) {
+__device__ __forceinline__ int count_before(const cg::cluster_group& cl, const int* refs, long long lo, long long hi,
+                                            int* tmp, int* share, int& total, F f) {
     int n = 0;
-    for (long long i = lo + threadIdx.x; i < hi; i += kScanThreads) n += f(i, __ldg(a.refs + i));
+    for (long long t0 = lo + 4 * threadIdx.x; t0 < hi; t0 += kScanTile)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (t0 + u < hi) n += f(__ldg(refs + t0 + u));
     int sum;
     block_scan(n, tmp, sum);
-    cg::cluster_group cl = cg::this_cluster();
+    if (cl.num_blocks() == 1) {
+        total = sum;
+        return 0;
+    }
     if (threadIdx.x == 0) *share = sum;
     cl.sync();
     int before = 0;
@@ -156,91 +170,121 @@ __device__ __forceinline__ int count_before(const ScanArgs& a, long long lo, lon
         if (r < cl.block_rank()) before += v;
         total += v;
     }
-    cl.sync();   // nobody overwrites or leaves with a count still to be read
+    cl.sync();   // nobody leaves with a count still to be read
     return before;
 }
 
+// What a new row asks for.
+struct NewRow {
+    int p, L, nl, tail_id, tail_ref;
+    bool live;
+};
+__device__ __forceinline__ NewRow new_row(const ScanArgs& a, int i) {
+    NewRow r = {-1, 0, 0, -1, 0, false};
+    if (i >= a.R) return r;
+    r.p = __ldg(a.parents + i);
+    const int g = a.new_tokens ? __ldg(a.new_tokens + i) : 0;
+    if (r.p < 0) return r;
+    if (r.p >= a.B) {
+        if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_SEQUENCE);
+        return r;
+    }
+    const long long max_ctx = (long long)a.MB * a.BS;
+    r.L = __ldg(a.context_lens + r.p);
+    if (r.L < 0 || r.L > max_ctx) {
+        if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
+        r.L = 0;
+    }
+    if (g < 0 || (long long)r.L + g > max_ctx) {
+        if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_POSITION);
+        return r;
+    }
+    r.nl = r.L + g;
+    r.live = true;
+    if (r.L % a.BS) {
+        r.tail_id = __ldg(a.block_table + (long long)r.p * a.MB + r.L / a.BS);
+        if (r.tail_id < 0 || r.tail_id >= a.NB) {
+            if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);   // carried along as it is
+        } else {
+            r.tail_ref = __ldg(a.refs + r.tail_id);
+        }
+    }
+    return r;
+}
+
 __global__ void __launch_bounds__(kScanThreads) pda_fork_scan_kernel(const ScanArgs a) {
-    __shared__ int tmp[32], share;
+    __shared__ int tmp[32], share, first_s[kScanThreads];
     __shared__ long long tmp64[32];
     allow_dependent_launch();
     grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    const long long per = ((a.NB + cl.num_blocks() - 1) / cl.num_blocks() + 3) & ~3ll;
-    const long long lo = min(a.NB, per * cl.block_rank()), hi = min(a.NB, lo + per);
+    // The last CTA lays out the rows.  What the first 1024 ask for is a chain of four loads, requested
+    // before the scan of the pool so that the two overlap.
+    const bool rows_here = cl.block_rank() == cl.num_blocks() - 1;
+    int* const first = a.B <= kScanThreads ? first_s : a.first;
+    NewRow row0 = {-1, 0, 0, -1, 0, false};
+    if (rows_here) {
+        for (int b = threadIdx.x; b < a.B; b += kScanThreads) first[b] = INT_MAX;
+        row0 = new_row(a, threadIdx.x);
+    }
+    long long lo, hi;
+    slice_of(cl, a.NB, lo, hi);
     int nfree;
-    int at = count_before(a, lo, hi, tmp, &share, nfree, [](long long, int r) { return r == 0 ? 1 : 0; });
-    for (long long t0 = lo; t0 < hi; t0 += kScanThreads) {
-        const long long i = t0 + threadIdx.x;
-        const int r = i < hi ? __ldg(a.refs + i) : 1;
+    int at = count_before(cl, a.refs, lo, hi, tmp, &share, nfree, [](int r) { return r == 0 ? 1 : 0; });
+    for (long long t0 = lo; t0 < hi; t0 += kScanTile) {
+        const long long i = t0 + 4 * threadIdx.x;
+        int r[4], c = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            r[u] = i + u < hi ? __ldg(a.refs + i + u) : 1;
+            c += r[u] == 0;
+        }
         int n;
-        const int rank = block_scan(r == 0 ? 1 : 0, tmp, n);
-        if (i < hi) a.out_refs[i] = r;
-        if (r == 0) a.free_ids[at + rank - 1] = (int)i;
+        int k = at + block_scan(c, tmp, n) - c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (i + u < hi) a.out_refs[i + u] = r[u];
+            if (r[u] == 0) a.free_ids[k++] = (int)(i + u);
+        }
         at += n;
     }
-    if (cl.block_rank() != cl.num_blocks() - 1) return;
-    // the last CTA lays out the rows: which one is the first of its parent, what each has to get,
-    // and where its blocks start in the list of free ones
-    for (int b = threadIdx.x; b < a.B; b += kScanThreads) a.first[b] = INT_MAX;
+    if (!rows_here) return;
+    // which row is the first of its parent, what each has to get, and where its blocks start in the
+    // list of free ones
     __syncthreads();
-    const long long max_ctx = (long long)a.MB * a.BS;
-    auto shape = [&](int i, int& p, int& L, int& nl) {   // false: the row stays empty
-        p = __ldg(a.parents + i);
-        if (p < 0) return false;
-        if (p >= a.B) {
-            if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_SEQUENCE);
-            return false;
-        }
-        L = __ldg(a.context_lens + p);
-        if (L < 0 || L > max_ctx) {
-            if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
-            L = 0;
-        }
-        const int g = a.new_tokens ? __ldg(a.new_tokens + i) : 0;
-        if (g < 0 || (long long)L + g > max_ctx) {
-            if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_POSITION);
-            return false;
-        }
-        nl = L + g;
-        return true;
-    };
-    int p, L, nl;
-    for (int i = threadIdx.x; i < a.R; i += kScanThreads)
-        if (shape(i, p, L, nl)) atomicMin(a.first + p, i);
+    for (int i = threadIdx.x; i < a.R; i += kScanThreads) {
+        const NewRow r = i < kScanThreads ? row0 : new_row(a, i);
+        if (r.live) atomicMin(first + r.p, i);
+    }
     __threadfence_block();
     __syncthreads();
     long long used = 0;   // 64 bits: the rows may ask for more than any pool has
     for (int i0 = 0; i0 < a.R; i0 += kScanThreads) {
         const int i = i0 + threadIdx.x;
-        p = -1;
-        L = nl = 0;
-        const bool live = i < a.R && shape(i, p, L, nl);
-        int need = 0, flags = 0, tail_id = -1;
-        if (live) {
-            if (__ldcg(a.first + p) == i) flags |= kRowFirst;
-            if (L % a.BS) {
-                tail_id = __ldg(a.block_table + (long long)p * a.MB + L / a.BS);
-                if (tail_id < 0 || tail_id >= a.NB) {
-                    if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);   // carried along as it is
-                } else if (!((flags & kRowFirst) && __ldg(a.refs + tail_id) == 1)) {
-                    flags |= kRowCopy;
-                }
-            }
-            need = (flags & kRowCopy) + (nl + a.BS - 1) / a.BS - (L + a.BS - 1) / a.BS;
+        const NewRow r = i0 == 0 ? row0 : new_row(a, i);
+        int need = 0, flags = 0;
+        if (r.live) {
+            if (*(volatile int*)(first + r.p) == i) flags |= kRowFirst;
+            const bool in_pool = r.tail_id >= 0 && r.tail_id < a.NB;
+            if (in_pool && !((flags & kRowFirst) && r.tail_ref == 1)) flags |= kRowCopy;
+            need = (flags & kRowCopy) + (r.nl + a.BS - 1) / a.BS - (r.L + a.BS - 1) / a.BS;
         }
         long long n;
         const long long off = used + block_scan((long long)need, tmp64, n) - need;
         used += n;
         if (i < a.R) {
-            const bool ok = live && (need == 0 || off + need <= nfree);
-            if (live && !ok && a.err_word) atomicOr(a.err_word, PDA_ERRW_OUT_OF_BLOCKS);
-            if (live && !ok && (flags & kRowFirst)) a.first[p] = -1;
+            const bool ok = r.live && (need == 0 || off + need <= nfree);
+            if (r.live && !ok && a.err_word) atomicOr(a.err_word, PDA_ERRW_OUT_OF_BLOCKS);
+            if (r.live && !ok && (flags & kRowFirst)) first[r.p] = -1;
             int4* rec = reinterpret_cast<int4*>(a.rows + (long long)i * kRowInts);
-            rec[0] = make_int4(ok ? p : -1, ok ? L : 0, ok ? nl : 0, ok ? (int)off : 0);
-            rec[1] = make_int4(ok ? flags : 0, tail_id, 0, 0);
-            a.out_lens[i] = ok ? nl : 0;
+            rec[0] = make_int4(ok ? r.p : -1, ok ? r.L : 0, ok ? r.nl : 0, ok ? (int)off : 0);
+            rec[1] = make_int4(ok ? flags : 0, r.tail_id, 0, 0);
+            a.out_lens[i] = ok ? r.nl : 0;
         }
+    }
+    if (first == first_s) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < a.B; b += kScanThreads) a.first[b] = first_s[b];
     }
 }
 
@@ -330,56 +374,64 @@ __global__ void __launch_bounds__(kPageThreads) pda_fork_apply_kernel(const Fork
     }
 }
 
-// U = blocks in use.  A block in use at or above U moves to the free block below U of the same rank.
+// U = blocks in use, of which V have ids below U.  The used block of rank r >= V (its id is at or above U)
+// moves to the free block below U of rank r - V.  One scan gives both ranks: a block's rank among the
+// used ones, and, as the rest of its id, among the free ones.
 __global__ void __launch_bounds__(kScanThreads) pda_compact_scan_kernel(const ScanArgs a) {
     __shared__ int tmp[32], share;
     allow_dependent_launch();
     grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    const long long per = ((a.NB + cl.num_blocks() - 1) / cl.num_blocks() + 3) & ~3ll;
-    const long long lo = min(a.NB, per * cl.block_rank()), hi = min(a.NB, lo + per);
-    int U, M;
-    const int used_before = count_before(a, lo, hi, tmp, &share, U, [](long long, int r) { return r > 0 ? 1 : 0; });
-    int mover_at = count_before(a, lo, hi, tmp, &share, M,
-                                [U](long long i, int r) { return r > 0 && i >= U ? 1 : 0; });
-    // blocks in use below min(lo, U): those before the slice that do not move
-    int hole_at = (int)min(lo, (long long)U) - (used_before - mover_at);
-    for (long long t0 = lo; t0 < hi; t0 += kScanThreads) {
-        const long long i = t0 + threadIdx.x;
-        const int r = i < hi ? __ldg(a.refs + i) : 0;
-        const bool in = i < hi, mover = in && r > 0 && i >= U, hole = in && r <= 0 && i < U;
-        int nm, nh;
-        const int km = block_scan(mover ? 1 : 0, tmp, nm), kh = block_scan(hole ? 1 : 0, tmp, nh);
-        if (mover) a.movers[mover_at + km - 1] = (int)i;
-        if (hole) a.holes[hole_at + kh - 1] = (int)i;
-        mover_at += nm;
-        hole_at += nh;
-        if (in && !mover) {
-            a.remap[i] = r > 0 ? (int)i : -1;
-            if (!hole) a.out_refs[i] = r > 0 ? r : 0;
+    long long lo, hi;
+    slice_of(cl, a.NB, lo, hi);
+    int U;
+    int at = count_before(cl, a.refs, lo, hi, tmp, &share, U, [](int r) { return r > 0 ? 1 : 0; });
+    if (U == 0 && cl.block_rank() == 0 && threadIdx.x == 0) a.scalars[0] = a.scalars[1] = 0;
+    for (long long t0 = lo; t0 < hi; t0 += kScanTile) {
+        const long long i = t0 + 4 * threadIdx.x;
+        int r[4], c = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            r[u] = i + u < hi ? __ldg(a.refs + i + u) : 0;
+            c += r[u] > 0;
         }
-        if (mover) a.out_refs[i] = 0;
+        int n;
+        int k = at + block_scan(c, tmp, n) - c;   // used blocks before this one
+        at += n;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long id = i + u;
+            if (id >= hi) break;
+            const bool used = r[u] > 0, low = id < U;
+            if (used && !low) a.used_ids[k] = (int)id;
+            if (!used && low) a.holes[id - k] = (int)id;
+            if (!used || low) a.remap[id] = used ? (int)id : -1;
+            if (used || !low) a.out_refs[id] = low ? r[u] : 0;
+            k += used;
+            if (id == U - 1) {
+                a.scalars[0] = U - k;
+                a.scalars[1] = k;
+            }
+        }
     }
     __threadfence();
     cl.sync();   // both lists are complete
+    const int M = __ldcg(a.scalars), V = __ldcg(a.scalars + 1);
     for (int k = cl.block_rank() * kScanThreads + threadIdx.x; k < M; k += cl.num_blocks() * kScanThreads) {
-        const int from = __ldcg(a.movers + k), to = __ldcg(a.holes + k);
+        const int from = __ldcg(a.used_ids + V + k), to = __ldcg(a.holes + k);
         a.remap[from] = to;
         a.out_refs[to] = __ldg(a.refs + from);
     }
-    if (cl.block_rank() == 0 && threadIdx.x == 0) {
-        *a.num_moved = M;
-        *a.num_used = U;
-    }
+    if (cl.block_rank() == 0 && threadIdx.x == 0) *a.num_used = U;
 }
 
 struct CompactArgs {
     uint8_t* cache;
     const int* block_table;
     const int* context_lens;
-    const int* movers;
+    const int* used_ids;
     const int* holes;
-    const int* num_moved;
+    const int* scalars;
     const int* remap;
     int* out_table;
     int* err_word;
@@ -391,7 +443,8 @@ template <int U>
 __global__ void __launch_bounds__(kPageThreads) pda_compact_apply_kernel(const CompactArgs a) {
     grid_dependency_wait();
     const long long cpb = chunks_of<U>(a.block_bytes), tables = (long long)a.B * a.segs;
-    const long long items = tables + (long long)__ldcg(a.num_moved) * cpb;
+    const long long items = tables + (long long)__ldcg(a.scalars) * cpb;
+    const int* movers = a.used_ids + __ldcg(a.scalars + 1);
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
         if (it < tables) {
             const int b = (int)(it / a.segs), seg = (int)(it - (long long)b * a.segs);
@@ -414,7 +467,7 @@ __global__ void __launch_bounds__(kPageThreads) pda_compact_apply_kernel(const C
             }
         } else {
             const long long r = it - tables, k = r / cpb;
-            copy_chunk<U>(a.cache + (long long)__ldcg(a.movers + k) * a.block_bytes,
+            copy_chunk<U>(a.cache + (long long)__ldcg(movers + k) * a.block_bytes,
                           a.cache + (long long)__ldcg(a.holes + k) * a.block_bytes, a.block_bytes, r - k * cpb);
         }
     }
@@ -582,9 +635,9 @@ int pda_compact_blocks(const pda_plan_t* plan, void* kv_cache, long long num_cac
     s.NB = NB;
     s.out_refs = out_refcounts;
     s.err_word = err_word;
-    s.movers = ws;
+    s.used_ids = ws;
     s.holes = ws + NB;
-    s.num_moved = ws + ((2 * NB + 3) & ~3ll);
+    s.scalars = ws + ((2 * NB + 3) & ~3ll);
     s.remap = remap;
     s.num_used = num_used;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -595,9 +648,9 @@ int pda_compact_blocks(const pda_plan_t* plan, void* kv_cache, long long num_cac
     c.cache = static_cast<uint8_t*>(kv_cache);
     c.block_table = block_table;
     c.context_lens = context_lens;
-    c.movers = s.movers;
+    c.used_ids = s.used_ids;
     c.holes = s.holes;
-    c.num_moved = s.num_moved;
+    c.scalars = s.scalars;
     c.remap = remap;
     c.out_table = out_table;
     c.err_word = err_word;
