@@ -59,6 +59,7 @@ __device__ __forceinline__ uint32_t bf16_down(float x) { return bf16_up(-x) ^ 0x
 // read once (a 256-byte run per bf16 row), 512 bytes are written.
 template <int KV, int BS>
 __global__ void __launch_bounds__(256) pda_summarize_kernel(const SumArgs a) {
+    allow_dependent_launch();
     grid_dependency_wait();
     constexpr int R16 = KV == PDA_KV_BF16 ? 16 : KV == PDA_KV_FP8_E4M3 ? 8 : 4;
     constexpr int TOK = 32 / R16, LOADS = BS / TOK, E = 128 / R16;   // E elements per word
@@ -171,9 +172,20 @@ constexpr int kScoreWarps = 4;
 // operands use it: lane (gid, tig) takes the 16-byte words tig, tig + 4, ... of the summary rows gid
 // and gid + 8 as they lie in memory (16 independent loads, 8 KB per warp in flight), and its B
 // fragments hold the same dimensions of [q+ | q-]; a bf16 value's part is itself or zero, so both
-// operands are exact and the sums are fp32.  Bound by HBM: 512 bytes per block and head, read once.
+// operands are exact and the sums are fp32.  Bound by HBM: 512 bytes per block and head, read once
+// (52 MB of them, 16 sequences of up to 32768 tokens: 10.1 us, 5.1 TB/s; three CTAs per SM and as many as are
+// resident at once, against 12.2 us with six and 1.4 waves; two tiles of words in flight per warp: 12 us;
+// 32-byte loads: 11.2 us).
+__device__ __forceinline__ uint4 load_once(const uint4* p) {   // in program order: every load before the first use
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 template <int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32) pda_score_kernel(const ScoreArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 3) pda_score_kernel(const ScoreArgs a) {
+    allow_dependent_launch();
     grid_dependency_wait();
     const int unit = blockIdx.x / a.ctas, cta = blockIdx.x - unit * a.ctas;
     const int b = unit / a.Hk, h = unit - b * a.Hk;
@@ -217,8 +229,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) pda_score_kernel(const Score
         uint4 v0[8], v1[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v0[i] = __ldg(r0 + 4 * i);
-            v1[i] = __ldg(r1 + 4 * i);
+            v0[i] = load_once(r0 + 4 * i);
+            v1[i] = load_once(r1 + 4 * i);
         }
         float d[NT][2][4];
 #pragma unroll
@@ -285,6 +297,7 @@ __global__ void __launch_bounds__(kSelThreads) pda_select_kernel(const SelectArg
     __shared__ uint32_t sums[kSelThreads / 32];
     __shared__ unsigned long long sums64[kSelThreads / 32];
     __shared__ uint32_t pick, left;
+    allow_dependent_launch();
     grid_dependency_wait();
     const int b = blockIdx.x / a.Hk, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool lead = blockIdx.x == (unsigned)(b * a.Hk) && tid == 0;
@@ -473,7 +486,7 @@ int pda_score_blocks(const pda_plan_t* plan, const void* query, const void* summ
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     const long long want = (plan->max_blocks_per_seq + 16 * kScoreWarps - 1) / (16 * kScoreWarps);
-    const long long cap = (8ll * sms + units - 1) / units;
+    const long long cap = (3ll * sms + units - 1) / units;
     const int ctas = (int)(want < cap ? want : cap);
     if (ctas * units > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
     const dim3 grid((unsigned)(ctas * units));
