@@ -412,14 +412,18 @@ PDA_API int pda_select_blocks(const pda_plan_t* plan, const float* scores, const
                               int* sel_lens, int* sel_blocks, int* err_word, void* stream);
 
 /*
- * pda_decode_selected -- a decode step over selected blocks: the partition pass and the reduce, with one
- * table row and one length per (sequence, KV head).
+ * pda_decode_selected -- a decode step over selected blocks, with one table row and one length per
+ * (sequence, KV head), in one launch: each (sequence, KV head) is split over the warps of a thread-block
+ * cluster and joined in its shared memory.  With kernel_variant head warps it is the partition pass and the
+ * reduce instead, whose partials are those of pda_decode over the same lists.
  *   plan        as for pda_decode, with max_blocks_per_seq = num_select (kernel_variant automatic or
  *               head warps, else PDA_ERR_UNSUPPORTED)
  *   centroids   device, fp32 [16] for a TQ4 plan, else NULL
  *   sel_table   device, int32 [num_seqs][num_kv_heads][max_blocks_per_seq]
  *   sel_lens    device, int32 [num_seqs][num_kv_heads]: tokens; all blocks but the last are full
- *   partials, out, out_dtype and the data errors as for pda_decode and pda_reduce
+ *   partial_out, exp_sums, max_logits   as for pda_decode with kernel_variant head warps; otherwise not
+ *               looked at (may be NULL)
+ *   out, out_dtype and the data errors as for pda_decode and pda_reduce
  * query may be pinned host memory as for pda_decode, and out as for pda_reduce.
  */
 PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* kv_cache,

@@ -510,23 +510,26 @@ def select_blocks(p: Plan, scores, block_table, context_lens, num_select: int, n
 def decode_selected(p: Plan, query, kv_cache, num_cache_blocks: int, sel_table, sel_lens, ws: dict | None = None,
                     out=None, out_dtype=torch.bfloat16, centroids=None, err_word=None, stream=None):
     """pda_decode_selected: a decode step over the blocks in sel_table [B][Hk][max_blocks_per_seq],
-    sel_lens [B][Hk] tokens (see include/pda.h); returns out [B][Hk*QG][D]."""
+    sel_lens [B][Hk] tokens (see include/pda.h); returns out [B][Hk*QG][D].  ws: the partials of a plan
+    with kernel_variant VARIANT_HEAD_WARPS (made if None); other plans need none."""
     c = _Call(kv_cache, "kv_cache")
     B, Hk, QG, D, P = p.num_seqs, p.num_kv_heads, p.query_group_size, p.head_dim, p.num_partitions
-    if ws is None:
-        ws = _scratch(workspace(p, kv_cache.device), stream)
     if out is None:
         out = torch.empty((B, Hk * QG, D), dtype=out_dtype, device=kv_cache.device)
     rows = B * Hk * QG
     f32 = out.dtype is torch.float32
+    partials = (None, None, None)
+    if p.kernel_variant == VARIANT_HEAD_WARPS:
+        if ws is None:
+            ws = _scratch(workspace(p, kv_cache.device), stream)
+        partials = (c.ptr(ws["partial_out"], "partial_out", _F32, rows * P * D * 4),
+                    c.ptr(ws["exp_sums"], "exp_sums", _F32, rows * P * 4),
+                    c.ptr(ws["max_logits"], "max_logits", _F32, rows * P * 4))
     args = (c.ptr(query, "query", _BF16, rows * D * 2, host_ok=True),
             c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
             c.opt(centroids, "centroids", _F32, 64),
             c.ptr(sel_table, "sel_table", _I32, B * Hk * p.max_blocks_per_seq * 4),
-            c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4),
-            c.ptr(ws["partial_out"], "partial_out", _F32, rows * P * D * 4),
-            c.ptr(ws["exp_sums"], "exp_sums", _F32, rows * P * 4),
-            c.ptr(ws["max_logits"], "max_logits", _F32, rows * P * 4),
+            c.ptr(sel_lens, "sel_lens", _I32, B * Hk * 4), *partials,
             c.ptr(out, "out", (torch.float32, torch.bfloat16), rows * D * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_selected", lib().pda_decode_selected, p, args, err_word, stream)

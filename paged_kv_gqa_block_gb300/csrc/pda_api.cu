@@ -456,7 +456,9 @@ int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* k
     // the other layouts share a block's copy between heads or take their units per sequence
     if (plan->kernel_variant > PDA_VARIANT_HEAD_WARPS) return PDA_ERR_UNSUPPORTED;
     if (plan->num_seqs == 0) return PDA_OK;
-    if (!query || !kv_cache || !sel_table || !sel_lens || !partial_out || !exp_sums || !max_logits || !out)
+    const bool partials = plan->kernel_variant == PDA_VARIANT_HEAD_WARPS;
+    if (!query || !kv_cache || !sel_table || !sel_lens || !out ||
+        (partials && (!partial_out || !exp_sums || !max_logits)))
         return PDA_ERR_INVALID_ARG;
     if (num_cache_blocks < 1 || num_cache_blocks > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
     if (!aligned16(query) || !aligned16(kv_cache) || !aligned16(partial_out)) return PDA_ERR_INVALID_ARG;
@@ -477,6 +479,9 @@ int pda_decode_selected(const pda_plan_t* plan, const void* query, const void* k
     else if (!encode_scale_map(&sc_map, kv_cache, plan, num_cache_blocks))
         return PDA_ERR_LAUNCH;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.out = out;
+    a.out_f32 = out_dtype == PDA_OUT_F32;
+    if (!partials) return launch_selected_clusters(plan->kv_dtype, a, kv_map, sc_map, s);
     const int rc = launch_decode_selected(plan->kv_dtype, a, kv_map, sc_map, s);
     if (rc != PDA_OK) return rc;
     ReduceArgs r;

@@ -66,6 +66,9 @@ int group_heads(int Hk);
 // Head warps with one table per (sequence, KV head); a.B, a.Hk and a.sel_heads as stated there.
 int launch_decode_selected(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                            cudaStream_t stream);
+// The same in one launch that writes a.out, without partials.
+int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                             cudaStream_t stream);
 // Head warps over the sequences' own tokens beside a shared prefix (bf16, fp8).
 int launch_decode_own(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                       cudaStream_t stream);

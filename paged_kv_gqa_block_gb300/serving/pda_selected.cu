@@ -1,0 +1,92 @@
+// pda_selected.cu -- the launch of pda_decode_selected in its one-launch form (pda_selected.cuh).
+#include <mutex>
+
+#include "pda.h"
+#include "pda_selected.cuh"
+
+namespace pda {
+
+// The cluster of a unit: C CTAs of nw warps.  `wps` warps fit an SM, in CTAs of at most `nwmax`; a unit has
+// `tiles` tiles (the table's capacity; the lengths are on the device).  Counted in a warp's tiles, a
+// round of CTAs takes a warp's run, and 6 for its start and its join, 3 more for a cluster's join; the rounds
+// that the units need are what the choice weighs against it.  Measured against the partition pass and
+// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.5 us against 16.1, 32 units 11.0 against
+// 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 44 against 63, 1024 units of 8192 287 against 383;
+// only 800 units of 4096 bf16 tokens were slower, 273 against 245.
+struct Shape {
+    int C, nw;
+};
+static Shape selected_shape(long long units, int tiles, int sms, int wps, int nwmax) {
+    long long best = 0;
+    Shape s = {1, 1};
+    for (int C = 1; C <= 8; C *= 2)
+        for (int nw = 1; nw <= nwmax; ++nw) {
+            const long long slots = (long long)sms * (wps / nw), rounds = (units * C + slots - 1) / slots;
+            const int pairs = (tiles + 1) / 2;
+            const long long t = rounds * (2 * ((pairs + C * nw - 1) / (C * nw)) + 6 + (C > 1 ? 3 : 0));
+            if (best == 0 || t < best) {
+                best = t;
+                s = Shape{C, nw};
+            }
+        }
+    return s;
+}
+
+template <int KV, int NT, int S, int NWMAX, int MINB>
+static int launch_clusters(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, Shape shape,
+                           cudaStream_t stream) {
+    auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB>;
+    static bool attr_set[64] = {false};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PDA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SelectedCfg<KV, S>::bytes(NWMAX)) !=
+                cudaSuccess)
+                return PDA_ERR_LAUNCH;
+            attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * shape.C));
+    cfg.blockDim = dim3(32 * shape.nw);
+    cfg.dynamicSmemBytes = SelectedCfg<KV, S>::bytes(shape.nw);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = shape.C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+template <int KV, int NT, int S, int NWMAX, int WPS>
+static int launch_clusters_of(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                              cudaStream_t stream) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return PDA_ERR_CUDA;
+    const Shape shape = selected_shape(a.B, (a.MB * a.BS + 15) / 16, sms, WPS, NWMAX);
+    if ((long long)a.B * shape.C > 0x7FFFFFFFll) return PDA_ERR_INVALID_ARG;
+    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX>(a, kv_map, sc_map, shape, stream);
+}
+
+int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                             cudaStream_t stream) {
+    if (kv_dtype == PDA_KV_BF16) {
+        if (a.QG <= 8) return launch_clusters_of<PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
+        return launch_clusters_of<PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
+    }
+    if (kv_dtype == PDA_KV_TQ4) {
+        if (a.QG <= 8) return launch_clusters_of<PDA_KV_TQ4, 1, 6, 6, 12>(a, kv_map, sc_map, stream);
+        return launch_clusters_of<PDA_KV_TQ4, 2, 6, 4, 8>(a, kv_map, sc_map, stream);
+    }
+    if (a.QG <= 8) return launch_clusters_of<PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
+    return launch_clusters_of<PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
+}
+
+}  // namespace pda

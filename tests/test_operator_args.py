@@ -103,7 +103,9 @@ def test_select_and_decode_selected(pda):
         ({3: 0}, INVALID), ({4: -1}, INVALID), ({5: -1}, INVALID), ({3: 2}, INVALID), ({4: 1 << 30, 5: 1 << 30, 3: 1 << 20}, INVALID),
         ({3: 1 << 27}, INVALID), ({8: off(BASE + 2)}, INVALID)])
     good = [at(0), at(1), 100, None, at(2), at(3), at(4), at(5), at(6), at(7), 0, None, None]
-    refused(L.pda_decode_selected, p, good, [({i: None}, INVALID) for i in (0, 1, 4, 5, 6, 7, 8, 9)] + [
+    warps = pda.plan(3, 2, 8, 16, 4, kernel_variant=pda.VARIANT_HEAD_WARPS)            # needs its partials
+    refused(L.pda_decode_selected, warps, good, [({i: None}, INVALID) for i in (0, 1, 4, 5, 6, 7, 8, 9)])
+    refused(L.pda_decode_selected, p, good, [({i: None}, INVALID) for i in (0, 1, 4, 5, 9)] + [
         ({2: 0}, INVALID), ({3: at(9)}, INVALID), ({10: 2}, INVALID), ({0: off(BASE + 8)}, INVALID), ({6: off(BASE + 8)}, INVALID),
         ({9: off(BASE + 4)}, INVALID), ({9: off(BASE + 8), 10: 1}, INVALID)])
     grouped = pda.plan(3, 2, 8, 16, 4, kv_dtype=pda.KV_FP8_E4M3, kernel_variant=pda.VARIANT_HEAD_GROUPS)

@@ -226,14 +226,15 @@ def check_selected(pda, w, inp, lists, p, d, K, out_dtype=torch.float32, err=Non
     return out
 
 
+@pytest.mark.parametrize("variant", [0, 1])                  # one launch of clusters; partition pass and reduce
 @pytest.mark.parametrize("kv", FORMATS)
 @pytest.mark.parametrize("QG,BS,Hk,G", [(6, 16, 3, 1), (8, 32, 2, 2), (16, 16, 1, 1)])
-def test_decode_selected(pda, kv, QG, BS, Hk, G):
+def test_decode_selected(pda, kv, QG, BS, Hk, G, variant):
     ctx = (0, 1, BS + 3, 40 * BS, 61 * BS - 2)
     w = wl.small(num_seqs=5, num_kv_heads=Hk, query_group_size=QG, kv_block_size=BS, ctx=ctx, kv_dtype=kv, seed=QG + kv)
     inp = wl.generate(w)
     d, K = to_device(inp), 37
-    p = pda.plan(5, Hk, QG, BS, K, tile_groups_per_partition=G, kv_dtype=kv)
+    p = pda.plan(5, Hk, QG, BS, K, tile_groups_per_partition=G, kv_dtype=kv, kernel_variant=variant)
     rng = np.random.default_rng(kv)
     lists = []
     for b in range(5):
@@ -255,7 +256,59 @@ def test_decode_selected_of_every_block_is_the_plain_step(pda):
     table = d["block_table"][:, None].expand(-1, 2, -1).contiguous()
     lens = d["context_lens"][:, None].expand(-1, 2).contiguous()
     out = pda.decode_selected(p, d["query"], d["cache"], w.num_cache_blocks, table, lens, out_dtype=torch.float32)
-    assert torch.equal(out, plain)
+    assert torch.equal(out, plain)                           # the same partitions
+    out = pda.decode_selected(plan_of(pda, w), d["query"], d["cache"], w.num_cache_blocks, table, lens, out_dtype=torch.float32)
+    # other runs of tokens: each weight is off by at most 2^-16 (P as two bf16) and a few steps of 2^-23, |V| < 6
+    assert (out - plain).abs().max() <= 2 * 6 * 2.0 ** -16 * 1.1
+
+
+@pytest.mark.parametrize("kv,QG", [(wl.KV_BF16, 8), (wl.KV_BF16, 16), (wl.KV_FP8_E4M3, 6), (wl.KV_TQ4, 8), (wl.KV_FP8_E4M3, 16)])
+@pytest.mark.parametrize("B,K", [(1, 70), (37, 9), (150, 33), (700, 2)])
+def test_decode_selected_shapes(pda, kv, QG, B, K):
+    # few long units (clusters of eight), many short ones (single CTAs), lists shorter than the warps, blocks shared by units
+    rng = np.random.default_rng(B)
+    w = wl.small(num_seqs=1, num_kv_heads=2, query_group_size=QG, ctx=(16 * 80,), kv_dtype=kv, seed=B)
+    inp = wl.generate(w)
+    d = to_device(inp)
+    p = pda.plan(B, 2, QG, 16, K, kv_dtype=kv)
+    sel, lens = np.full((B, 2, K), -1, np.int32), np.zeros((B, 2), np.int32)
+    for b in range(B):
+        for h in range(2):
+            n = rng.integers(0, K + 1) if b else K
+            sel[b, h, :n] = inp.block_table[0, rng.permutation(80)[:n]]
+            lens[b, h] = max(0, n * 16 - rng.integers(0, 16))
+    q = wl.round_bf16(rng.standard_normal((B, 2 * QG, 128)).astype(np.float32))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pda.decode_selected(p, torch.from_numpy(q.view(np.int16)).cuda().view(torch.bfloat16), d["cache"], w.num_cache_blocks,
+                              torch.from_numpy(sel).cuda(), torch.from_numpy(lens).cuda(), out_dtype=torch.float32,
+                              centroids=d.get("centroids"), err_word=err)
+    got, q64 = out.double().cpu().numpy(), wl.bf16_bits_to_f32(q).astype(np.float64)
+    kst, vst = pp.block_values(w, inp.cache, inp.extra.get("centroids"))
+    for b in range(B):
+        for h in range(2):
+            ids, n, rows = sel[b, h, :-(-lens[b, h] // 16)], lens[b, h], slice(h * QG, (h + 1) * QG)
+            ref = pp.attention(q64[b, rows], kst[ids, :, h].reshape(-1, 128)[:n], vst[ids, :, h].reshape(-1, 128)[:n], 128 ** -0.5)
+            assert np.abs(got[b, rows] - ref).max() <= TOL[kv], (b, h)
+    assert int(err.item()) == 0
+
+
+def test_decode_selected_timeout_sets_the_error_bit_and_the_next_call_is_correct(pda):
+    w = wl.small(num_seqs=16, num_kv_heads=8, ctx=(4096,) * 16, seed=61, extra_blocks=0)
+    inp = wl.generate(w)
+    d = to_device(inp)
+    table = d["block_table"][:, None].expand(-1, 8, -1).contiguous()
+    lens = torch.full((16, 8), 4096, dtype=torch.int32, device="cuda")
+    args = (d["query"], d["cache"], w.num_cache_blocks, table, lens)
+    for variant in (0, 1):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pda.decode_selected(plan_of(pda, w, wait_timeout_ns=1, kernel_variant=variant), *args, err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) & pda.ERRW_PIPELINE_TIMEOUT
+        err.zero_()
+        out = pda.decode_selected(plan_of(pda, w, kernel_variant=variant), *args, out_dtype=torch.float32, err_word=err)
+        plain = pda.decode_step(plan_of(pda, w), d["query"], d["cache"], w.num_cache_blocks, d["block_table"], d["context_lens"],
+                                out_dtype=torch.float32)
+        assert int(err.item()) == 0 and (out - plain).abs().max() <= 2 * 6 * 2.0 ** -16 * 1.1
 
 
 def test_decode_selected_data_errors(pda):
@@ -265,11 +318,13 @@ def test_decode_selected_data_errors(pda):
     table = d["block_table"][:, None].expand(-1, 2, -1).contiguous()
     table[0, 1, 2] = w.num_cache_blocks + 9
     lens = torch.tensor([[64, 64], [65, 0]], dtype=torch.int32, device="cuda")
-    err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = pda.decode_selected(p, d["query"], d["cache"], w.num_cache_blocks, table, lens, out_dtype=torch.float32, err_word=err)
-    torch.cuda.synchronize()
-    assert int(err.item()) == pda.ERRW_BAD_BLOCK_ID | pda.ERRW_BAD_CONTEXT_LEN
-    assert (out[1] == 0).all() and torch.isfinite(out).all()
+    for variant in (0, 1):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = pda.decode_selected(plan_of(pda, w, kernel_variant=variant), d["query"], d["cache"], w.num_cache_blocks, table, lens,
+                                  out_dtype=torch.float32, err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == pda.ERRW_BAD_BLOCK_ID | pda.ERRW_BAD_CONTEXT_LEN
+        assert (out[1] == 0).all() and torch.isfinite(out).all()
 
 
 @pytest.mark.parametrize("kv", FORMATS)
