@@ -452,9 +452,13 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  *   query, out, out_dtype as for pda_decode and pda_reduce (query and out may be pinned host memory)
  * The weights of the prefix part are rounded to bf16 (bf16 KV), or they and the scaled V to f16 (fp8 KV), before
  * their product, so an fp32 out carries that rounding (at most 2^-8, or 3 * 2^-11, of each term).
- * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN), a group that is not
- * ascending or leaves [0, num_seqs] as empty (PDA_ERRW_BAD_GROUP; where other groups then overlap, their
- * rows are undefined), block ids as for pda_decode.
+ * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN); group_starts that are not
+ * ascending within [0, num_seqs] set PDA_ERRW_BAD_GROUP, and the step runs without prefixes; block ids as
+ * for pda_decode.
+ *
+ * pda_shared_tile_groups -- host only: tile_groups_per_partition of a prefix plan for num_groups prefixes of up
+ * to prefix_blocks blocks, with which a prefix is cut into as many pieces as the GPU's SMs have room for.
+ * pda_shared_workspace_size -- bytes of the workspace; -1 where the plans do not belong together.
  */
 PDA_API int pda_shared_tile_groups(const pda_plan_t* plan, int num_groups, int prefix_blocks);
 PDA_API long long pda_shared_workspace_size(const pda_plan_t* prefix_plan, const pda_plan_t* plan);

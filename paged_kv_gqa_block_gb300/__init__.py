@@ -418,6 +418,8 @@ def copy_blocks(p: Plan, src_cache, src_blocks: int, dst_cache, dst_blocks: int,
     include/pda.h).  pairs: int32 [n][2].  Either cache may be pinned host memory."""
     c = _Call(pairs, "pairs")
     n = pairs.numel() // 2
+    if pairs.numel() != 2 * n:
+        raise ValueError("pairs must hold two ids per pair")
     cbb = p.cache_block_bytes
     args = (c.ptr(src_cache, "src_cache", None, src_blocks * cbb, host_ok=True), src_blocks,
             c.ptr(dst_cache, "dst_cache", None, dst_blocks * cbb, host_ok=True), dst_blocks,

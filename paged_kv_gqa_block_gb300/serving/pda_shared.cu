@@ -134,7 +134,7 @@ __device__ __forceinline__ Group group_shape(const SharedArgs& a, int g, int& ba
     return x;
 }
 // How one warp sees the split: lane i holds group i (and re-reads the others where there are more
-// than 32).  The host has made sure that the number of all steps fits an int.
+// than 32).  The host has made sure that the number of all steps of ascending groups fits an int.
 struct Split {
     Group mine;
     int before, total;     // steps of the groups before lane i's (of the first 32), and of all
@@ -168,6 +168,8 @@ __device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool 
         s.total += __reduce_add_sync(kLanes, more);
     }
     longest = __reduce_max_sync(kLanes, longest);
+    // groups that are not ascending may overlap, and name more rows than there are: no prefix then
+    if (__any_sync(kLanes, bad & PDA_ERRW_BAD_GROUP)) s.total = 0;
     if (report && bad && a.err_word) atomicOr(a.err_word, bad);
     s.per = max(max((s.total + ctas - 1) / ctas, (longest + a.P - 1) / a.P), 1);
     return s;
@@ -872,12 +874,6 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
         prefetch_tensormap(&kv_map);
         if (Cfg::kF16) prefetch_tensormap(&sc_map);
     }
-    if (warp == 9) tmem_alloc(bars + kTmemAt, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = lds32v(bars + kTmemAt);
-    allow_dependent_launch();
     // No wait for the previous grid here: it is this call's pass over the sequences' own tokens, which lets
     // this one start only after everything before it has ended, and of which nothing is read.
     Prefix<KV> p(a, sm);
@@ -885,6 +881,12 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     p.at = (int)min((long long)blockIdx.x * p.split.per, (long long)p.split.total);
     p.end = p.at + min(p.split.per, p.split.total - p.at);
     p.look_up();
+    if (warp == 9) tmem_alloc(bars + kTmemAt, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds32v(bars + kTmemAt);
+    allow_dependent_launch();
     // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
@@ -940,16 +942,14 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
     // asked for at once, whether or not the sequence has a prefix (the row's entry is then not used)
     const int pieces = __ldg(a.pieces + unit * a.QG + q);
     int ctx = __ldg(a.context_lens + b);
-    bool prefix = false;
-    for (int g0 = 0; g0 < a.NG; g0 += 32) {
-        bool in = false;
-        if (g0 + lane < a.NG) {
-            const int s0 = __ldg(a.group_starts + g0 + lane), s1 = __ldg(a.group_starts + g0 + lane + 1);
-            const int len = __ldg(a.prefix_lens + g0 + lane);
-            in = s0 >= 0 && s1 <= a.B && s0 <= b && b < s1 && len > 0 && len <= a.MP * a.BS;
-        }
-        prefix |= __any_sync(kLanes, in) != 0;
+    bool in = false, bad = false;   // as the prefix pass: one group that is not ascending, and there is no prefix
+    for (int g = lane; g < a.NG; g += 32) {
+        const int s0 = __ldg(a.group_starts + g), s1 = __ldg(a.group_starts + g + 1);
+        const int len = __ldg(a.prefix_lens + g);
+        bad |= s0 < 0 || s1 < s0 || s1 > a.B;
+        in |= s0 <= b && b < s1 && len > 0 && len <= a.MP * a.BS;
     }
+    const bool prefix = __any_sync(kLanes, in) && !__any_sync(kLanes, bad);
     const int np = prefix ? max(0, min(a.slots, pieces)) : 0;
     if (ctx < 0 || ctx > a.MB * a.BS) ctx = 0;   // reported by the partition pass
     const int total = np + (ctx + a.W - 1) / a.W;
@@ -1139,7 +1139,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
         return PDA_ERR_INVALID_ARG;
     const SharedLayout w = shared_layout(prefix_plan, plan);
     if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;
-    if (most_steps(prefix_plan, plan) > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;   // the split counts in ints
+    if (most_steps(prefix_plan, plan) > 2000000000ll) return PDA_ERR_INVALID_ARG;   // the split counts in ints
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -115,6 +115,46 @@ def test_select_and_decode_selected(pda):
     assert L.pda_decode_selected(ctypes.byref(pda.plan(0, 2, 8, 16, 4)), *good) == OK
 
 
+def test_decode_shared(pda):
+    L = pda.lib()
+    pp, p = pda.shared_plans(6, 2, 2, 8, 16, 40, 4)
+    need = L.pda_shared_workspace_size(ctypes.byref(pp), ctypes.byref(p))
+    assert need > 0
+    good = [ctypes.byref(p)] + [at(k) for k in range(2)] + [100] + [at(k) for k in range(2, 8)] + [need, at(8), 0, None, None]
+    off = ctypes.c_void_p
+    refused(L.pda_decode_shared, pp, good, [({i: None}, INVALID) for i in (0, 1, 2, 4, 5, 6, 7, 8, 9, 11)] + [
+        ({3: 0}, INVALID), ({10: need - 1}, SMALL), ({12: 5}, INVALID), ({1: off(BASE + 8)}, INVALID), ({2: off(BASE + 8)}, INVALID),
+        ({9: off(BASE + 16)}, INVALID), ({4: off(BASE + 2)}, INVALID), ({11: off(BASE + 4)}, INVALID), ({13: off(BASE + 2)}, INVALID)])
+    for other in (dict(num_kv_heads=1), dict(query_group_size=6), dict(kv_block_size=32), dict(kv_dtype=1), dict(softmax_scale=0.5)):
+        args = dict(num_seqs=6, num_kv_heads=2, query_group_size=8, kv_block_size=16, max_blocks_per_seq=4)
+        q = pda.plan(**{**args, **other})
+        assert L.pda_shared_workspace_size(ctypes.byref(pp), ctypes.byref(q)) == -1
+        refused(L.pda_decode_shared, pp, [ctypes.byref(q)] + good[1:], [({}, INVALID)])
+    tpp, tp = pda.shared_plans(6, 2, 2, 8, 16, 40, 4, kv_dtype=pda.KV_TQ4)
+    refused(L.pda_decode_shared, tpp, [ctypes.byref(tp)] + good[1:10] + [1 << 30] + good[11:], [({}, UNSUPPORTED)])
+    none = pda.plan(0, 2, 8, 16, 40, 2)                                                # no groups
+    refused(L.pda_decode_shared, none, good[:10] + [1 << 30] + good[11:], [({}, INVALID)])
+    empty = pda.plan(0, 2, 8, 16, 4)
+    refused(L.pda_decode_shared, pp, [ctypes.byref(empty)] + good[1:], [({}, OK)])
+    huge = pda.shared_plans(1 << 20, 1 << 16, 8, 16, 32, 1 << 20, 1)                   # more steps than an int counts
+    big = L.pda_shared_workspace_size(ctypes.byref(huge[0]), ctypes.byref(huge[1]))
+    refused(L.pda_decode_shared, huge[0], [ctypes.byref(huge[1])] + good[1:10] + [big] + good[11:], [({}, INVALID)])
+
+
+def test_shared_plans(pda):
+    for B, NG, Hk, QG, BS, blocks in ((2, 1, 1, 8, 16, 16), (64, 1, 8, 6, 16, 251), (128, 1, 8, 8, 32, 1024), (32, 4, 4, 16, 32, 256),
+                                      (1, 1, 1, 6, 16, 100000)):
+        pp, p = pda.shared_plans(B, NG, Hk, QG, BS, blocks, 4)
+        assert pp.num_seqs == NG and p.num_seqs == B and pp.max_blocks_per_seq == blocks
+        assert pp.partition_tokens >= 512 and pp.num_partitions * pp.partition_tokens >= blocks * BS
+        assert pp.num_partitions <= max(1, 2 * 152)
+    assert pda.lib().pda_shared_tile_groups(None, 1, 1) == INVALID
+    assert pda.lib().pda_shared_tile_groups(ctypes.byref(p), 0, 1) == INVALID
+    assert pda.lib().pda_shared_tile_groups(ctypes.byref(p), 1, 0) == INVALID
+    pp, _ = pda.shared_plans(8, 1, 8, 8, 16, 1000, 4, prefix_tile_groups=3)
+    assert pp.resolved_tile_groups == 3
+
+
 def test_the_binding_refuses_host_tensors(pda):
     p = pda.plan(1, 1, 8, 16, 4)
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)

@@ -336,3 +336,62 @@ def test_fork_in_a_graph_and_on_another_stream(pda):
         pda.fork_sequences(p, d["cache"], 12, d["table"], d["lens"], d["refs"], d["par"], ot, ol, orf, ws, stream=s)
     s.synchronize()
     assert np.array_equal(ot.cpu().numpy(), want[1])
+
+
+def test_fork_into_nothing_frees_everything_and_from_nothing_stays_empty(pda):
+    rng = np.random.default_rng(11)
+    lens = np.array([20, 37], np.int32)
+    p = pda.plan(2, 1, 8, 16, 4)
+    table, refs = batch(rng, lens, 16, 4, 12)
+    cache = pool(rng, 12, p.cache_block_bytes)
+    assert not check_fork(pda, p, cache, 12, table, lens, refs, [], None)[3].any()
+    p0 = pda.plan(0, 1, 8, 16, 4)
+    got = check_fork(pda, p0, cache, 12, np.zeros((0, 4), np.int32), np.zeros(0, np.int32), refs, [-1, -1], [5, 0])
+    assert not got[2].any() and np.array_equal(got[3], refs)
+
+
+def test_two_forks_at_once_with_workspaces_of_their_own(pda):
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 200, 40).astype(np.int32)
+    p = pda.plan(40, 2, 8, 16, 16)
+    sides = []
+    for k in range(2):
+        table, refs = batch(rng, lens, 16, 16, 900)
+        sides.append(dict(cache=pool(rng, 900, p.cache_block_bytes), table=table, refs=refs, par=rng.integers(-1, 40, 50).astype(np.int32),
+                          s=torch.cuda.Stream(), ws=pda.page_workspace(p, 50, 900, "cuda"),
+                          out=[torch.empty(n, dtype=torch.int32, device="cuda") for n in ((50, 16), (50,), (900,))]))
+    dv = [{k: dev(x[k]) for k in ("cache", "table", "refs", "par")} for x in sides]
+    L = dev(lens)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, d in zip(sides, dv):
+            pda.fork_sequences(p, d["cache"], 900, d["table"], L, d["refs"], d["par"], *x["out"], x["ws"], stream=x["s"])
+    torch.cuda.synchronize()
+    for x, d in zip(sides, dv):
+        want = pp.fork(x["cache"], p.cache_block_bytes, 16, x["table"], lens, x["refs"], x["par"], None)
+        for a, b in zip((d["cache"], *x["out"]), want):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_the_binding_refuses(pda):
+    p = pda.plan(2, 1, 8, 16, 4)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    cache = torch.zeros(12 * p.cache_block_bytes, dtype=torch.uint8, device="cuda")
+    ws = pda.page_workspace(p, 3, 12, "cuda")
+    good = dict(kv_cache=cache, num_cache_blocks=12, block_table=i32(2, 4), context_lens=i32(2), refcounts=i32(12), parents=i32(3),
+                out_table=i32(3, 4), out_lens=i32(3), out_refcounts=i32(12), workspace=ws)
+    pda.fork_sequences(p, **good)
+    for name, bad, what in (("block_table", i32(8, 2).t(), "contiguous"), ("block_table", i32(7), "too small"),
+                            ("parents", i32(3).long(), "dtype"), ("out_refcounts", i32(12).cpu(), "cuda:0"),
+                            ("kv_cache", cache[:-1], "too small"), ("context_lens", None, "CUDA tensor")):
+        with pytest.raises(ValueError, match=what):
+            pda.fork_sequences(p, **{**good, name: bad})
+    for name, bad, status in (("workspace", ws[:-16], -3), ("workspace", torch.cat([ws, ws])[8:], -1), ("out_table", good["block_table"], None),
+                              ("out_refcounts", good["refcounts"], -1)):
+        with pytest.raises((pda.PdaError, ValueError)) as e:
+            pda.fork_sequences(p, **{**good, name: bad})
+        assert status is None or e.value.status == status
+    with pytest.raises(ValueError, match="pair"):
+        pda.copy_blocks(p, cache, 12, cache, 12, i32(3))
+    with pytest.raises(pda.PdaError):
+        pda.copy_blocks(p, cache, 6, cache[5 * p.cache_block_bytes:], 6, i32(1, 2))      # pools that overlap
