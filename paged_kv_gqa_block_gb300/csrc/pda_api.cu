@@ -380,17 +380,18 @@ static DecodeArgs plan_args(const pda_plan_t* plan, const void* query, long long
 
 int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
                const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
-               int W, int P, int* err_word, cudaStream_t stream) {
+               int* err_word, cudaStream_t stream) {
     DecodeArgs a = plan_args(plan, query, num_cache_blocks, block_table, context_lens, partial_out, exp_sums, max_logits,
                              err_word);
-    a.W = W;
-    a.P = P;
+    a.B = plan->num_seqs * plan->num_kv_heads;   // as the selected lists: units of one KV head
+    a.Hk = 1;
+    a.sel_heads = plan->num_kv_heads;
     CUtensorMap kv_map, sc_map;
     if (!encode_kv_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
     sc_map = kv_map;
     if (plan->kv_dtype != PDA_KV_BF16 && !encode_scale_map(&sc_map, kv_cache, plan, num_cache_blocks))
         return PDA_ERR_LAUNCH;
-    return launch_decode_own(plan->kv_dtype, a, kv_map, sc_map, stream);
+    return launch_own_clusters(plan->kv_dtype, a, kv_map, sc_map, stream);
 }
 }  // namespace pda
 

@@ -228,12 +228,9 @@ __device__ inline void find_range(const DecodeArgs& a, UnitIt& u, long long& hi)
 // ---------------------------------------------------------------------------------------------
 // EAGER: the eager softmax update even where kLazy would apply (the QG = 16 row-half kernel,
 // whose 8-row blocks must give the bits of this kernel's two n-tiles).
-// MODE: kSelected: one block table and one length per (sequence, KV head) (pda_decode_selected): the
-// arguments then describe B * Hk sequences of one KV head each, and a.sel_heads is the cache's head count.
-// kOwnTokens: the sequences' own tokens in pda_decode_shared: the next grid may start once this one's
-// inputs are there, since it reads nothing of this one's (it waits for this one before it ends).
-enum { kWholeContext = 0, kSelected = 1, kOwnTokens = 2 };
-template <int KV, int NT, int S, bool FUSED, bool EAGER = false, int MODE = kWholeContext>
+// SEL: one block table and one length per (sequence, KV head) (pda_decode_selected): the arguments
+// then describe B * Hk sequences of one KV head each, and a.sel_heads is the cache's head count.
+template <int KV, int NT, int S, bool FUSED, bool EAGER = false, bool SEL = false>
 struct Decode {
     using Cfg = DecodeCfg<KV, S>;
     static constexpr bool FP8 = KV == PDA_KV_FP8_E4M3;
@@ -300,7 +297,7 @@ struct Decode {
         const int phys = __shfl_sync(kFull, f.ent, (f.t >> ts) - f.e0);
         if (lane == 0) {
             const int slot0 = (f.t & ((1 << ts) - 1)) * kTileTokens;
-            const int head = MODE == kSelected ? f.u.b % a.sel_heads : f.u.h;
+            const int head = SEL ? f.u.b % a.sel_heads : f.u.h;
             mbar_arrive_expect_tx(bar, Cfg::kTileBytes + Cfg::kScaleTx);
             tma_load_5d(sbase + Cfg::kOffStages + stage * Cfg::kTileBytes, kv_map, bar, 0, slot0, 0, head, phys,
                         f.policy);
@@ -952,10 +949,8 @@ struct Decode {
             if (F16) prefetch_tensormap(sc_map);
         }
         __syncwarp();
-        if constexpr (MODE != kOwnTokens)
-            allow_dependent_launch();   // the reduce may be scheduled as soon as CTAs of this grid retire
+        allow_dependent_launch();   // the reduce may be scheduled as soon as CTAs of this grid retire
         grid_dependency_wait();     // inputs may come from the previous grid on the stream
-        if constexpr (MODE == kOwnTokens) allow_dependent_launch();
 
         UnitIt cu;
         long long hi;
@@ -1262,7 +1257,7 @@ struct Decode {
 
 // MINB: CTAs per SM the register allocation must allow (more resident warps hide the latency of
 // each warp's serial chain of loads, MMAs and shuffles).
-template <int KV, int NT, int S, int MINB, bool FUSED, int MODE = kWholeContext>
+template <int KV, int NT, int S, int MINB, bool FUSED, bool SEL = false>
 __global__ void __launch_bounds__(32, MINB) pda_partition_kernel(const __grid_constant__ CUtensorMap kv_map,
                                                           const __grid_constant__ CUtensorMap sc_map,
                                                           const DecodeArgs a) {
@@ -1270,7 +1265,7 @@ __global__ void __launch_bounds__(32, MINB) pda_partition_kernel(const __grid_co
     // TQ4 centroid table: static, so that its lookups address it with an immediate offset
     __shared__ uint32_t tq_lut[KV == PDA_KV_TQ4 ? 256 : 1];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Decode<KV, NT, S, FUSED, false, MODE>::run(a, &kv_map, &sc_map, smem, tq_lut);
+    Decode<KV, NT, S, FUSED, false, SEL>::run(a, &kv_map, &sc_map, smem, tq_lut);
 }
 
 }  // namespace pda

@@ -69,9 +69,10 @@ int launch_decode_selected(int kv_dtype, const DecodeArgs& a, const CUtensorMap&
 // The same in one launch that writes a.out, without partials.
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream);
-// Head warps over the sequences' own tokens beside a shared prefix (bf16, fp8).
-int launch_decode_own(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
-                      cudaStream_t stream);
+// The sequences' own tokens beside a shared prefix, in the same kernel: one partial per (sequence, KV head) and
+// query row to a.partial_out, a.exp_sums and a.max_logits (a sequence without tokens writes none).
+int launch_own_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                        cudaStream_t stream);
 int launch_decode_tq4(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, cudaStream_t stream);
 int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 
@@ -79,11 +80,10 @@ int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 // it zero).  Sets *status to a pda_status value.
 unsigned int* launch_counter_slot(int* status);
 
-// The partition pass of pda_decode_shared over the sequences' own tokens: partials of W tokens (a multiple of
-// 16), P of them per sequence and KV head.  The plan and the pointers have been checked.
+// The sequences' own tokens in pda_decode_shared.  The plan and the pointers have been checked.
 int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
                const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
-               int W, int P, int* err_word, cudaStream_t stream);
+               int* err_word, cudaStream_t stream);
 // Tensor maps of pda_decode_shared: one (block, KV head) and 128-byte chunk, or its scales, per copy.
 bool encode_block_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);
 bool encode_block_scale_map(CUtensorMap* m, const void* cache, const pda_plan_t* p, long long num_cache_blocks);

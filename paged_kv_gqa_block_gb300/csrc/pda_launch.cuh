@@ -9,10 +9,10 @@
 namespace pda {
 
 // Persistent grid of one-warp CTAs: (SMs x resident CTAs per SM), capped by the number of units.
-template <int KV, int NT, int S, int MINB, bool FUSED, int MODE = kWholeContext>
+template <int KV, int NT, int S, int MINB, bool FUSED, bool SEL = false>
 int launch_partition(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, cudaStream_t stream) {
     using Cfg = DecodeCfg<KV, S>;
-    auto kernel = pda_partition_kernel<KV, NT, S, MINB, FUSED, MODE>;
+    auto kernel = pda_partition_kernel<KV, NT, S, MINB, FUSED, SEL>;
     static int occ_cache[64] = {0};
     static std::mutex mu;
     int dev = 0;

@@ -1,4 +1,5 @@
-// pda_selected.cu -- the launch of pda_decode_selected in its one-launch form (pda_selected.cuh).
+// pda_selected.cu -- launches of the one-launch kernel over short lists (pda_selected.cuh): selected blocks,
+// and own tokens beside a shared prefix.
 #include <mutex>
 
 #include "pda.h"
@@ -32,10 +33,10 @@ static Shape selected_shape(long long units, int tiles, int sms, int wps, int nw
     return s;
 }
 
-template <int KV, int NT, int S, int NWMAX, int MINB>
+template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
 static int launch_clusters(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, Shape shape,
                            cudaStream_t stream) {
-    auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB>;
+    auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB, OWN>;
     static bool attr_set[64] = {false};
     static std::mutex mu;
     int dev = 0;
@@ -65,28 +66,38 @@ static int launch_clusters(const DecodeArgs& a, const CUtensorMap& kv_map, const
     return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
 }
 
-template <int KV, int NT, int S, int NWMAX, int WPS>
+template <bool OWN, int KV, int NT, int S, int NWMAX, int WPS>
 static int launch_clusters_of(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                               cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     const Shape shape = selected_shape(a.B, (a.MB * a.BS + 15) / 16, sms, WPS, NWMAX);
     if ((long long)a.B * shape.C > 0x7FFFFFFFll) return PDA_ERR_INVALID_ARG;
-    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX>(a, kv_map, sc_map, shape, stream);
+    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, OWN>(a, kv_map, sc_map, shape, stream);
 }
 
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
-        return launch_clusters_of<PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
+        return launch_clusters_of<false, PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
     }
     if (kv_dtype == PDA_KV_TQ4) {
-        if (a.QG <= 8) return launch_clusters_of<PDA_KV_TQ4, 1, 6, 6, 12>(a, kv_map, sc_map, stream);
-        return launch_clusters_of<PDA_KV_TQ4, 2, 6, 4, 8>(a, kv_map, sc_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_TQ4, 1, 6, 6, 12>(a, kv_map, sc_map, stream);
+        return launch_clusters_of<false, PDA_KV_TQ4, 2, 6, 4, 8>(a, kv_map, sc_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
-    return launch_clusters_of<PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
+    return launch_clusters_of<false, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
+}
+
+int launch_own_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+                        cudaStream_t stream) {
+    if (kv_dtype == PDA_KV_BF16) {
+        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
+        return launch_clusters_of<true, PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
+    }
+    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
+    return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
 }
 
 }  // namespace pda

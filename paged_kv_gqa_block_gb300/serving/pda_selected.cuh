@@ -1,7 +1,9 @@
-// pda_selected.cuh -- attention over selected blocks in one launch: the tiles of a (sequence, KV head) are
-// split over the warps of a thread-block cluster, whose results are joined in shared memory.
+// pda_selected.cuh -- attention over short lists in one launch: the tiles of a (sequence, KV head) are split
+// over the warps of a thread-block cluster, whose results are joined in shared memory.  Two lists: the selected
+// blocks of each (sequence, KV head) (pda_decode_selected), whose result is the output, and a sequence's own
+// tokens beside a shared prefix (OWN, pda_decode_shared), whose result is a partial for the join there.
 //
-// Selected lists are short (a few thousand tokens) and of like length, so a unit needs neither partials in
+// Such lists are a few thousand tokens and of like length, so a unit needs neither partials in
 // global memory nor a second launch: C CTAs of nw warps take an equal run of its 16-token tiles each,
 // with the arithmetic and the private copy rings of the head-warp kernel (pda_decode.cuh); each warp
 // leaves (m, l, o), the maximum, the sum of exponentials and the normalised output of its run, in its
@@ -41,11 +43,27 @@ __device__ __forceinline__ void store_row4(void* out, int f32, long long row, in
     }
 }
 
-template <int KV, int NT, int S, int NWMAX, int MINB>
+// A row's joined result: o = sum w_i o_i (to be divided by L), M and L as above (log2 units).
+template <bool OWN>
+__device__ __forceinline__ void store_joined(const DecodeArgs& a, long long row, int c, float4 o, float M, float L) {
+    const float r = L == 0.f ? 0.f : 1.f / L;
+    const float4 v = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+    if constexpr (OWN) {
+        store_row4(a.partial_out, 1, row, c, v);
+        if (c == 0) {
+            a.exp_sums[row] = L;
+            a.max_logits[row] = M * kLn2;
+        }
+    } else {
+        store_row4(a.out, a.out_f32, row, c, v);
+    }
+}
+
+template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
 __global__ void __launch_bounds__(32 * NWMAX, MINB)
     pda_selected_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                         const DecodeArgs a, const int C) {
-    using D = Decode<KV, NT, S, false, false, kSelected>;
+    using D = Decode<KV, NT, S, false>;
     using Cfg = DecodeCfg<KV, S>;
     using Sel = SelectedCfg<KV, S>;
     constexpr bool FP8 = D::FP8, TQ = D::TQ, F16 = D::F16;
@@ -66,15 +84,20 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         if (F16) prefetch_tensormap(&sc_map);
     }
     __syncwarp();
-    allow_dependent_launch();
+    if constexpr (!OWN) allow_dependent_launch();
     grid_dependency_wait();
+    // Own tokens: the prefix pass that follows reads nothing of this grid's (it waits for it before it ends),
+    // so it may start once everything before this grid has ended.
+    if constexpr (OWN) allow_dependent_launch();
 
     const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
+    const int head = unit % a.sel_heads, list = OWN ? unit / a.sel_heads : unit;   // the table row and length
     const int max_ctx = a.MB * a.BS;
-    const int raw = __ldg(a.context_lens + unit);
-    if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && a.err_word)
+    const int raw = __ldg(a.context_lens + list);
+    if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!OWN || head == 0) && a.err_word)
         atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
     const int ctx = sanitize_ctx(raw, max_ctx);
+    if (OWN && ctx == 0) return;   // every CTA of the cluster
     const int T = (ctx + 15) >> 4;
     const long long pairs = (T + 1) >> 1;   // runs of whole pairs: a step takes two tiles
     const int n = C * nw, wi = rank * nw + warp;
@@ -88,11 +111,10 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         float cent = 0.f;
         if constexpr (TQ) cent = __ldg(a.centroids + (lane & 15));
         const int ts = a.bs_shift - 4, entries = ((t1 - 1) >> ts) + 1;
-        const int* table = a.block_table + (long long)unit * a.MB;
+        const int* table = a.block_table + (long long)list * a.MB;
         int e0 = t0 >> ts;
         int ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
         const uint64_t policy = l2_policy_evict_first();
-        const int head = unit % a.sel_heads;
         int issued = 0;
         auto issue = [&](int t, int stage) {   // tiles in order
             if ((t >> ts) - e0 >= 32) {
@@ -314,8 +336,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             o.w = fmaf(f, v.w, o.w);
         }
         if (C == 1) {
-            const float r = L == 0.f ? 0.f : 1.f / L;
-            store_row4(a.out, a.out_f32, (long long)unit * a.QG + q, c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+            store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
         } else {
             *reinterpret_cast<float4*>(joined + q * kHeadDim + 4 * c) = o;
             if (c == 0) {
@@ -344,8 +365,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
-        const float r = L == 0.f ? 0.f : 1.f / L;
-        store_row4(a.out, a.out_f32, (long long)unit * a.QG + q, c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+        store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
     }
     cl.sync();   // nobody leaves while its rows are read
 }

@@ -923,13 +923,13 @@ struct JoinArgs {
     const int* group_starts;
     const int* prefix_lens;
     const int* context_lens;
-    const float* part_o[2];   // prefix pieces [B][Hk][slots][QG][D]; own partitions [B][Hk][P][QG][D]
+    const float* part_o[2];   // prefix pieces [B][Hk][slots][QG][D]; own tokens [B][Hk][QG][D]
     const float* part_l[2];
     const float* part_m[2];
     const int* pieces;
     void* out;
     int* err_word;
-    int B, NG, Hk, QG, MP, MB, BS, W, slots, P, out_f32;
+    int B, NG, Hk, QG, MP, MB, BS, slots, out_f32;
 };
 
 // One CTA per (sequence, KV head), one warp per query row: lane i holds (m, l) of partials i, i + 32,
@@ -951,12 +951,12 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
     }
     const bool prefix = __any_sync(kLanes, in) && !__any_sync(kLanes, bad);
     const int np = prefix ? max(0, min(a.slots, pieces)) : 0;
-    if (ctx < 0 || ctx > a.MB * a.BS) ctx = 0;   // reported by the partition pass
-    const int total = np + (ctx + a.W - 1) / a.W;
-    const long long row0 = unit * a.slots * a.QG + q, row1 = unit * a.P * a.QG + q;
+    if (ctx < 0 || ctx > a.MB * a.BS) ctx = 0;   // reported by the own pass
+    const int total = np + (ctx > 0 ? 1 : 0);
+    const long long row0 = unit * a.slots * a.QG + q, row1 = unit * a.QG + q;
     auto at = [&](int i, int& part) {   // index of partial i's row in its part
         part = i >= np;
-        return part ? row1 + (long long)(i - np) * a.QG : row0 + (long long)i * a.QG;
+        return part ? row1 : row0 + (long long)i * a.QG;
     };
     auto stats = [&](int i, float& m, float& l) {
         m = -INFINITY;
@@ -1023,25 +1023,13 @@ __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) 
 // ------------------------------------------------------------------------- host side
 static long long up256(long long x) { return (x + 255) & ~255ll; }
 
-// Tokens of a partial of the sequences' own part.  A warp takes 0.6 us per 16 tokens, so short partials end
-// sooner; they are worth their join while there are few of them.
-static int own_tokens(const pda_plan_t* p) {
-    const long long units = (long long)p->num_seqs * p->num_kv_heads, most = (long long)p->max_blocks_per_seq * p->kv_block_size;
-    for (int W = 64; W < p->partition_tokens; W *= 2)
-        if (units * ((most + W - 1) / W) <= 8192) return W;
-    return p->partition_tokens;
-}
-
 struct SharedLayout {
-    long long o0, l0, m0, pieces, o1, l1, m1, bytes;
-    int W, P;   // the own part's partials
+    long long o0, l0, m0, pieces, o1, l1, m1, bytes;   // the prefix pieces', and the own part's one partial per row
 };
 static SharedLayout shared_layout(const pda_plan_t* pp, const pda_plan_t* p) {
     const long long heads = (long long)p->num_seqs * p->num_kv_heads * p->query_group_size;
     SharedLayout s;
-    s.W = own_tokens(p);
-    s.P = (int)(((long long)p->max_blocks_per_seq * p->kv_block_size + s.W - 1) / s.W);
-    const long long r0 = heads * (pp->num_partitions + 1), r1 = heads * s.P;
+    const long long r0 = heads * (pp->num_partitions + 1), r1 = heads;
     s.o0 = 0;
     s.l0 = s.o0 + up256(r0 * kHeadDim * 4);
     s.m0 = s.l0 + up256(r0 * 4);
@@ -1171,7 +1159,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     // The sequences' own tokens first: the prefix pass, which takes whole SMs, starts on each SM as that
     // one's short work ends.
     int rc = decode_own(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
-                        w.W, w.P, err_word, s);
+                        err_word, s);
     if (rc != PDA_OK) return rc;
     const long long most = most_steps(prefix_plan, plan);   // no more CTAs than there can be steps
     const int ctas = (int)(most < sms ? most : sms);
@@ -1202,9 +1190,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     j.MP = a.MP;
     j.MB = plan->max_blocks_per_seq;
     j.BS = a.BS;
-    j.W = w.W;
     j.slots = a.slots;
-    j.P = w.P;
     j.out_f32 = out_dtype == PDA_OUT_F32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hk));
