@@ -10,7 +10,9 @@ namespace pda {
 // The cluster of a unit: C CTAs of nw warps.  `wps` warps fit an SM, in CTAs of at most `nwmax`; a unit has
 // `tiles` tiles (the table's capacity; the lengths are on the device).  Counted in a warp's tiles, a
 // round of CTAs takes a warp's run, and 6 for its start and its join, 3 more for a cluster's join; the rounds
-// that the units need are what the choice weighs against it.  Measured against the partition pass and
+// that the units need are what the choice weighs against it.  A cluster lies within one group of SMs, so of 152
+// SMs clusters of four CTAs reach 144, and of eight 120 with one CTA per SM (144, 136 with two, three): 16
+// units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and take 8.7 us.  Measured against the partition pass and
 // reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.5 us against 16.1, 32 units 11.0 against
 // 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 44 against 63, 1024 units of 8192 287 against 383;
 // only 800 units of 4096 bf16 tokens were slower, 273 against 245.
@@ -22,7 +24,8 @@ static Shape selected_shape(long long units, int tiles, int sms, int wps, int nw
     Shape s = {1, 1};
     for (int C = 1; C <= 8; C *= 2)
         for (int nw = 1; nw <= nwmax; ++nw) {
-            const long long slots = (long long)sms * (wps / nw), rounds = (units * C + slots - 1) / slots;
+            const int per = wps / nw, part = C <= 2 ? 19 : C == 4 || per == 2 || per > 3 ? 18 : per == 3 ? 17 : 15;
+            const long long slots = (long long)sms * per * part / 19, rounds = (units * C + slots - 1) / slots;
             const int pairs = (tiles + 1) / 2;
             const long long t = rounds * (2 * ((pairs + C * nw - 1) / (C * nw)) + 6 + (C > 1 ? 3 : 0));
             if (best == 0 || t < best) {
