@@ -451,7 +451,8 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  *   workspace      device, pda_shared_workspace_size bytes, 32-byte aligned
  *   query, out, out_dtype as for pda_decode and pda_reduce (query and out may be pinned host memory)
  * The weights of the prefix part are rounded to bf16 (bf16 KV), or they and the scaled V to f16 (fp8 KV), before
- * their product, so an fp32 out carries that rounding (at most 2^-8, or 3 * 2^-11, of each term).
+ * their product, so an fp32 out carries that rounding (at most 2^-8, or 3 * 2^-11, of each term; fp8 tokens whose
+ * V scale is below 2^-15 of the largest among the prefix's aligned 128 tokens around them lose further bits of it).
  * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN); group_starts that are not
  * ascending within [0, num_seqs] set PDA_ERRW_BAD_GROUP, and the step runs without prefixes; block ids as
  * for pda_decode.

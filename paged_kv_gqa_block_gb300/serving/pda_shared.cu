@@ -410,8 +410,9 @@ struct Prefix {
     // an f16 value), V times its token's scale over F (two roundings to f16, 2^-11 each, beside P's one; it spares
     // the softmax a product per weight).  Rows past the prefix become zeros, since a weight of zero does
     // not silence a NaN.  The first warp also lays the step's scales out as [128 K scales][128 V scales / F]: the K
-    // scales for the softmax.  F keeps V in f16's range: it is the step's largest V scale, and stays
-    // as it is while the largest lies in [F/64, 64F] (the accumulator counts in units of F).
+    // scales for the softmax.  F keeps V in f16's range (the accumulator counts in units of F): 16 F is the
+    // step's largest V scale f, and F stays as it is while f lies in [2F, 128F].  So the largest products stay
+    // below 448 * 128 = 57344, and a scale keeps its 11 bits down to 2^-15 f (2 F * 2^-15 = 2^-14 F).
     __device__ void convert() {
         const int t = threadIdx.x - 384, lane = t & 31;
         unsigned seq = 0, step = 0;
@@ -438,7 +439,7 @@ struct Prefix {
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
                         if (!(f > 0.f)) f = 1.f;
-                        if (j == 0 || f > F * 64.f || f < F * 0.015625f) F = f;
+                        if (j == 0 || f > F * 128.f || f < F * 2.f) F = fmaxf(f * 0.0625f, 1e-37f);   // 1 / F is finite
                         const float rF = 1.f / F;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {   // the shuffles above come after every lane's reads

@@ -184,6 +184,34 @@ def test_rising_logits_rescale_every_step(pda, kv):
     check(pda, c)
 
 
+def test_v_scales_far_below_their_neighbours(pda):
+    """fp8: the tokens that a row attends to have V scales 2^-13 of the largest in their 128 tokens, which itself is 2^-5 of that in
+    the 128 tokens before.  A term is off by the three f16 roundings, 3 * 2^-11, and a weight by at most itself or half a step
+    of f16's smallest, 2^-25; a V code of few bits by 2^-25 in units of at most half the largest scale."""
+    c = Case(FP8, 1, 8, 16, [256], [1], [0], seed=12)
+    rng = np.random.default_rng(12)
+    k = np.zeros((256, 1, 128), np.float32)
+    k[:128, 0, 8] = -10.0
+    k[128 + np.arange(8), 0, np.arange(8)] = 3.0
+    size = np.where(np.arange(256) < 128, 1.0, 2.0 ** -5)
+    size[128:136] = 2.0 ** -18
+    v = (rng.standard_normal((256, 1, 128)) * size[:, None, None]).astype(np.float32)
+    wl.write_tokens(c.w, c.cache, c.ptable[0], k, v)
+    q = np.zeros((1, 8, 128), np.float32)
+    q[0, np.arange(8), np.arange(8)] = 100.0
+    q[0, :, 8] = 100.0
+    c.q = wl.round_bf16(q)
+    out = pda.decode_shared(*c.plans(pda), **c.device(), out_dtype=torch.float32).double().cpu().numpy()[0]
+    K, V = (x[c.ptable[0], :, 0].reshape(256, 128) for x in pp.block_values(c.w, c.cache))
+    s = 128 ** -0.5 * wl.bf16_bits_to_f32(c.q)[0].astype(np.float64) @ K.T
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    ds = 128 ** -0.5 * 4 * 1300 * 2.0 ** -23                 # two products, at most 300 and 1000, their sum and scale in fp32
+    bound = (3 * 2.0 ** -11 * (1 + 2.0 ** -10) + 2 * ds + 320 * 2.0 ** -23) * (p @ np.abs(V))
+    bound += np.minimum(p, 2.0 ** -25) @ np.abs(V) + 2.0 ** -26 * 2.0 ** -5 * 5 / 448
+    assert (np.abs(out - p @ V) <= bound).all()
+
+
 def test_infinite_and_nan_data_stay_in_their_rows(pda):
     for kv in (BF16, FP8):
         c = Case(kv, 1, 8, 16, [300], [20], [3] * 20, seed=11)
