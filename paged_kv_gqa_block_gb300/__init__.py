@@ -10,6 +10,22 @@ missing library raises.  PyTorch provides device memory and streams only.
     ws  = workspace(p, device)                    # partial_out, exp_sums, max_logits
     decode(p, query, kv_cache, num_cache_blocks, block_table, context_lens, **ws)
     reduce(p, context_lens, out=out, **ws)        # or decode_step(...) for both
+
+A pool of blocks with counts on the device: fork_sequences lays a batch out anew (forks, reorders, grows,
+frees), append_kv writes the new tokens, copy_blocks and compact_blocks move blocks.
+
+    fork_sequences(p, kv_cache, NB, table, lens, refs, parents, new_table, new_lens, new_refs,
+                   page_workspace(p, rows, NB, device), new_tokens=ones)
+
+Sequences that share prefixes, and long contexts of which a step attends to selected blocks only:
+
+    pp, p = shared_plans(B, groups, Hk, QG, BS, prefix_blocks, max_blocks_per_seq)
+    decode_shared(pp, p, query, kv_cache, NB, group_starts, prefix_table, prefix_lens, table, lens)
+
+    summarize_blocks(p, kv_cache, NB, table, lens, summaries, since=appended_at)
+    score_blocks(p, query, summaries, NB, table, lens, scores)
+    select_blocks(p, scores, table, lens, K, 1, 1, sel_table, sel_lens)
+    decode_selected(plan(..., max_blocks_per_seq=K), query, kv_cache, NB, sel_table, sel_lens)
 """
 from __future__ import annotations
 

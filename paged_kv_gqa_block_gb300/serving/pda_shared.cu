@@ -4,8 +4,8 @@
 //   out = softmax(scale [q.K_g ; q.K_b]) [V_g ; V_b],
 // with K_g, V_g the group's prefix and K_b, V_b the sequence's own tokens.  The two parts are
 // computed apart as (m, l, o), the running maximum, the sum of exponentials and the normalised
-// output, and joined: w = l e^(m - M), out = sum w o / sum w.  The own part is the library's
-// partition pass (pda_decode).  The prefix part is one matrix product per group and KV head for the
+// output, and joined: w = l e^(m - M), out = sum w o / sum w.  The own part is the cluster kernel of
+// pda_selected.cuh.  The prefix part is one matrix product per group and KV head for the
 // query rows of all its sequences, n_g * QG of them, and this file's first kernel.
 //
 // The prefix pass.  A CTA holds 256 query rows of one (group, KV head) in two tiles of 128 and walks
@@ -16,6 +16,7 @@
 //             no shuffles; S is read from TMEM, P written back
 //   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
 //   9         the matrix products (one thread issues)
+//   10, 11    none: registers move between roles in groups of four warps
 //   12-15     fp8 only: e4m3 codes to f16 between the copy and the product
 // The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
 // The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
@@ -929,7 +930,6 @@ struct JoinArgs {
     const float* part_m[2];
     const int* pieces;
     void* out;
-    int* err_word;
     int B, NG, Hk, QG, MP, MB, BS, slots, out_f32;
 };
 
@@ -1183,7 +1183,6 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     j.part_m[1] = f32(w.m1);
     j.pieces = a.pieces;
     j.out = out;
-    j.err_word = err_word;
     j.B = a.B;
     j.NG = a.NG;
     j.Hk = a.Hk;

@@ -1,6 +1,6 @@
 // pda_sparse.cu -- choosing the cache blocks a decode step attends to: pda_summarize_blocks,
-// pda_score_blocks, pda_select_blocks.  (pda_decode_selected, the attention over them, is the
-// partition pass of pda_decode.cuh with one table per (sequence, KV head); see pda_api.cu.)
+// pda_score_blocks, pda_select_blocks.  (pda_decode_selected, the attention over them, has its kernel in
+// pda_selected.cuh and its checks in pda_api.cu.)
 //
 // A block's summary is, per KV head, the largest and smallest value of each key dimension over the
 // block's tokens.  For a query row q every key k of the block satisfies
