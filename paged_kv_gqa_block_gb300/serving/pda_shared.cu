@@ -89,7 +89,7 @@ enum {
     kBarEmpty = 40,      // [5] the products that read a slot are done
     kBarQ = 80,          // [2] a tile's query rows are in shared memory
     kBarS = 96,          // [2] S is in TMEM
-    kBarP = 112,         // [2] P is in TMEM
+    kBarP = 112,         // [2] the first half of P (64 tokens) is in TMEM
     kBarO = 128,         // [2] the unit's last product of a tile is done
     kBarRawFull = 144,   // [3]
     kBarRawEmpty = 168,  // [3]
@@ -98,7 +98,8 @@ enum {
     kBarDrain = 240,
     kTmemAt = 248,       // TMEM address
     kAbortAt = 252,      // a wait gave up
-    kFAt = 256           // [3] what a step's V scales are divided by
+    kFAt = 256,          // [3] what a step's V scales are divided by
+    kBarP2 = 272         // [2] the second half of P is in TMEM
 };
 
 // ------------------------------------------------------------------------- the split
@@ -504,9 +505,10 @@ struct Prefix {
             umma_ss(leader, d, q + o, k + o, kIdescQK, i > 0);
         }
     }
+    template <int HALF>
     static __device__ __forceinline__ void pv(uint32_t leader, uint32_t d, uint32_t p, uint64_t v, bool accumulate) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 4 * HALF; i < 4 * HALF + 4; ++i)
             umma_ts(leader, d, p + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
     }
     __device__ void products(uint32_t tmem_base) {
@@ -572,9 +574,12 @@ struct Prefix {
                     if (w >= tiles) break;
                     uint32_t& n = w ? p1 : p0;
                     if (!(ok = wait(bar + kBarP + 8 * w, n))) break;
+                    tc_fence_after();
+                    pv<0>(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, j > 0);
+                    if (!(ok = wait(bar + kBarP2 + 8 * w, n))) break;
                     n ^= 1;
                     tc_fence_after();
-                    pv(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, j > 0);
+                    pv<1>(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, true);
                     if (w == 0 && more && !(ok = full(k))) break;
                     if (more) qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + k.slot * kSlot16);
                     umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
@@ -763,12 +768,14 @@ struct Prefix {
                             p[i / 2 + 1] = F16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
                         }
                         tmem_st16(tS + 16 * k, p);   // over S, which is in registers
+                        if (k & 1) {   // the product of the first half runs while the second is computed
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bars + (k == 1 ? kBarP : kBarP2) + 8 * tile);
+                        }
                     }
                     l += (la.x + la.y) + (lb.x + lb.y);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + kBarP + 8 * tile);
                 }
                 if (F16) {
                     __syncwarp();
@@ -862,6 +869,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
             mbar_init(bars + kBarQ + 8 * i, 4);
             mbar_init(bars + kBarS + 8 * i, 1);
             mbar_init(bars + kBarP + 8 * i, 4);
+            mbar_init(bars + kBarP2 + 8 * i, 4);
             mbar_init(bars + kBarO + 8 * i, 1);
         }
         for (int i = 0; i < 3; ++i) {
