@@ -26,9 +26,10 @@ template <int KV, int S>
 struct SelectedCfg {
     static constexpr int kRing = S * DecodeCfg<KV, S>::kTileBytes;     // a multiple of 1024
     static constexpr int kScales = S * DecodeCfg<KV, S>::kScaleBytes;
-    // per warp: ring, scales, barriers, the rows' m and l; per CTA: joined rows and their m and l
+    // per warp: ring, scales, the rows' m and l, barriers; per CTA: the joined rows' m and l (the rows themselves
+    // take the place of the first warp's: with 8 KB of their own, one CTA fewer fitted an SM)
     static constexpr int bytes(int nw) {
-        return nw * (kRing + kScales + S * 8 + 2 * kSelRows * 4) + kSelRows * (kHeadDim * 4 + 8) + 1024;
+        return nw * (kRing + kScales + S * 8 + 2 * kSelRows * 4) + 2 * kSelRows * 4 + 1024;
     }
 };
 
@@ -71,11 +72,13 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     __shared__ uint32_t tq_lut[TQ ? 256 : 1];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    static_assert(Sel::kRing >= kSelRows * kHeadDim * 4, "a ring holds its warp's rows");
     uint8_t* ring = smem + warp * Sel::kRing;
     uint8_t* scales = smem + nw * Sel::kRing + warp * Sel::kScales;
-    float* joined = reinterpret_cast<float*>(smem + nw * (Sel::kRing + Sel::kScales));   // [16][128], m [16], l [16]
-    float* stats = joined + kSelRows * (kHeadDim + 2);                                    // [nw][2: m, l][16]
-    const uint32_t bar0 = smem_addr(stats + nw * 2 * kSelRows) + warp * S * 8;
+    float* stats = reinterpret_cast<float*>(smem + nw * (Sel::kRing + Sel::kScales));   // [nw][2: m, l][16]
+    float* jm = stats + nw * 2 * kSelRows;                                               // joined: m [16], l [16]
+    float* jl = jm + kSelRows;
+    const uint32_t bar0 = smem_addr(jl + kSelRows) + warp * S * 8;
     const uint32_t sring = smem_addr(ring), sscale = smem_addr(scales);
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -314,9 +317,10 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         stats[(warp * 2 + 1) * kSelRows + lane] = 0.f;
     }
     __syncthreads();
-    // The CTA's rows: a weight of exactly zero leaves its warp out (its memory holds no rows then).
-    float* jm = joined + kSelRows * kHeadDim;
-    float* jl = jm + kSelRows;
+    // The CTA's rows: a weight of exactly zero leaves its warp out (its memory holds no rows then).  The joined
+    // rows take the place of the first warp's: each four values are read and written by one thread.
+    float* joined = reinterpret_cast<float*>(smem);
+    auto place = [](int q, int c) { return q * kHeadDim + ((c ^ (q & 6)) << 2); };
     for (int i = threadIdx.x; i < a.QG * 32; i += blockDim.x) {
         const int q = i >> 5, c = i & 31;
         float M = -INFINITY;
@@ -327,8 +331,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             const float l = stats[(w * 2 + 1) * kSelRows + q];
             if (l == 0.f) continue;
             const float f = l * ex2(stats[w * 2 * kSelRows + q] - M);
-            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * Sel::kRing) + q * kHeadDim +
-                                                              ((c ^ (q & 6)) << 2));
+            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * Sel::kRing) + place(q, c));
             L += f;
             o.x = fmaf(f, v.x, o.x);
             o.y = fmaf(f, v.y, o.y);
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         if (C == 1) {
             store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
         } else {
-            *reinterpret_cast<float4*>(joined + q * kHeadDim + 4 * c) = o;
+            *reinterpret_cast<float4*>(joined + place(q, c)) = o;
             if (c == 0) {
                 jm[q] = M;
                 jl[q] = L;
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             const float l = *cl.map_shared_rank(jl + q, r);
             if (l == 0.f) continue;
             const float f = ex2(*cl.map_shared_rank(jm + q, r) - M);
-            const float4 v = *reinterpret_cast<const float4*>(cl.map_shared_rank(joined + q * kHeadDim + 4 * c, r));
+            const float4 v = *reinterpret_cast<const float4*>(cl.map_shared_rank(joined + place(q, c), r));
             L += l * f;
             o.x = fmaf(f, v.x, o.x);
             o.y = fmaf(f, v.y, o.y);
