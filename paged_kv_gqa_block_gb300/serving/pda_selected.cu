@@ -99,7 +99,7 @@ int launch_own_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv
         if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
         return launch_clusters_of<true, PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(a, kv_map, sc_map, stream);
     return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
 }
 

@@ -16,7 +16,7 @@
 //             no shuffles; S is read from TMEM, P written back
 //   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
 //   9         the matrix products (one thread issues)
-//   10, 11    none: registers move between roles in groups of four warps
+//   10        fp8 only: the scales of a step
 //   12-15     fp8 only: e4m3 codes to f16 between the copy and the product
 // The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
 // The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
@@ -99,7 +99,8 @@ enum {
     kTmemAt = 248,       // TMEM address
     kAbortAt = 252,      // a wait gave up
     kFAt = 256,          // [3] what a step's V scales are divided by
-    kBarP2 = 272         // [2] the second half of P is in TMEM
+    kBarP2 = 272,        // [2] the second half of P is in TMEM
+    kBarScRaw = 288      // [3] scales as copied
 };
 
 // ------------------------------------------------------------------------- the split
@@ -384,14 +385,17 @@ struct Prefix {
                     const uint32_t bar = bars + kFull0 + 8 * s;
                     const uint32_t row_bytes = (uint32_t)n * a.BS * 128u * kHalves;
                     const bool scales = F16 && v == 0;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, row_bytes + (scales ? (uint32_t)n * a.BS * 8u : 0u));
+                    if (lane == 0) {
+                        if (scales) mbar_arrive_expect_tx(bars + kBarScRaw + 8 * st, (uint32_t)n * a.BS * 8u);
+                        mbar_arrive_expect_tx(bar, row_bytes);
+                    }
                     __syncwarp();
                     if (mine) {
                         tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
                                     v * kHalves + half, u.h, id, policy);
                         if (scales)
-                            tma_load_4d(sm + Cfg::kOffScales + st * kScaleBytes + blk * a.BS * 8, sc_map, bar, 0, 0,
-                                        u.h, id, policy);
+                            tma_load_4d(sm + Cfg::kOffScales + st * kScaleBytes + blk * a.BS * 8, sc_map,
+                                        bars + kBarScRaw + 8 * st, 0, 0, u.h, id, policy);
                     }
                     __syncwarp();
                 }
@@ -405,86 +409,119 @@ struct Prefix {
                 const unsigned q = (seq - 1 - s) / kNS;   // the slot's last use
                 (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
             }
+        if (F16) {
+            const unsigned issued = (seq + 1) / 2;   // steps whose scales were asked for
+            for (int s = 0; s < Cfg::kScales; ++s)
+                if (issued > (unsigned)s)
+                    (void)mbar_wait(bars + kBarScRaw + 8 * s, (issued - 1 - s) / Cfg::kScales & 1, kDefaultTimeoutNs);
+        }
     }
 
     // ---------------------------------------------------------------- conversion (fp8)
-    // Thread t turns token t's 128 codes into f16: K as it is (exact: every e4m3 value is
-    // an f16 value), V times its token's scale over F (two roundings to f16, 2^-11 each, beside P's one; it spares
-    // the softmax a product per weight).  Rows past the prefix become zeros, since a weight of zero does
-    // not silence a NaN.  The first warp also lays the step's scales out as [128 K scales][128 V scales / F]: the K
-    // scales for the softmax.  F keeps V in f16's range (the accumulator counts in units of F): 16 F is the
+    // One warp lays a step's scales out as [128 K scales][128 V scales / F]: the K scales for the softmax, the
+    // others for the conversion.  F keeps V in f16's range (the accumulator counts in units of F): 16 F is the
     // step's largest V scale f, and F stays as it is while f lies in [2F, 128F].  So the largest products stay
     // below 448 * 128 = 57344, and a scale keeps its 11 bits down to 2^-15 f (2 F * 2^-15 = 2^-14 F).
-    __device__ void convert() {
-        const int t = threadIdx.x - 384, lane = t & 31;
-        unsigned seq = 0, step = 0;
+    __device__ void scales() {
+        const int lane = threadIdx.x & 31;
+        unsigned st = 0, ph = 0;
         float F = 1.f;
         Unit u;
         while (next(u)) {
-            for (int j = 0; j < u.steps; ++j, ++step) {
+            for (int j = 0; j < u.steps; ++j) {
                 const int valid = tokens_of(u, j);
+                if (!wait(bars + kBarScRaw + 8 * st, ph)) return;
+                const uint32_t sc = sm + Cfg::kOffScales + st * kScaleBytes;
+                float ks[4], vs[4], f = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = lane + 32 * i;
+                    ks[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 0))) : 0.f;
+                    vs[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 1))) : 0.f;
+                    f = fmaxf(f, fabsf(vs[i]));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
+                if (!(f > 0.f)) f = 1.f;
+                if (j == 0 || f > F * 128.f || f < F * 2.f) F = fmaxf(f * 0.0625f, 1e-37f);   // 1 / F is finite
+                const float rF = 1.f / F;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // the shuffles above come after every lane's reads
+                    sts32v(sc + (lane + 32 * i) * 4, __float_as_uint(ks[i]));
+                    sts32v(sc + 512 + (lane + 32 * i) * 4, __float_as_uint(vs[i] * rF));
+                }
+                if (lane == 0) sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
+                fence_proxy_async_shared();   // the next copy into this stage comes after these stores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * st);
+                if (++st == Cfg::kScales) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    }
+    // Thread t of the converting warps turns token t's 128 codes into f16: K as it is (exact: every e4m3 value is
+    // an f16 value; the factor is 1), V times its token's scale over F (two roundings to f16, 2^-11 each, beside
+    // P's one; it spares the softmax a product per weight).  Rows past the prefix become zeros, since a
+    // weight of zero does not silence a NaN.  This chain (raw codes landed, read, convert, store, announce) paces the fp8
+    // pass, so nothing else stands in it: no scales, no branches, and the reads are requested before the slot is free.
+    __device__ void convert() {
+        const int t = threadIdx.x - 384, lane = t & 31, x = t & 7;
+        const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
+        const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4;
+        unsigned r = 0, r_ph = 0, s = 0, s_ph = 1, st = 0, st_ph = 0;   // s_ph 1: the slots start free
+        Unit u;
+        while (next(u)) {
+            for (int j = 0; j < u.steps; ++j) {
+                const bool zero = t >= tokens_of(u, j);
 #pragma unroll 1
-                for (int v = 0; v < 2; ++v, ++seq) {
-                    const int r = seq % Cfg::kRaw, s = seq % Cfg::kSlots;
-                    const unsigned st = step % Cfg::kScales, st_ph = step / Cfg::kScales & 1;
-                    if (!wait(bars + kBarRawFull + 8 * r, seq / Cfg::kRaw & 1)) return;
-                    if (v == 0 && t < 32) {
-                        const uint32_t sc = sm + Cfg::kOffScales + st * kScaleBytes;
-                        float ks[4], vs[4], f = 0.f;
+                for (int v = 0; v < 2; ++v) {
+                    if (!wait(bars + kBarRawFull + 8 * r, r_ph)) return;
+                    const uint32_t src = raw0 + r * kRawBytes, dst = slot0 + s * kSlotBytes;
+                    uint32_t w[8][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = lane + 32 * i;
-                            ks[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 0))) : 0.f;
-                            vs[i] = tok < valid ? __uint_as_float(lds32v(scale_at(sc, tok, 1))) : 0.f;
-                            f = fmaxf(f, fabsf(vs[i]));
+                    for (int c = 0; c < 8; ++c) lds128(src + ((c ^ x) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                    float vs = 1.f;
+                    if (v) {
+                        if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                        vs = __uint_as_float(lds32v(scale0 + st * kScaleBytes));
+                        if (++st == Cfg::kScales) {
+                            st = 0;
+                            st_ph ^= 1;
                         }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
-                        if (!(f > 0.f)) f = 1.f;
-                        if (j == 0 || f > F * 128.f || f < F * 2.f) F = fmaxf(f * 0.0625f, 1e-37f);   // 1 / F is finite
-                        const float rF = 1.f / F;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {   // the shuffles above come after every lane's reads
-                            sts32v(sc + (lane + 32 * i) * 4, __float_as_uint(ks[i]));
-                            sts32v(sc + 512 + (lane + 32 * i) * 4, __float_as_uint(vs[i] * rF));
-                        }
-                        if (lane == 0) sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * st);
                     }
-                    if (seq >= Cfg::kSlots && !wait(bars + kBarEmpty + 8 * s, (seq / Cfg::kSlots - 1) & 1)) return;
-                    const int x = t & 7;
-                    if (v && !wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                    const uint32_t vs2 = pack_f16(vs, vs);
+                    if (!wait(bars + kBarEmpty + 8 * s, s_ph)) return;
+                    if (zero) {
 #pragma unroll
-                    for (int row = t; row < kStep; row += 32 * kConvertWarps) {
-                        const uint32_t src = sm + Cfg::kOffRaw + r * kRawBytes + row * 128;
-                        const uint32_t dst = sm + Cfg::kOffSlots + s * kSlotBytes + row * 128;
-                        const float vs = v ? __uint_as_float(lds32v(sm + Cfg::kOffScales + st * kScaleBytes + 512 + row * 4)) : 1.f;
-                        const uint32_t vs2 = pack_f16(vs, vs);
-                        uint32_t w[8][4];
+                        for (int c = 0; c < 8; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+                    }
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) lds128(src + ((c ^ x) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[8];
-                            if (row >= valid) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
-                            if (v) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
-                            }
-                            const uint32_t d = dst + (c >> 2) * 16384;
-                            const int k = 2 * (c & 3);
-                            sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
-                            sts128(d + (((k + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
-                        }
+                        for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
+                        const uint32_t d = dst + (c >> 2) * 16384;
+                        const int k = 2 * (c & 3);
+                        sts128(d + ((k ^ x) << 4), o[0], o[1], o[2], o[3]);
+                        sts128(d + (((k + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
                     }
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bars + kBarFull + 8 * s);
                         mbar_arrive(bars + kBarRawEmpty + 8 * r);
+                    }
+                    if (++r == Cfg::kRaw) {
+                        r = 0;
+                        r_ph ^= 1;
+                    }
+                    if (++s == Cfg::kSlots) {
+                        s = 0;
+                        s_ph ^= 1;
                     }
                 }
             }
@@ -875,6 +912,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
         for (int i = 0; i < 3; ++i) {
             mbar_init(bars + kBarRawFull + 8 * i, 1);
             mbar_init(bars + kBarRawEmpty + 8 * i, kConvertWarps);
+            mbar_init(bars + kBarScRaw + 8 * i, 1);
             mbar_init(bars + kBarScFull + 8 * i, 1);
             mbar_init(bars + kBarScEmpty + 8 * i, 8);
         }
@@ -915,6 +953,8 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
                 p.copies(&kv_map, &sc_map);
             else if (warp == 9)
                 p.products(tmem);
+            else if (Cfg::kF16 && warp == 10)
+                p.scales();
             else if (Cfg::kF16 && warp >= 12)
                 p.convert();
         }
