@@ -96,27 +96,40 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
     const int head = unit % a.sel_heads, list = OWN ? unit / a.sel_heads : unit;   // the table row and length
     const int max_ctx = a.MB * a.BS;
+    // What a warp needs first is asked for at once: the length, its part of the table as if the list were full (a
+    // selected list mostly is, and the first warp's part does not depend on it), and the query rows.
+    const int ts = a.bs_shift - 4, n = C * nw, wi = rank * nw + warp;
+    const int* table = a.block_table + (long long)list * a.MB;
+    auto run_of = [&](int tiles, int& t0, int& t1) {   // runs of whole pairs: a step takes two tiles
+        const long long pairs = (tiles + 1) >> 1;
+        t0 = 2 * (int)(wi * pairs / n);
+        t1 = min(tiles, 2 * (int)((wi + 1) * pairs / n));
+    };
+    int t0, t1;
+    run_of(max_ctx >> 4, t0, t1);
+    int e0 = t0 >> ts;
+    int ent = e0 + lane < a.MB ? __ldg(table + e0 + lane) : 0;
     const int raw = __ldg(a.context_lens + list);
+    uint32_t qn[NT][16];
+    {
+        UnitIt u = {unit, 0, 0, 0, 0, 0};
+        D::load_q(a, u, qn, lane);
+    }
     if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!OWN || head == 0) && a.err_word)
         atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
     const int ctx = sanitize_ctx(raw, max_ctx);
     if (OWN && ctx == 0) return;   // every CTA of the cluster
-    const int T = (ctx + 15) >> 4;
-    const long long pairs = (T + 1) >> 1;   // runs of whole pairs: a step takes two tiles
-    const int n = C * nw, wi = rank * nw + warp;
-    const int t0 = 2 * (int)(wi * pairs / n), t1 = min(T, 2 * (int)((wi + 1) * pairs / n));
+    run_of((ctx + 15) >> 4, t0, t1);
     bool ok = true;
 
     if (t0 < t1) {
-        UnitIt u = {unit, 0, 0, ctx, 0, 0};
-        uint32_t qn[NT][16];
-        D::load_q(a, u, qn, lane);
         float cent = 0.f;
         if constexpr (TQ) cent = __ldg(a.centroids + (lane & 15));
-        const int ts = a.bs_shift - 4, entries = ((t1 - 1) >> ts) + 1;
-        const int* table = a.block_table + (long long)list * a.MB;
-        int e0 = t0 >> ts;
-        int ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
+        const int entries = ((t1 - 1) >> ts) + 1;
+        if (e0 != t0 >> ts) {
+            e0 = t0 >> ts;
+            ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
+        }
         const uint64_t policy = l2_policy_evict_first();
         int issued = 0;
         auto issue = [&](int t, int stage) {   // tiles in order
