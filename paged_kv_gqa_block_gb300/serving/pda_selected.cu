@@ -12,8 +12,8 @@ namespace pda {
 // round of CTAs takes a warp's run, and 6 for its start and its join, 3 more for a cluster's join; the rounds
 // that the units need are what the choice weighs against it.  A cluster lies within one group of SMs, so of 152
 // SMs clusters of four CTAs reach 144, and of eight 120 with one CTA per SM (144, 136 with two, three): 16
-// units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and take 8.7 us.  Measured against the partition pass and
-// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.5 us against 16.1, 32 units 11.0 against
+// units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and take 8.6 us.  Measured against the partition pass and
+// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.3 us against 16.1, 32 units 10.9 against
 // 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 44 against 63, 1024 units of 8192 287 against 383;
 // only 800 units of 4096 bf16 tokens were slower, 273 against 245.
 struct Shape {

@@ -23,14 +23,22 @@
 // softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
 // row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
 // TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
+// P is announced in halves, so that PV starts while the second half is computed.
 // P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11; V carries two more such
-// roundings, see the conversion); m, l, S and O
-// are fp32.
+// roundings, see the conversion); m, l, S and O are fp32.
 //
 // Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
 // row tile) are laid end to end and every CTA takes an equal run; a row tile that is cut leaves one
 // partial per piece.  Nothing depends on how lengths and groups fall.  Bound by the tensor cores
 // where a group has many rows (4 * 256 * D flops per token and pair of tiles), by HBM where it has few.
+//
+// Measured, whole calls: 128 sequences of 64 query heads over 32768 bf16 tokens 107 us (1.28 PFLOP/s; this pass 87 us,
+// 143 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 110 us, fp8 148 us.  A further step of 256 rows costs a CTA
+// 1.38 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us: 350 KB of
+// shared-memory traffic (operands 192, conversion 96, copies 32, scales 32) at 128 bytes per cycle.  Few rows: 4 sequences
+// over 38912 tokens 36.6 us (bf16, 4.4 TB/s with the launches) and 39.8 us (fp8).  The launches, first copies, last
+// stores and the join around the steps take 10 to 20 us, more with more rows: a call of four steps per CTA is 18 us
+// with 4 sequences, 22 us with 32.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -983,7 +991,8 @@ struct JoinArgs {
 
 // One CTA per (sequence, KV head), one warp per query row: lane i holds (m, l) of partials i, i + 32,
 // ... of both parts, prefix pieces first; each lane then sums four dimensions over the partials in
-// that order, eight loads in flight.  Bound by latency (a row's partials are a few KB, in L2).
+// that order, eight loads in flight.  Bound by latency (a row's partials are a few KB, in L2): a call of 32
+// sequences of 64 heads without prefixes or tokens, its three launches, takes 5.5 us.
 __global__ void __launch_bounds__(512) pda_shared_join_kernel(const JoinArgs a) {
     grid_dependency_wait();
     const int b = blockIdx.x / a.Hk, lane = threadIdx.x & 31, q = threadIdx.x >> 5;
