@@ -442,7 +442,8 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  *                  most num_partitions + 1 pieces.  kernel_variant is not looked at.
  *   plan           num_seqs = sequences; as for pda_decode over the sequences' own tokens
  *                  (heads, group size, block size, kv_dtype and softmax_scale equal in both plans;
- *                  bf16 and fp8: a TQ4 plan is PDA_ERR_UNSUPPORTED)
+ *                  bf16 and fp8: a TQ4 plan is PDA_ERR_UNSUPPORTED; kernel_variant and the partition length
+ *                  are not looked at)
  *   group_starts   device, int32 [groups + 1], ascending; sequences outside [group_starts[0],
  *                  group_starts[groups]) have no prefix
  *   prefix_table   device, int32 [groups][prefix_plan->max_blocks_per_seq]
