@@ -17,6 +17,7 @@
 //   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
 //   9         the matrix products (one thread issues)
 //   10        fp8 only: the scales of a step
+//   11        the split: which rows and which tokens this CTA takes
 //   12-15     fp8 only: e4m3 codes to f16 between the copy and the product
 // The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
 // The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
@@ -60,6 +61,7 @@ constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bi
 constexpr int kRawBytes = 16384;           // the same in 8 bits
 constexpr int kScaleBytes = 1024;          // 128 tokens x {K scale, V scale}
 constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
+constexpr int kSwitch = 3;                 // what a change of row tiles costs a CTA, in steps
 constexpr float kLazy = 8.f;
 
 struct SharedArgs {
@@ -89,7 +91,8 @@ struct SharedCfg {
     static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;
     static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
     static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
-    static constexpr int kSmem = kOffBars + 320;
+    static constexpr int kSmem = kOffBars + 448;
+    static constexpr int kReaders = kF16 ? 15 : 10;               // warps that take units
 };
 // barriers and scalars after kOffBars
 enum {
@@ -108,7 +111,10 @@ enum {
     kAbortAt = 252,      // a wait gave up
     kFAt = 256,          // [3] what a step's V scales are divided by
     kBarP2 = 272,        // [2] the second half of P is in TMEM
-    kBarScRaw = 288      // [3] scales as copied
+    kBarScRaw = 288,     // [3] scales as copied
+    kBarUnitFull = 312,  // [2] the next unit is in shared memory
+    kBarUnitEmpty = 328, // [2]
+    kUnitAt = 352        // [2] units, 48 bytes each
 };
 
 // ------------------------------------------------------------------------- the split
@@ -144,92 +150,132 @@ __device__ __forceinline__ Group group_shape(const SharedArgs& a, int g, int& ba
     x.steps = (x.len + kStep - 1) / kStep;
     return x;
 }
+// Of numbers that are not negative.  A CTA waits for this code's first fetch longer than for its execution, so
+// quotients that are wanted together are computed by lanes of one warp.
+__device__ __forceinline__ int quotient(int x, int d) { return (int)((unsigned)x / (unsigned)d); }
+
 // How one warp sees the split: lane i holds group i (and re-reads the others where there are more
-// than 32).  The host has made sure that the number of all steps of ascending groups fits an int.
+// than 32).  The host has made sure that the places of all steps of ascending groups fit an int.
 struct Split {
     Group mine;
-    int before, total;     // steps of the groups before lane i's (of the first 32), and of all
-    int per;               // steps of a CTA's run
+    int before, total;     // places of the groups before lane i's (of the first 32), and of all
+    int per;               // places of a CTA's run
+    int whole;             // if not 0: places of every row tile
+    // Places of a row tile: its steps, and unused ones after them.  A CTA whose run goes on into another row tile
+    // pays for it (store the rows, load others, refill the pipeline: kSwitch steps); either that is counted
+    // as places between two tiles, or every tile has whole runs of its own.
+    __device__ __forceinline__ int span(int steps) const { return steps == 0 ? 0 : whole ? whole : steps + kSwitch; }
 };
 
-// `per` is an even share of the steps, and at least 1/P of the longest prefix, so that a row tile is cut
-// into at most P + 1 pieces (the workspace's slots).
+// `per`: an even share of all places, or, where that is no longer, the longest tile's share of the runs that every
+// tile can have; and at least 1/P of the longest prefix, so that a row tile is cut into at most P + 1 pieces
+// (the workspace's slots).
 __device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool report) {
     const int lane = threadIdx.x & 31;
     Split s;
     int bad = 0;
     s.mine = group_shape(a, lane, bad);
-    const int steps = s.mine.tiles * a.Hk * s.mine.steps;
-    int incl = steps;
+    int tiles = s.mine.steps > 0 ? s.mine.tiles * a.Hk : 0, steps = tiles * s.mine.steps;
+    int longest = tiles > 0 ? s.mine.steps : 0;
+#pragma unroll 1
+    for (int g = lane + 32; g < a.NG; g += 32) {
+        const Group x = group_shape(a, g, bad);
+        const int n = x.steps > 0 ? x.tiles * a.Hk : 0;
+        tiles += n;
+        steps += n * x.steps;
+        if (n > 0) longest = max(longest, x.steps);
+    }
+    tiles = __reduce_add_sync(kLanes, tiles);
+    steps = __reduce_add_sync(kLanes, steps);
+    longest = __reduce_max_sync(kLanes, longest);
+    const int q = quotient(lane == 0 ? longest + a.P - 1 : lane == 1 ? steps + kSwitch * tiles + ctas - 1 : ctas,
+                           lane == 0 ? a.P : lane == 1 ? ctas : max(tiles, 1));
+    const int least = max(__shfl_sync(kLanes, q, 0), 1), even = max(__shfl_sync(kLanes, q, 1), least);
+    const int runs = __shfl_sync(kLanes, q, 2);
+    const int own = runs > 0 ? max(quotient(longest + runs - 1, runs), least) : even + 1;
+    s.per = min(own, even);
+    s.whole = own <= even ? quotient(longest + own - 1, own) * own : 0;   // the first CTAs work: they start first
+    const int mine = s.mine.tiles * a.Hk * s.span(s.mine.steps);
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(kLanes, incl, o);
         if (lane >= o) incl += x;
     }
-    s.before = incl - steps;
+    s.before = incl - mine;
     s.total = __shfl_sync(kLanes, incl, 31);
-    int longest = s.mine.tiles > 0 ? s.mine.steps : 0;
     if (a.NG > 32) {
         int more = 0;
+#pragma unroll 1
         for (int g = lane + 32; g < a.NG; g += 32) {
             const Group x = group_shape(a, g, bad);
-            more += x.tiles * a.Hk * x.steps;
-            if (x.tiles > 0) longest = max(longest, x.steps);
+            more += x.tiles * a.Hk * s.span(x.steps);
         }
         s.total += __reduce_add_sync(kLanes, more);
     }
-    longest = __reduce_max_sync(kLanes, longest);
     // groups that are not ascending may overlap, and name more rows than there are: no prefix then
     if (__any_sync(kLanes, bad & PDA_ERRW_BAD_GROUP)) s.total = 0;
     if (report && bad && a.err_word) atomicOr(a.err_word, bad);
-    s.per = max(max((s.total + ctas - 1) / ctas, (longest + a.P - 1) / a.P), 1);
     return s;
 }
 
-// One warp: the piece that starts at step `at` of the run of all steps and ends with its row tile or at `end`.
-__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, int at, int end) {
+// One warp: the piece that starts at place `at` of the run of all places, or after the unused ones there, and ends
+// with its row tile or at `end`; `at` moves past it.  Without steps: there is none.
+__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, int& at, int end) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
-    Group x = s.mine;
-    int lo = s.before, g0 = 0;
-    unsigned hit;
-    for (;;) {
-        const int n = x.tiles * a.Hk * x.steps;
-        hit = __ballot_sync(kLanes, lo <= at && at < lo + n);
-        if (hit || (g0 += 32) >= a.NG) break;
-        const int next = __shfl_sync(kLanes, lo + n, 31);   // the next 32 groups
-        int bad = 0;
-        x = group_shape(a, g0 + lane, bad);
-        const int m = x.tiles * a.Hk * x.steps;
-        int incl = m;
+#pragma unroll 1
+    while (at < end) {
+        Group x = s.mine;
+        int lo = s.before, g0 = 0;
+        unsigned hit;
+#pragma unroll 1
+        for (;;) {
+            const int n = x.tiles * a.Hk * s.span(x.steps);
+            hit = __ballot_sync(kLanes, lo <= at && at < lo + n);
+            if (hit || (g0 += 32) >= a.NG) break;
+            const int next = __shfl_sync(kLanes, lo + n, 31);   // the next 32 groups
+            int bad = 0;
+            x = group_shape(a, g0 + lane, bad);
+            const int m = x.tiles * a.Hk * s.span(x.steps);
+            int incl = m;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kLanes, incl, o);
-            if (lane >= o) incl += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kLanes, incl, o);
+                if (lane >= o) incl += y;
+            }
+            lo = next + incl - m;
         }
-        lo = next + incl - m;
+        if (!hit) break;
+        const int src = __ffs(hit) - 1;
+        const int nt = __shfl_sync(kLanes, x.tiles, src), ns = __shfl_sync(kLanes, x.steps, src);
+        const int base = __shfl_sync(kLanes, lo, src), span = s.span(ns);
+        const int tile = quotient(at - base, span), first = base + tile * span;   // the row tile's own first place
+        u.step0 = at - first;
+        if (u.step0 >= ns) {
+            at = first + span;
+            continue;
+        }
+        u.g = g0 + src;
+        u.seq0 = __shfl_sync(kLanes, x.seq0, src);
+        u.rows = __shfl_sync(kLanes, x.rows, src);
+        u.len = __shfl_sync(kLanes, x.len, src);
+        u.steps = min(ns - u.step0, end - at);
+        const int q = quotient(lane == 0 ? tile : lane == 1 ? first : lane == 2 ? at : lane == 3 ? first + ns - 1 : u.step0 + s.per - 1,
+                               lane == 0 ? nt : s.per);
+        u.h = __shfl_sync(kLanes, q, 0);
+        u.rt = tile - u.h * nt;
+        const int c0 = __shfl_sync(kLanes, q, 1);
+        u.slot = __shfl_sync(kLanes, q, 2) - c0;
+        u.pieces = __shfl_sync(kLanes, q, 3) - c0 + 1;
+        // The row tiles of one (group, KV head) read the same tokens, but are cut at different places.
+        // Taking the steps of a piece from the first multiple of `per` on makes every CTA read, at
+        // time t, tokens of step t mod per of its tile: the copies of other row tiles then hit L2.
+        const int s0 = __shfl_sync(kLanes, q, 4) * s.per;
+        u.rot = s0 < u.step0 + u.steps ? s0 - u.step0 : 0;
+        at += u.steps;
+        break;
     }
-    if (!hit) return u;
-    const int src = __ffs(hit) - 1;
-    u.g = g0 + src;
-    u.seq0 = __shfl_sync(kLanes, x.seq0, src);
-    u.rows = __shfl_sync(kLanes, x.rows, src);
-    u.len = __shfl_sync(kLanes, x.len, src);
-    const int nt = __shfl_sync(kLanes, x.tiles, src), ns = __shfl_sync(kLanes, x.steps, src);
-    const int base = __shfl_sync(kLanes, lo, src);
-    const int tile = (at - base) / ns, first = base + tile * ns;   // the row tile's own first step
-    u.step0 = at - first;
-    u.h = tile / nt;
-    u.rt = tile - u.h * nt;
-    u.steps = min(ns - u.step0, end - at);
-    const int c0 = first / s.per;
-    u.slot = at / s.per - c0;
-    u.pieces = (first + ns - 1) / s.per - c0 + 1;
-    // The row tiles of one (group, KV head) read the same tokens, but are cut at different places.
-    // Taking the steps of a piece from the first multiple of `per` on makes every CTA read, at
-    // time t, tokens of step t mod per of its tile: the copies of other row tiles then hit L2.
-    const int s0 = (u.step0 + s.per - 1) / s.per * s.per;
-    u.rot = s0 < u.step0 + u.steps ? s0 - u.step0 : 0;
     return u;
 }
 
@@ -289,8 +335,7 @@ struct Prefix {
     const SharedArgs& a;
     const uint32_t sm;         // shared memory base
     const uint32_t bars;
-    Split split;
-    int at, end;               // this CTA's run
+    unsigned units = 0;        // units taken (or given) by this warp
 
     __device__ __forceinline__ Prefix(const SharedArgs& args, uint32_t base)
         : a(args), sm(base), bars(base + Cfg::kOffBars) {}
@@ -315,21 +360,38 @@ struct Prefix {
         }
     }
 
-    // The CTA's first unit, looked up by all warps at once (one fetch of this code), and the ones after it.
-    Unit first_unit;
-    __device__ __forceinline__ void look_up() {
-        first_unit = find_unit(a, split, at, end);
-        at += first_unit.steps;
+    // One warp looks the CTA's units up, ahead of the others, which read them from shared memory; a unit without
+    // steps is the end.  (Looked up by every warp for itself, the split took registers from the softmax.)
+    __device__ __forceinline__ void put(const Unit& u) const {
+        const uint32_t at = bars + kUnitAt + (units & 1) * 48;
+        if ((threadIdx.x & 31) == 0) {
+            sts128(at, u.g, u.h, u.rt, u.seq0);
+            sts128(at + 16, u.rows, u.len, u.step0, u.steps);
+            sts128(at + 32, u.rot, u.slot, u.pieces, 0);
+        }
+    }
+    __device__ void give(const Split& split, Unit u, int at, int end) {   // the first one is there already
+        for (;;) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitFull + 8 * (units & 1));
+            ++units;
+            if (u.steps == 0) return;
+            u = find_unit(a, split, at, end);
+            if (units > 1 && !wait(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
+            put(u);
+        }
     }
     __device__ __forceinline__ bool next(Unit& u) {
-        if (first_unit.steps > 0) {
-            u = first_unit;
-            first_unit.steps = 0;
-            return true;
-        }
-        if (at >= end) return false;
-        u = find_unit(a, split, at, end);
-        at += u.steps;
+        const uint32_t slot = units & 1, at = bars + kUnitAt + slot * 48;
+        if (!wait(bars + kBarUnitFull + 8 * slot, units >> 1 & 1)) return false;
+        uint32_t x[12];
+#pragma unroll
+        for (int i = 0; i < 12; i += 4) lds128(at + 4 * i, x[i], x[i + 1], x[i + 2], x[i + 3]);
+        u.g = x[0], u.h = x[1], u.rt = x[2], u.seq0 = x[3], u.rows = x[4], u.len = x[5], u.step0 = x[6], u.steps = x[7];
+        u.rot = x[8], u.slot = x[9], u.pieces = x[10];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitEmpty + 8 * slot);
+        ++units;
         return u.steps > 0;
     }
     // Step number of the piece's j-th step, and its tokens.
@@ -924,6 +986,10 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
             mbar_init(bars + kBarScFull + 8 * i, 1);
             mbar_init(bars + kBarScEmpty + 8 * i, 8);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + kBarUnitFull + 8 * i, 1);
+            mbar_init(bars + kBarUnitEmpty + 8 * i, Cfg::kReaders);
+        }
         mbar_init(bars + kBarDrain, 1);
         sts32v(bars + kAbortAt, (sm & 1023u) ? 1u : 0u);   // the operands' swizzle needs the alignment
         fence_mbar_init();
@@ -933,27 +999,33 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     // No wait for the previous grid here: it is this call's pass over the sequences' own tokens, which lets
     // this one start only after everything before it has ended, and of which nothing is read.
     Prefix<KV> p(a, sm);
-    p.split = make_split(a, gridDim.x, blockIdx.x == 0 && warp == 8);
-    p.at = (int)min((long long)blockIdx.x * p.split.per, (long long)p.split.total);
-    p.end = p.at + min(p.split.per, p.split.total - p.at);
-    p.look_up();
+    Split split;
+    Unit first;
+    int at, end;
+    if (warp == 11) {
+        split = make_split(a, gridDim.x, blockIdx.x == 0);
+        at = (int)min((long long)blockIdx.x * split.per, (long long)split.total);
+        end = at + min(split.per, split.total - at);
+        first = find_unit(a, split, at, end);
+        p.put(first);
+    }
     if (warp == 9) tmem_alloc(bars + kTmemAt, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lds32v(bars + kTmemAt);
     allow_dependent_launch();
-    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
+    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 184 + 256 x 72
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
         if constexpr (Cfg::kF16)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         if (fine) p.softmax(tmem, warp >> 2);
     } else {
         if constexpr (Cfg::kF16)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (fine) {
@@ -961,6 +1033,8 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
                 p.copies(&kv_map, &sc_map);
             else if (warp == 9)
                 p.products(tmem);
+            else if (warp == 11)
+                p.give(split, first, at, end);
             else if (Cfg::kF16 && warp == 10)
                 p.scales();
             else if (Cfg::kF16 && warp >= 12)
@@ -1185,7 +1259,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
         return PDA_ERR_INVALID_ARG;
     const SharedLayout w = shared_layout(prefix_plan, plan);
     if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;
-    if (most_steps(prefix_plan, plan) > 2000000000ll) return PDA_ERR_INVALID_ARG;   // the split counts in ints
+    if (most_steps(prefix_plan, plan) > 2000000000ll / (1 + kSwitch)) return PDA_ERR_INVALID_ARG;   // places are ints
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
