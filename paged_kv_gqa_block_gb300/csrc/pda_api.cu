@@ -378,7 +378,7 @@ static DecodeArgs plan_args(const pda_plan_t* plan, const void* query, long long
     return a;
 }
 
-int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+int decode_own(const pda_plan_t* plan, bool behind, const void* query, const void* kv_cache, long long num_cache_blocks,
                const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
                int* err_word, cudaStream_t stream) {
     DecodeArgs a = plan_args(plan, query, num_cache_blocks, block_table, context_lens, partial_out, exp_sums, max_logits,
@@ -391,7 +391,7 @@ int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, 
     sc_map = kv_map;
     if (plan->kv_dtype != PDA_KV_BF16 && !encode_scale_map(&sc_map, kv_cache, plan, num_cache_blocks))
         return PDA_ERR_LAUNCH;
-    return launch_own_clusters(plan->kv_dtype, a, kv_map, sc_map, stream);
+    return launch_own_clusters(plan->kv_dtype, behind, a, kv_map, sc_map, stream);
 }
 }  // namespace pda
 

@@ -70,9 +70,12 @@ int launch_decode_selected(int kv_dtype, const DecodeArgs& a, const CUtensorMap&
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream);
 // The sequences' own tokens beside a shared prefix, in the same kernel: one partial per (sequence, KV head) and
-// query row to a.partial_out, a.exp_sums and a.max_logits (a sequence without tokens writes none).
-int launch_own_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
-                        cudaStream_t stream);
+// query row to a.partial_out, a.exp_sums and a.max_logits (a sequence without tokens writes none).  `behind`: the
+// launch before it is the prefix pass (else that comes after it).
+int launch_own_clusters(int kv_dtype, bool behind, const DecodeArgs& a, const CUtensorMap& kv_map,
+                        const CUtensorMap& sc_map, cudaStream_t stream);
+// The CTAs of that launch.
+long long own_clusters_ctas(const pda_plan_t* plan, int sms);
 int launch_decode_tq4(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, cudaStream_t stream);
 int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 
@@ -81,7 +84,7 @@ int launch_reduce(const ReduceArgs& r, cudaStream_t stream);
 unsigned int* launch_counter_slot(int* status);
 
 // The sequences' own tokens in pda_decode_shared.  The plan and the pointers have been checked.
-int decode_own(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+int decode_own(const pda_plan_t* plan, bool behind, const void* query, const void* kv_cache, long long num_cache_blocks,
                const int* block_table, const int* context_lens, float* partial_out, float* exp_sums, float* max_logits,
                int* err_word, cudaStream_t stream);
 // Tensor maps of pda_decode_shared: one (block, KV head) and 128-byte chunk, or its scales, per copy.

@@ -37,7 +37,7 @@ static Shape selected_shape(long long units, int tiles, int sms, int wps, int nw
 }
 
 template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
-static int launch_clusters(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, Shape shape,
+static int launch_clusters(bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, Shape shape,
                            cudaStream_t stream) {
     auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB, OWN>;
     static bool attr_set[64] = {false};
@@ -66,41 +66,48 @@ static int launch_clusters(const DecodeArgs& a, const CUtensorMap& kv_map, const
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C, (int)behind) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
 }
 
 template <bool OWN, int KV, int NT, int S, int NWMAX, int WPS>
-static int launch_clusters_of(const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+static int launch_clusters_of(bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                               cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
     const Shape shape = selected_shape(a.B, (a.MB * a.BS + 15) / 16, sms, WPS, NWMAX);
     if ((long long)a.B * shape.C > 0x7FFFFFFFll) return PDA_ERR_INVALID_ARG;
-    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, OWN>(a, kv_map, sc_map, shape, stream);
+    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, OWN>(behind, a, kv_map, sc_map, shape, stream);
 }
 
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
-        return launch_clusters_of<false, PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 4, 6, 6>(false, a, kv_map, kv_map, stream);
+        return launch_clusters_of<false, PDA_KV_BF16, 2, 4, 6, 6>(false, a, kv_map, kv_map, stream);
     }
     if (kv_dtype == PDA_KV_TQ4) {
-        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_TQ4, 1, 6, 6, 12>(a, kv_map, sc_map, stream);
-        return launch_clusters_of<false, PDA_KV_TQ4, 2, 6, 4, 8>(a, kv_map, sc_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_TQ4, 1, 6, 6, 12>(false, a, kv_map, sc_map, stream);
+        return launch_clusters_of<false, PDA_KV_TQ4, 2, 6, 4, 8>(false, a, kv_map, sc_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(a, kv_map, sc_map, stream);
-    return launch_clusters_of<false, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(false, a, kv_map, sc_map, stream);
+    return launch_clusters_of<false, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(false, a, kv_map, sc_map, stream);
 }
 
-int launch_own_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
+long long own_clusters_ctas(const pda_plan_t* p, int sms) {
+    const long long units = (long long)p->num_seqs * p->num_kv_heads;
+    const bool bf16 = p->kv_dtype == PDA_KV_BF16, wide = p->query_group_size > 8;   // as below
+    return units * selected_shape(units, (p->max_blocks_per_seq * p->kv_block_size + 15) / 16, sms, bf16 ? 6 : wide ? 8 : 12,
+                                  !bf16 && wide ? 4 : 6).C;
+}
+
+int launch_own_clusters(int kv_dtype, bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                         cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 4, 6, 6>(a, kv_map, kv_map, stream);
-        return launch_clusters_of<true, PDA_KV_BF16, 2, 4, 6, 6>(a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 4, 6, 6>(behind, a, kv_map, kv_map, stream);
+        return launch_clusters_of<true, PDA_KV_BF16, 2, 4, 6, 6>(behind, a, kv_map, kv_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(a, kv_map, sc_map, stream);
-    return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(behind, a, kv_map, sc_map, stream);
+    return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(behind, a, kv_map, sc_map, stream);
 }
 
 }  // namespace pda

@@ -64,7 +64,7 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, long long row,
 template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
 __global__ void __launch_bounds__(32 * NWMAX, MINB)
     pda_selected_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
-                        const DecodeArgs a, const int C) {
+                        const DecodeArgs a, const int C, const int behind) {
     using D = Decode<KV, NT, S, false>;
     using Cfg = DecodeCfg<KV, S>;
     using Sel = SelectedCfg<KV, S>;
@@ -88,11 +88,15 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         if (F16) prefetch_tensormap(&sc_map);
     }
     __syncwarp();
+    // Own tokens and the prefix pass read nothing of one another's.  The first of the two waits for everything
+    // before them and then lets the other start; the second waits for the first before it ends (one CTA of it: the
+    // others make room), so that the join waits for both.
     if constexpr (!OWN) allow_dependent_launch();
-    grid_dependency_wait();
-    // Own tokens: the prefix pass that follows reads nothing of this grid's (it waits for it before it ends),
-    // so it may start once everything before this grid has ended.
+    if (!OWN || !behind) grid_dependency_wait();
     if constexpr (OWN) allow_dependent_launch();
+    auto leave = [&] {
+        if (OWN && behind && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+    };
 
     const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
     const int head = unit % a.sel_heads, list = OWN ? unit / a.sel_heads : unit;   // the table row and length
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!OWN || head == 0) && a.err_word)
         atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
     const int ctx = sanitize_ctx(raw, max_ctx);
-    if (OWN && ctx == 0) return;   // every CTA of the cluster
+    if (OWN && ctx == 0) return leave();   // every CTA of the cluster
     run_of((ctx + 15) >> 4, t0, t1);
     bool ok = true;
 
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             }
         }
     }
-    if (C == 1) return;
+    if (C == 1) return leave();
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     for (int i = rank * blockDim.x + threadIdx.x; i < a.QG * 32; i += C * blockDim.x) {
@@ -385,6 +389,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
     }
     cl.sync();   // nobody leaves while its rows are read
+    leave();
 }
 
 }  // namespace pda

@@ -76,6 +76,7 @@ struct SharedArgs {
     int* err_word;
     long long num_cache_blocks;
     int B, NG, Hk, QG, MP, BS, P, slots;
+    int first;                   // this pass comes before the own tokens' one
     float qk_scale_log2;
     unsigned long long timeout_ns;
 };
@@ -996,8 +997,9 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
         prefetch_tensormap(&kv_map);
         if (Cfg::kF16) prefetch_tensormap(&sc_map);
     }
-    // No wait for the previous grid here: it is this call's pass over the sequences' own tokens, which lets
-    // this one start only after everything before it has ended, and of which nothing is read.
+    // Behind the pass over the sequences' own tokens no wait for it here: it lets this one start only after
+    // everything before it has ended, and nothing of it is read.
+    if (a.first) grid_dependency_wait();
     Prefix<KV> p(a, sm);
     Split split;
     Unit first;
@@ -1047,7 +1049,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     tc_fence_after();
     if (threadIdx.x == 0 && lds32v(bars + kAbortAt) && a.err_word) atomicOr(a.err_word, PDA_ERRW_PIPELINE_TIMEOUT);
     if (warp == 9) tmem_free(tmem, 512);
-    grid_dependency_wait();   // this grid ends after the own pass: the join waits for this one alone
+    grid_dependency_wait();   // behind the own pass this grid ends after it: the join waits for one grid alone
 }
 
 // ------------------------------------------------------------------------- the join
@@ -1182,6 +1184,21 @@ static long long most_steps(const pda_plan_t* pp, const pda_plan_t* p) {
     const long long tiles = ((long long)p->num_seqs * p->query_group_size + kUnitRows - 1) / kUnitRows + pp->num_seqs;
     return tiles * p->num_kv_heads * (((long long)pp->max_blocks_per_seq * pp->kv_block_size + kStep - 1) / kStep);
 }
+// The row tiles that the groups can have.
+static long long most_tiles(const pda_plan_t* p, int groups) {
+    return (((long long)p->num_seqs * p->query_group_size + kUnitRows - 1) / kUnitRows + groups - 1) * p->num_kv_heads;
+}
+// A prefix CTA takes a whole SM.  Where the prefixes can keep half of the SMs busy at most, their pass comes first and
+// the own tokens run beside it (32 sequences of 32 heads over 6000 bf16 tokens 23.7 -> 18.8 us), unless they are few and
+// there is room for both anyway: the join then waits for one launch less (2 sequences of 8 heads over 250 tokens 12.4
+// -> 11.4 us; but with 63 pieces, 4 sequences over 16000 tokens, 17.8 us against 17.0).
+// Else the own tokens come first, and the prefix pass, which wants every SM, starts on each as its short work ends.
+static bool prefix_first(const pda_plan_t* pp, const pda_plan_t* p, int sms) {
+    const long long steps = ((long long)pp->max_blocks_per_seq * pp->kv_block_size + kStep - 1) / kStep;
+    const long long pieces = pp->num_partitions < steps ? pp->num_partitions : steps;
+    const long long work = most_tiles(p, pp->num_seqs) * pieces;
+    return 2 * work <= sms && (work > 16 || work + own_clusters_ctas(p, sms) > sms);
+}
 static bool odd(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
 template <int KV>
@@ -1230,8 +1247,13 @@ int pda_shared_tile_groups(const pda_plan_t* plan, int num_groups, int prefix_bl
     const long long tiles = (rows > num_groups ? rows : num_groups) * plan->num_kv_heads;
     const long long pieces = (sms + tiles - 1) / tiles * (num_groups > 1 ? 2 : 1);
     const long long tokens = (long long)prefix_blocks * plan->kv_block_size;
+    // pieces of 256 or 512 tokens where half of the SMs hold them all, and the own tokens run beside them (32 sequences
+    // of 64 heads over 1500 bf16 tokens 15.7 us in pieces of 256, 18.1 of 512, 21.2 of 1024); more and shorter
+    // pieces cost the join more than they save (8 sequences of 64 heads over 4000: 20.4 us in 128 pieces, 15.6 in 64)
+    for (int G = 1; G <= 2; ++G)
+        if (2 * most_tiles(plan, num_groups) * ((tokens + G * kTokensPerTileGroup - 1) / (G * kTokensPerTileGroup)) <= sms)
+            return G;
     const long long G = (tokens + pieces * kTokensPerTileGroup - 1) / (pieces * kTokensPerTileGroup);
-    // a piece of fewer than 512 tokens would cost the join more than it saves
     return (int)(G < 2 ? 2 : G > (1 << 22) ? (1 << 22) : G);
 }
 
@@ -1288,10 +1310,12 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap kv_map, sc_map;
     if (!encode_block_map(&kv_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
-    // The sequences' own tokens first: the prefix pass, which takes whole SMs, starts on each SM as that
-    // one's short work ends.
-    int rc = decode_own(plan, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1), f32(w.m1),
-                        err_word, s);
+    a.first = prefix_first(prefix_plan, plan, sms);
+    auto own = [&] {
+        return decode_own(plan, a.first, query, kv_cache, num_cache_blocks, block_table, context_lens, f32(w.o1), f32(w.l1),
+                          f32(w.m1), err_word, s);
+    };
+    int rc = a.first ? PDA_OK : own();
     if (rc != PDA_OK) return rc;
     const long long most = most_steps(prefix_plan, plan);   // no more CTAs than there can be steps
     const int ctas = (int)(most < sms ? most : sms);
@@ -1301,6 +1325,7 @@ int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* plan, con
         if (!encode_block_scale_map(&sc_map, kv_cache, plan, num_cache_blocks)) return PDA_ERR_LAUNCH;
         rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, ctas, s);
     }
+    if (rc == PDA_OK && a.first) rc = own();
     if (rc != PDA_OK) return rc;
     JoinArgs j = {};
     j.group_starts = group_starts;
