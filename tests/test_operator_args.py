@@ -146,7 +146,7 @@ def test_shared_plans(pda):
                                       (1, 1, 1, 6, 16, 100000)):
         pp, p = pda.shared_plans(B, NG, Hk, QG, BS, blocks, 4)
         assert pp.num_seqs == NG and p.num_seqs == B and pp.max_blocks_per_seq == blocks
-        assert pp.partition_tokens >= 512 and pp.num_partitions * pp.partition_tokens >= blocks * BS
+        assert pp.partition_tokens >= 256 and pp.num_partitions * pp.partition_tokens >= blocks * BS
         assert pp.num_partitions <= max(1, 2 * 152)
     assert pda.lib().pda_shared_tile_groups(None, 1, 1) == INVALID
     assert pda.lib().pda_shared_tile_groups(ctypes.byref(p), 0, 1) == INVALID

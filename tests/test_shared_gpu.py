@@ -320,6 +320,28 @@ def test_captured_and_on_another_stream(pda, kv):
     assert torch.equal(out, out2) and (np.abs(out.cpu().numpy() - ref) <= bound + 1e-30).all()
 
 
+@pytest.mark.parametrize("kv", [BF16, FP8])
+def test_steps_without_a_pause_share_a_workspace(pda, kv):
+    """Short prefixes run before the own tokens and long ones after: steps of both orders, one behind the other on one stream and
+    in one workspace, give what each gives alone."""
+    cases = [Case(kv, 4, 8, 16, [900], [40], [3 * b % 60 for b in range(40)], seed=13),          # 32 pieces, beside 160 units
+             Case(kv, 1, 8, 16, [250], [3], [5, 0, 17], seed=14),                                # one piece
+             Case(kv, 8, 16, 32, [3000, 700], [30, 20], [0] * 10 + [70] * 45, seed=15, before=5),  # every SM
+             Case(kv, 8, 8, 16, [256], [100], [b % 9 for b in range(100)], seed=16)]
+    plans, dev = [c.plans(pda) for c in cases], [c.device() for c in cases]
+    alone = [check(pda, c) for c in cases]
+    ws = torch.full((max(pda.lib().pda_shared_workspace_size(*p) for p in plans),), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = [[torch.full_like(alone[i], float("nan")) for i in range(len(cases))] for _ in range(6)]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i in (range(4) if r % 2 else (2, 0, 3, 1)):
+            pda.decode_shared(*plans[i], **dev[i], ws=ws, out=outs[r][i])
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i in range(len(cases)):
+            assert torch.equal(outs[r][i], alone[i]), (r, i)
+
+
 def test_fork_then_shared_decode(pda):
     """A prompt's sequence is forked into samples that decode with the prompt as their shared prefix: the same as a decode over
     the forked tables."""
