@@ -14,9 +14,9 @@
 //      used block its rank.  One launch in place of count / prefix / write;
 //   2. a grid over the table segments and the 4 KB chunks of the blocks to copy.
 // What bounds them: the copies HBM (read + write), everything else launch and load latency.  Measured: 2048
-// blocks of 64 KB copied in 44.6 us (6.0 TB/s, read and written; under counters 39 us); 4 sequences forked from two
+// blocks of 64 KB copied in 44.0 us (6.1 TB/s, read and written; under counters 39 us); 4 sequences forked from two
 // parents 6.0 us, 64 from 16 parents of up to 16000 tokens in a pool of 16384 blocks 9.6 us (the second launch 7.3
-// us under counters); a pool of 8192 blocks of 64 KB compacted in 50.6 us, of which the copies are 38 us (246 MB
+// us under counters); a pool of 8192 blocks of 64 KB compacted in 49.4 us, of which the copies are 38 us (246 MB
 // read and written, 6.4 TB/s) and the rest the scan in front of them.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

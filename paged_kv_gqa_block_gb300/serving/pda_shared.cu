@@ -30,16 +30,18 @@
 //
 // Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
 // row tile) are laid end to end and every CTA takes an equal run; a row tile that is cut leaves one
-// partial per piece.  Nothing depends on how lengths and groups fall.  Bound by the tensor cores
+// partial per piece.  A change of row tiles is counted as steps too, or every tile gets runs of its own, whichever
+// ends sooner (64 sequences of 64 heads in 3 groups 37.2 -> 33.0 us, 100 of 32 heads in 7 groups 49.3 -> 34.5).
+// Nothing depends on how lengths and groups fall.  Bound by the tensor cores
 // where a group has many rows (4 * 256 * D flops per token and pair of tiles), by HBM where it has few.
 //
-// Measured, whole calls: 128 sequences of 64 query heads over 32768 bf16 tokens 107 us (1.28 PFLOP/s; this pass 87 us,
-// 143 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 110 us, fp8 148 us.  A further step of 256 rows costs a CTA
-// 1.38 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us: 350 KB of
+// Measured, whole calls: 128 sequences of 64 query heads over 32768 bf16 tokens 102 us (1.35 PFLOP/s; this pass 83 us,
+// 141 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 105 us, fp8 145 us.  A further step of 256 rows costs a CTA
+// 1.4 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us: 350 KB of
 // shared-memory traffic (operands 192, conversion 96, copies 32, scales 32) at 128 bytes per cycle.  Few rows: 4 sequences
-// over 38912 tokens 36.6 us (bf16, 4.4 TB/s with the launches) and 39.8 us (fp8).  The launches, first copies, last
-// stores and the join around the steps take 10 to 20 us, more with more rows: a call of four steps per CTA is 18 us
-// with 4 sequences, 22 us with 32.
+// over 38912 tokens 36.4 us (bf16, 4.4 TB/s with the launches) and 41 us (fp8).  The launches, first copies, last
+// stores and the join around the steps take 10 to 20 us, more with more rows: a call of two steps per CTA is 13.4 us
+// with 4 sequences, 17.0 us with 32.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1017,17 +1019,17 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = lds32v(bars + kTmemAt);
     allow_dependent_launch();
-    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 184 + 256 x 72
+    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
         if constexpr (Cfg::kF16)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         if (fine) p.softmax(tmem, warp >> 2);
     } else {
         if constexpr (Cfg::kF16)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (fine) {
