@@ -339,6 +339,7 @@ struct Prefix {
     const uint32_t sm;         // shared memory base
     const uint32_t bars;
     unsigned units = 0;        // units taken (or given) by this warp
+    unsigned busy = 0;         // their steps
 
     __device__ __forceinline__ Prefix(const SharedArgs& args, uint32_t base)
         : a(args), sm(base), bars(base + Cfg::kOffBars) {}
@@ -348,14 +349,14 @@ struct Prefix {
         const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
         bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
         if (__all_sync(kLanes, ok)) return true;
-        return wait_on(bar, parity, poll);
+        return wait_on(bar, parity, poll, a.timeout_ns);
     }
-    __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool poll) const {
+    __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool poll, uint64_t limit) const {
         const uint64_t t0 = global_timer_ns();
         for (;;) {
             const bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
             if (__all_sync(kLanes, ok)) return true;
-            const bool late = global_timer_ns() - t0 > a.timeout_ns;
+            const bool late = global_timer_ns() - t0 > limit;
             if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
                 sts32v(bars + kAbortAt, 1u);
                 return false;
@@ -365,6 +366,12 @@ struct Prefix {
 
     // One warp looks the CTA's units up, ahead of the others, which read them from shared memory; a unit without
     // steps is the end.  (Looked up by every warp for itself, the split took registers from the softmax.)
+    // A unit, or its place, may come only when warps that are behind have finished one that was taken before: the
+    // limit is that of their waits, a few per step (long limits, from 0.27 s on, do for any unit).
+    __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity) const {
+        const uint64_t limit = a.timeout_ns >> 28 ? a.timeout_ns : a.timeout_ns * (64 + 8ull * busy);
+        return wait_on(bar, parity, a.timeout_ns < 1000000ull, limit);
+    }
     __device__ __forceinline__ void put(const Unit& u) const {
         const uint32_t at = bars + kUnitAt + (units & 1) * 48;
         if ((threadIdx.x & 31) == 0) {
@@ -379,14 +386,15 @@ struct Prefix {
             if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitFull + 8 * (units & 1));
             ++units;
             if (u.steps == 0) return;
+            busy += u.steps;
             u = find_unit(a, split, at, end);
-            if (units > 1 && !wait(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
+            if (units > 1 && !wait_unit(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
             put(u);
         }
     }
     __device__ __forceinline__ bool next(Unit& u) {
         const uint32_t slot = units & 1, at = bars + kUnitAt + slot * 48;
-        if (!wait(bars + kBarUnitFull + 8 * slot, units >> 1 & 1)) return false;
+        if (!wait_unit(bars + kBarUnitFull + 8 * slot, units >> 1 & 1)) return false;
         uint32_t x[12];
 #pragma unroll
         for (int i = 0; i < 12; i += 4) lds128(at + 4 * i, x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -395,6 +403,7 @@ struct Prefix {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitEmpty + 8 * slot);
         ++units;
+        busy += u.steps;
         return u.steps > 0;
     }
     // Step number of the piece's j-th step, and its tokens.

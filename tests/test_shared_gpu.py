@@ -273,6 +273,26 @@ def test_wait_timeout_sets_the_error_bit_and_the_next_call_is_correct(pda):
         check(pda, c)
 
 
+@pytest.mark.parametrize("kv", [BF16, FP8])
+def test_a_short_wait_limit_is_one_of_single_waits(pda, kv):
+    """Hundreds of row tiles of one piece each: a CTA takes several units of some 0.2 ms, far more than the limit of one wait."""
+    groups, Hk = 120, 4
+    c = Case(kv, Hk, 8, 32, [20000], [groups], [0] * groups, seed=17)
+    d = c.device()
+    d["group_starts"] = torch.arange(groups + 1, dtype=torch.int32, device="cuda")
+    d["prefix_table"] = d["prefix_table"].expand(groups, -1).contiguous()
+    d["prefix_lens"] = torch.full((groups,), 20000, dtype=torch.int32, device="cuda")
+    outs = []
+    for limit in (0, 100000):
+        p2 = pda.shared_plans(groups, groups, Hk, 8, 32, c.MP, c.MB, kv_dtype=kv, prefix_tile_groups=79, wait_timeout_ns=limit)
+        assert p2[0].num_partitions == 1
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        outs.append(pda.decode_shared(*p2, **d, err_word=err))
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+    assert torch.equal(*outs)
+
+
 def test_pool_past_4_gib_and_pinned_query(pda):
     c = Case(BF16, 2, 8, 16, [300], [5], [20] * 5, seed=15)
     d, p2 = c.device(), c.plans(pda)
