@@ -419,13 +419,14 @@ class _Call:
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _scratch(ws: dict, stream) -> dict:
-    """A workspace of the call's own, not handed out again before `stream` has passed the call."""
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        for t in ws.values():
-            t.record_stream(s)
-    return ws
+def _made(make, index: int, stream):
+    """What a call allocates for itself is its stream's: no other stream uses it still, and it comes back in the
+    stream's order."""
+    if stream is None:
+        return make()
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=index)
+    with torch.cuda.stream(s):
+        return make()
 
 
 def copy_blocks(p: Plan, src_cache, src_blocks: int, dst_cache, dst_blocks: int, pairs, err_word=None,
@@ -533,13 +534,13 @@ def decode_selected(p: Plan, query, kv_cache, num_cache_blocks: int, sel_table, 
     c = _Call(kv_cache, "kv_cache")
     B, Hk, QG, D, P = p.num_seqs, p.num_kv_heads, p.query_group_size, p.head_dim, p.num_partitions
     if out is None:
-        out = torch.empty((B, Hk * QG, D), dtype=out_dtype, device=kv_cache.device)
+        out = _made(lambda: torch.empty((B, Hk * QG, D), dtype=out_dtype, device=kv_cache.device), c.index, stream)
     rows = B * Hk * QG
     f32 = out.dtype is torch.float32
     partials = (None, None, None)
     if p.kernel_variant == VARIANT_HEAD_WARPS:
         if ws is None:
-            ws = _scratch(workspace(p, kv_cache.device), stream)
+            ws = _made(lambda: workspace(p, kv_cache.device), c.index, stream)
         partials = (c.ptr(ws["partial_out"], "partial_out", _F32, rows * P * D * 4),
                     c.ptr(ws["exp_sums"], "exp_sums", _F32, rows * P * 4),
                     c.ptr(ws["max_logits"], "max_logits", _F32, rows * P * 4))
@@ -586,9 +587,10 @@ def decode_shared(prefix_plan: Plan, p: Plan, query, kv_cache, num_cache_blocks:
     c = _Call(kv_cache, "kv_cache")
     B, NG = p.num_seqs, prefix_plan.num_seqs
     if ws is None:
-        ws = _scratch({"ws": shared_workspace(prefix_plan, p, kv_cache.device)}, stream)["ws"]
+        ws = _made(lambda: shared_workspace(prefix_plan, p, kv_cache.device), c.index, stream)
     if out is None:
-        out = torch.empty((B, p.num_kv_heads * p.query_group_size, p.head_dim), dtype=out_dtype, device=kv_cache.device)
+        shape = (B, p.num_kv_heads * p.query_group_size, p.head_dim)
+        out = _made(lambda: torch.empty(shape, dtype=out_dtype, device=kv_cache.device), c.index, stream)
     n = B * p.num_kv_heads * p.query_group_size * p.head_dim
     f32 = out.dtype is torch.float32
     args = (p, c.ptr(query, "query", _BF16, n * 2, host_ok=True),

@@ -362,6 +362,27 @@ def test_steps_without_a_pause_share_a_workspace(pda, kv):
             assert torch.equal(outs[r][i], alone[i]), (r, i)
 
 
+@pytest.mark.parametrize("as_int", [False, True])
+def test_what_a_call_allocates_belongs_to_its_stream(pda, as_int):
+    """Calls on a side stream that make their own workspace and output, between allocations of the current stream that are still
+    being written: neither writes the other's memory."""
+    c = Case(BF16, 2, 8, 16, [1200], [20], [30] * 20, seed=18)
+    p2, d = c.plans(pda), c.device()
+    want = check(pda, c)
+    n = pda.lib().pda_shared_workspace_size(*p2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for size in (n, want.nbytes):                        # freed while the current stream writes them
+            x = torch.empty(size, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(200000)
+            x.fill_(0xFF)
+            del x
+        out = pda.decode_shared(*p2, **d, out_dtype=torch.float32, stream=side.cuda_stream if as_int else side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_fork_then_shared_decode(pda):
     """A prompt's sequence is forked into samples that decode with the prompt as their shared prefix: the same as a decode over
     the forked tables."""
