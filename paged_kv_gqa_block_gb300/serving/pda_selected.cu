@@ -13,9 +13,10 @@ namespace pda {
 // that the units need are what the choice weighs against it.  A cluster lies within one group of SMs, so of 152
 // SMs clusters of four CTAs reach 144, and of eight 120 with one CTA per SM (144, 136 with two, three): 16
 // units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and take 8.6 us.  Measured against the partition pass and
-// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.3 us against 16.1, 32 units 10.9 against
-// 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 44 against 63, 1024 units of 8192 287 against 383;
-// only 800 units of 4096 bf16 tokens were slower, 273 against 245.
+// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.0 us against 16.1, 32 units 10.9 against
+// 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 45 against 63, 1024 units of 8192 285 against 383, 800 of
+// 4096 bf16 tokens 179 against 239; only few units of long lists were slower (8 of 65536 fp8 tokens 66 against 60 us:
+// eight clusters of eight CTAs are less than half of the SMs).
 struct Shape {
     int C, nw;
 };
@@ -79,11 +80,14 @@ static int launch_clusters_of(bool behind, const DecodeArgs& a, const CUtensorMa
     return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, OWN>(behind, a, kv_map, sc_map, shape, stream);
 }
 
+// bf16: eight warps per SM with rings of three tiles, where six with four took longer: 512 units of 512 tokens at 16
+// rows 33.5 -> 26.3 us, 16 of 8192 26.0 -> 23.3, 128 sequences of 64 heads with 100 tokens of their own beside a
+// prefix of 32768 104.3 -> 101.9; 800 units of 2048 98.1 -> 99.8 us the other way.
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 4, 6, 6>(false, a, kv_map, kv_map, stream);
-        return launch_clusters_of<false, PDA_KV_BF16, 2, 4, 6, 6>(false, a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 3, 8, 8>(false, a, kv_map, kv_map, stream);
+        return launch_clusters_of<false, PDA_KV_BF16, 2, 3, 8, 8>(false, a, kv_map, kv_map, stream);
     }
     if (kv_dtype == PDA_KV_TQ4) {
         if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_TQ4, 1, 6, 6, 12>(false, a, kv_map, sc_map, stream);
@@ -96,15 +100,15 @@ int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMa
 long long own_clusters_ctas(const pda_plan_t* p, int sms) {
     const long long units = (long long)p->num_seqs * p->num_kv_heads;
     const bool bf16 = p->kv_dtype == PDA_KV_BF16, wide = p->query_group_size > 8;   // as below
-    return units * selected_shape(units, (p->max_blocks_per_seq * p->kv_block_size + 15) / 16, sms, bf16 ? 6 : wide ? 8 : 12,
-                                  !bf16 && wide ? 4 : 6).C;
+    return units * selected_shape(units, (p->max_blocks_per_seq * p->kv_block_size + 15) / 16, sms, bf16 || wide ? 8 : 12,
+                                  bf16 ? 8 : wide ? 4 : 6).C;
 }
 
 int launch_own_clusters(int kv_dtype, bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                         cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 4, 6, 6>(behind, a, kv_map, kv_map, stream);
-        return launch_clusters_of<true, PDA_KV_BF16, 2, 4, 6, 6>(behind, a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
+        return launch_clusters_of<true, PDA_KV_BF16, 2, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
     }
     if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(behind, a, kv_map, sc_map, stream);
     return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(behind, a, kv_map, sc_map, stream);
