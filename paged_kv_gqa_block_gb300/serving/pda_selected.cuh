@@ -8,9 +8,9 @@
 // with the arithmetic and the private copy rings of the head-warp kernel (pda_decode.cuh); each warp
 // leaves (m, l, o), the maximum, the sum of exponentials and the normalised output of its run, in its
 // ring; the CTA joins its warps, w = l 2^(m - M), and the cluster its CTAs through distributed shared
-// memory, each CTA a share of the rows.  Bound by HBM for large batches (512 units of 2048 fp8 tokens 44.4 us, 6.3
+// memory, each CTA a share of the rows.  Bound by HBM for large batches (512 units of 2048 fp8 tokens 45 us, 6.2
 // TB/s) and by the chain of one warp (lengths, table, copies, 0.6 us per two tiles) for small ones (32 units of 2048 bf16
-// tokens 10.9 us, 3.1 TB/s; 8 units 7.3 us).
+// tokens 11.2 us, 3.0 TB/s; 8 units 7.0 us).
 #pragma once
 
 #include <cooperative_groups.h>
