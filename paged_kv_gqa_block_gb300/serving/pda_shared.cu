@@ -370,7 +370,9 @@ struct Prefix {
     // limit is that of their waits, a few per step (long limits, from 0.27 s on, do for any unit).
     __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity) const {
         const uint64_t limit = a.timeout_ns >> 28 ? a.timeout_ns : a.timeout_ns * (64 + 8ull * busy);
-        return wait_on(bar, parity, a.timeout_ns < 1000000ull, limit);
+        const bool poll = a.timeout_ns < 1000000ull;
+        if (__all_sync(kLanes, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) return true;
+        return wait_on(bar, parity, poll, limit);
     }
     __device__ __forceinline__ void put(const Unit& u) const {
         const uint32_t at = bars + kUnitAt + (units & 1) * 48;
@@ -552,15 +554,16 @@ struct Prefix {
         const int t = threadIdx.x - 384, lane = t & 31, x = t & 7;
         const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
         const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4;
-        unsigned r = 0, r_ph = 0, s = 0, s_ph = 1, st = 0, st_ph = 0;   // s_ph 1: the slots start free
+        static_assert(!F16 || Cfg::kRaw == Cfg::kSlots, "a raw slot and its slot are counted together");
+        unsigned s = 0, ph = 0, st = 0, st_ph = 0;
         Unit u;
         while (next(u)) {
             for (int j = 0; j < u.steps; ++j) {
                 const bool zero = t >= tokens_of(u, j);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
-                    if (!wait(bars + kBarRawFull + 8 * r, r_ph)) return;
-                    const uint32_t src = raw0 + r * kRawBytes, dst = slot0 + s * kSlotBytes;
+                    if (!wait(bars + kBarRawFull + 8 * s, ph)) return;
+                    const uint32_t src = raw0 + s * kRawBytes, dst = slot0 + s * kSlotBytes;
                     uint32_t w[8][4];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) lds128(src + ((c ^ x) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
@@ -574,7 +577,7 @@ struct Prefix {
                         }
                     }
                     const uint32_t vs2 = pack_f16(vs, vs);
-                    if (!wait(bars + kBarEmpty + 8 * s, s_ph)) return;
+                    if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;   // the slots start free
                     if (zero) {
 #pragma unroll
                         for (int c = 0; c < 8; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
@@ -595,15 +598,11 @@ struct Prefix {
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bars + kBarFull + 8 * s);
-                        mbar_arrive(bars + kBarRawEmpty + 8 * r);
-                    }
-                    if (++r == Cfg::kRaw) {
-                        r = 0;
-                        r_ph ^= 1;
+                        mbar_arrive(bars + kBarRawEmpty + 8 * s);
                     }
                     if (++s == Cfg::kSlots) {
                         s = 0;
-                        s_ph ^= 1;
+                        ph ^= 1;
                     }
                 }
             }
