@@ -10,13 +10,14 @@
 // Both are two launches, the second a programmatic dependent of the first:
 //   1. a scan by one thread-block cluster (kScanCtas CTAs of 1024 threads; one CTA for a small
 //      pool): every CTA counts its slice of the counts, the totals are exchanged through
-//      distributed shared memory, and a second sweep over the slice (now in L1) gives each free or
-//      used block its rank.  One launch in place of count / prefix / write;
+//      distributed shared memory, and each free or used block gets its rank (slices of up to 4096 counts
+//      from the registers, longer ones in a second sweep, now in L1: 6.1 -> 5.7 and 9.5 -> 9.2 us for the forks
+//      below).  One launch in place of count / prefix / write;
 //   2. a grid over the table segments and the 4 KB chunks of the blocks to copy.
 // What bounds them: the copies HBM (read + write), everything else launch and load latency.  Measured: 2048
 // blocks of 64 KB copied in 44.0 us (6.1 TB/s, read and written; under counters 39 us); 4 sequences forked from two
-// parents 6.0 us, 64 from 16 parents of up to 16000 tokens in a pool of 16384 blocks 9.6 us (the second launch 7.3
-// us under counters); a pool of 8192 blocks of 64 KB compacted in 49.4 us, of which the copies are 38 us (246 MB
+// parents 5.7 us, 64 from 16 parents of up to 16000 tokens in a pool of 16384 blocks 9.2 us (the second launch 7.3
+// us under counters); a pool of 8192 blocks of 64 KB compacted in 49.6 us, of which the copies are 38 us (246 MB
 // read and written, 6.4 TB/s) and the rest the scan in front of them.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -149,33 +150,33 @@ __device__ __forceinline__ void slice_of(const cg::cluster_group& cl, long long 
     hi = min(NB, lo + per);
 }
 
-// Counts the entries of this CTA's slice for which `f` holds; returns how many there are before the
-// slice, and their number in the pool.
+// The entries of this CTA's slice for which `f` holds are counted: `before` are those ahead of the slice, `total` those of
+// the pool.  A slice of one tile is not read again: the thread keeps its four entries, their count and the
+// inclusive sum over the threads.  The caller syncs the cluster once more (the totals are read from the other CTAs).
+struct Count {
+    int before, total, r[4], n, incl;
+};
 template <class F>
-__device__ __forceinline__ int count_before(const cg::cluster_group& cl, const int* refs, long long lo, long long hi,
-                                            int* tmp, int* share, int& total, F f) {
-    int n = 0;
+__device__ __forceinline__ Count count_slice(const cg::cluster_group& cl, const int* refs, long long lo, long long hi,
+                                             int none, int* tmp, int* share, F f) {
+    Count c = {0, 0, {none, none, none, none}, 0, 0};
     for (long long t0 = lo + 4 * threadIdx.x; t0 < hi; t0 += kScanTile)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (t0 + u < hi) n += f(__ldg(refs + t0 + u));
-    int sum;
-    block_scan(n, tmp, sum);
-    if (cl.num_blocks() == 1) {
-        total = sum;
-        return 0;
-    }
-    if (threadIdx.x == 0) *share = sum;
+        for (int u = 0; u < 4; ++u) {
+            c.r[u] = t0 + u < hi ? __ldg(refs + t0 + u) : none;
+            c.n += f(c.r[u]);
+        }
+    c.incl = block_scan(c.n, tmp, c.total);
+    if (cl.num_blocks() == 1) return c;
+    if (threadIdx.x == 0) *share = c.total;
     cl.sync();
-    int before = 0;
-    total = 0;
+    c.total = 0;
     for (unsigned r = 0; r < cl.num_blocks(); ++r) {
         const int v = *cl.map_shared_rank(share, r);
-        if (r < cl.block_rank()) before += v;
-        total += v;
+        if (r < cl.block_rank()) c.before += v;
+        c.total += v;
     }
-    cl.sync();   // nobody leaves with a count still to be read
-    return before;
+    return c;
 }
 
 // What a new row asks for.
@@ -233,18 +234,24 @@ __global__ void __launch_bounds__(kScanThreads) pda_fork_scan_kernel(const ScanA
     }
     long long lo, hi;
     slice_of(cl, a.NB, lo, hi);
-    int nfree;
-    int at = count_before(cl, a.refs, lo, hi, tmp, &share, nfree, [](int r) { return r == 0 ? 1 : 0; });
+    const bool one = hi - lo <= kScanTile;
+    Count q = count_slice(cl, a.refs, lo, hi, 1, tmp, &share, [](int r) { return r == 0 ? 1 : 0; });
+    const int nfree = q.total;
+    int at = q.before;
     for (long long t0 = lo; t0 < hi; t0 += kScanTile) {
         const long long i = t0 + 4 * threadIdx.x;
-        int r[4], c = 0;
+        int (&r)[4] = q.r;
+        int n = 0;
+        if (!one) {
+            q.n = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            r[u] = i + u < hi ? __ldg(a.refs + i + u) : 1;
-            c += r[u] == 0;
+            for (int u = 0; u < 4; ++u) {
+                r[u] = i + u < hi ? __ldg(a.refs + i + u) : 1;
+                q.n += r[u] == 0;
+            }
+            q.incl = block_scan(q.n, tmp, n);
         }
-        int n;
-        int k = at + block_scan(c, tmp, n) - c;
+        int k = at + q.incl - q.n;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (i + u < hi) a.out_refs[i + u] = r[u];
@@ -252,6 +259,7 @@ __global__ void __launch_bounds__(kScanThreads) pda_fork_scan_kernel(const ScanA
         }
         at += n;
     }
+    if (cl.num_blocks() > 1) cl.sync();   // nobody leaves with a total still to be read
     if (!rows_here) return;
     // which row is the first of its parent, what each has to get, and where its blocks start in the
     // list of free ones
@@ -388,19 +396,25 @@ __global__ void __launch_bounds__(kScanThreads) pda_compact_scan_kernel(const Sc
     cg::cluster_group cl = cg::this_cluster();
     long long lo, hi;
     slice_of(cl, a.NB, lo, hi);
-    int U;
-    int at = count_before(cl, a.refs, lo, hi, tmp, &share, U, [](int r) { return r > 0 ? 1 : 0; });
+    const bool one = hi - lo <= kScanTile;
+    Count q = count_slice(cl, a.refs, lo, hi, 0, tmp, &share, [](int r) { return r > 0 ? 1 : 0; });
+    const int U = q.total;
+    int at = q.before;
     if (U == 0 && cl.block_rank() == 0 && threadIdx.x == 0) a.scalars[0] = a.scalars[1] = 0;
     for (long long t0 = lo; t0 < hi; t0 += kScanTile) {
         const long long i = t0 + 4 * threadIdx.x;
-        int r[4], c = 0;
+        int (&r)[4] = q.r;
+        int n = 0;
+        if (!one) {
+            q.n = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            r[u] = i + u < hi ? __ldg(a.refs + i + u) : 0;
-            c += r[u] > 0;
+            for (int u = 0; u < 4; ++u) {
+                r[u] = i + u < hi ? __ldg(a.refs + i + u) : 0;
+                q.n += r[u] > 0;
+            }
+            q.incl = block_scan(q.n, tmp, n);
         }
-        int n;
-        int k = at + block_scan(c, tmp, n) - c;   // used blocks before this one
+        int k = at + q.incl - q.n;   // used blocks before this one
         at += n;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
