@@ -384,10 +384,13 @@ class _Call:
         self.index = t.get_device()
 
     def ptr(self, t, name: str, dtype, nbytes: int, host_ok: bool = False):
-        # the common case in one line: a step of many short kernels waits for this code
-        if (isinstance(t, torch.Tensor) and t.get_device() == self.index and (dtype is None or t.dtype in dtype)
-                and t.is_contiguous() and t.nbytes >= nbytes):
-            return t.data_ptr()
+        # the common case first and short: a step of many short kernels waits for this code
+        try:
+            if (t.get_device() == self.index and (dtype is None or t.dtype in dtype) and t.is_contiguous()
+                    and t.nbytes >= nbytes):
+                return t.data_ptr()
+        except AttributeError:   # no tensor
+            pass
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.get_device() != self.index and not (host_ok and t.device.type == "cpu" and t.is_pinned()):
@@ -405,7 +408,7 @@ class _Call:
 
     def run(self, what: str, fn, p: Plan, args: tuple, err_word, stream) -> None:
         err = None if err_word is None else self.ptr(err_word, "err_word", _I32, 4)
-        if torch.cuda.current_device() == self.index:
+        if torch._C._cuda_getDevice() == self.index:
             rc = fn(p, *args, err, self._stream(stream))
         else:
             with torch.cuda.device(self.index):
