@@ -198,7 +198,7 @@ __device__ inline void merge_unit_smem(const MergeArgs& r, int b, int h, int ctx
     float coef = 0.f;
     bool ok = true;
     for (int k = 0; k < nch; ++k) {
-        if (!mbar_wait(full0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), kDefaultTimeoutNs)) {
+        if (!mbar_wait_warp(full0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), kDefaultTimeoutNs)) {
             ok = false;
             break;
         }
@@ -232,10 +232,10 @@ __device__ inline void merge_unit_smem(const MergeArgs& r, int b, int h, int ctx
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * (k & 1));
-        if (threadIdx.x == 0 && k + 2 < nch) {   // refill this buffer once every row is done with it
-            if (!mbar_wait(empty0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), kDefaultTimeoutNs)) {
+        if (threadIdx.x < 32 && k + 2 < nch) {   // warp 0 refills this buffer once every row is done with it
+            if (!mbar_wait_warp(empty0 + 8 * (k & 1), (uint32_t)((k >> 1) & 1), kDefaultTimeoutNs)) {
                 ok = false;
-            } else {
+            } else if (lane == 0) {
                 issue(k + 2);
                 ++issued;
             }

@@ -76,6 +76,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
     return true;
 }
+// The same for a whole (convergent) warp: every lane sees the phase complete, or all give up.  Each lane reads the
+// timer for itself, so near the limit lanes of mbar_wait can disagree; a warp whose next step is a product or a
+// shuffle of all lanes must not part there.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    constexpr uint32_t kAllLanes = 0xFFFFFFFFu;
+    const bool poll = limit_ns < 1000000ull;
+    if (__all_sync(kAllLanes, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        const bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(kAllLanes, ok)) return true;
+        if (__any_sync(kAllLanes, global_timer_ns() - t0 > limit_ns)) return false;
+    }
+}
 
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void prefetch_tensormap(const void* tmap) {

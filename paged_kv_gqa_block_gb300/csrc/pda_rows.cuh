@@ -56,7 +56,7 @@ struct RowsDecode {
                                    unsigned long long timeout) {
         const int slot = (int)(i % R);
         const long long n = i / R;
-        if (n > 0 && !mbar_wait(m.uempty0 + 8 * slot, (uint32_t)((n - 1) & 1), timeout)) {
+        if (n > 0 && !mbar_wait_warp(m.uempty0 + 8 * slot, (uint32_t)((n - 1) & 1), timeout)) {
             ok = false;
             return;
         }
@@ -100,7 +100,7 @@ struct RowsDecode {
                 const int phys = __shfl_sync(kFull, ent, e & 31);
                 const int st = (int)(issued % S);
                 const long long n = issued / S;
-                if (n > 0 && !mbar_wait(m.empty0 + 8 * st, (uint32_t)((n - 1) & 1), a.timeout_ns)) {
+                if (n > 0 && !mbar_wait_warp(m.empty0 + 8 * st, (uint32_t)((n - 1) & 1), a.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -145,7 +145,7 @@ struct RowsDecode {
         u.valid = false;
         u.b = u.g = u.p = u.ctx = 0;
         const int slot = (int)(i % R);
-        if (!mbar_wait(m.ufull0 + 8 * slot, (uint32_t)((i / R) & 1), timeout)) {
+        if (!mbar_wait_warp(m.ufull0 + 8 * slot, (uint32_t)((i / R) & 1), timeout)) {
             ok = false;
             return u;
         }
@@ -209,8 +209,8 @@ struct RowsDecode {
                 const uint32_t ph0 = cph;
                 const int s1 = s0 + 1 == S ? 0 : s0 + 1;
                 const uint32_t ph1 = s0 + 1 == S ? cph ^ 1u : cph;
-                if (!mbar_wait(m.full0 + 8 * s0, ph0, a.timeout_ns) ||
-                    (two && !mbar_wait(m.full0 + 8 * s1, ph1, a.timeout_ns))) {
+                if (!mbar_wait_warp(m.full0 + 8 * s0, ph0, a.timeout_ns) ||
+                    (two && !mbar_wait_warp(m.full0 + 8 * s1, ph1, a.timeout_ns))) {
                     ok = false;
                     break;
                 }

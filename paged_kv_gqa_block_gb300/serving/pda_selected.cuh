@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             const bool two = t + 1 < t1;
             const int s0 = cs, s1 = s0 + 1 == S ? 0 : s0 + 1;
             const uint32_t ph0 = cph, ph1 = s0 + 1 == S ? cph ^ 1u : cph;
-            if (!mbar_wait(bar0 + 8 * s0, ph0, a.timeout_ns) || (two && !mbar_wait(bar0 + 8 * s1, ph1, a.timeout_ns))) {
+            if (!mbar_wait_warp(bar0 + 8 * s0, ph0, a.timeout_ns) || (two && !mbar_wait_warp(bar0 + 8 * s1, ph1, a.timeout_ns))) {
                 ok = false;
                 break;
             }
