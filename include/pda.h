@@ -451,9 +451,12 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  *   block_table, context_lens   device, the sequences' own blocks and lengths (0: prefix only)
  *   workspace      device, pda_shared_workspace_size bytes, 32-byte aligned
  *   query, out, out_dtype as for pda_decode and pda_reduce (query and out may be pinned host memory)
- * The weights of the prefix part are rounded to bf16 (bf16 KV), or they and the scaled V to f16 (fp8 KV), before
- * their product, so an fp32 out carries that rounding (at most 2^-8, or 3 * 2^-11, of each term; fp8 tokens whose
- * V scale is below 2^-15 of the largest among the prefix's aligned 128 tokens around them lose further bits of it).
+ * The weights of the prefix part are rounded to bf16 (bf16 KV), or they, V's scale and the scaled V to f16 (fp8 KV),
+ * before their product, so an fp32 out carries that rounding: at most 2^-8, or 3 * 2^-11, of each term.  With fp8 KV
+ * a weight below 2^-21 of its row's largest is off by at most 2^-32 of that one instead; and of the prefix's aligned
+ * 128 tokens, with f the largest V scale among them, one whose scale is below 2^-15 f has that scale off by up to
+ * 2^-26 f, and an element of V below 2^-15 f is off by up to 2^-26 f.  pda_decode rounds less (bf16 KV: weights to
+ * 2^-16; fp8 KV: once to f16): moving a batch here from there changes an fp32 out by this much.
  * Data errors: a prefix length out of range counts as 0 (PDA_ERRW_BAD_CONTEXT_LEN); group_starts that are not
  * ascending within [0, num_seqs] set PDA_ERRW_BAD_GROUP, and the step runs without prefixes; block ids as
  * for pda_decode.

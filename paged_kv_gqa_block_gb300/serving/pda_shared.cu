@@ -3,8 +3,8 @@
 // For query row r of sequence b in group g,
 //   out = softmax(scale [q.K_g ; q.K_b]) [V_g ; V_b],
 // with K_g, V_g the group's prefix and K_b, V_b the sequence's own tokens.  The two parts are
-// computed apart as (m, l, o), the running maximum, the sum of exponentials and the normalised
-// output, and joined: w = l e^(m - M), out = sum w o / sum w.  The own part is the cluster kernel of
+// computed apart as (m, l, o), a reference near the maximum, the sum of exponentials from it and the normalised
+// output, and joined: w = l e^(m - M), out = sum w o / sum w, M the largest m.  The own part is the cluster kernel of
 // pda_selected.cuh.  The prefix part is one matrix product per group and KV head for the
 // query rows of all its sequences, n_g * QG of them, and this file's first kernel.
 //
@@ -26,7 +26,10 @@
 // TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
 // P is announced in halves, so that PV starts while the second half is computed.
 // P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11; V carries two more such
-// roundings, see the conversion); m, l, S and O are fp32.
+// roundings, see the conversion); m, l, S and O are fp32.  f16 has few exponents: below 2^-14 a value loses bits, and
+// below 2^-25 it is zero, while l counts it; a long even prefix behind one large weight would lose a share of the
+// output.  So with f16 the reference is 7 below the maximum: with the 8 of its lazy move P still ends at 2^15, weights
+// keep their 11 bits down to 2^-21 of the largest, and smaller ones are off by at most 2^-32 of it.
 //
 // Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
 // row tile) are laid end to end and every CTA takes an equal run; a row tile that is cut leaves one
@@ -64,7 +67,8 @@ constexpr int kRawBytes = 16384;           // the same in 8 bits
 constexpr int kScaleBytes = 1024;          // 128 tokens x {K scale, V scale}
 constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
 constexpr int kSwitch = 3;                 // what a change of row tiles costs a CTA, in steps
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f;               // log2 units that a row's maximum may rise before its reference follows
+constexpr float kBelow = 7.f;              // f16 P: the reference below the maximum
 
 struct SharedArgs {
     const uint16_t* query;       // bf16 [B][Hk*QG][D]
@@ -806,7 +810,8 @@ struct Prefix {
         Unit u;
         while (next(u)) {
             const Rows w = start_unit(u, tile, r);
-            float m = 0.f, l = 0.f, F = 1.f;
+            constexpr float below = F16 ? kBelow : 0.f;
+            float m = 0.f, l = 0.f, F = 1.f;   // m: the reference, which l and O count from
             for (int j = 0; j < u.steps; ++j, ++step) {
                 const int valid = tokens_of(u, j);
                 const unsigned st = step % Cfg::kScales;
@@ -851,15 +856,15 @@ struct Prefix {
                     float nF = 1.f;
                     if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
                     if (j == 0) {
-                        m = top;
+                        m = top - below;
                     } else {
-                        const bool up = top > m + kLazy;
+                        const bool up = top > m + (kLazy + below);
                         if (__any_sync(kLanes, up || nF != F)) {
                             float f = F / nF;
                             if (nF == F) f = 1.f;
                             if (up) {
-                                const float e = ex2(m - top);
-                                m = top;
+                                const float e = ex2(m - (top - below));
+                                m = top - below;
                                 l *= e;
                                 f *= e;
                             }
