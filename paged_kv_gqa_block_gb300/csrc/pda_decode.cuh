@@ -329,6 +329,7 @@ struct Decode {
     // Raw words of the unit's Q rows as this lane needs them (rows >= QG read as zero).
     //   bf16: w[n][2kk + j] = Q[8n + gid][16kk + 8j + 2tig .. +1]  (the mma B fragments)
     //   fp8, TQ4: w[n][c]   = Q[8n + gid][32tig + 2c .. +1]         (converted at unit start)
+    template <bool L2 = false>
     static __device__ __forceinline__ void load_q(const DecodeArgs& a, const UnitIt& u, uint32_t (&w)[NT][16],
                                                   int lane) {
         const int gid = lane >> 2, tig = lane & 3;
@@ -342,7 +343,7 @@ struct Decode {
                     const uint4* p4 = reinterpret_cast<const uint4*>(row + tig * 16);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint4 v = __ldg(p4 + c);
+                        const uint4 v = load_input<L2>(p4 + c);
                         w[n][4 * c] = v.x;
                         w[n][4 * c + 1] = v.y;
                         w[n][4 * c + 2] = v.z;
@@ -351,8 +352,8 @@ struct Decode {
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
-                        w[n][2 * kk] = __ldg(row + kk * 8 + tig);
-                        w[n][2 * kk + 1] = __ldg(row + kk * 8 + 4 + tig);
+                        w[n][2 * kk] = load_input<L2>(row + kk * 8 + tig);
+                        w[n][2 * kk + 1] = load_input<L2>(row + kk * 8 + 4 + tig);
                     }
                 }
             } else {

@@ -242,6 +242,13 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// One of the caller's inputs: read-only and cached, or (L2) past L1, for a grid that reads before its own dependency wait.
+template <bool L2, class T>
+__device__ __forceinline__ T load_input(const T* p) {
+    if constexpr (L2) return __ldcg(p);
+    return __ldg(p);
+}
+
 // Programmatic dependent launch: wait until the preceding grid on the stream has completed and
 // its memory is visible (returns at once when the launch had no programmatic dependency) ...
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

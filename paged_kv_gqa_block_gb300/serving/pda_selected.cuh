@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     __syncwarp();
     // Own tokens and the prefix pass read nothing of one another's.  The first of the two waits for everything
     // before them and then lets the other start; the second waits for the first before it ends (one CTA of it: the
-    // others make room), so that the join waits for both.
+    // others make room), so that the join waits for both.  The second has not waited when it reads the step's inputs:
+    // they lie in L2 by then, and it reads them there (ld.cg, TMA), past any line that an earlier grid left in L1.
     if constexpr (!OWN) allow_dependent_launch();
     if (!OWN || !behind) grid_dependency_wait();
     if constexpr (OWN) allow_dependent_launch();
@@ -113,12 +114,12 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     int t0, t1;
     run_of(max_ctx >> 4, t0, t1);
     int e0 = t0 >> ts;
-    int ent = e0 + lane < a.MB ? __ldg(table + e0 + lane) : 0;
-    const int raw = __ldg(a.context_lens + list);
+    int ent = e0 + lane < a.MB ? load_input<OWN>(table + e0 + lane) : 0;
+    const int raw = load_input<OWN>(a.context_lens + list);
     uint32_t qn[NT][16];
     {
         UnitIt u = {unit, 0, 0, 0, 0, 0};
-        D::load_q(a, u, qn, lane);
+        D::template load_q<OWN>(a, u, qn, lane);
     }
     if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!OWN || head == 0) && a.err_word)
         atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
@@ -133,14 +134,14 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         const int entries = ((t1 - 1) >> ts) + 1;
         if (e0 != t0 >> ts) {
             e0 = t0 >> ts;
-            ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
+            ent = e0 + lane < entries ? load_input<OWN>(table + e0 + lane) : 0;
         }
         const uint64_t policy = l2_policy_evict_first();
         int issued = 0;
         auto issue = [&](int t, int stage) {   // tiles in order
             if ((t >> ts) - e0 >= 32) {
                 e0 += 32;
-                ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
+                ent = e0 + lane < entries ? load_input<OWN>(table + e0 + lane) : 0;
             }
             const int phys = __shfl_sync(kFull, ent, (t >> ts) - e0);
             if (lane == 0) {

@@ -142,8 +142,8 @@ struct Group {
 __device__ __forceinline__ Group group_shape(const SharedArgs& a, int g, int& bad) {
     Group x = {};
     if (g >= a.NG) return x;
-    const int s0 = __ldg(a.group_starts + g), s1 = __ldg(a.group_starts + g + 1);
-    x.len = __ldg(a.prefix_lens + g);
+    const int s0 = __ldcg(a.group_starts + g), s1 = __ldcg(a.group_starts + g + 1);
+    x.len = __ldcg(a.prefix_lens + g);
     if (x.len < 0 || x.len > a.MP * a.BS) {
         bad |= PDA_ERRW_BAD_CONTEXT_LEN;
         x.len = 0;
@@ -447,14 +447,14 @@ struct Prefix {
             const int last = (u.len + a.BS - 1) / a.BS;   // blocks of the prefix
             int id = 0;
             int b0 = step_of(u, 0) * nblk;
-            if (blk < nblk && b0 + blk < last) id = __ldg(table + b0 + blk);
+            if (blk < nblk && b0 + blk < last) id = __ldcg(table + b0 + blk);
             for (int j = 0; ok && j < u.steps; ++j, ++step) {
                 const int n = min(nblk, last - b0);
                 const bool mine = blk < n;
                 int nid = 0, b1 = 0;
                 if (j + 1 < u.steps) {
                     b1 = step_of(u, j + 1) * nblk;
-                    if (blk < nblk && b1 + blk < last) nid = __ldg(table + b1 + blk);
+                    if (blk < nblk && b1 + blk < last) nid = __ldcg(table + b1 + blk);
                 }
                 if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
                     atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
@@ -1012,8 +1012,10 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
         prefetch_tensormap(&kv_map);
         if (Cfg::kF16) prefetch_tensormap(&sc_map);
     }
-    // Behind the pass over the sequences' own tokens no wait for it here: it lets this one start only after
-    // everything before it has ended, and nothing of it is read.
+    // Behind the pass over the sequences' own tokens there is no wait for it here: every CTA of that pass has waited for
+    // everything before the step before it lets this grid start, and nothing of its own is read.  What was written
+    // before the step lies in L2 then, and every read of it in this grid goes there (ld.cg, cp.async.cg, TMA): a line
+    // that an earlier grid left in this SM's L1 is not looked at.
     if (a.first) grid_dependency_wait();
     Prefix<KV> p(a, sm);
     Split split;
