@@ -297,6 +297,16 @@ PDA_API int pda_kernel_variant(const pda_plan_t* plan);
  * ceil(context_lens[b] / kv_block_size) entries of its table row.  The plan gives the block size
  * in bytes (any kv_dtype), num_seqs, max_blocks_per_seq and kv_block_size.
  *
+ * A call moves the blocks of the pool it is given, and nothing else that block ids index:
+ *   - Other pools under the same tables (one per layer of a model).  After a fork they need the same copies: for each
+ *     new row i whose parent p's length L is no multiple of kv_block_size, the pair (block_table[p][j],
+ *     out_table[i][j]) with j = L / kv_block_size, where the two differ.  After a compaction: the pairs
+ *     (id, remap[id]) for every id.  Both by pda_copy_blocks within each pool.
+ *   - Block summaries (pda_summarize_blocks).  After a compaction or a copy the rows of moved blocks have to be moved
+ *     by the same pairs, or renewed (pda_summarize_blocks with since NULL and the new tables); until then
+ *     pda_score_blocks reads what the id stood for before, without an error bit.  After a fork a copied block's row is
+ *     renewed by the call that follows the next append; before that, by since[i] = out_lens[i] - 1.
+ *
  * pda_copy_blocks: block pairs[2i] of src_cache to block pairs[2i+1] of dst_cache, whole
  * (data and metadata region), for i < num_pairs.
  *   src_cache, dst_cache   device memory, or pinned host memory that the device can address (a
@@ -368,7 +378,8 @@ PDA_API int pda_compact_blocks(const pda_plan_t* plan, void* kv_cache, long long
  *
  * A summary holds, per KV head, the largest and the smallest value of each key dimension over the
  * block's tokens: bf16 [num_cache_blocks][num_kv_heads][2: max, min][128], rounded outwards (bf16
- * keys exactly), pda_summary_size bytes, 16-byte aligned.  Keys must be finite.
+ * keys exactly), pda_summary_size bytes, 16-byte aligned.  Keys must be finite.  Rows belong to block ids: the page
+ * operators move blocks, not summaries (see there).
  */
 PDA_API long long pda_summary_size(const pda_plan_t* plan, long long num_cache_blocks);
 
@@ -388,7 +399,7 @@ PDA_API int pda_summarize_blocks(const pda_plan_t* plan, const void* kv_cache, l
 /*
  * pda_score_blocks -- scores[b][h][j] = softmax_scale * max over the query rows r of KV head h of
  *   sum_d max(q_rd, 0) * kmax_d + min(q_rd, 0) * kmin_d,
- * an upper bound of every logit of block j.  scores: device, fp32 [num_seqs][num_kv_heads]
+ * an upper bound of every logit of block j, but for the rounding of the fp32 sums.  scores: device, fp32 [num_seqs][num_kv_heads]
  * [max_blocks_per_seq]; entries past the context are left as they are.  A block id outside the pool
  * scores -inf (PDA_ERRW_BAD_BLOCK_ID).  query as for pda_decode, in device memory.
  */

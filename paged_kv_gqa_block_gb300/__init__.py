@@ -458,7 +458,8 @@ def page_workspace(p: Plan, num_rows: int, num_cache_blocks: int, device):
 def fork_sequences(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, refcounts, parents, out_table,
                    out_lens, out_refcounts, workspace, new_tokens=None, err_word=None, stream=None) -> None:
     """pda_fork_sequences: row i of the new batch is old sequence parents[i] grown by new_tokens[i]
-    positions; sequences that no row names are freed (see include/pda.h).  parents: int32 [R];
+    positions; sequences that no row names are freed (see include/pda.h, also for what a model's other pools and
+    block summaries need).  parents: int32 [R];
     out_table: int32 [R][max_blocks_per_seq]; workspace: page_workspace(p, R, ...) or larger."""
     c = _Call(kv_cache, "kv_cache")
     B, MB, NB, R = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks, parents.numel()
@@ -473,7 +474,8 @@ def fork_sequences(p: Plan, kv_cache, num_cache_blocks: int, block_table, contex
 
 def compact_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, refcounts, out_table,
                    out_refcounts, remap, num_used, workspace, err_word=None, stream=None) -> None:
-    """pda_compact_blocks: moves the blocks in use to the low end of the pool (see include/pda.h)."""
+    """pda_compact_blocks: moves the blocks in use to the low end of the pool (see include/pda.h).  Block summaries and other
+    pools under the same tables are not moved: copy_blocks with the pairs (id, remap[id]), summaries[remap] = summaries."""
     c = _Call(kv_cache, "kv_cache")
     B, MB, NB = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks
     args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,
