@@ -426,7 +426,8 @@ PDA_API int pda_select_blocks(const pda_plan_t* plan, const float* scores, const
  * pda_decode_selected -- a decode step over selected blocks, with one table row and one length per
  * (sequence, KV head), in one launch: each (sequence, KV head) is split over the warps of a thread-block
  * cluster and joined in its shared memory.  With kernel_variant head warps it is the partition pass and the
- * reduce instead, whose partials are those of pda_decode over the same lists.
+ * reduce instead, whose partials are those of pda_decode over the same lists.  That form is slower but for few units
+ * of long lists (8 units of 65536 fp8 tokens 61 us against 66): a unit's cluster is at most eight SMs.
  *   plan        as for pda_decode, with max_blocks_per_seq = num_select (kernel_variant automatic or
  *               head warps, else PDA_ERR_UNSUPPORTED)
  *   centroids   device, fp32 [16] for a TQ4 plan, else NULL
@@ -447,7 +448,9 @@ PDA_API int pda_decode_selected(const pda_plan_t* plan, const void* query, const
  * group_starts[g] .. group_starts[g+1]-1 attend over the first prefix_lens[g] tokens of group g's blocks and then
  * over the context_lens[b] tokens of their own.  The prefix is read once for all of a group's query rows
  * (tensor-core products over 256 rows at a time) instead of once per sequence; out equals a decode over
- * the concatenation.
+ * the concatenation.  It pays where a prefix is shared and is the larger part.  Own tokens of one (sequence, KV head)
+ * run on at most eight SMs, and fp8 prefixes are converted whatever the rows, so groups of one sequence, and few
+ * sequences with thousands of tokens of their own, are better served by pda_decode over concatenated tables.
  *   prefix_plan    num_seqs = groups (>= 1), max_blocks_per_seq = row length of prefix_table, and
  *                  tile_groups_per_partition (pda_shared_tile_groups gives a good one): a prefix is cut into at
  *                  most num_partitions + 1 pieces.  kernel_variant is not looked at.

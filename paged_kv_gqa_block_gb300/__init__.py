@@ -475,7 +475,7 @@ def fork_sequences(p: Plan, kv_cache, num_cache_blocks: int, block_table, contex
 def compact_blocks(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, refcounts, out_table,
                    out_refcounts, remap, num_used, workspace, err_word=None, stream=None) -> None:
     """pda_compact_blocks: moves the blocks in use to the low end of the pool (see include/pda.h).  Block summaries and other
-    pools under the same tables are not moved: copy_blocks with the pairs (id, remap[id]), summaries[remap] = summaries."""
+    pools under the same tables are not moved: copy_blocks with the pairs (id, remap[id]); summaries[remap[used]] = summaries[used] with used = remap >= 0."""
     c = _Call(kv_cache, "kv_cache")
     B, MB, NB = p.num_seqs, p.max_blocks_per_seq, num_cache_blocks
     args = (c.ptr(kv_cache, "kv_cache", None, NB * p.cache_block_bytes), NB,

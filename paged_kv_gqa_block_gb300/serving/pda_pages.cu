@@ -15,10 +15,11 @@
 //      below).  One launch in place of count / prefix / write;
 //   2. a grid over the table segments and the 4 KB chunks of the blocks to copy.
 // What bounds them: the copies HBM (read + write), everything else launch and load latency.  Measured: 2048
-// blocks of 64 KB copied in 44.0 us (6.1 TB/s, read and written; under counters 39 us); 4 sequences forked from two
-// parents 5.7 us, 64 from 16 parents of up to 16000 tokens in a pool of 16384 blocks 9.2 us (the second launch 7.3
-// us under counters); a pool of 8192 blocks of 64 KB compacted in 49.6 us, of which the copies are 38 us (246 MB
-// read and written, 6.4 TB/s) and the rest the scan in front of them.
+// blocks of 64 KB copied in 44.4 us (6.0 TB/s, read and written; under counters 39 us), to pinned host memory in 695 and
+// from it in 638 us (193 and 210 GB/s, what one plain copy of as many bytes takes); 4 sequences forked from two
+// parents 5.7 us, 64 from 16 parents of up to 16000 tokens in a pool of 16384 blocks 9.3 us (the second launch 7.5
+// us under counters); a pool of 8192 blocks of 64 KB compacted in 49.5 us, of which the copies are 39 us (246 MB
+// read and written, 6.3 TB/s) and the rest the scan in front of them.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

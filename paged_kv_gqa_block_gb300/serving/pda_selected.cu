@@ -12,11 +12,12 @@ namespace pda {
 // round of CTAs takes a warp's run, and 6 for its start and its join, 3 more for a cluster's join; the rounds
 // that the units need are what the choice weighs against it.  A cluster lies within one group of SMs, so of 152
 // SMs clusters of four CTAs reach 144, and of eight 120 with one CTA per SM (144, 136 with two, three): 16
-// units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and take 8.6 us.  Measured against the partition pass and
-// reduce (kernel_variant head warps): 8 units of 2048 bf16 tokens 7.0 us against 16.1, 32 units 10.9 against
-// 16.2, 256 units of 2048 fp8 tokens 22 against 42, 512 units 45 against 63, 1024 units of 8192 285 against 383, 800 of
-// 4096 bf16 tokens 179 against 239; only few units of long lists were slower (8 of 65536 fp8 tokens 66 against 60 us:
-// eight clusters of eight CTAs are less than half of the SMs).
+// units of 2048 bf16 tokens took 13.7 us in two rounds of eight, and 8.7 us by this rule.  Measured against the partition
+// pass and reduce (kernel_variant head warps), every list of blocks of its own and none in L2: 8 units of 2048 bf16
+// tokens 7.7 us against 15.7, 32 units 11.5 against 16.4, 256 units of 2048 fp8 tokens 26.7 against 43.6, 512 units 47.8
+// against 64.5, 1024 units of 8192 347 against 392, 800 of 4096 bf16 tokens 245 against 295, 512 of 2048 TQ4 tokens 53
+// against 74; only few units of long lists were slower (8 of 65536 fp8 tokens 66 against 61 us, one of them 64 against
+// 60: a unit is one cluster, and eight clusters of eight CTAs are less than half of the SMs).
 struct Shape {
     int C, nw;
 };
@@ -82,7 +83,8 @@ static int launch_clusters_of(bool behind, const DecodeArgs& a, const CUtensorMa
 
 // bf16: eight warps per SM with rings of three tiles, where six with four took longer: 512 units of 512 tokens at 16
 // rows 33.5 -> 26.3 us, 16 of 8192 26.0 -> 23.3, 128 sequences of 64 heads with 100 tokens of their own beside a
-// prefix of 32768 104.3 -> 101.9; 800 units of 2048 98.1 -> 99.8 us the other way.
+// prefix of 32768 104.3 -> 101.9; 800 units of 2048 98.1 -> 99.8 us the other way (lists drawn from one pool, whose
+// blocks units share in L2; of their own blocks the 800 take 128.5 us).
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {

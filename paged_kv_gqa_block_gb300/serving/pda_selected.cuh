@@ -8,9 +8,10 @@
 // with the arithmetic and the private copy rings of the head-warp kernel (pda_decode.cuh); each warp
 // leaves (m, l, o), the maximum, the sum of exponentials and the normalised output of its run, in its
 // ring; the CTA joins its warps, w = l 2^(m - M), and the cluster its CTAs through distributed shared
-// memory, each CTA a share of the rows.  Bound by HBM for large batches (512 units of 2048 fp8 tokens 45 us, 6.2
-// TB/s) and by the chain of one warp (lengths, table, copies, 0.6 us per two tiles) for small ones (32 units of 2048 bf16
-// tokens 11.2 us, 3.0 TB/s; 8 units 7.0 us).
+// memory, each CTA a share of the rows.  Bound by HBM for large batches (lists of
+// blocks of their own: 800 units of 4096 bf16 tokens 245 us, 6.9 TB/s; 512 of 2048 fp8 tokens 47.8 us, 5.8 TB/s, of
+// which the last, uneven round of units is a part) and by the chain of one warp (lengths, table, copies, 0.6 us per two
+// tiles) for small ones (32 units of 2048 bf16 tokens 11.5 us, 2.9 TB/s; 8 units 7.7 us).
 #pragma once
 
 #include <cooperative_groups.h>

@@ -38,13 +38,14 @@
 // Nothing depends on how lengths and groups fall.  Bound by the tensor cores
 // where a group has many rows (4 * 256 * D flops per token and pair of tiles), by HBM where it has few.
 //
-// Measured, whole calls: 128 sequences of 64 query heads over 32768 bf16 tokens 102 us (1.35 PFLOP/s; this pass 83 to 86
-// us, 141 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 105 us, fp8 145 us.  A further step of 256 rows costs a CTA
-// 1.4 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us: 350 KB of
-// shared-memory traffic (operands 192, conversion 96, copies 32, scales 32) at 128 bytes per cycle.  Few rows: 4 sequences
-// over 38912 tokens 36.4 us (bf16, 4.4 TB/s with the launches) and 41 us (fp8).  The launches, first copies, last
-// stores and the join around the steps take 10 to 20 us, more with more rows: a call of two steps per CTA is 13.4 us
-// with 4 sequences, 17.0 us with 32.
+// Measured, whole calls from a graph: 128 sequences of 64 query heads over 32768 bf16 tokens 99.4 us (1.39 PFLOP/s; this
+// pass 82 us, 141 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 109 us, fp8 149 us.  A further step of 256
+// rows costs a CTA 1.4 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us:
+// 350 KB of shared-memory traffic (operands 192, conversion 96, copies 32, scales 32) at 128 bytes per cycle, which
+// account for 1.4 to 1.5 of it.  Few rows: 4 sequences with up to 20 tokens of their own over 38912 tokens 40 us (bf16,
+// 4.0 TB/s with the launches) and 46 us (fp8, which converts every token whatever the rows: 1.55 us per step).  The
+// launches, first copies, last stores and the join around the steps take 10 to 20 us, more with more rows: a call of two
+// steps per CTA is 13.4 us with 4 sequences, 17.0 us with 32.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -56,8 +56,8 @@ __device__ __forceinline__ uint32_t bf16_down(float x) { return bf16_up(-x) ^ 0x
 // tokens are loaded by one instruction and a lane keeps the words of its dimensions; the lanes that
 // hold the same dimensions of other tokens are joined by shuffles at the end.  All of a block's
 // loads (BS / (32/R16) per lane) are requested before the first is used.  Bound by HBM: the keys are
-// read once (a 256-byte run per bf16 row), 512 bytes are written; by latency where only the newest blocks are
-// renewed (16 sequences of 8 heads: 3.8 us).
+// read once (a 256-byte run per bf16 row), 512 bytes are written (whole contexts, 390146 tokens of 8 heads: 152 us, 5.6
+// TB/s); by latency where only the newest blocks are renewed (16 sequences of 8 heads: 3.7 us).
 template <int KV, int BS>
 __global__ void __launch_bounds__(256) pda_summarize_kernel(const SumArgs a) {
     allow_dependent_launch();
