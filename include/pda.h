@@ -70,10 +70,13 @@ enum {
     PDA_ERRW_BAD_BLOCK_ID = 2,      /* a block-table entry used by the context is outside [0, NB) */
     PDA_ERRW_PIPELINE_TIMEOUT = 4,  /* a bounded wait inside the kernel gave up */
     PDA_ERRW_BAD_POSITION = 8,      /* pda_append_kv: a position >= max_blocks_per_seq*kv_block_size;
-                                       pda_fork_sequences: a row that would grow past it, or by < 0 */
+                                       pda_fork_sequences: a row that would grow past it, or by < 0;
+                                       the token operators: a token that would lie past it */
     PDA_ERRW_BAD_SEQUENCE = 16,     /* pda_fork_sequences: parents[i] >= num_seqs */
     PDA_ERRW_OUT_OF_BLOCKS = 32,    /* pda_fork_sequences: fewer free blocks than the rows need */
-    PDA_ERRW_BAD_GROUP = 64         /* pda_decode_shared: group_starts not ascending within [0, num_seqs] */
+    PDA_ERRW_BAD_GROUP = 64,        /* pda_decode_shared: group_starts not ascending within [0, num_seqs] */
+    PDA_ERRW_BAD_TOKENS = 128       /* token_starts not ascending within [0, num_tokens]; pda_accept_tokens: a path not ascending
+                                       from an index >= 0, or longer than max_path */
 };
 
 /*
@@ -486,6 +489,108 @@ PDA_API int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* p
                               const int* prefix_table, const int* prefix_lens, const int* block_table,
                               const int* context_lens, void* workspace, long long workspace_bytes, void* out,
                               int out_dtype, int* err_word, void* stream);
+
+/* ---------------------------------------------------------------- many tokens of the cache
+ * Tokens of a batch, several per sequence, are rows of packed arrays: rows token_starts[b] .. token_starts[b+1]-1 are
+ * sequence b's.
+ *   token_starts   device, int32 [num_seqs + 1], ascending within [0, num_tokens]; rows before the first start and from the
+ *                  last one on (a padded batch) are not looked at and not written
+ * token_starts that do not ascend set PDA_ERRW_BAD_TOKENS, and the call moves or computes nothing.
+ *
+ * pda_write_kv -- K and V of any number of new tokens per sequence into the cache, in its format: a prompt, a part of one, or
+ * drafted tokens.  Row i of sequence b goes to position positions[b] + i - token_starts[b].
+ *   k_new, v_new   device, bf16, 16-byte aligned; row i starts k_stride (v_stride) elements after row i-1, a multiple of 8 and
+ *                  at least Hk*128, and holds [Hk][128]: rows of a fused projection need no copy
+ *   positions      device, int32 [num_seqs]; negative: none of the sequence's rows is written
+ *   centroids      device, fp32 [16], finite, in any order, for a TQ4 plan, else NULL
+ * bf16 and fp8 caches get the bytes that pda_append_kv would give them.  TQ4 (keys already in the basis of the codebook, as the
+ * query; K and V finite): K: k_norm = the norm of the row rounded to fp16 (from the exact sum of squares, at most 65504),
+ * code = how many midpoints of neighbouring centroids, (c + c') / 2 in fp32, lie below k_d / k_norm in fp32 (of the sorted
+ * codebook; a row of norm 0 is divided by 1); V: v_zero = fp16(min v), v_scale = fp16((max v - min v) / 15), code =
+ * (v_d - v_zero) / v_scale (by 1 where v_scale is 0), rounded to the nearest even integer and brought into 0 .. 15; all
+ * quotients and differences correctly rounded in fp32.
+ * Data errors: a row past max_blocks_per_seq*kv_block_size (PDA_ERRW_BAD_POSITION) or whose block id is outside the pool
+ * (PDA_ERRW_BAD_BLOCK_ID) is not written.  Rows that name the same slot race.
+ */
+PDA_API int pda_write_kv(const pda_plan_t* plan, const void* k_new, const void* v_new, long long k_stride,
+                         long long v_stride, long long num_tokens, void* kv_cache, long long num_cache_blocks,
+                         const float* centroids, const int* block_table, const int* token_starts, const int* positions,
+                         int* err_word, void* stream);
+
+/*
+ * pda_read_kv -- the other direction: tokens of the cache, gathered and dequantised.
+ *   k_out, v_out   device, [num_tokens][Hk][128], bf16 (PDA_OUT_BF16, rounded to nearest even) or fp32, 16-byte aligned;
+ *                  one of them may be NULL
+ *   the others, and the data errors, as for pda_write_kv: rows that it would not write are left as they are
+ * Values: bf16 as stored; fp8 code * scale, TQ4 centroids[code] * k_norm and code * v_scale + v_zero, in fp32.
+ */
+PDA_API int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long num_cache_blocks, const float* centroids,
+                        const int* block_table, const int* token_starts, const int* positions, long long num_tokens,
+                        void* k_out, void* v_out, int out_dtype, int* err_word, void* stream);
+
+/* ---------------------------------------------------------------- drafted tokens
+ * pda_decode_tree -- a step for drafted tokens, several per sequence, in a chain or a tree: token i of sequence b attends over
+ * the context_lens[b] cached tokens and over those of the sequence's drafted tokens that its mask names.  The drafted tokens'
+ * K and V lie in the cache behind the cached ones, token i at position context_lens[b] + i (pda_write_kv with positions =
+ * context_lens).
+ *   plan          num_seqs, heads, block size and max_blocks_per_seq; any kv_dtype.  kernel_variant and the partition length are
+ *                 not looked at.
+ *   query         device, bf16 [num_tokens][Hk*QG][128], 16-byte aligned, in device memory or pinned host memory
+ *   centroids     device, fp32 [16], finite, for a TQ4 plan, else NULL
+ *   block_table, context_lens   device, int32, as for pda_decode; context_lens without the drafted tokens
+ *   token_starts  device, int32 [num_seqs + 1] (see above); a sequence may have no drafted token
+ *   tree_masks    device, 64-bit words [num_tokens][mask_words], 8-byte aligned: bit j % 64 of word j / 64 of row i says
+ *                 whether token i sees drafted token j of its sequence (its own bit too).  Tokens past the words' bits are seen
+ *                 by none; bits past the sequence's tokens are not looked at.  NULL (and mask_words 0): a chain, i sees 0 .. i.
+ *   window        0: every cached token is seen.  Else a token at position p sees the cached tokens t with p - t < window, and
+ *                 t < num_first.  p is context_lens[b] + the number of drafted tokens other than itself that it sees.  Masks
+ *                 alone say which drafted tokens are seen; in a chain they count as cached ones.
+ *   workspace     device, pda_tree_workspace_size bytes, 32-byte aligned
+ *   out           [num_tokens][Hk*QG][128], as for pda_reduce; a row that sees nothing is 0
+ * K and V of the tokens that any of the sequence's rows sees must be finite: a row that does not see one of them still has it in
+ * its products, with weight 0.  What no row sees (before the window, behind the drafted tokens) is not read, or not used,
+ * whatever it holds; block ids of blocks wholly before the window are not looked at.
+ * The roundings are those of the prefix in pda_decode_shared; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11
+ * of its value, or 2^-24 of 1/256 of the step's largest 15 |v_scale| + |v_zero|), centroids to f16.
+ * Data errors: a context length out of range (PDA_ERRW_BAD_CONTEXT_LEN) or drafted tokens that do not fit behind it
+ * (PDA_ERRW_BAD_POSITION) give zeros for the sequence's rows; block ids as for pda_decode.
+ */
+PDA_API long long pda_tree_workspace_size(const pda_plan_t* plan, long long num_tokens);
+PDA_API int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tokens, const void* kv_cache,
+                            long long num_cache_blocks, const float* centroids, const int* block_table,
+                            const int* context_lens, const int* token_starts, const unsigned long long* tree_masks,
+                            int mask_words, int window, int num_first, void* workspace, long long workspace_bytes, void* out,
+                            int out_dtype, int* err_word, void* stream);
+
+/*
+ * pda_accept_tokens -- keeps the accepted drafted tokens: token path[b][k] of sequence b moves to position context_lens[b] + k,
+ * for k < path_lens[b] (whole tokens, any kv_dtype), and out_lens[b] = context_lens[b] + path_lens[b].  What lies behind is
+ * free to be overwritten.
+ *   path       device, int32 [num_seqs][max_path]: ascending indices of drafted tokens (an ancestor before its descendants)
+ *   path_lens  device, int32 [num_seqs], each in [0, max_path]
+ *   out_lens   device, int32 [num_seqs]; must not overlap context_lens or path_lens
+ * The call works within the pool it is given; the pools of a model's other layers need the same call each.  Sequences must not
+ * share the blocks that hold drafted tokens.
+ * Data errors: a context length out of range (PDA_ERRW_BAD_CONTEXT_LEN), a path that does not ascend or is too long
+ * (PDA_ERRW_BAD_TOKENS) or leaves the table (PDA_ERRW_BAD_POSITION): nothing of the sequence moves and its length stays.  A
+ * token whose block id, or its place's, is outside the pool does not move (PDA_ERRW_BAD_BLOCK_ID).
+ */
+PDA_API int pda_accept_tokens(const pda_plan_t* plan, void* kv_cache, long long num_cache_blocks, const int* block_table,
+                              const int* context_lens, const int* path, const int* path_lens, int max_path, int* out_lens,
+                              int* err_word, void* stream);
+
+/* ---------------------------------------------------------------- sliding window
+ * pda_decode_window -- a decode step in which the query of sequence b, at position context_lens[b] - 1, sees the tokens t with
+ * context_lens[b] - 1 - t < window and those with t < num_first.  The others are not read, and block ids of blocks that hold
+ * none of the seen ones are not looked at.  One launch, no partials.
+ *   plan        as for pda_decode; any kv_dtype; kernel_variant automatic (else PDA_ERR_UNSUPPORTED)
+ *   centroids   device, fp32 [16] for a TQ4 plan, else NULL
+ *   window      >= 1;  num_first >= 0
+ *   query, block_table, context_lens, out, out_dtype and the data errors as for pda_decode and pda_reduce
+ */
+PDA_API int pda_decode_window(const pda_plan_t* plan, const void* query, const void* kv_cache, long long num_cache_blocks,
+                              const float* centroids, const int* block_table, const int* context_lens, int window,
+                              int num_first, void* out, int out_dtype, int* err_word, void* stream);
 
 /* Human-readable name of a pda_status value (static string; never NULL). */
 PDA_API const char* pda_status_string(int status);

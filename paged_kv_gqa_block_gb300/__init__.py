@@ -26,6 +26,14 @@ Sequences that share prefixes, and long contexts of which a step attends to sele
     score_blocks(p, query, summaries, NB, table, lens, scores)
     select_blocks(p, scores, table, lens, K, 1, 1, sel_table, sel_lens)
     decode_selected(plan(..., max_blocks_per_seq=K), query, kv_cache, NB, sel_table, sel_lens)
+
+Many tokens per sequence, written in the cache's format and read back; drafted tokens in chains or trees; sliding windows:
+
+    write_kv(p, k, v, kv_cache, NB, table, token_starts, positions)
+    read_kv(p, kv_cache, NB, table, token_starts, positions, k_out, v_out)
+    decode_tree(p, query, kv_cache, NB, table, lens, token_starts, tree_masks=masks)
+    accept_tokens(p, kv_cache, NB, table, lens, path, path_lens, new_lens)
+    decode_window(p, query, kv_cache, NB, table, lens, 4096, num_first=4)
 """
 from __future__ import annotations
 
@@ -50,6 +58,7 @@ ERRW_BAD_POSITION = 8
 ERRW_BAD_SEQUENCE = 16
 ERRW_OUT_OF_BLOCKS = 32
 ERRW_BAD_GROUP = 64
+ERRW_BAD_TOKENS = 128
 HEAD_DIM = 128
 VARIANT_AUTO = 0
 VARIANT_HEAD_WARPS = 1
@@ -136,6 +145,16 @@ def lib():
             L.pda_shared_workspace_size.restype = CLL
             L.pda_decode_shared.argtypes = [P, P, _VP, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP, CLL, _VP, CI, _VP, _VP]
             L.pda_decode_shared.restype = CI
+            L.pda_write_kv.argtypes = [P, _VP, _VP, CLL, CLL, CLL, _VP, CLL, _VP, _VP, _VP, _VP, _VP, _VP]
+            L.pda_read_kv.argtypes = [P, _VP, CLL, _VP, _VP, _VP, _VP, CLL, _VP, _VP, CI, _VP, _VP]
+            L.pda_tree_workspace_size.argtypes = [P, CLL]
+            L.pda_tree_workspace_size.restype = CLL
+            L.pda_decode_tree.argtypes = [P, _VP, CLL, _VP, CLL, _VP, _VP, _VP, _VP, _VP, CI, CI, CI, _VP, CLL, _VP, CI, _VP,
+                                          _VP]
+            L.pda_accept_tokens.argtypes = [P, _VP, CLL, _VP, _VP, _VP, _VP, CI, _VP, _VP, _VP]
+            L.pda_decode_window.argtypes = [P, _VP, _VP, CLL, _VP, _VP, _VP, CI, CI, _VP, CI, _VP, _VP]
+            for f in (L.pda_write_kv, L.pda_read_kv, L.pda_decode_tree, L.pda_accept_tokens, L.pda_decode_window):
+                f.restype = CI
             for f in (L.pda_copy_blocks, L.pda_fork_sequences, L.pda_compact_blocks, L.pda_summarize_blocks,
                       L.pda_score_blocks, L.pda_select_blocks, L.pda_decode_selected):
                 f.restype = CI
@@ -608,4 +627,136 @@ def decode_shared(prefix_plan: Plan, p: Plan, query, kv_cache, num_cache_blocks:
             c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_shared", lib().pda_decode_shared, prefix_plan, args, err_word, stream)
+    return out
+
+
+# ------------------------------------------------------------------------------------------------
+# Many tokens per sequence, drafted tokens, sliding windows.  Rows token_starts[b] .. token_starts[b+1]-1 of the packed
+# arrays are sequence b's.
+def _rows(c: _Call, t, name: str, p: Plan):
+    """Pointer and row stride (elements) of bf16 [N][Hk][128] whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != c.index:
+        raise ValueError(f"{name} must be on cuda:{c.index}")
+    if t.dtype not in _BF16:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != p.num_kv_heads or t.shape[2] != p.head_dim:
+        raise ValueError(f"{name} must be [tokens][{p.num_kv_heads}][{p.head_dim}]")
+    row = p.num_kv_heads * p.head_dim
+    if t.shape[0] <= 1 or t.numel() == 0:
+        stride = row
+    else:
+        stride = t.stride(0)
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != p.head_dim) or stride < row):
+        raise ValueError(f"{name} must hold whole rows: only the first stride is free")
+    return t.data_ptr(), stride
+
+
+def write_kv(p: Plan, k_new, v_new, kv_cache, num_cache_blocks: int, block_table, token_starts, positions, centroids=None,
+             err_word=None, stream=None) -> None:
+    """pda_write_kv: K and V of any number of new tokens per sequence, in the cache's format (see include/pda.h).
+    k_new, v_new: bf16 [N][Hk][128], rows of any stride that is a multiple of 8 elements; token_starts: int32 [B + 1];
+    positions: int32 [B]; centroids: fp32 [16], for a TQ4 plan."""
+    c = _Call(kv_cache, "kv_cache")
+    B = p.num_seqs
+    (k, ks), (v, vs) = _rows(c, k_new, "k_new", p), _rows(c, v_new, "v_new", p)
+    N = k_new.shape[0]
+    if v_new.shape[0] != N:
+        raise ValueError("k_new and v_new must hold the same tokens")
+    args = (k, v, ks, vs, N, c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.opt(centroids, "centroids", _F32, 64), c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
+            c.ptr(token_starts, "token_starts", _I32, (B + 1) * 4), c.ptr(positions, "positions", _I32, B * 4))
+    c.run("pda_write_kv", lib().pda_write_kv, p, args, err_word, stream)
+
+
+def read_kv(p: Plan, kv_cache, num_cache_blocks: int, block_table, token_starts, positions, k_out, v_out, centroids=None,
+            err_word=None, stream=None) -> None:
+    """pda_read_kv: tokens of the cache, gathered and dequantised into k_out, v_out [N][Hk][128], bf16 or fp32 (see
+    include/pda.h).  One of the two may be None."""
+    c = _Call(kv_cache, "kv_cache")
+    B, row = p.num_seqs, p.num_kv_heads * p.head_dim
+    given = [t for t in (k_out, v_out) if t is not None]
+    if not given:
+        raise ValueError("k_out or v_out must be given")
+    dtype = given[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"k_out and v_out have dtype {dtype}")
+    N = given[0].numel() // row
+    outs = tuple(c.opt(t, n, (dtype,), N * row * given[0].element_size()) for t, n in ((k_out, "k_out"), (v_out, "v_out")))
+    args = (c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.opt(centroids, "centroids", _F32, 64), c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
+            c.ptr(token_starts, "token_starts", _I32, (B + 1) * 4), c.ptr(positions, "positions", _I32, B * 4), N, *outs,
+            OUT_F32 if dtype is torch.float32 else OUT_BF16)
+    c.run("pda_read_kv", lib().pda_read_kv, p, args, err_word, stream)
+
+
+def tree_workspace(p: Plan, num_tokens: int, device):
+    """The workspace of decode_tree with num_tokens drafted tokens in all (one made for more tokens may be too small)."""
+    n = lib().pda_tree_workspace_size(p, num_tokens)
+    if n < 0:
+        raise PdaError(-1, "pda_tree_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def decode_tree(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, context_lens, token_starts, tree_masks=None,
+                window: int = 0, num_first: int = 0, centroids=None, ws=None, out=None, out_dtype=torch.bfloat16,
+                err_word=None, stream=None):
+    """pda_decode_tree: a step for drafted tokens in chains (tree_masks None) or trees (see include/pda.h); query: bf16
+    [N][Hk*QG][128], tree_masks: int64 [N][words]; returns out [N][Hk*QG][128]."""
+    c = _Call(kv_cache, "kv_cache")
+    B, rows, D = p.num_seqs, p.num_kv_heads * p.query_group_size, p.head_dim
+    N = query.numel() // (rows * D)
+    words = 0
+    if tree_masks is not None:
+        if tree_masks.dim() != 2 or tree_masks.shape[0] < N or tree_masks.shape[1] < 1:
+            raise ValueError("tree_masks must be [tokens][words]")
+        words = tree_masks.shape[1]
+    if ws is None:
+        ws = _made(lambda: tree_workspace(p, N, kv_cache.device), c.index, stream)
+    if out is None:
+        out = _made(lambda: torch.zeros((N, rows, D), dtype=out_dtype, device=kv_cache.device), c.index, stream)
+    n = N * rows * D
+    f32 = out.dtype is torch.float32
+    args = (c.ptr(query, "query", _BF16, n * 2, host_ok=True), N,
+            c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.opt(centroids, "centroids", _F32, 64), c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
+            c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(token_starts, "token_starts", _I32, (B + 1) * 4),
+            c.opt(tree_masks, "tree_masks", (torch.int64, torch.uint64), N * words * 8), words, window, num_first,
+            c.ptr(ws, "ws", _U8, 0), ws.nbytes, c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
+            OUT_F32 if f32 else OUT_BF16)
+    c.run("pda_decode_tree", lib().pda_decode_tree, p, args, err_word, stream)
+    return out
+
+
+def accept_tokens(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, path, path_lens, out_lens,
+                  err_word=None, stream=None) -> None:
+    """pda_accept_tokens: the accepted drafted tokens move to consecutive positions (see include/pda.h).
+    path: int32 [B][max_path], ascending; path_lens, out_lens: int32 [B]."""
+    c = _Call(kv_cache, "kv_cache")
+    B = p.num_seqs
+    A = path.numel() // B if B else 0
+    args = (c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
+            c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(path, "path", _I32, B * A * 4),
+            c.ptr(path_lens, "path_lens", _I32, B * 4), A, c.ptr(out_lens, "out_lens", _I32, B * 4))
+    c.run("pda_accept_tokens", lib().pda_accept_tokens, p, args, err_word, stream)
+
+
+def decode_window(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, context_lens, window: int,
+                  num_first: int = 0, centroids=None, out=None, out_dtype=torch.bfloat16, err_word=None, stream=None):
+    """pda_decode_window: a decode step over the last `window` tokens and the first num_first (see include/pda.h);
+    returns out [B][Hk*QG][D]."""
+    c = _Call(kv_cache, "kv_cache")
+    B, rows, D = p.num_seqs, p.num_kv_heads * p.query_group_size, p.head_dim
+    if out is None:
+        out = _made(lambda: torch.empty((B, rows, D), dtype=out_dtype, device=kv_cache.device), c.index, stream)
+    n = B * rows * D
+    f32 = out.dtype is torch.float32
+    args = (c.ptr(query, "query", _BF16, n * 2, host_ok=True),
+            c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
+            c.opt(centroids, "centroids", _F32, 64),
+            c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4, host_ok=True),
+            c.ptr(context_lens, "context_lens", _I32, B * 4, host_ok=True), window, num_first,
+            c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
+            OUT_F32 if f32 else OUT_BF16)
+    c.run("pda_decode_window", lib().pda_decode_window, p, args, err_word, stream)
     return out

@@ -31,7 +31,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(HERE, "serving", "*.cuh")) + \
+        glob.glob(os.path.join(HERE, "serving", "*.cuh")) + glob.glob(os.path.join(HERE, "serving", "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 

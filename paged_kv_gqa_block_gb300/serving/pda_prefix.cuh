@@ -1,0 +1,1148 @@
+// pda_prefix.cuh -- attention of many query rows over the tokens of one (sequence or group, KV head), on the tensor cores: the
+// prefix pass of pda_decode_shared, and the only pass of pda_decode_tree.
+//
+// pda_decode_shared: for query row r of sequence b in group g,
+//   out = softmax(scale [q.K_g ; q.K_b]) [V_g ; V_b],
+// with K_g, V_g the group's prefix and K_b, V_b the sequence's own tokens.  The two parts are
+// computed apart as (m, l, o), a reference near the maximum, the sum of exponentials from it and the normalised
+// output, and joined: w = l e^(m - M), out = sum w o / sum w, M the largest m.  The own part is the cluster kernel of
+// pda_selected.cuh.  The prefix part is one matrix product per group and KV head for the
+// query rows of all its sequences, n_g * QG of them, and this file's kernel.
+//
+// pda_decode_tree: a group is one sequence, its rows are those of its drafted tokens, its tokens the cached ones and the
+// drafted behind them.  A row does not see every token: see Visible.
+//
+// The prefix pass.  A CTA holds 256 query rows of one (group, KV head) in two tiles of 128 and walks
+// the prefix in steps of 128 tokens: S = Q K^T and O += P V by tcgen05.mma (M = N = 128), S, P and
+// O in tensor memory (two tiles x (128 + 128) columns = all 512; P, 16-bit, lies over the S it was
+// made of).  Warps take one role each:
+//   0-3, 4-7  softmax of tile 0, tile 1: one query row per thread, so a row's maximum and sum need
+//             no shuffles; S is read from TMEM, P written back
+//   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
+//   9         the matrix products (one thread issues)
+//   10        fp8 and TQ4: the scales of a step
+//   11        the split: which rows and which tokens this CTA takes
+//   12-15     fp8 and TQ4: codes to f16 between the copy and the product
+// The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
+// The products are issued in the order PV(0, j), QK(0, j+1), PV(1, j), QK(1, j+1): while one tile's
+// softmax runs the tensor cores work for the other.  A tile's reference point m moves only when a
+// row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
+// TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
+// P is announced in halves, so that PV starts while the second half is computed.
+// P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11; V carries two more such
+// roundings, see the conversion); m, l, S and O are fp32.  f16 has few exponents: below 2^-14 a value loses bits, and
+// below 2^-25 it is zero, while l counts it; a long even prefix behind one large weight would lose a share of the
+// output.  So with f16 the reference is 7 below the maximum: with the 8 of its lazy move P still ends at 2^15, weights
+// keep their 11 bits down to 2^-21 of the largest, and smaller ones are off by at most 2^-32 of it.
+//
+// Work is split over the CTAs (one per SM) by steps, not by units: the steps of all (group, KV head,
+// row tile) are laid end to end and every CTA takes an equal run; a row tile that is cut leaves one
+// partial per piece.  A change of row tiles is counted as steps too, or every tile gets runs of its own, whichever
+// ends sooner (64 sequences of 64 heads in 3 groups 37.2 -> 33.0 us, 100 of 32 heads in 7 groups 49.3 -> 34.5).
+// Nothing depends on how lengths and groups fall.  Bound by the tensor cores
+// where a group has many rows (4 * 256 * D flops per token and pair of tiles), by HBM where it has few.
+//
+// Measured, whole calls from a graph: 128 sequences of 64 query heads over 32768 bf16 tokens 99.4 us (1.39 PFLOP/s; this
+// pass 82 us, 141 MB read of a prefix of 134 MB), 64 over 77824 bf16 tokens 109 us, fp8 149 us.  A further step of 256
+// rows costs a CTA 1.4 us (bf16), of which its products' 2048 cycles are 1.3 at the clock of this load; fp8 1.95 us:
+// 350 KB of shared-memory traffic (operands 192, conversion 96, copies 32, scales 32) at 128 bytes per cycle, which
+// account for 1.4 to 1.5 of it.  Few rows: 4 sequences with up to 20 tokens of their own over 38912 tokens 40 us (bf16,
+// 4.0 TB/s with the launches) and 46 us (fp8, which converts every token whatever the rows: 1.55 us per step).  The
+// launches, first copies, last stores and the join around the steps take 10 to 20 us, more with more rows: a call of two
+// steps per CTA is 13.4 us with 4 sequences, 17.0 us with 32.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include "pda.h"
+#include "pda_internal.h"
+#include "pda_ptx.cuh"
+#include "pda_split.cuh"
+#include "pda_tc.cuh"
+
+namespace pda {
+
+constexpr int kConvertWarps = 4;
+constexpr int kTileRows = 128;
+constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bits
+constexpr int kRawBytes = 16384;           // the same in 8 bits
+constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
+constexpr float kLazy = 8.f;               // log2 units that a row's maximum may rise before its reference follows
+constexpr float kBelow = 7.f;              // f16 P: the reference below the maximum
+
+template <int KV>
+struct SharedCfg {
+    static constexpr bool kF16 = KV != PDA_KV_BF16;              // f16 products, converter warps
+    static constexpr bool kTq = KV == PDA_KV_TQ4;
+    static constexpr int kScaleBytes = kTq ? 1536 : 1024;        // 128 tokens x {K scale, V scale (, V zero)}
+    static constexpr int kTiles = kTq ? 1 : 2;                   // copies of a step: a TQ4 row holds K and V
+    static constexpr int kSlots = kF16 ? 3 : 5;
+    static constexpr int kRaw = 3, kScales = 3;                  // fp8, TQ4: raw slots, scale stages
+    static constexpr int kThreads = kF16 ? 512 : 384;
+    static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
+    static constexpr int kOffSlots = 2 * kSlotBytes;
+    static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;
+    static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
+    static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
+    static constexpr int kOffTable = kOffBars + 464;              // TQ4: the centroids of a byte's two codes, f16
+    static constexpr int kSmem = kTq ? kOffTable + 1024 : kOffBars + 448;
+    static constexpr int kReaders = kF16 ? 15 : 10;               // warps that take units
+};
+// barriers and scalars after kOffBars
+enum {
+    kBarFull = 0,        // [5] a slot holds its tile
+    kBarEmpty = 40,      // [5] the products that read a slot are done
+    kBarQ = 80,          // [2] a tile's query rows are in shared memory
+    kBarS = 96,          // [2] S is in TMEM
+    kBarP = 112,         // [2] the first half of P (64 tokens) is in TMEM
+    kBarO = 128,         // [2] the unit's last product of a tile is done
+    kBarRawFull = 144,   // [3]
+    kBarRawEmpty = 168,  // [3]
+    kBarScFull = 192,    // [3] scales are laid out
+    kBarScEmpty = 216,   // [3]
+    kBarDrain = 240,
+    kTmemAt = 248,       // TMEM address
+    kAbortAt = 252,      // a wait gave up
+    kFAt = 256,          // [3] what a step's V scales are divided by
+    kBarP2 = 272,        // [2] the second half of P is in TMEM
+    kBarScRaw = 288,     // [3] scales as copied
+    kBarUnitFull = 312,  // [2] the next unit is in shared memory
+    kBarUnitEmpty = 328, // [2]
+    kUnitAt = 352,       // [2] units, 48 bytes each
+    kPowerAt = 448       // TQ4: 1 over the power of two that the table's centroids carry
+};
+
+// ------------------------------------------------------------------------- the prefix pass
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// 16 bytes global -> shared, of which `bytes` (16 or 0) are read and the rest are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds32v(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32v(uint32_t addr, uint32_t v) {
+    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two fp32 operations per instruction.
+__device__ __forceinline__ void mul2(uint32_t& x, uint32_t& y, uint32_t a, uint32_t b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "r"(a), "r"(b));
+}
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float c, float d) {   // x c + d
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float2& x, const float2& y) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x.x), "+f"(x.y)
+        : "f"(y.x), "f"(y.y));
+}
+
+template <int KV, class Args>
+struct Prefix {
+    using Cfg = SharedCfg<KV>;
+    static constexpr bool F16 = Cfg::kF16, TQ = Cfg::kTq, TREE = std::is_same<Args, TreeArgs>::value;
+    static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
+
+    const Args& a;
+    const uint32_t sm;         // shared memory base
+    const uint32_t bars;
+    unsigned units = 0;        // units taken (or given) by this warp
+    unsigned busy = 0;         // their steps
+
+    __device__ __forceinline__ Prefix(const Args& args, uint32_t base)
+        : a(args), sm(base), bars(base + Cfg::kOffBars) {}
+
+    // A whole warp waits (bounded).  False once any wait of the CTA has given up.
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
+        bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(kLanes, ok)) return true;
+        return wait_on(bar, parity, poll, a.timeout_ns);
+    }
+    __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool poll, uint64_t limit) const {
+        const uint64_t t0 = global_timer_ns();
+        for (;;) {
+            const bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+            if (__all_sync(kLanes, ok)) return true;
+            const bool late = global_timer_ns() - t0 > limit;
+            if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
+                sts32v(bars + kAbortAt, 1u);
+                return false;
+            }
+        }
+    }
+
+    // One warp looks the CTA's units up, ahead of the others, which read them from shared memory; a unit without
+    // steps is the end.  (Looked up by every warp for itself, the split took registers from the softmax.)
+    // A unit, or its place, may come only when warps that are behind have finished one that was taken before: the
+    // limit is that of their waits, a few per step (long limits, from 0.27 s on, do for any unit).
+    __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity) const {
+        const uint64_t limit = a.timeout_ns >> 28 ? a.timeout_ns : a.timeout_ns * (64 + 8ull * busy);
+        const bool poll = a.timeout_ns < 1000000ull;
+        if (__all_sync(kLanes, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) return true;
+        return wait_on(bar, parity, poll, limit);
+    }
+    __device__ __forceinline__ void put(const Unit& u) const {
+        const uint32_t at = bars + kUnitAt + (units & 1) * 48;
+        if ((threadIdx.x & 31) == 0) {
+            sts128(at, u.g, u.h, u.rt, u.seq0);
+            sts128(at + 16, u.rows, u.len, u.step0, u.steps);
+            sts128(at + 32, u.rot, u.slot, u.pieces, 0);
+        }
+    }
+    __device__ void give(const Split& split, Unit u, int at, int end) {   // the first one is there already
+        for (;;) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitFull + 8 * (units & 1));
+            ++units;
+            if (u.steps == 0) return;
+            busy += u.steps;
+            u = find_unit(a, split, at, end);
+            if (units > 1 && !wait_unit(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
+            put(u);
+        }
+    }
+    __device__ __forceinline__ bool next(Unit& u) {
+        const uint32_t slot = units & 1, at = bars + kUnitAt + slot * 48;
+        if (!wait_unit(bars + kBarUnitFull + 8 * slot, units >> 1 & 1)) return false;
+        uint32_t x[12];
+#pragma unroll
+        for (int i = 0; i < 12; i += 4) lds128(at + 4 * i, x[i], x[i + 1], x[i + 2], x[i + 3]);
+        u.g = x[0], u.h = x[1], u.rt = x[2], u.seq0 = x[3], u.rows = x[4], u.len = x[5], u.step0 = x[6], u.steps = x[7];
+        u.rot = x[8], u.slot = x[9], u.pieces = x[10];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitEmpty + 8 * slot);
+        ++units;
+        busy += u.steps;
+        return u.steps > 0;
+    }
+    // What the unit's rows see (TREE); constant, and gone, without.
+    __device__ __forceinline__ Sight sight(const Unit& u) const {
+        if constexpr (TREE)
+            return sight_of(a, u.len, u.rows / a.QG);
+        else
+            return Sight{};
+    }
+    // Step number of the piece's j-th step, and its tokens.
+    __device__ __forceinline__ static int step_of(const Unit& u, const Sight& x, int j) {
+        const int i = j + u.rot, n = u.step0 + (i < u.steps ? i : i - u.steps);
+        return TREE && n >= x.at ? n + x.skip : n;
+    }
+    __device__ __forceinline__ static int tokens_of(const Unit& u, const Sight& x, int j) {
+        return min(kStep, u.len - step_of(u, x, j) * kStep);
+    }
+    // Whether token t of the sequence, below its length, is one that all rows miss.
+    __device__ __forceinline__ static bool missed(const Sight& x, int t) { return TREE && t >= x.hole0 && t < x.hole1; }
+    __device__ __forceinline__ static bool active(const Unit& u, int tile) {
+        return u.rt * kUnitRows + tile * kTileRows < u.rows;
+    }
+
+    // ---------------------------------------------------------------- copies
+    // Slot order K(0), V(0), K(1), V(1), ...  Each lane copies one (block, 64-dimension half): box
+    // {128 bytes, BS tokens}; the halves are 16 KB apart, so that a slot is the products' operand as
+    // it lands ([half][token][128 bytes], swizzled).  fp8 rows are one 128-byte piece, copied to the
+    // raw slots with the step's scales.
+    __device__ void copies(const CUtensorMap* kv_map, const CUtensorMap* sc_map) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? Cfg::kRaw : Cfg::kSlots, kTiles = Cfg::kTiles;
+        constexpr uint32_t kField = TQ ? 6u : 8u;   // bytes of a token's scales
+        constexpr uint32_t kFull0 = F16 ? kBarRawFull : kBarFull, kEmpty0 = F16 ? kBarRawEmpty : kBarEmpty;
+        constexpr int kBytes = F16 ? kRawBytes : kSlotBytes;
+        const uint32_t base = sm + (F16 ? Cfg::kOffRaw : Cfg::kOffSlots);
+        const int nblk = kStep / a.BS;
+        const int blk = lane / kHalves, half = lane % kHalves;
+        const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+        unsigned seq = 0, step = 0;
+        bool ok = true;
+        Unit u;
+        while (ok && next(u)) {
+            const Sight x = sight(u);
+            const uint64_t policy = u.rows > kUnitRows ? again : once;   // other row tiles read it too
+            const int* table = a.prefix_table + (long long)u.g * a.MP;
+            const int last = (u.len + a.BS - 1) / a.BS;   // blocks of the prefix
+            int id = 0;
+            int b0 = step_of(u, x, 0) * nblk;
+            if (blk < nblk && b0 + blk < last) id = __ldcg(table + b0 + blk);
+            for (int j = 0; ok && j < u.steps; ++j, ++step) {
+                int n = min(nblk, last - b0);
+                bool mine = blk < n;
+                if constexpr (TREE) {   // a block that all rows miss may be another's by now, or none: it is not looked at
+                    if ((b0 + blk) * a.BS >= x.hole0 && (b0 + blk + 1) * a.BS <= x.hole1) mine = false;
+                    n = __popc(__ballot_sync(kLanes, mine && half == 0));
+                }
+                int nid = 0, b1 = 0;
+                if (j + 1 < u.steps) {
+                    b1 = step_of(u, x, j + 1) * nblk;
+                    if (blk < nblk && b1 + blk < last) nid = __ldcg(table + b1 + blk);
+                }
+                if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
+                    atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
+                const unsigned st = step % Cfg::kScales;
+                if (F16 && step >= Cfg::kScales && !wait(bars + kBarScEmpty + 8 * st, (step / Cfg::kScales - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int v = 0; v < kTiles; ++v, ++seq) {   // K, then V
+                    const int s = seq % kNS;
+                    if (seq >= kNS && !wait(bars + kEmpty0 + 8 * s, (seq / kNS - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = bars + kFull0 + 8 * s;
+                    const uint32_t row_bytes = (uint32_t)n * a.BS * 128u * kHalves;
+                    const bool scales = F16 && v == 0;
+                    if (lane == 0) {
+                        if (scales) mbar_arrive_expect_tx(bars + kBarScRaw + 8 * st, (uint32_t)n * a.BS * kField);
+                        mbar_arrive_expect_tx(bar, row_bytes);
+                    }
+                    __syncwarp();
+                    if (mine) {
+                        tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
+                                    v * kHalves + half, u.h, id, policy);
+                        if (scales)
+                            tma_load_4d(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + blk * a.BS * 8, sc_map,
+                                        bars + kBarScRaw + 8 * st, 0, 0, u.h, id, policy);
+                    }
+                    __syncwarp();
+                }
+                id = nid;
+                b0 = b1;
+            }
+        }
+        // no copy may land in this CTA's memory after it leaves, whichever role gave up
+        for (int s = 0; s < kNS; ++s)
+            if (seq > (unsigned)s) {
+                const unsigned q = (seq - 1 - s) / kNS;   // the slot's last use
+                (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
+            }
+        if (F16) {
+            const unsigned issued = (seq + kTiles - 1) / kTiles;   // steps whose scales were asked for
+            for (int s = 0; s < Cfg::kScales; ++s)
+                if (issued > (unsigned)s)
+                    (void)mbar_wait(bars + kBarScRaw + 8 * s, (issued - 1 - s) / Cfg::kScales & 1, kDefaultTimeoutNs);
+        }
+    }
+
+    // ---------------------------------------------------------------- conversion (fp8)
+    // One warp lays a step's scales out as [128 K scales][128 V scales / F]: the K scales for the softmax, the
+    // others for the conversion.  F keeps V in f16's range (the accumulator counts in units of F): 16 F is the
+    // step's largest V scale f, and F stays as it is while f lies in [2F, 128F].  So the largest products stay
+    // below 448 * 128 = 57344, and a scale keeps its 11 bits down to 2^-15 f (2 F * 2^-15 = 2^-14 F).
+    // TQ4: a token's values lie within 15 |v_scale| + |v_zero|; f is the largest such bound, 2048 F = f, and F stays while f lies
+    // in [256 F, 32768 F].  The values are computed in 32 bits and rounded to f16 once.
+    __device__ void scales() {
+        const int lane = threadIdx.x & 31;
+        unsigned st = 0, ph = 0;
+        float F = 1.f;
+        Unit u;
+        while (next(u)) {
+            const Sight x = sight(u);
+            for (int j = 0; j < u.steps; ++j) {
+                const int valid = tokens_of(u, x, j), t0 = step_of(u, x, j) * kStep;
+                if (!wait(bars + kBarScRaw + 8 * st, ph)) return;
+                const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
+                float ks[4], vs[4], vz[4], f = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = lane + 32 * i;
+                    const bool there = tok < valid && !missed(x, t0 + tok);
+                    if constexpr (TQ) {
+                        ks[i] = there ? field_at(sc, tok, 0) : 0.f;
+                        vs[i] = there ? field_at(sc, tok, 1) : 0.f;
+                        vz[i] = there ? field_at(sc, tok, 2) : 0.f;
+                        f = fmaxf(f, fmaf(15.f, fabsf(vs[i]), fabsf(vz[i])));
+                    } else {
+                        ks[i] = there ? __uint_as_float(lds32v(scale_at(sc, tok, 0))) : 0.f;
+                        vs[i] = there ? __uint_as_float(lds32v(scale_at(sc, tok, 1))) : 0.f;
+                        vz[i] = 0.f;
+                        f = fmaxf(f, fabsf(vs[i]));
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(kLanes, f, o));
+                if (!(f > 0.f)) f = 1.f;
+                constexpr float kHigh = TQ ? 32768.f : 128.f, kLow = TQ ? 256.f : 2.f, kMid = TQ ? 1.f / 2048.f : 0.0625f;
+                if (j == 0 || f > F * kHigh || f < F * kLow) F = fmaxf(f * kMid, 1e-37f);   // 1 / F is finite
+                const float rF = 1.f / F;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // the shuffles above come after every lane's reads
+                    sts32v(sc + (lane + 32 * i) * 4, __float_as_uint(ks[i]));
+                    sts32v(sc + 512 + (lane + 32 * i) * 4, __float_as_uint(vs[i] * rF));
+                    if constexpr (TQ) sts32v(sc + 1024 + (lane + 32 * i) * 4, __float_as_uint(vz[i] * rF));
+                }
+                if (lane == 0) sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
+                fence_proxy_async_shared();   // the next copy into this stage comes after these stores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * st);
+                if (++st == Cfg::kScales) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    }
+    // Thread t of the converting warps turns token t's 128 codes into f16: K as it is (exact: every e4m3 value is
+    // an f16 value; the factor is 1), V times its token's scale over F (two roundings to f16, 2^-11 each, beside
+    // P's one; it spares the softmax a product per weight).  Rows past the prefix become zeros, since a
+    // weight of zero does not silence a NaN.  This chain (raw codes landed, read, convert, store, announce) paces the fp8
+    // pass, so nothing else stands in it: no scales, no branches, and the reads are requested before the slot is free.
+    __device__ void convert() {
+        if constexpr (TQ)
+            convert_tq4();
+        else
+            convert_fp8();
+    }
+    __device__ void convert_fp8() {
+        const int t = threadIdx.x - 384, lane = t & 31, sw = t & 7;
+        const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
+        const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4;
+        static_assert(!F16 || Cfg::kRaw == Cfg::kSlots, "a raw slot and its slot are counted together");
+        unsigned s = 0, ph = 0, st = 0, st_ph = 0;
+        Unit u;
+        while (next(u)) {
+            const Sight x = sight(u);
+            for (int j = 0; j < u.steps; ++j) {
+                const bool zero = t >= tokens_of(u, x, j) || missed(x, step_of(u, x, j) * kStep + t);
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    if (!wait(bars + kBarRawFull + 8 * s, ph)) return;
+                    const uint32_t src = raw0 + s * kRawBytes, dst = slot0 + s * kSlotBytes;
+                    uint32_t w[8][4];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) lds128(src + ((c ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                    float vs = 1.f;
+                    if (v) {
+                        if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                        vs = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes));
+                        if (++st == Cfg::kScales) {
+                            st = 0;
+                            st_ph ^= 1;
+                        }
+                    }
+                    const uint32_t vs2 = pack_f16(vs, vs);
+                    if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;   // the slots start free
+                    if (zero) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
+                        const uint32_t d = dst + (c >> 2) * 16384;
+                        const int k = 2 * (c & 3);
+                        sts128(d + ((k ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                        sts128(d + (((k + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bars + kBarFull + 8 * s);
+                        mbar_arrive(bars + kBarRawEmpty + 8 * s);
+                    }
+                    if (++s == Cfg::kSlots) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+        }
+    }
+    // TQ4.  Thread t turns token t's 64 + 64 bytes of codes into f16: K's through the table of byte pairs (centroids times a
+    // power of two; k_norm is the step's K scale), V as code * v_scale + v_zero over F in 32 bits, rounded once.  Step by step
+    // K, then V, out of one raw slot.
+    __device__ void convert_tq4() {
+        const int t = threadIdx.x - 384, lane = t & 31, sw = t & 7;
+        const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
+        const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4, table = sm + Cfg::kOffTable;
+        unsigned s = 0, ph = 0, rs = 0, rph = 0, st = 0, st_ph = 0;
+        Unit u;
+        while (next(u)) {
+            const Sight x = sight(u);
+            for (int j = 0; j < u.steps; ++j) {
+                const bool zero = t >= tokens_of(u, x, j) || missed(x, step_of(u, x, j) * kStep + t);
+                if (!wait(bars + kBarRawFull + 8 * rs, rph)) return;
+                uint32_t w[8][4];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) lds128(raw0 + rs * kRawBytes + ((c ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                if (zero) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+                }
+                if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;   // the slots start free
+                uint32_t dst = slot0 + s * kSlotBytes;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {   // 16 bytes of f16 from 4 of codes
+                    const uint32_t code = w[c >> 2][c & 3];
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = lds32v(table + ((code >> (8 * i)) & 0xFFu) * 4);
+                    sts128(dst + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + kBarFull + 8 * s);
+                if (++s == Cfg::kSlots) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                // 1 + code / 16 costs one instruction: V = (1 + code / 16) 16 v_scale + (v_zero - 16 v_scale).  A token that is
+                // not there has both 0.
+                const float vs = 16.f * __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes));
+                const float vz = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes + 512)) - vs;
+                if (++st == Cfg::kScales) {
+                    st = 0;
+                    st_ph ^= 1;
+                }
+                if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;
+                dst = slot0 + s * kSlotBytes;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const uint32_t code = w[4 + (c >> 2)][c & 3];
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float lo = __uint_as_float(((code >> (8 * i)) & 0xFu) << 19 | 0x3F800000u);
+                        const float hi = __uint_as_float(((code >> (8 * i + 4)) & 0xFu) << 19 | 0x3F800000u);
+                        o[i] = pack_f16(fmaf(lo, vs, vz), fmaf(hi, vs, vz));
+                    }
+                    sts128(dst + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bars + kBarFull + 8 * s);
+                    mbar_arrive(bars + kBarRawEmpty + 8 * rs);
+                }
+                if (++s == Cfg::kSlots) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++rs == Cfg::kRaw) {
+                    rs = 0;
+                    rph ^= 1;
+                }
+            }
+        }
+    }
+    // One warp lays out the table of the centroids, times a power of two that brings the largest into [2^14, 2^15), in f16.
+    __device__ __forceinline__ void make_table() const {
+        const int lane = threadIdx.x & 31;
+        const float c = __ldcg(a.centroids + (lane & 15));
+        float top = fabsf(c);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kLanes, top, o));
+        int e = top > 0.f ? 14 - ((int)(__float_as_uint(top) >> 23 & 0xFF) - 127) : 0;
+        e = max(-100, min(100, e));
+        if (lane == 0) sts32v(bars + kPowerAt, (uint32_t)(127 - e) << 23);
+        const uint32_t h = __half_as_ushort(__float2half_rn(c * __uint_as_float((uint32_t)(e + 127) << 23)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int x = 8 * lane + i;
+            const uint32_t lo = __shfl_sync(kLanes, h, x & 15), hi = __shfl_sync(kLanes, h, x >> 4);
+            sts32v(sm + Cfg::kOffTable + 4 * x, lo | hi << 16);
+        }
+    }
+    // A TQ4 field of token tok as copied: [block][field][BS], f16.
+    __device__ __forceinline__ float field_at(uint32_t sc, int tok, int field) const {
+        const int b = a.BS == 32 ? tok >> 5 : tok >> 4;
+        const uint32_t at = sc + b * a.BS * 8 + (field * a.BS + (tok - b * a.BS)) * 2;   // a copy starts at 128 bytes
+        const uint32_t w = lds32v(at & ~3u);
+        return __half2float(__ushort_as_half((uint16_t)(at & 2u ? w >> 16 : w & 0xFFFFu)));
+    }
+    // Address of token tok's K (field 0) or V (field 1) scale as copied: [block][field][BS].
+    __device__ __forceinline__ uint32_t scale_at(uint32_t sc, int tok, int field) const {
+        const int b = a.BS == 32 ? tok >> 5 : tok >> 4;
+        return sc + (b * a.BS * 2 + field * a.BS + (tok - b * a.BS)) * 4;
+    }
+
+    // ---------------------------------------------------------------- products
+    static constexpr uint32_t kSlot16 = kSlotBytes >> 4;   // descriptors count 16 bytes
+    static __device__ __forceinline__ void qk(uint32_t leader, uint32_t d, uint64_t q, uint64_t k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t o = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
+            umma_ss(leader, d, q + o, k + o, kIdescQK, i > 0);
+        }
+    }
+    template <int HALF>
+    static __device__ __forceinline__ void pv(uint32_t leader, uint32_t d, uint32_t p, uint64_t v, bool accumulate) {
+#pragma unroll
+        for (int i = 4 * HALF; i < 4 * HALF + 4; ++i)
+            umma_ts(leader, d, p + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
+    }
+    __device__ void products(uint32_t tmem_base) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm);
+        const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024);
+        const uint64_t k0 = umma_desc(smu + Cfg::kOffSlots, 16, 1024), v0 = umma_desc(smu + Cfg::kOffSlots, 16384, 1024);
+        const uint32_t bar = uniform(bars);
+        constexpr uint32_t NS = Cfg::kSlots;
+        // Position in the ring: slot and parity of its full barrier.
+        struct Pos {
+            uint32_t slot, ph;
+            __device__ __forceinline__ Pos next() const {
+                return slot + 1 == NS ? Pos{0, ph ^ 1} : Pos{slot + 1, ph};
+            }
+        };
+        Pos pos = {0, 0};        // the next tile
+        uint32_t unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
+        bool ok = true;
+        Unit u;
+        auto full = [&](const Pos& x) { return wait(bar + kBarFull + 8 * x.slot, x.ph); };
+        while (ok && uniform((int)next(u))) {
+            const int tiles = uniform(active(u, 1) ? 2 : 1), steps = uniform(u.steps);
+            const Sight x = sight(u);
+            // the step that holds the prefix's last, partly filled tile (-1: none)
+            int ragged = -1;
+            if (!F16 && !TREE && u.len % kStep) {
+                const int i = u.len / kStep - u.step0 - u.rot;
+                if (u.len / kStep < u.step0 + u.steps) ragged = i < 0 ? i + u.steps : i;
+            }
+            ragged = uniform(ragged);
+            if (!(ok = full(pos))) break;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (w >= tiles) break;
+                uint32_t& n = w ? unit1 : unit0;
+                if (!(ok = wait(bar + kBarQ + 8 * w, n))) break;
+                n ^= 1;
+                tc_fence_after();
+                qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + pos.slot * kSlot16);
+                umma_commit(leader, bar + kBarS + 8 * w);
+            }
+            if (!ok) break;
+            umma_commit(leader, bar + kBarEmpty + 8 * pos.slot);
+            if (!(ok = full(pos.next()))) break;
+            // Between one step's last product and the next step's first only the wait for P stands: K(j + 1) is
+            // waited for while PV(0, j) runs, V(j + 1) while QK(0, j + 1) does.
+            for (int j = 0; j < steps; ++j) {
+                const bool more = j + 1 < steps;
+                const Pos v = pos.next(), k = v.next();   // V(j), K(j + 1)
+                if constexpr (TREE && !F16) {   // the same for the first tokens' end and the window's start
+                    const int t0 = uniform(step_of(u, x, j) * kStep), valid = min(kStep, u.len - t0);
+                    const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
+                    if (valid < kStep || h0 < h1) {
+                        const uint32_t s = sm + Cfg::kOffSlots + v.slot * kSlotBytes;
+                        for (int i = lane; i < kStep * 8; i += 32)
+                            if (const int r = i >> 3; r >= valid || (r >= h0 && r < h1)) {
+                                sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                                sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
+                            }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                    }
+                }
+                if (!TREE && j == ragged) {
+                    // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
+                    const int valid = u.len % kStep;
+                    const uint32_t s = sm + Cfg::kOffSlots + v.slot * kSlotBytes;
+                    for (int i = valid * 8 + lane; i < kStep * 8; i += 32) {
+                        sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                        sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= tiles) break;
+                    uint32_t& n = w ? p1 : p0;
+                    if (!(ok = wait(bar + kBarP + 8 * w, n))) break;
+                    tc_fence_after();
+                    pv<0>(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, j > 0);
+                    if (!(ok = wait(bar + kBarP2 + 8 * w, n))) break;
+                    n ^= 1;
+                    tc_fence_after();
+                    pv<1>(leader, tmem + 256 + w * 128, tmem + w * 128, v0 + v.slot * kSlot16, true);
+                    if (w == 0 && more && !(ok = full(k))) break;
+                    if (more) qk(leader, tmem + w * 128, q0 + w * kSlot16, k0 + k.slot * kSlot16);
+                    umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
+                    if (w == 0 && more && !(ok = full(k.next()))) break;
+                }
+                if (!ok) break;
+                umma_commit(leader, bar + kBarEmpty + 8 * v.slot);
+                if (more) umma_commit(leader, bar + kBarEmpty + 8 * k.slot);
+                pos = k;   // after the last step: the next unit's K(0)
+            }
+        }
+        // products in flight read shared memory and TMEM: let them end, whichever role gave up
+        umma_commit(leader, bar + kBarDrain);
+        __syncwarp();
+        (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
+    }
+
+    // ---------------------------------------------------------------- softmax
+    // The warp's 32 query rows into its tile's operand, two rows (16 lanes each) per asynchronous copy; returns
+    // the factor from S to log2 units of this lane's own row, 32 * (warp % 4) + lane.  The loops stay
+    // rolled: a short prefix waits for this code's first fetch longer than for its execution.
+    __device__ __forceinline__ float load_q(const Unit& u, int tile) const {
+        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, half = lane >> 4, w = lane & 15;
+        const uint32_t base = sm + Cfg::kOffQ + tile * kSlotBytes;
+        {
+            const uint32_t dst = base + (w >> 3) * 16384;
+            const int row0 = u.rt * kUnitRows + tile * kTileRows + r0 + half;
+            int seq = row0 / a.QG, q = row0 - seq * a.QG;
+            const uint16_t* src = a.query + ((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG * kHeadDim + 8 * w;
+            const long long skip = (long long)a.Hk * a.QG * kHeadDim;
+#pragma unroll 2
+            for (int i = 0; i < 16; ++i) {
+                const int r = r0 + 2 * i + half;
+                const bool live = row0 + 2 * i < u.rows;   // else: zeros, and no read
+                cp_async16(dst + r * 128 + (((w & 7) ^ (r & 7)) << 4), live ? src + q * kHeadDim : a.query, live ? 16u : 0u);
+                q += 2;
+                if (q >= a.QG) {   // the group size is above 2
+                    q -= a.QG;
+                    src += skip;
+                }
+            }
+            cp_async_wait_all();
+            __syncwarp();
+        }
+        float c = a.qk_scale_log2;
+        if constexpr (TQ) c *= __uint_as_float(lds32v(bars + kPowerAt));
+        if constexpr (F16) {
+            // This lane's row times a power of two that brings its largest |q| into [2^14, 2^15): f16 then
+            // keeps every bf16 bit.  The magnitudes of bf16 values order like their bits.
+            const uint32_t row = base + (r0 + lane) * 128;
+            const int x = lane & 7;
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                uint32_t v[4];
+                lds128(row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4), v[0], v[1], v[2], v[3]);
+                mx = __vmaxs2(mx, __vmaxs2(__vmaxs2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu),
+                                           __vmaxs2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu)));
+            }
+            const int top = max(mx & 0xFFFFu, mx >> 16);   // bf16 bits
+            int e = top ? 14 - ((top >> 7) - 127) : 0;
+            e = max(-100, min(100, e));
+            const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
+            c *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t at = row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4);
+                uint32_t v[4];
+                lds128(at, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = pack_f16(bf16_lo(v[k]) * pw, bf16_hi(v[k]) * pw);
+                sts128(at, v[0], v[1], v[2], v[3]);
+            }
+        }
+        fence_proxy_async_shared();
+        return c;
+    }
+
+    // Query rows of one unit for this thread's tile.
+    struct Rows {
+        bool on, live;       // the tile has rows; this thread has one
+        long long head;      // (sequence, KV head)
+        int q;
+        float c;             // from S to log2 units
+        int i, lo;           // TREE: drafted token; the first token of its window
+    };
+    __device__ __forceinline__ Rows start_unit(const Unit& u, int tile, int r) const {
+        Rows w;
+        w.on = active(u, tile);
+        const int row = u.rt * kUnitRows + tile * kTileRows + r;
+        w.live = row < u.rows;
+        w.head = (long long)(u.seq0 + row / a.QG) * a.Hk + u.h;
+        w.q = row % a.QG;
+        w.c = 0.f;
+        w.i = w.lo = 0;
+        if constexpr (TREE) {
+            w.i = row / a.QG;
+            if (a.window > 0 && w.live) {
+                // its position: behind the cached tokens and the drafted ones that it sees
+                int before = w.i;
+                if (a.masks) {
+                    const int drafted = u.rows / a.QG;
+                    const uint32_t* m = a.masks + (long long)(u.seq0 + w.i) * a.words;
+                    before = 0;
+                    for (int k = 0; k < a.words && 32 * k < drafted; ++k) {
+                        uint32_t bits = __ldcg(m + k) & below(drafted - 32 * k);
+                        if (w.i >> 5 == k) bits &= ~(1u << (w.i & 31));
+                        before += __popc(bits);
+                    }
+                }
+                w.lo = max(0, u.len - u.rows / a.QG + before + 1 - min(a.window, 1 << 30));
+            }
+        }
+        if (w.on) {   // every product with the last unit's rows has ended: their S was read
+            w.c = load_q(u, tile);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarQ + 8 * tile);
+        }
+        return w;
+    }
+
+    static __device__ __forceinline__ uint32_t below(int n) {   // bits 0 .. n-1
+        return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+    }
+    // The tokens t0 .. t0+31 of the sequence that this row sees, a bit each.  Cached token t: inside the row's window, or one of
+    // the first.  Drafted token j: its bit of the row's mask; without masks j <= i, and the window as for cached tokens.
+    __device__ __forceinline__ uint32_t visible(const Unit& u, const Rows& w, const Sight& x, int t0) const {
+        uint32_t in = 0xFFFFFFFFu;
+        if (a.window > 0) in = below(a.num_first - t0) | ~below(w.lo - t0);
+        const uint32_t old = below(x.ctx - t0);
+        const int j0 = t0 - x.ctx;                  // drafted token of bit 0
+        const uint32_t fresh = below(x.drafted - j0) & ~old;
+        if (!a.masks) return in & (old | (fresh & below(w.i + 1 - j0)));
+        uint32_t bits = 0;
+        if (fresh && w.live) {
+            const uint32_t* m = a.masks + (long long)(u.seq0 + w.i) * a.words;
+            auto word = [&](int k) { return k >= 0 && k < a.words ? __ldcg(m + k) : 0u; };
+            const int k = j0 >> 5, sh = j0 & 31;    // floor and remainder, also below zero
+            bits = __funnelshift_r(word(k), sh ? word(k + 1) : 0u, sh);
+        }
+        return (in & old) | (fresh & bits);
+    }
+
+    __device__ void softmax(uint32_t tmem_base, int tile) {
+        const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+        const uint32_t lanes = (uint32_t)(r & ~31) << 16;
+        const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
+        unsigned ns = 0, no = 0, step = 0;
+        Unit u;
+        while (next(u)) {
+            const Rows w = start_unit(u, tile, r);
+            const Sight x = sight(u);
+            constexpr float below = F16 ? kBelow : 0.f;
+            float m = 0.f, l = 0.f, F = 1.f;   // m: the reference, which l and O count from
+            for (int j = 0; j < u.steps; ++j, ++step) {
+                const int valid = tokens_of(u, x, j);
+                const unsigned st = step % Cfg::kScales;
+                if (F16 && !wait(bars + kBarScFull + 8 * st, step / Cfg::kScales & 1)) return;
+                if (w.on) {
+                    if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
+                    tc_fence_after();
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld32(s[k], tS + 32 * k);
+                    tmem_wait_ld();
+                    if constexpr (F16) {   // the K scales
+                        const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t f[16];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const int c = (k & 1) * 16 + i;
+                                mul2(s[k >> 1][c], s[k >> 1][c + 1], f[i], f[i + 1]);
+                            }
+                        }
+                    }
+                    if constexpr (TREE) {
+                        // only the steps with drafted tokens and those where some row's window starts are looked at bit by bit
+                        const int t0 = step_of(u, x, j) * kStep;
+                        if (t0 + kStep > x.ctx || (a.window > 0 && t0 < u.len - a.window && t0 + kStep > a.num_first)) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t see = visible(u, w, x, t0 + 32 * k);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(see >> i & 1u)) s[k][i] = 0xFF800000u;   // -inf
+                            }
+                        }
+                    } else if (valid < kStep) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * k + i >= valid) s[k][i] = 0xFF800000u;   // -inf
+                    }
+                    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[0][i]), __uint_as_float(s[0][i + 1])));
+                        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[1][i]), __uint_as_float(s[1][i + 1])));
+                        t2 = fmaxf(t2, fmaxf(__uint_as_float(s[2][i]), __uint_as_float(s[2][i + 1])));
+                        t3 = fmaxf(t3, fmaxf(__uint_as_float(s[3][i]), __uint_as_float(s[3][i + 1])));
+                    }
+                    const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * w.c, -1e30f);
+                    float nF = 1.f;
+                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
+                    if (j == 0) {
+                        m = top - below;
+                    } else {
+                        const bool up = top > m + (kLazy + below);
+                        if (__any_sync(kLanes, up || nF != F)) {
+                            float f = F / nF;
+                            if (nF == F) f = 1.f;
+                            if (up) {
+                                const float e = ex2(m - (top - below));
+                                m = top - below;
+                                l *= e;
+                                f *= e;
+                            }
+                            rescale(tO, f);
+                        }
+                    }
+                    F = nF;
+                    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            fma2(s[k][i], s[k][i + 1], w.c, -m);
+                            fma2(s[k][i + 2], s[k][i + 3], w.c, -m);
+                            float2 x, y;
+                            x.x = ex2(__uint_as_float(s[k][i]));
+                            x.y = ex2(__uint_as_float(s[k][i + 1]));
+                            y.x = ex2(__uint_as_float(s[k][i + 2]));
+                            y.y = ex2(__uint_as_float(s[k][i + 3]));
+                            add2(la, x);
+                            add2(lb, y);
+                            p[i / 2] = F16 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                            p[i / 2 + 1] = F16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                        }
+                        tmem_st16(tS + 16 * k, p);   // over S, which is in registers
+                        if (k & 1) {   // the product of the first half runs while the second is computed
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bars + (k == 1 ? kBarP : kBarP2) + 8 * tile);
+                        }
+                    }
+                    l += (la.x + la.y) + (lb.x + lb.y);
+                }
+                if (F16) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * st);
+                }
+            }
+            if (!w.on) continue;
+            if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
+            tc_fence_after();
+            store_partial(u, tile, tO, w, m, l, l > 0.f ? F / l : 0.f);
+            tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
+        }
+    }
+
+    // The warp's 32 rows of O, times inv, to the partials.  A thread holds a row, and storing rows from
+    // there would touch 32 lines per instruction; each half (64 columns) goes through the warp's own rows of
+    // its tile's query operand, which no product reads any more, and out two rows per instruction.
+    __device__ __forceinline__ void store_partial(const Unit& u, int tile, uint32_t tO, const Rows& w, float m, float l,
+                                                  float inv) const {
+        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96;
+        const uint32_t stage = sm + Cfg::kOffQ + tile * kSlotBytes + r0 * 128;
+        auto at = [&](int r, int c) {   // 16 bytes c of the half row r
+            return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        };
+        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
+        const int rows = min(32, u.rows - row0);   // may be negative
+        const long long mine = (w.head * a.slots + u.slot) * a.QG + w.q;
+        if (w.live) {
+            a.part_l[mine] = l;
+            a.part_m[mine] = m * kLn2S;
+            if (u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
+        }
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            uint32_t s[2][32];
+            tmem_ld32(s[0], tO + 64 * half);
+            tmem_ld32(s[1], tO + 64 * half + 32);
+            tmem_wait_ld();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t* x = &s[c >> 3][(c & 7) * 4];
+                sts128(at(lane, c), __float_as_uint(__uint_as_float(x[0]) * inv),
+                       __float_as_uint(__uint_as_float(x[1]) * inv), __float_as_uint(__uint_as_float(x[2]) * inv),
+                       __float_as_uint(__uint_as_float(x[3]) * inv));
+            }
+            __syncwarp();
+            const int c = lane & 15;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                const long long dst = __shfl_sync(kLanes, mine, r);
+                uint32_t v0, v1, v2, v3;
+                lds128(at(r, c), v0, v1, v2, v3);
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(a.part_o + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
+            }
+        }
+        __syncwarp();   // the next unit's query rows are written by other lanes
+    }
+    // O *= f, one row per thread (rare; few registers, since S is held meanwhile).
+    static __device__ __forceinline__ void rescale(uint32_t tO, float f) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o, tO + 16 * k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(tO + 16 * k, o);
+        }
+        tmem_wait_st();
+    }
+};
+
+template <int KV, class Args>
+__global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
+    pda_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
+                      const Args a) {
+    using Cfg = SharedCfg<KV>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sm = smem_addr(smem);
+    const uint32_t bars = sm + Cfg::kOffBars;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Cfg::kSlots; ++i) {
+            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 ? kConvertWarps : 1);
+            mbar_init(bars + kBarEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + kBarQ + 8 * i, 4);
+            mbar_init(bars + kBarS + 8 * i, 1);
+            mbar_init(bars + kBarP + 8 * i, 4);
+            mbar_init(bars + kBarP2 + 8 * i, 4);
+            mbar_init(bars + kBarO + 8 * i, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(bars + kBarRawFull + 8 * i, 1);
+            mbar_init(bars + kBarRawEmpty + 8 * i, kConvertWarps);
+            mbar_init(bars + kBarScRaw + 8 * i, 1);
+            mbar_init(bars + kBarScFull + 8 * i, 1);
+            mbar_init(bars + kBarScEmpty + 8 * i, 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + kBarUnitFull + 8 * i, 1);
+            mbar_init(bars + kBarUnitEmpty + 8 * i, Cfg::kReaders);
+        }
+        mbar_init(bars + kBarDrain, 1);
+        sts32v(bars + kAbortAt, (sm & 1023u) ? 1u : 0u);   // the operands' swizzle needs the alignment
+        fence_mbar_init();
+        prefetch_tensormap(&kv_map);
+        if (Cfg::kF16) prefetch_tensormap(&sc_map);
+    }
+    // Behind the pass over the sequences' own tokens there is no wait for it here: every CTA of that pass has waited for
+    // everything before the step before it lets this grid start, and nothing of its own is read.  What was written
+    // before the step lies in L2 then, and every read of it in this grid goes there (ld.cg, cp.async.cg, TMA): a line
+    // that an earlier grid left in this SM's L1 is not looked at.
+    if (a.first) grid_dependency_wait();
+    Prefix<KV, Args> p(a, sm);
+    Split split;
+    Unit first;
+    int at, end;
+    if (warp == 11) {
+        split = make_split(a, gridDim.x, blockIdx.x == 0);
+        if constexpr (std::is_same<Args, TreeArgs>::value)
+            if (blockIdx.x == 0 && (threadIdx.x & 31) == 0) *a.refused = split.refused;
+        at = (int)min((long long)blockIdx.x * split.per, (long long)split.total);
+        end = at + min(split.per, split.total - at);
+        first = find_unit(a, split, at, end);
+        p.put(first);
+    }
+    if constexpr (Cfg::kTq) {
+        if (warp == 12) p.make_table();
+    }
+    if (warp == 9) tmem_alloc(bars + kTmemAt, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = lds32v(bars + kTmemAt);
+    allow_dependent_launch();
+    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
+    const bool fine = lds32v(bars + kAbortAt) == 0u;
+    if (warp < 8) {
+        if constexpr (Cfg::kF16)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if (fine) p.softmax(tmem, warp >> 2);
+    } else {
+        if constexpr (Cfg::kF16)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (fine) {
+            if (warp == 8)
+                p.copies(&kv_map, &sc_map);
+            else if (warp == 9)
+                p.products(tmem);
+            else if (warp == 11)
+                p.give(split, first, at, end);
+            else if (Cfg::kF16 && warp == 10)
+                p.scales();
+            else if (Cfg::kF16 && warp >= 12)
+                p.convert();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0 && lds32v(bars + kAbortAt) && a.err_word) atomicOr(a.err_word, PDA_ERRW_PIPELINE_TIMEOUT);
+    if (warp == 9) tmem_free(tmem, 512);
+    grid_dependency_wait();   // behind the own pass this grid ends after it: the join waits for one grid alone
+}
+
+template <int KV, class Args>
+static int launch_prefix(const Args& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int ctas,
+                         cudaStream_t stream) {
+    using Cfg = SharedCfg<KV>;
+    static bool attr_set[64] = {false};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PDA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(pda_prefix_kernel<KV, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
+                cudaSuccess)
+                return PDA_ERR_LAUNCH;
+            attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pda_prefix_kernel<KV, Args>, kv_map, sc_map, a) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+}  // namespace pda

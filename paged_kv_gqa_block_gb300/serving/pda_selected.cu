@@ -1,5 +1,5 @@
 // pda_selected.cu -- launches of the one-launch kernel over short lists (pda_selected.cuh): selected blocks,
-// and own tokens beside a shared prefix.
+// own tokens beside a shared prefix, and the window of pda_decode_window.
 #include <mutex>
 
 #include "pda.h"
@@ -38,10 +38,10 @@ static Shape selected_shape(long long units, int tiles, int sms, int wps, int nw
     return s;
 }
 
-template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
+template <int KV, int NT, int S, int NWMAX, int MINB, int LIST>
 static int launch_clusters(bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, Shape shape,
-                           cudaStream_t stream) {
-    auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB, OWN>;
+                           int window, int num_first, cudaStream_t stream) {
+    auto kernel = pda_selected_kernel<KV, NT, S, NWMAX, MINB, LIST>;
     static bool attr_set[64] = {false};
     static std::mutex mu;
     int dev = 0;
@@ -68,17 +68,22 @@ static int launch_clusters(bool behind, const DecodeArgs& a, const CUtensorMap& 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C, (int)behind) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C, (int)behind, window, num_first) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
 }
 
-template <bool OWN, int KV, int NT, int S, int NWMAX, int WPS>
+template <int LIST, int KV, int NT, int S, int NWMAX, int WPS>
 static int launch_clusters_of(bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
-                              cudaStream_t stream) {
+                              cudaStream_t stream, int window = 0, int num_first = 0) {
     const int sms = device_sm_count();
     if (sms <= 0) return PDA_ERR_CUDA;
-    const Shape shape = selected_shape(a.B, (a.MB * a.BS + 15) / 16, sms, WPS, NWMAX);
+    int tiles = (a.MB * a.BS + 15) / 16;
+    if (LIST == kListWindow) {   // at most: the window may begin and end within a tile
+        const long long seen = ((long long)num_first + 15) / 16 + ((long long)window + 30) / 16;
+        tiles = (int)(seen < tiles ? seen : tiles);
+    }
+    const Shape shape = selected_shape(a.B, tiles, sms, WPS, NWMAX);
     if ((long long)a.B * shape.C > 0x7FFFFFFFll) return PDA_ERR_INVALID_ARG;
-    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, OWN>(behind, a, kv_map, sc_map, shape, stream);
+    return launch_clusters<KV, NT, S, NWMAX, WPS / NWMAX, LIST>(behind, a, kv_map, sc_map, shape, window, num_first, stream);
 }
 
 // bf16: eight warps per SM with rings of three tiles, where six with four took longer: 512 units of 512 tokens at 16
@@ -88,15 +93,15 @@ static int launch_clusters_of(bool behind, const DecodeArgs& a, const CUtensorMa
 int launch_selected_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                              cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_BF16, 1, 3, 8, 8>(false, a, kv_map, kv_map, stream);
-        return launch_clusters_of<false, PDA_KV_BF16, 2, 3, 8, 8>(false, a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<kListSelected, PDA_KV_BF16, 1, 3, 8, 8>(false, a, kv_map, kv_map, stream);
+        return launch_clusters_of<kListSelected, PDA_KV_BF16, 2, 3, 8, 8>(false, a, kv_map, kv_map, stream);
     }
     if (kv_dtype == PDA_KV_TQ4) {
-        if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_TQ4, 1, 6, 6, 12>(false, a, kv_map, sc_map, stream);
-        return launch_clusters_of<false, PDA_KV_TQ4, 2, 6, 4, 8>(false, a, kv_map, sc_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<kListSelected, PDA_KV_TQ4, 1, 6, 6, 12>(false, a, kv_map, sc_map, stream);
+        return launch_clusters_of<kListSelected, PDA_KV_TQ4, 2, 6, 4, 8>(false, a, kv_map, sc_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<false, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(false, a, kv_map, sc_map, stream);
-    return launch_clusters_of<false, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(false, a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<kListSelected, PDA_KV_FP8_E4M3, 1, 3, 6, 12>(false, a, kv_map, sc_map, stream);
+    return launch_clusters_of<kListSelected, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(false, a, kv_map, sc_map, stream);
 }
 
 long long own_clusters_ctas(const pda_plan_t* p, int sms) {
@@ -109,11 +114,22 @@ long long own_clusters_ctas(const pda_plan_t* p, int sms) {
 int launch_own_clusters(int kv_dtype, bool behind, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                         cudaStream_t stream) {
     if (kv_dtype == PDA_KV_BF16) {
-        if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_BF16, 1, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
-        return launch_clusters_of<true, PDA_KV_BF16, 2, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
+        if (a.QG <= 8) return launch_clusters_of<kListOwn, PDA_KV_BF16, 1, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
+        return launch_clusters_of<kListOwn, PDA_KV_BF16, 2, 3, 8, 8>(behind, a, kv_map, kv_map, stream);
     }
-    if (a.QG <= 8) return launch_clusters_of<true, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(behind, a, kv_map, sc_map, stream);
-    return launch_clusters_of<true, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(behind, a, kv_map, sc_map, stream);
+    if (a.QG <= 8) return launch_clusters_of<kListOwn, PDA_KV_FP8_E4M3, 1, 4, 6, 12>(behind, a, kv_map, sc_map, stream);
+    return launch_clusters_of<kListOwn, PDA_KV_FP8_E4M3, 2, 4, 4, 8>(behind, a, kv_map, sc_map, stream);
+}
+
+int launch_window_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int window,
+                           int num_first, cudaStream_t stream) {
+    auto of = [&](auto launch) { return launch(false, a, kv_map, sc_map, stream, window, num_first); };
+    const bool narrow = a.QG <= 8;
+    if (kv_dtype == PDA_KV_BF16)
+        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_BF16, 1, 3, 8, 8>) : of(launch_clusters_of<kListWindow, PDA_KV_BF16, 2, 3, 8, 8>);
+    if (kv_dtype == PDA_KV_TQ4)
+        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 1, 6, 6, 12>) : of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 2, 6, 4, 8>);
+    return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 1, 3, 6, 12>) : of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 2, 4, 4, 8>);
 }
 
 }  // namespace pda

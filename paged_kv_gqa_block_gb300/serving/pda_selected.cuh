@@ -1,7 +1,8 @@
 // pda_selected.cuh -- attention over short lists in one launch: the tiles of a (sequence, KV head) are split
-// over the warps of a thread-block cluster, whose results are joined in shared memory.  Two lists: the selected
-// blocks of each (sequence, KV head) (pda_decode_selected), whose result is the output, and a sequence's own
-// tokens beside a shared prefix (OWN, pda_decode_shared), whose result is a partial for the join there.
+// over the warps of a thread-block cluster, whose results are joined in shared memory.  Three lists: the selected
+// blocks of each (sequence, KV head) (pda_decode_selected) and the first and last tokens of a sequence
+// (WINDOW, pda_decode_window), whose result is the output, and a sequence's own tokens beside a shared prefix
+// (OWN, pda_decode_shared), whose result is a partial for the join there.
 //
 // Such lists are a few thousand tokens and of like length, so a unit needs neither partials in
 // global memory nor a second launch: C CTAs of nw warps take an equal run of its 16-token tiles each,
@@ -17,12 +18,14 @@
 #include <cooperative_groups.h>
 
 #include "pda_decode.cuh"
+#include "pda_window.cuh"
 
 namespace pda {
 
 namespace cg = cooperative_groups;
 
 constexpr int kSelRows = 16;   // query rows of a unit, at most
+enum { kListSelected = 0, kListOwn = 1, kListWindow = 2 };
 
 template <int KV, int S>
 struct SelectedCfg {
@@ -62,10 +65,11 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, long long row,
     }
 }
 
-template <int KV, int NT, int S, int NWMAX, int MINB, bool OWN>
+template <int KV, int NT, int S, int NWMAX, int MINB, int LIST>
 __global__ void __launch_bounds__(32 * NWMAX, MINB)
     pda_selected_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
-                        const DecodeArgs a, const int C, const int behind) {
+                        const DecodeArgs a, const int C, const int behind, const int window, const int num_first) {
+    constexpr bool OWN = LIST == kListOwn, WINDOW = LIST == kListWindow;
     using D = Decode<KV, NT, S, false>;
     using Cfg = DecodeCfg<KV, S>;
     using Sel = SelectedCfg<KV, S>;
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     };
 
     const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
-    const int head = unit % a.sel_heads, list = OWN ? unit / a.sel_heads : unit;   // the table row and length
+    const int head = unit % a.sel_heads, list = OWN || WINDOW ? unit / a.sel_heads : unit;   // the table row and length
     const int max_ctx = a.MB * a.BS;
     // What a warp needs first is asked for at once: the length, its part of the table as if the list were full (a
     // selected list mostly is, and the first warp's part does not depend on it), and the query rows.
@@ -115,43 +119,48 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     int t0, t1;
     run_of(max_ctx >> 4, t0, t1);
     int e0 = t0 >> ts;
-    int ent = e0 + lane < a.MB ? load_input<OWN>(table + e0 + lane) : 0;
+    int ent = !WINDOW && e0 + lane < a.MB ? load_input<OWN>(table + e0 + lane) : 0;
     const int raw = load_input<OWN>(a.context_lens + list);
     uint32_t qn[NT][16];
     {
         UnitIt u = {unit, 0, 0, 0, 0, 0};
         D::template load_q<OWN>(a, u, qn, lane);
     }
-    if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!OWN || head == 0) && a.err_word)
+    if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!(OWN || WINDOW) || head == 0) && a.err_word)
         atomicOr(a.err_word, PDA_ERRW_BAD_CONTEXT_LEN);
     const int ctx = sanitize_ctx(raw, max_ctx);
     if (OWN && ctx == 0) return leave();   // every CTA of the cluster
-    run_of((ctx + 15) >> 4, t0, t1);
+    const WindowTiles win(WINDOW ? ctx : 0, window, num_first);
+    run_of(WINDOW ? win.tiles : (ctx + 15) >> 4, t0, t1);
     bool ok = true;
 
     if (t0 < t1) {
         float cent = 0.f;
         if constexpr (TQ) cent = __ldg(a.centroids + (lane & 15));
-        const int entries = ((t1 - 1) >> ts) + 1;
-        if (e0 != t0 >> ts) {
+        const int entries = WINDOW ? (ctx + a.BS - 1) >> a.bs_shift : ((t1 - 1) >> ts) + 1;
+        if constexpr (WINDOW) {
+            e0 = win.token(t0) >> a.bs_shift;
+            ent = e0 + lane < entries ? __ldg(table + e0 + lane) : 0;
+        } else if (e0 != t0 >> ts) {
             e0 = t0 >> ts;
             ent = e0 + lane < entries ? load_input<OWN>(table + e0 + lane) : 0;
         }
         const uint64_t policy = l2_policy_evict_first();
         int issued = 0;
         auto issue = [&](int t, int stage) {   // tiles in order
-            if ((t >> ts) - e0 >= 32) {
-                e0 += 32;
+            const int e = WINDOW ? win.token(t) >> a.bs_shift : t >> ts;
+            if (e - e0 >= 32) {
+                e0 = WINDOW ? e : e0 + 32;
                 ent = e0 + lane < entries ? load_input<OWN>(table + e0 + lane) : 0;
             }
-            const int phys = __shfl_sync(kFull, ent, (t >> ts) - e0);
+            const int phys = __shfl_sync(kFull, ent, e - e0);
             if (lane == 0) {
-                const int slot0 = (t & ((1 << ts) - 1)) * kTileTokens;
+                const int slot0 = WINDOW ? win.token(t) & (a.BS - 1) : (t & ((1 << ts) - 1)) * kTileTokens;
                 const uint32_t bar = bar0 + 8 * stage;
                 mbar_arrive_expect_tx(bar, Cfg::kTileBytes + Cfg::kScaleTx);
                 tma_load_5d(sring + stage * Cfg::kTileBytes, &kv_map, bar, 0, slot0, 0, head, phys, policy);
-                if constexpr (F16)
-                    tma_load_4d(sscale + stage * Cfg::kScaleBytes, &sc_map, bar, slot0, 0, head, phys, policy);
+                if constexpr (F16)   // whole tiles of scales: a copy's innermost coordinate keeps its 16 bytes' alignment
+                    tma_load_4d(sscale + stage * Cfg::kScaleBytes, &sc_map, bar, WINDOW ? slot0 & ~15 : slot0, 0, head, phys, policy);
                 if ((phys < 0 || (long long)phys >= a.num_cache_blocks) && a.err_word)
                     atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
             }
@@ -225,20 +234,26 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
         int cs = 0;
         uint32_t cph = 0;
         for (int t = t0; t < t1;) {
-            const bool two = t + 1 < t1;
+            // only a step's last tile may be partly seen
+            const bool two = t + 1 < t1 && (!WINDOW || win.count(t) == kTileTokens);
             const int s0 = cs, s1 = s0 + 1 == S ? 0 : s0 + 1;
             const uint32_t ph0 = cph, ph1 = s0 + 1 == S ? cph ^ 1u : cph;
             if (!mbar_wait_warp(bar0 + 8 * s0, ph0, a.timeout_ns) || (two && !mbar_wait_warp(bar0 + 8 * s1, ph1, a.timeout_ns))) {
                 ok = false;
                 break;
             }
-            const int v0 = ctx - t * kTileTokens;
+            const int v0 = WINDOW ? win.count(t) : ctx - t * kTileTokens, v1 = WINDOW ? (two ? win.count(t + 1) : 0) : v0 - kTileTokens;
             const uint32_t a0 = sring + s0 * Cfg::kTileBytes, a1 = sring + s1 * Cfg::kTileBytes;
             const uint8_t* c0 = scales + s0 * Cfg::kScaleBytes;
             const uint8_t* c1 = scales + s1 * Cfg::kScaleBytes;
+            if constexpr (WINDOW && F16) {   // the tile in which the window begins: its tokens' scales start as far into their tile
+                constexpr int field = FP8 ? 4 : 2;
+                c0 += (win.token(t) & 15) * field;
+                if (two) c1 += (win.token(t + 1) & 15) * field;
+            }
             if (two) {
                 const uint32_t st[2] = {a0, a1};
-                const int vv[2] = {v0, v0 - kTileTokens};
+                const int vv[2] = {v0, v1};
                 if constexpr (TQ) {
                     const __half* const sc[2] = {reinterpret_cast<const __half*>(c0), reinterpret_cast<const __half*>(c1)};
                     D::template step_tq<2>(st, sc, vv, cq, tq_lut, qf, acc, m2, mt, ls, zs, F, rF, lane);

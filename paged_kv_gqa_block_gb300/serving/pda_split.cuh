@@ -1,5 +1,6 @@
-// pda_split.cuh -- which rows and which tokens a CTA of pda_decode_shared's prefix pass takes.  Only integers and warp-wide
-// exchanges, so that the same code also compiles for the host, where its pieces are checked.
+// pda_split.cuh -- which rows and which tokens a CTA of the prefix pass (pda_prefix.cuh) takes: of pda_decode_shared's prefixes,
+// or of pda_decode_tree's sequences.  Only integers and warp-wide exchanges, so that the same code also compiles for the host,
+// where its pieces are checked.
 #pragma once
 
 #include <cstdint>
@@ -28,7 +29,42 @@ struct SharedArgs {
     int first;                   // this pass comes before the own tokens' one
     float qk_scale_log2;
     unsigned long long timeout_ns;
+    static constexpr int kBadStarts = PDA_ERRW_BAD_GROUP;
 };
+
+// pda_decode_tree: a group is a sequence, its rows are those of its drafted tokens, and its tokens are the cached ones and,
+// behind them, the drafted.  group_starts: token_starts, over B = num_tokens tokens; prefix_table, prefix_lens: block_table,
+// context_lens.
+struct TreeArgs : SharedArgs {
+    const uint32_t* masks;       // [B][words], or null: token i sees the drafted tokens 0 .. i
+    const float* centroids;      // TQ4: [16]
+    int* refused;                // set to 1 by a call whose token_starts do not ascend, else to 0
+    int words;                   // 32-bit words of a mask
+    int window, num_first;       // window 0: none
+    static constexpr int kBadStarts = PDA_ERRW_BAD_TOKENS;
+};
+
+// What a sequence's drafted tokens see of it: every one of them misses tokens hole0 .. hole1-1, and the steps at, ..,
+// at + skip - 1 lie wholly within those.
+struct Sight {
+    int ctx, drafted;
+    int hole0, hole1;
+    int at, skip;
+};
+__device__ __forceinline__ Sight sight_of(const TreeArgs& a, int len, int drafted) {
+    Sight x = {};
+    x.ctx = len - drafted;
+    x.drafted = drafted;
+    // the first of them stands at position ctx at the earliest
+    const int start = a.window > 0 && a.window <= x.ctx ? x.ctx - a.window + 1 : 0;
+    if (start > a.num_first) {
+        x.hole0 = a.num_first;
+        x.hole1 = start;
+        x.at = (int)(((long long)a.num_first + kStep - 1) / kStep);
+        x.skip = start / kStep > x.at ? start / kStep - x.at : 0;
+    }
+    return x;
+}
 
 struct Unit {
     int g, h, rt;          // group, KV head, row tile
@@ -62,6 +98,28 @@ __device__ __forceinline__ Group group_shape(const SharedArgs& a, int g, int& ba
     x.steps = (x.len + kStep - 1) / kStep;
     return x;
 }
+__device__ __forceinline__ Group group_shape(const TreeArgs& a, int g, int& bad) {
+    Group x = {};
+    if (g >= a.NG) return x;
+    const int s0 = __ldcg(a.group_starts + g), s1 = __ldcg(a.group_starts + g + 1), ctx = __ldcg(a.prefix_lens + g);
+    x.seq0 = s0;
+    if (s0 < 0 || s1 < s0 || s1 > a.B) {
+        bad |= PDA_ERRW_BAD_TOKENS;
+        return x;
+    }
+    const int drafted = s1 - s0;
+    if (ctx < 0 || ctx > a.MP * a.BS) {
+        bad |= PDA_ERRW_BAD_CONTEXT_LEN;
+    } else if (drafted > a.MP * a.BS - ctx) {
+        bad |= PDA_ERRW_BAD_POSITION;
+    } else if (drafted > 0) {
+        x.len = ctx + drafted;
+        x.rows = drafted * a.QG;
+        x.tiles = (x.rows + kUnitRows - 1) / kUnitRows;
+        x.steps = (x.len + kStep - 1) / kStep - sight_of(a, x.len, drafted).skip;
+    }
+    return x;
+}
 // Of numbers that are not negative.  A CTA waits for this code's first fetch longer than for its execution, so
 // quotients that are wanted together are computed by lanes of one warp.
 __device__ __forceinline__ int quotient(int x, int d) { return (int)((unsigned)x / (unsigned)d); }
@@ -73,6 +131,7 @@ struct Split {
     int before, total;     // places of the groups before lane i's (of the first 32), and of all
     int per;               // places of a CTA's run
     int whole;             // if not 0: places of every row tile
+    bool refused;          // starts that do not ascend: there are no steps
     // Places of a row tile: its steps, and unused ones after them.  A CTA whose run goes on into another row tile
     // pays for it (store the rows, load others, refill the pipeline: kSwitch steps); either that is counted
     // as places between two tiles, or every tile has whole runs of its own.
@@ -82,7 +141,8 @@ struct Split {
 // `per`: an even share of all places, or, where that is no longer, the longest tile's share of the runs that every
 // tile can have; and at least 1/P of the longest prefix, so that a row tile is cut into at most P + 1 pieces
 // (the workspace's slots).
-__device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool report) {
+template <class Args>
+__device__ __forceinline__ Split make_split(const Args& a, int ctas, bool report) {
     const int lane = threadIdx.x & 31;
     Split s;
     int bad = 0;
@@ -126,14 +186,16 @@ __device__ __forceinline__ Split make_split(const SharedArgs& a, int ctas, bool 
         s.total += __reduce_add_sync(kLanes, more);
     }
     // groups that are not ascending may overlap, and name more rows than there are: no prefix then
-    if (__any_sync(kLanes, bad & PDA_ERRW_BAD_GROUP)) s.total = 0;
+    s.refused = __any_sync(kLanes, bad & Args::kBadStarts);
+    if (s.refused) s.total = 0;
     if (report && bad && a.err_word) atomicOr(a.err_word, bad);
     return s;
 }
 
 // One warp: the piece that starts at place `at` of the run of all places, or after the unused ones there, and ends
 // with its row tile or at `end`; `at` moves past it.  Without steps: there is none.
-__device__ __forceinline__ Unit find_unit(const SharedArgs& a, const Split& s, int& at, int end) {
+template <class Args>
+__device__ __forceinline__ Unit find_unit(const Args& a, const Split& s, int& at, int end) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
 #pragma unroll 1

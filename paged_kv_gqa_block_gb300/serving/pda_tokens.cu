@@ -1,0 +1,542 @@
+// pda_tokens.cu -- tokens of the cache, many at a time: pda_write_kv (stored in the cache's format), pda_read_kv (gathered
+// and dequantised) and pda_accept_tokens (the accepted path of drafted tokens moves to consecutive positions).
+//
+// The formats, per token and KV head, K and V apart:
+//   bf16   as given
+//   e4m3   scale = max |x| / 448 (1 for a row of zeros), code = e4m3(x / scale): pda_append_kv's arithmetic, division by
+//          division, so that a token has the same bytes whichever call wrote it
+//   TQ4    K: k_norm = f16(|k|), code = the number of midpoints of neighbouring centroids below fp32(k_d / k_norm)
+//          V: v_zero = f16(min v), v_scale = f16((max v - min v) / 15), code = rint((v_d - v_zero) / v_scale) in 0 .. 15
+// Every quotient is an IEEE division and |k| is rounded once, from 64 bits where 32 cannot tell to which f16 value, so that the
+// codes are a function of the values alone: two writes of one token, on any grid, give the same bytes.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pda.h"
+#include "pda_internal.h"
+#include "pda_ptx.cuh"
+
+namespace pda {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kTokThreads = 256;
+constexpr int kTokWarps = kTokThreads / 32;
+constexpr int kMaxTokensPerCta = 16;
+
+struct TokenArgs {
+    uint8_t* cache;              // read_kv does not write it
+    const int* block_table;      // [B][MB]
+    const int* token_starts;     // [B + 1]
+    const int* positions;        // [B]
+    const float* centroids;      // TQ4: [16]
+    int* err_word;
+    const uint16_t* k_new;       // write: rows k_stride elements apart
+    const uint16_t* v_new;
+    void* k_out;                 // read: [N][Hk][128]
+    void* v_out;
+    long long k_stride, v_stride;
+    long long num_cache_blocks, cache_block_bytes, meta_offset_bytes;
+    int num_tokens, B, Hk, MB, BS, bs_shift, per_cta;
+};
+
+// Where the CTA's tokens lie: byte offset of the block in the pool and slot, or a negative offset for a token that is no
+// sequence's or has no place.  False (in every thread) where token_starts do not ascend within [0, num_tokens].
+struct Places {
+    long long block[kMaxTokensPerCta];
+    int slot[kMaxTokensPerCta];
+};
+__device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int first, int n) {
+    bool bad = false;
+    for (int b = threadIdx.x; b <= a.B; b += kTokThreads) {
+        const int s = __ldg(a.token_starts + b);
+        bad |= s < 0 || s > a.num_tokens || (b < a.B && __ldg(a.token_starts + b + 1) < s);
+    }
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0 && a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_TOKENS);
+        return false;
+    }
+    if ((int)threadIdx.x < n) {
+        const int i = first + threadIdx.x;
+        int lo = 0, hi = a.B + 1;   // the number of starts that are not above i
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.token_starts + mid) <= i)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        const int b = lo - 1;
+        long long block = -1;
+        int slot = 0;
+        if (b >= 0 && b < a.B) {
+            const int p0 = __ldg(a.positions + b);
+            const long long pos = (long long)p0 + (i - __ldg(a.token_starts + b));
+            if (p0 >= 0) {
+                if (pos >= (long long)a.MB * a.BS) {
+                    if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_POSITION);
+                } else {
+                    const int id = __ldg(a.block_table + (long long)b * a.MB + (pos >> a.bs_shift));
+                    if (id < 0 || id >= a.num_cache_blocks) {
+                        if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
+                    } else {
+                        block = id * a.cache_block_bytes;
+                        slot = (int)pos & (a.BS - 1);
+                    }
+                }
+            }
+        }
+        at.block[threadIdx.x] = block;
+        at.slot[threadIdx.x] = slot;
+    }
+    __syncthreads();
+    return true;
+}
+
+// ------------------------------------------------------------------------- writing
+// The sorted codebook: midpoints of neighbours (15, then +inf) and the code of each rank.
+struct Codebook {
+    float mid[16];
+    uint32_t code[16];
+};
+__device__ __forceinline__ void sort_codebook(const float* centroids, Codebook& book, float* sorted) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const float c = __ldg(centroids + (lane & 15));
+        int rank = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float o = __shfl_sync(kAll, c, j);
+            rank += o < c || (o == c && j < lane);
+        }
+        if (lane < 16) {
+            sorted[rank] = c;
+            book.code[rank] = lane;
+        }
+        __syncwarp();
+        if (lane < 16) book.mid[lane] = lane < 15 ? __fmul_rn(__fadd_rn(sorted[lane], sorted[lane + 1]), 0.5f) : INFINITY;
+    }
+}
+
+__device__ __forceinline__ float half_warp_max(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
+    return x;
+}
+__device__ __forceinline__ float f16_saturated(float x) {
+    return __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
+}
+
+// fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.
+__device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS, int slot) {
+    float x[8];
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+        top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    top = half_warp_max(top);
+    const float scale = top > 0.f ? __fdiv_rn(top, 448.f) : 1.f;
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+    *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if ((lane & 15) == 0) scales[(lane >> 4) * BS + slot] = scale;
+}
+
+// TQ4: every lane holds four dimensions of K and of V, 4l .. 4l+3.
+__device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, uint2 kraw, uint2 vraw, const Codebook& book, int lane,
+                                          int BS, int slot) {
+    const float k[4] = {bf16_lo(kraw.x), bf16_hi(kraw.x), bf16_lo(kraw.y), bf16_hi(kraw.y)};
+    const float v[4] = {bf16_lo(vraw.x), bf16_hi(vraw.x), bf16_lo(vraw.y), bf16_hi(vraw.y)};
+    float sum = fmaf(k[0], k[0], fmaf(k[1], k[1], fmaf(k[2], k[2], k[3] * k[3])));
+    float lo = fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), hi = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(kAll, sum, o);
+        lo = fminf(lo, __shfl_xor_sync(kAll, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, o));
+    }
+    // |k| is rounded to f16 once: nine fp32 roundings of positive terms and the root are off by less than 2^-20, and where
+    // that does not decide the f16 value (one row in a thousand) the sum is taken again in 64 bits.  The sum is the same in
+    // every lane (a butterfly adds the same pairs), so the warp stays together.
+    const float root = sqrtf(sum);
+    uint16_t norm_bits = __half_as_ushort(__float2half_rn(fminf(root, 65504.f)));
+    const float up = fminf(__fmul_rn(root, 1.f + 9.5367431640625e-7f), 65504.f);
+    const float down = fminf(__fmul_rn(root, 1.f - 9.5367431640625e-7f), 65504.f);
+    if (__half_as_ushort(__float2half_rn(up)) != __half_as_ushort(__float2half_rn(down))) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += (double)k[i] * (double)k[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        // by way of fp32 without rounding twice: cut, and odd where something was cut off
+        const double exact = fmin(sqrt(s), 65504.0);
+        float cut = __double2float_rz(exact);
+        if ((double)cut != exact) cut = __uint_as_float(__float_as_uint(cut) | 1u);
+        norm_bits = __half_as_ushort(__float2half_rn(cut));
+    }
+    const float norm = __half2float(__ushort_as_half(norm_bits));
+    const float by = norm > 0.f ? norm : 1.f;
+    uint32_t kc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __fdiv_rn(k[i], by);
+        int r = book.mid[7] < x ? 8 : 0;
+        r += book.mid[r + 3] < x ? 4 : 0;
+        r += book.mid[r + 1] < x ? 2 : 0;
+        r += book.mid[r] < x ? 1 : 0;
+        kc |= book.code[r] << (4 * i);
+    }
+    const float zero = f16_saturated(lo), step = f16_saturated(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+    const float vby = step > 0.f ? step : 1.f;
+    uint32_t vc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[i], zero), vby)), 0.f), 15.f);
+        vc |= (uint32_t)c << (4 * i);
+    }
+    // even lanes store eight codes of K, odd lanes of V
+    const uint32_t give = lane & 1 ? kc : vc, got = __shfl_xor_sync(kAll, give, 1);
+    const uint32_t word = lane & 1 ? got | vc << 16 : kc | got << 16;
+    *reinterpret_cast<uint32_t*>(row + (lane & 1) * 64 + (lane >> 1) * 4) = word;
+    if (lane < 3) {
+        const uint16_t f = lane == 0 ? norm_bits : __half_as_ushort(__float2half_rn(lane == 1 ? step : zero));
+        fields[lane * BS + slot] = f;
+    }
+}
+
+// One warp per (token, KV head) at a time.
+template <int KV>
+__global__ void __launch_bounds__(kTokThreads) pda_write_kernel(const TokenArgs a) {
+    __shared__ Places at;
+    __shared__ Codebook book;
+    __shared__ float sorted[16];
+    const int first = blockIdx.x * a.per_cta, n = min(a.per_cta, a.num_tokens - first);
+    if constexpr (KV == PDA_KV_TQ4) sort_codebook(a.centroids, book, sorted);
+    if (!find_places(a, at, first, n)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;   // K and V of one head
+    for (int r = warp; r < n * a.Hk; r += kTokWarps) {
+        const int t = r / a.Hk, h = r - t * a.Hk;
+        if (at.block[t] < 0) continue;
+        const long long i = first + t;
+        const uint16_t* k = a.k_new + i * a.k_stride + h * kHeadDim;
+        const uint16_t* v = a.v_new + i * a.v_stride + h * kHeadDim;
+        uint8_t* block = a.cache + at.block[t];
+        const int slot = at.slot[t];
+        uint8_t* row = block + ((long long)slot * a.Hk + h) * kRow;
+        uint8_t* meta = block + a.meta_offset_bytes;
+        if constexpr (KV == PDA_KV_TQ4) {
+            write_tq4(row, reinterpret_cast<uint16_t*>(meta) + (long long)h * 3 * a.BS, __ldg(reinterpret_cast<const uint2*>(k) + lane),
+                      __ldg(reinterpret_cast<const uint2*>(v) + lane), book, lane, a.BS, slot);
+        } else {
+            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(lane < 16 ? k : v) + (lane & 15));
+            if constexpr (KV == PDA_KV_BF16)
+                *reinterpret_cast<uint4*>(row + 16 * lane) = raw;
+            else
+                write_fp8(row, reinterpret_cast<float*>(meta) + (long long)h * 2 * a.BS, raw, lane, a.BS, slot);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- reading
+// Lane l < 16 reads dimensions 8l .. 8l+7 of K, lane 16 + l those of V.
+template <int KV, bool F32>
+__global__ void __launch_bounds__(kTokThreads) pda_read_kernel(const TokenArgs a) {
+    __shared__ Places at;
+    __shared__ float book[16];
+    const int first = blockIdx.x * a.per_cta, n = min(a.per_cta, a.num_tokens - first);
+    if (KV == PDA_KV_TQ4 && threadIdx.x < 16) book[threadIdx.x] = __ldg(a.centroids + threadIdx.x);
+    if (!find_places(a, at, first, n)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;
+    for (int r = warp; r < n * a.Hk; r += kTokWarps) {
+        const int t = r / a.Hk, h = r - t * a.Hk;
+        if (at.block[t] < 0) continue;
+        const uint8_t* block = a.cache + at.block[t];
+        const int slot = at.slot[t];
+        const uint8_t* row = block + ((long long)slot * a.Hk + h) * kRow;
+        const uint8_t* meta = block + a.meta_offset_bytes;
+        float x[8];
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if constexpr (KV == PDA_KV_BF16) {
+            raw = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
+            }
+        } else if constexpr (KV == PDA_KV_FP8_E4M3) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+            const float scale = __ldg(reinterpret_cast<const float*>(meta) + ((long long)h * 2 + half) * a.BS + slot);
+            uint32_t p[4];
+            e4m3x4_to_f16x2x2(c.x, p[0], p[1]);
+            e4m3x4_to_f16x2x2(c.y, p[2], p[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+                x[2 * i] = f.x * scale;
+                x[2 * i + 1] = f.y * scale;
+            }
+        } else {
+            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
+            const __half* f = reinterpret_cast<const __half*>(meta) + (long long)h * 3 * a.BS + slot;
+            const float m = __half2float(__ldg(f + half * a.BS));              // k_norm or v_scale
+            const float z = half ? __half2float(__ldg(f + 2 * a.BS)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t code = c >> (4 * i) & 15u;
+                x[i] = half ? fmaf((float)code, m, z) : book[code] * m;        // code * v_scale is exact
+            }
+        }
+        void* out = half ? a.v_out : a.k_out;
+        if (!out) continue;
+        const long long o = ((long long)(first + t) * a.Hk + h) * kHeadDim + 8 * l;
+        if constexpr (F32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            if constexpr (KV != PDA_KV_BF16)
+                raw = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = raw;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- accepting
+struct AcceptArgs {
+    uint8_t* cache;
+    const int* block_table;
+    const int* context_lens;
+    const int* path;             // [B][A]
+    const int* path_lens;        // [B]
+    int* out_lens;               // [B]
+    int* err_word;
+    long long num_cache_blocks, cache_block_bytes, meta_offset_bytes;
+    int B, MB, BS, bs_shift, A;
+    int row_bytes;               // a token's data, all heads
+    int fields, field_bytes;     // its metadata: [heads * fields][BS]
+};
+constexpr int kPathChunk = 128;
+
+// A CTA moves a share of the bytes of one sequence's tokens.  Token k of the path goes from drafted index path[k] >= k to k, in
+// the path's order, and every byte is one thread's: a place is read no later than it is overwritten (it is a source only of
+// path[k'] = k, k' <= k), so reads may run ahead of the writes and nothing else has to be ordered.
+__global__ void __launch_bounds__(kTokThreads) pda_accept_kernel(const AcceptArgs a) {
+    __shared__ long long src_block[kPathChunk], dst_block[kPathChunk];
+    __shared__ int src_slot[kPathChunk], dst_slot[kPathChunk];
+    const int b = blockIdx.x;
+    const int* path = a.path + (long long)b * a.A;
+    const int ctx = __ldg(a.context_lens + b), n = __ldg(a.path_lens + b);
+    const long long room = (long long)a.MB * a.BS;
+    int bad = 0;
+    if (ctx < 0 || ctx > room) bad |= PDA_ERRW_BAD_CONTEXT_LEN;
+    if (n < 0 || n > a.A) bad |= PDA_ERRW_BAD_TOKENS;
+    if (!bad)
+        for (int k = threadIdx.x; k < n; k += kTokThreads) {
+            const int p = __ldg(path + k), before = k ? __ldg(path + k - 1) : -1;
+            if (p <= before) bad |= PDA_ERRW_BAD_TOKENS;
+            if (p >= room - ctx) bad |= PDA_ERRW_BAD_POSITION;
+        }
+    const bool refused = __syncthreads_or(bad);
+    if (bad && a.err_word) atomicOr(a.err_word, bad);
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.out_lens[b] = refused ? ctx : ctx + n;
+    if (refused) return;
+    const int* table = a.block_table + (long long)b * a.MB;
+    const int words = a.row_bytes / 16, metas = a.fields, stride = gridDim.y * kTokThreads;
+    const int me = blockIdx.y * kTokThreads + threadIdx.x;
+    for (int k0 = 0; k0 < n; k0 += kPathChunk) {
+        const int m = min(kPathChunk, n - k0);
+        __syncthreads();
+        for (int k = threadIdx.x; k < m; k += kTokThreads) {
+            const int from = ctx + __ldg(path + k0 + k), to = ctx + k0 + k;
+            const int f = __ldg(table + (from >> a.bs_shift)), t = __ldg(table + (to >> a.bs_shift));
+            const bool out = f < 0 || f >= a.num_cache_blocks || t < 0 || t >= a.num_cache_blocks;
+            if (out && from != to && a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
+            src_block[k] = out || from == to ? -1 : f * a.cache_block_bytes;
+            dst_block[k] = t * a.cache_block_bytes;
+            src_slot[k] = from & (a.BS - 1);
+            dst_slot[k] = to & (a.BS - 1);
+        }
+        __syncthreads();
+        for (int u = me; u < words + metas; u += stride) {
+            if (u < words) {
+                for (int k = 0; k < m; k += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < m && src_block[k + i] >= 0)
+                            v[i] = *reinterpret_cast<const uint4*>(a.cache + src_block[k + i] + (long long)src_slot[k + i] * a.row_bytes + 16 * u);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < m && src_block[k + i] >= 0)
+                            *reinterpret_cast<uint4*>(a.cache + dst_block[k + i] + (long long)dst_slot[k + i] * a.row_bytes + 16 * u) = v[i];
+                }
+            } else {
+                const long long base = a.meta_offset_bytes + (long long)(u - words) * a.BS * a.field_bytes;
+                for (int k = 0; k < m; k += 8) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < m && src_block[k + i] >= 0) {
+                            const uint8_t* p = a.cache + src_block[k + i] + base + src_slot[k + i] * a.field_bytes;
+                            v[i] = a.field_bytes == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < m && src_block[k + i] >= 0) {
+                            uint8_t* p = a.cache + dst_block[k + i] + base + dst_slot[k + i] * a.field_bytes;
+                            if (a.field_bytes == 4)
+                                *reinterpret_cast<uint32_t*>(p) = v[i];
+                            else
+                                *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[i];
+                        }
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------- host side
+static bool off(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
+static bool bad_pool(long long nb) { return nb < 1 || nb > (1ll << 31) - 1; }
+
+// What both directions check and fill in.  A status other than OK ends the call; *nothing: there is no token to move.
+static int token_args(const pda_plan_t* plan, const void* kv_cache, long long num_cache_blocks, const float* centroids,
+                      const int* block_table, const int* token_starts, const int* positions, long long num_tokens,
+                      int* err_word, TokenArgs& a, unsigned& grid) {
+    if (!plan || pda_workspace_size(plan) < 0) return PDA_ERR_INVALID_ARG;
+    if ((plan->kv_dtype == PDA_KV_TQ4) != (centroids != nullptr)) return PDA_ERR_INVALID_ARG;
+    if (num_tokens < 0 || num_tokens > (1ll << 31) - 1 - kMaxTokensPerCta || bad_pool(num_cache_blocks)) return PDA_ERR_INVALID_ARG;
+    grid = 0;
+    if (plan->num_seqs == 0 || num_tokens == 0) return PDA_OK;
+    if (!kv_cache || !block_table || !token_starts || !positions) return PDA_ERR_INVALID_ARG;
+    if (off(kv_cache, 16) || off(block_table, 4) || off(token_starts, 4) || off(positions, 4) || off(centroids, 4) || off(err_word, 4))
+        return PDA_ERR_INVALID_ARG;
+    a.cache = static_cast<uint8_t*>(const_cast<void*>(kv_cache));
+    a.block_table = block_table;
+    a.token_starts = token_starts;
+    a.positions = positions;
+    a.centroids = centroids;
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.cache_block_bytes = plan->cache_block_bytes;
+    a.meta_offset_bytes = plan->meta_offset_bytes;
+    a.num_tokens = (int)num_tokens;
+    a.B = plan->num_seqs;
+    a.Hk = plan->num_kv_heads;
+    a.MB = plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.bs_shift = a.BS == 32 ? 5 : 4;
+    const long long even = num_tokens / (4 * 152);
+    a.per_cta = (int)(even < 1 ? 1 : even > kMaxTokensPerCta ? kMaxTokensPerCta : even);
+    grid = (unsigned)((num_tokens + a.per_cta - 1) / a.per_cta);
+    return PDA_OK;
+}
+
+}  // namespace pda
+
+using namespace pda;
+
+extern "C" {
+
+int pda_write_kv(const pda_plan_t* plan, const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                 long long num_tokens, void* kv_cache, long long num_cache_blocks, const float* centroids,
+                 const int* block_table, const int* token_starts, const int* positions, int* err_word, void* stream) {
+    TokenArgs a = {};
+    unsigned grid;
+    const int rc = token_args(plan, kv_cache, num_cache_blocks, centroids, block_table, token_starts, positions, num_tokens,
+                              err_word, a, grid);
+    if (rc != PDA_OK) return rc;
+    const long long row = (long long)plan->num_kv_heads * kHeadDim;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return PDA_ERR_INVALID_ARG;
+    if (grid == 0) return PDA_OK;
+    if (!k_new || !v_new || off(k_new, 16) || off(v_new, 16)) return PDA_ERR_INVALID_ARG;
+    a.k_new = static_cast<const uint16_t*>(k_new);
+    a.v_new = static_cast<const uint16_t*>(v_new);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (plan->kv_dtype == PDA_KV_BF16)
+        pda_write_kernel<PDA_KV_BF16><<<grid, kTokThreads, 0, s>>>(a);
+    else if (plan->kv_dtype == PDA_KV_FP8_E4M3)
+        pda_write_kernel<PDA_KV_FP8_E4M3><<<grid, kTokThreads, 0, s>>>(a);
+    else
+        pda_write_kernel<PDA_KV_TQ4><<<grid, kTokThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long num_cache_blocks, const float* centroids,
+                const int* block_table, const int* token_starts, const int* positions, long long num_tokens, void* k_out,
+                void* v_out, int out_dtype, int* err_word, void* stream) {
+    if (out_dtype != PDA_OUT_BF16 && out_dtype != PDA_OUT_F32) return PDA_ERR_INVALID_ARG;
+    TokenArgs a = {};
+    unsigned grid;
+    const int rc = token_args(plan, kv_cache, num_cache_blocks, centroids, block_table, token_starts, positions, num_tokens,
+                              err_word, a, grid);
+    if (rc != PDA_OK || grid == 0) return rc;
+    if ((!k_out && !v_out) || off(k_out, 16) || off(v_out, 16)) return PDA_ERR_INVALID_ARG;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = out_dtype == PDA_OUT_F32;
+    auto launch = [&](auto kernel) { kernel<<<grid, kTokThreads, 0, s>>>(a); };
+    if (plan->kv_dtype == PDA_KV_BF16)
+        f32 ? launch(pda_read_kernel<PDA_KV_BF16, true>) : launch(pda_read_kernel<PDA_KV_BF16, false>);
+    else if (plan->kv_dtype == PDA_KV_FP8_E4M3)
+        f32 ? launch(pda_read_kernel<PDA_KV_FP8_E4M3, true>) : launch(pda_read_kernel<PDA_KV_FP8_E4M3, false>);
+    else
+        f32 ? launch(pda_read_kernel<PDA_KV_TQ4, true>) : launch(pda_read_kernel<PDA_KV_TQ4, false>);
+    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+int pda_accept_tokens(const pda_plan_t* plan, void* kv_cache, long long num_cache_blocks, const int* block_table,
+                      const int* context_lens, const int* path, const int* path_lens, int max_path, int* out_lens,
+                      int* err_word, void* stream) {
+    if (!plan || pda_workspace_size(plan) < 0 || bad_pool(num_cache_blocks) || max_path < 0) return PDA_ERR_INVALID_ARG;
+    if (plan->num_seqs == 0) return PDA_OK;
+    if (!kv_cache || !block_table || !context_lens || (!path && max_path > 0) || !path_lens || !out_lens)
+        return PDA_ERR_INVALID_ARG;
+    if (off(kv_cache, 16) || off(block_table, 4) || off(context_lens, 4) || off(path, 4) || off(path_lens, 4) ||
+        off(out_lens, 4) || off(err_word, 4))
+        return PDA_ERR_INVALID_ARG;
+    auto overlap = [&](const int* p) {   // CTAs of a sequence read what one of them would have written
+        const uintptr_t x = (uintptr_t)p, y = (uintptr_t)out_lens, n = 4ull * plan->num_seqs;
+        return x < y + n && y < x + n;
+    };
+    if (overlap(context_lens) || overlap(path_lens)) return PDA_ERR_INVALID_ARG;
+    AcceptArgs a = {};
+    a.cache = static_cast<uint8_t*>(kv_cache);
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.path = path;
+    a.path_lens = path_lens;
+    a.out_lens = out_lens;
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.cache_block_bytes = plan->cache_block_bytes;
+    a.meta_offset_bytes = plan->meta_offset_bytes;
+    a.B = plan->num_seqs;
+    a.MB = plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.bs_shift = a.BS == 32 ? 5 : 4;
+    a.A = max_path;
+    const int kv = plan->kv_dtype, Hk = plan->num_kv_heads;
+    const long long row = (long long)Hk * (kv == PDA_KV_BF16 ? 512 : kv == PDA_KV_FP8_E4M3 ? 256 : 128);
+    if (row > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
+    a.row_bytes = (int)row;
+    a.fields = kv == PDA_KV_BF16 ? 0 : kv == PDA_KV_FP8_E4M3 ? 2 * Hk : 3 * Hk;
+    a.field_bytes = kv == PDA_KV_FP8_E4M3 ? 4 : 2;
+    const long long units = row / 16 + a.fields;
+    const dim3 grid((unsigned)a.B, (unsigned)((units + kTokThreads - 1) / kTokThreads < 64 ? (units + kTokThreads - 1) / kTokThreads : 64));
+    pda_accept_kernel<<<grid, kTokThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+}  // extern "C"

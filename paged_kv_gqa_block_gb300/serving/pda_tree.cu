@@ -1,0 +1,265 @@
+// pda_tree.cu -- pda_decode_tree: a step for drafted tokens, several per sequence, over their cache.
+//
+// For drafted token i of a sequence with ctx cached tokens and KV head h, its QG query rows
+//   out = softmax(scale [q.K ; mask]) V
+// over the cached tokens t < ctx (of a window, those with ctx + before(i) - t < window and the first num_first) and over the
+// drafted tokens j that the row of its mask names; before(i) is the number of drafted tokens other than i that it sees.  The
+// drafted tokens' K and V lie in the cache behind the cached ones (pda_write_kv).
+//
+// The rows of all drafted tokens of a sequence and KV head are one matrix product with its cache, so K and V are read once per
+// 256 rows and not once per drafted token: pda_prefix.cuh, where a sequence takes the place of a group.  Its pieces are joined
+// here.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pda_maps.h"
+#include "pda_prefix.cuh"
+
+namespace pda {
+
+struct TreeJoinArgs {
+    const int* token_starts;
+    const int* context_lens;
+    const int* refused;
+    const float* part_o;   // [N][Hk][slots][QG][D]
+    const float* part_l;   // [N][Hk][slots][QG]
+    const float* part_m;
+    const int* pieces;     // [N][Hk][QG]
+    void* out;
+    int N, B, Hk, QG, room, slots, out_f32;
+};
+
+// One CTA per (drafted token, KV head), one warp per query row; lane i holds (m, l) of pieces i, i + 32, ..; each lane sums four
+// dimensions over the pieces in order.  Rows of tokens that no sequence has stay as they are.
+__global__ void __launch_bounds__(512) pda_tree_join_kernel(const TreeJoinArgs a) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const long long unit = blockIdx.x;
+    const int token = (int)(unit / a.Hk);
+    const int pieces = __ldcg(a.pieces + unit * a.QG + q);   // not written for a sequence in error; not used then
+    if (__ldcg(a.refused)) return;
+    // the sequence: the last start that is not above the token, 32 starts at a time
+    int lo = 0, n = a.B + 1;   // starts lo .. lo+n-1 hold the first that is above it, or none does
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool below = lane * step < n && __ldg(a.token_starts + at) <= token;
+        const int k = __popc(__ballot_sync(kLanes, below));
+        if (k == 0) break;                       // the first of them is above
+        const int base = lo + (k - 1) * step;    // not above
+        const int end = min(lo + n, base + step);
+        lo = base + 1;
+        n = step == 1 ? 0 : end - lo;
+    }
+    const int b = lo - 1;
+    if (b < 0 || b >= a.B) return;
+    const int drafted = __ldg(a.token_starts + b + 1) - __ldg(a.token_starts + b), ctx = __ldg(a.context_lens + b);
+    const bool fine = ctx >= 0 && ctx <= a.room && drafted <= a.room - ctx;
+    const int total = fine ? max(0, min(a.slots, pieces)) : 0;
+    const long long row0 = unit * a.slots * a.QG + q;
+    auto stats = [&](int i, float& m, float& l) {
+        m = -INFINITY;
+        l = 0.f;
+        if (i < total) {
+            m = __ldcg(a.part_m + row0 + (long long)i * a.QG);
+            l = __ldcg(a.part_l + row0 + (long long)i * a.QG);
+            if (l == 0.f) m = -INFINITY;   // a piece of which the row sees nothing
+        }
+    };
+    float m0, l0;
+    stats(lane, m0, l0);
+    float M = m0;
+    for (int i = lane + 32; i < total; i += 32) {
+        float m, l;
+        stats(i, m, l);
+        M = fmaxf(M, m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kLanes, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int i0 = 0; i0 < total; i0 += 32) {
+        if (i0 > 0) stats(i0 + lane, m0, l0);
+        const float w = l0 != 0.f ? partition_weight(l0, m0, M) : 0.f;
+        sum += w;
+        const int n = min(32, total - i0);
+        for (int j0 = 0; j0 < n; j0 += 8) {
+            float4 o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row0 + (long long)(i0 + min(j0 + j, n - 1)) * a.QG) * kHeadDim) + lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = __shfl_sync(kLanes, w, (j0 + j) & 31);
+                if (j0 + j < n) {
+                    acc.x = fmaf(f, o[j].x, acc.x);
+                    acc.y = fmaf(f, o[j].y, acc.y);
+                    acc.z = fmaf(f, o[j].z, acc.z);
+                    acc.w = fmaf(f, o[j].w, acc.w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kLanes, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing gives zeros
+    const long long row = unit * a.QG + q;
+    if (a.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + 4 * lane) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+        uint2 v;
+        v.x = pack_bf16(acc.x * inv, acc.y * inv);
+        v.y = pack_bf16(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kHeadDim + 4 * lane) = v;
+    }
+}
+
+// ------------------------------------------------------------------------- host side
+static long long up256(long long x) { return (x + 255) & ~255ll; }
+static bool odd(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+static long long steps_of(const pda_plan_t* p) { return ((long long)p->max_blocks_per_seq * p->kv_block_size + kStep - 1) / kStep; }
+// The most row tiles (times steps) that the drafted tokens can have.
+static long long most_tree_tiles(const pda_plan_t* p, long long tokens) {
+    const long long seqs = p->num_seqs < tokens ? p->num_seqs : tokens;
+    return (tokens * p->query_group_size / kUnitRows + seqs) * p->num_kv_heads;
+}
+// Pieces of the longest sequence: four times as many as give every SM one, since lengths differ, and of two steps at least.
+static int tree_pieces(const pda_plan_t* p, long long tokens) {
+    int sms = device_sm_count();
+    if (sms <= 0) sms = 152;
+    const long long rows = (tokens * p->query_group_size + kUnitRows - 1) / kUnitRows;
+    const long long seqs = p->num_seqs < tokens ? p->num_seqs : tokens;
+    const long long tiles = (rows > seqs ? rows : seqs) * p->num_kv_heads;
+    const long long want = (4ll * sms + tiles - 1) / tiles, most = (steps_of(p) + 1) / 2;
+    return (int)(want < most ? want : most);
+}
+static bool tree_fits(const pda_plan_t* p, long long tokens) {
+    return tokens >= 0 && tokens * p->query_group_size <= 1ll << 30 &&
+           most_tree_tiles(p, tokens) * (steps_of(p) + kSwitch) <= 2000000000ll;   // places are ints
+}
+struct TreeLayout {
+    long long o, l, m, pieces, refused, bytes;
+    int slots;
+};
+static TreeLayout tree_layout(const pda_plan_t* p, long long tokens) {
+    TreeLayout w;
+    w.slots = tree_pieces(p, tokens) + 1;
+    const long long rows = tokens * p->num_kv_heads * p->query_group_size;
+    w.o = 0;
+    w.l = w.o + up256(rows * w.slots * kHeadDim * 4);
+    w.m = w.l + up256(rows * w.slots * 4);
+    w.pieces = w.m + up256(rows * w.slots * 4);
+    w.refused = w.pieces + up256(rows * 4);
+    w.bytes = w.refused + 256;
+    return w;
+}
+
+}  // namespace pda
+
+using namespace pda;
+
+extern "C" {
+
+long long pda_tree_workspace_size(const pda_plan_t* plan, long long num_tokens) {
+    if (!plan || pda_workspace_size(plan) < 0 || !tree_fits(plan, num_tokens)) return -1;
+    if (num_tokens == 0 || plan->num_seqs == 0) return 0;
+    return tree_layout(plan, num_tokens).bytes;
+}
+
+int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tokens, const void* kv_cache,
+                    long long num_cache_blocks, const float* centroids, const int* block_table, const int* context_lens,
+                    const int* token_starts, const unsigned long long* tree_masks, int mask_words, int window, int num_first,
+                    void* workspace, long long workspace_bytes, void* out, int out_dtype, int* err_word, void* stream) {
+    if (!plan || pda_workspace_size(plan) < 0 || !tree_fits(plan, num_tokens)) return PDA_ERR_INVALID_ARG;
+    if ((plan->kv_dtype == PDA_KV_TQ4) != (centroids != nullptr) || (out_dtype != PDA_OUT_BF16 && out_dtype != PDA_OUT_F32))
+        return PDA_ERR_INVALID_ARG;
+    if (window < 0 || num_first < 0 || (tree_masks && (mask_words < 1 || mask_words > 1 << 20)) || (!tree_masks && mask_words != 0))
+        return PDA_ERR_INVALID_ARG;
+    if (num_cache_blocks < 1 || num_cache_blocks > (1ll << 31) - 1) return PDA_ERR_INVALID_ARG;
+    if (plan->num_seqs == 0 || num_tokens == 0) return PDA_OK;
+    if (!query || !kv_cache || !block_table || !context_lens || !token_starts || !workspace || !out) return PDA_ERR_INVALID_ARG;
+    if (odd(query, 16) || odd(kv_cache, 16) || odd(centroids, 4) || odd(block_table, 4) || odd(context_lens, 4) ||
+        odd(token_starts, 4) || odd(tree_masks, 8) || odd(workspace, 32) || odd(err_word, 4) ||
+        odd(out, out_dtype == PDA_OUT_F32 ? 16 : 8))
+        return PDA_ERR_INVALID_ARG;
+    const TreeLayout w = tree_layout(plan, num_tokens);
+    if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;
+    const int sms = device_sm_count();
+    if (sms <= 0) return PDA_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    auto f32 = [&](long long at) { return reinterpret_cast<float*>(ws + at); };
+    TreeArgs a = {};
+    a.query = static_cast<const uint16_t*>(query);
+    a.group_starts = token_starts;
+    a.prefix_table = block_table;
+    a.prefix_lens = context_lens;
+    a.part_o = f32(w.o);
+    a.part_l = f32(w.l);
+    a.part_m = f32(w.m);
+    a.pieces = reinterpret_cast<int*>(ws + w.pieces);
+    a.err_word = err_word;
+    a.num_cache_blocks = num_cache_blocks;
+    a.B = (int)num_tokens;
+    a.NG = plan->num_seqs;
+    a.Hk = plan->num_kv_heads;
+    a.QG = plan->query_group_size;
+    a.MP = plan->max_blocks_per_seq;
+    a.BS = plan->kv_block_size;
+    a.P = w.slots - 1;
+    a.slots = w.slots;
+    a.first = 1;
+    a.qk_scale_log2 = plan->resolved_softmax_scale * kLog2eS;
+    a.timeout_ns = plan->wait_timeout_ns > 0 ? (unsigned long long)plan->wait_timeout_ns : kDefaultTimeoutNs;
+    a.masks = reinterpret_cast<const uint32_t*>(tree_masks);
+    a.centroids = centroids;
+    a.refused = reinterpret_cast<int*>(ws + w.refused);
+    a.words = 2 * mask_words;
+    a.window = window;
+    a.num_first = num_first;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap kv_map, sc_map;
+    if (!encode_tokens_map(&kv_map, kv_cache, plan, num_cache_blocks, a.BS, 1)) return PDA_ERR_LAUNCH;
+    sc_map = kv_map;
+    if (plan->kv_dtype != PDA_KV_BF16 && !encode_fields_map(&sc_map, kv_cache, plan, num_cache_blocks, a.BS)) return PDA_ERR_LAUNCH;
+    const long long most = most_tree_tiles(plan, num_tokens) * steps_of(plan);   // no more CTAs than there can be steps
+    const int ctas = (int)(most < sms ? most : sms);
+    int rc;
+    if (plan->kv_dtype == PDA_KV_BF16)
+        rc = launch_prefix<PDA_KV_BF16>(a, kv_map, sc_map, ctas, s);
+    else if (plan->kv_dtype == PDA_KV_FP8_E4M3)
+        rc = launch_prefix<PDA_KV_FP8_E4M3>(a, kv_map, sc_map, ctas, s);
+    else
+        rc = launch_prefix<PDA_KV_TQ4>(a, kv_map, sc_map, ctas, s);
+    if (rc != PDA_OK) return rc;
+    TreeJoinArgs j = {};
+    j.token_starts = token_starts;
+    j.context_lens = context_lens;
+    j.refused = a.refused;
+    j.part_o = a.part_o;
+    j.part_l = a.part_l;
+    j.part_m = a.part_m;
+    j.pieces = a.pieces;
+    j.out = out;
+    j.N = a.B;
+    j.B = a.NG;
+    j.Hk = a.Hk;
+    j.QG = a.QG;
+    j.room = a.MP * a.BS;
+    j.slots = a.slots;
+    j.out_f32 = out_dtype == PDA_OUT_F32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hk));
+    cfg.blockDim = dim3(a.QG * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pda_tree_join_kernel, j) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+}
+
+}  // extern "C"
