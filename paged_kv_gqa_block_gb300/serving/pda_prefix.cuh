@@ -75,22 +75,27 @@ constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
 constexpr float kLazy = 8.f;               // log2 units that a row's maximum may rise before its reference follows
 constexpr float kBelow = 7.f;              // f16 P: the reference below the maximum
 
-template <int KV>
+// What a KV format and a kind of call take of shared memory, barriers and threads.  Q8 (drafted tokens over fp8 KV): the score
+// product takes K's codes as they are, so that only V is converted, in halves of 64 tokens.
+template <int KV, class Args>
 struct SharedCfg {
     static constexpr bool kF16 = KV != PDA_KV_BF16;              // f16 products, converter warps
-    static constexpr bool kTq = KV == PDA_KV_TQ4;
+    static constexpr bool kTq = KV == PDA_KV_TQ4, kTree = std::is_same<Args, TreeArgs>::value, kQ8 = kTree && KV == PDA_KV_FP8_E4M3;
     static constexpr int kScaleBytes = kTq ? 1536 : 1024;        // 128 tokens x {K scale, V scale (, V zero)}
     static constexpr int kTiles = kTq ? 1 : 2;                   // copies of a step: a TQ4 row holds K and V
     static constexpr int kSlots = kF16 ? 3 : 5;
     static constexpr int kRaw = 3, kScales = 3;                  // fp8, TQ4: raw slots, scale stages
     static constexpr int kThreads = kF16 ? 512 : 384;
     static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
-    static constexpr int kOffSlots = 2 * kSlotBytes;
-    static constexpr int kOffRaw = kOffSlots + kSlots * kSlotBytes;
+    static constexpr int kKeys = kQ8 ? 3 : 0, kHalves = 3;        // Q8: slots of K's codes, and of converted halves of V
+    static constexpr int kOffKeys = 2 * kSlotBytes;
+    static constexpr int kOffSlots = kOffKeys + kKeys * kRawBytes;
+    static constexpr int kOffRaw = kOffSlots + (kQ8 ? kHalves * kRawBytes : kSlots * kSlotBytes);
     static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
     static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
-    static constexpr int kOffTable = kOffBars + 464;              // TQ4: the centroids of a byte's two codes, f16
-    static constexpr int kSmem = kTq ? kOffTable + 1024 : kOffBars + 448;
+    static constexpr int kOffTable = kOffBars + 512;              // TQ4: the centroids of a byte's two codes, f16
+    static constexpr int kSmem = kTq ? kOffTable + 1024 : kOffBars + (kQ8 ? 512 : 448);
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
     static constexpr int kReaders = kF16 ? 15 : 10;               // warps that take units
 };
 // barriers and scalars after kOffBars
@@ -114,7 +119,9 @@ enum {
     kBarUnitFull = 312,  // [2] the next unit is in shared memory
     kBarUnitEmpty = 328, // [2]
     kUnitAt = 352,       // [2] units, 48 bytes each
-    kPowerAt = 448       // TQ4: 1 over the power of two that the table's centroids carry
+    kPowerAt = 448,      // TQ4: 1 over the power of two that the table's centroids carry
+    kBarVFull = 456,     // [3] Q8: a half of V is converted
+    kBarVEmpty = 480     // [3] the products that read it are done
 };
 
 // ------------------------------------------------------------------------- the prefix pass
@@ -166,8 +173,9 @@ __device__ __forceinline__ void add2(float2& x, const float2& y) {
 
 template <int KV, class Args>
 struct Prefix {
-    using Cfg = SharedCfg<KV>;
-    static constexpr bool F16 = Cfg::kF16, TQ = Cfg::kTq, TREE = std::is_same<Args, TreeArgs>::value;
+    using Cfg = SharedCfg<KV, Args>;
+    static constexpr bool F16 = Cfg::kF16, TQ = Cfg::kTq, TREE = Cfg::kTree, Q8 = Cfg::kQ8;
+    static constexpr uint32_t kIdescQ8 = umma_idesc_e4m3(128, 128);
     static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
 
     const Args& a;
@@ -311,12 +319,15 @@ struct Prefix {
                 }
 #pragma unroll
                 for (int v = 0; v < kTiles; ++v, ++seq) {   // K, then V
-                    const int s = seq % kNS;
-                    if (seq >= kNS && !wait(bars + kEmpty0 + 8 * s, (seq / kNS - 1) & 1)) {
+                    // Q8: a ring of its own for each
+                    const bool keys = Q8 && v == 0;
+                    const unsigned at = Q8 ? step : seq, ring = keys ? Cfg::kKeys : kNS;
+                    const unsigned s = at % ring;
+                    if (at >= ring && !wait(bars + (keys ? kBarEmpty : kEmpty0) + 8 * s, (at / ring - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = bars + kFull0 + 8 * s;
+                    const uint32_t bar = bars + (keys ? kBarFull : kFull0) + 8 * s;
                     const uint32_t row_bytes = (uint32_t)n * a.BS * 128u * kHalves;
                     const bool scales = F16 && v == 0;
                     if (lane == 0) {
@@ -325,7 +336,7 @@ struct Prefix {
                     }
                     __syncwarp();
                     if (mine) {
-                        tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
+                        tma_load_5d((keys ? sm + Cfg::kOffKeys : base) + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
                                     v * kHalves + half, u.h, id, policy);
                         if (scales)
                             tma_load_4d(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + blk * a.BS * 8, sc_map,
@@ -338,11 +349,14 @@ struct Prefix {
             }
         }
         // no copy may land in this CTA's memory after it leaves, whichever role gave up
+        const unsigned raws = Q8 ? seq / 2 : seq, keys = Q8 ? (seq + 1) / 2 : 0;   // slots filled of each ring
         for (int s = 0; s < kNS; ++s)
-            if (seq > (unsigned)s) {
-                const unsigned q = (seq - 1 - s) / kNS;   // the slot's last use
+            if (raws > (unsigned)s) {
+                const unsigned q = (raws - 1 - s) / kNS;   // the slot's last use
                 (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
             }
+        for (int s = 0; s < Cfg::kKeys; ++s)
+            if (keys > (unsigned)s) (void)mbar_wait(bars + kBarFull + 8 * s, (keys - 1 - s) / Cfg::kKeys & 1, kDefaultTimeoutNs);
         if (F16) {
             const unsigned issued = (seq + kTiles - 1) / kTiles;   // steps whose scales were asked for
             for (int s = 0; s < Cfg::kScales; ++s)
@@ -417,10 +431,74 @@ struct Prefix {
     __device__ void convert() {
         if constexpr (TQ)
             convert_tq4();
+        else if constexpr (Q8)
+            convert_values();
         else
             convert_fp8();
     }
-    __device__ void convert_fp8() {
+    // Q8: V alone, in halves of 64 tokens.  Thread t takes dimensions 64 (t / 64) .. of token t % 64 of the half: its codes
+    // times the token's scale over F, as in convert_fp8.
+    __device__ __forceinline__ void convert_values() {
+        const int t = threadIdx.x - 384, lane = t & 31, r = t & 63, side = t >> 6, sw = r & 7;
+        const uint32_t raw0 = sm + Cfg::kOffRaw + r * 128, slot0 = sm + Cfg::kOffSlots + side * 8192 + r * 128;
+        const uint32_t scale0 = sm + Cfg::kOffScales + 512 + r * 4;
+        unsigned s = 0, ph = 0, st = 0, st_ph = 0, h = 0, h_ph = 0;
+        static_assert(!Q8 || Cfg::kRaw == Cfg::kScales, "a raw slot and its scales are counted together");
+        Unit u;
+        while (next(u)) {
+            const Sight x = sight(u);
+            for (int j = 0; j < u.steps; ++j) {
+                const int valid = tokens_of(u, x, j), t0 = step_of(u, x, j) * kStep;
+                if (!wait(bars + kBarRawFull + 8 * s, ph)) return;
+                if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int tok = 64 * half + r;
+                    const uint32_t src = raw0 + s * kRawBytes + half * 8192;
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) lds128(src + (((4 * side + c) ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                    const float vs = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes + half * 256));
+                    const uint32_t vs2 = pack_f16(vs, vs);
+                    if (!wait(bars + kBarVEmpty + 8 * h, h_ph ^ 1)) return;   // the slots start free
+                    if (tok >= valid || missed(x, t0 + tok)) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+                    }
+                    const uint32_t dst = slot0 + h * kRawBytes;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
+                        sts128(dst + (((2 * c) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                        sts128(dst + (((2 * c + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bars + kBarVFull + 8 * h);
+                        if (half) mbar_arrive(bars + kBarRawEmpty + 8 * s);
+                    }
+                    if (++h == Cfg::kHalves) {
+                        h = 0;
+                        h_ph ^= 1;
+                    }
+                }
+                if (++s == Cfg::kRaw) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++st == Cfg::kScales) {
+                    st = 0;
+                    st_ph ^= 1;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void convert_fp8() {
         const int t = threadIdx.x - 384, lane = t & 31, sw = t & 7;
         const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
         const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4;
@@ -482,7 +560,7 @@ struct Prefix {
     // TQ4.  Thread t turns token t's 64 + 64 bytes of codes into f16: K's through the table of byte pairs (centroids times a
     // power of two; k_norm is the step's K scale), V as code * v_scale + v_zero over F in 32 bits, rounded once.  Step by step
     // K, then V, out of one raw slot.
-    __device__ void convert_tq4() {
+    __device__ __forceinline__ void convert_tq4() {
         const int t = threadIdx.x - 384, lane = t & 31, sw = t & 7;
         const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + t * 128;
         const uint32_t scale0 = sm + Cfg::kOffScales + 512 + t * 4, table = sm + Cfg::kOffTable;
@@ -604,6 +682,97 @@ struct Prefix {
             umma_ts(leader, d, p + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
     }
     __device__ void products(uint32_t tmem_base) {
+        if constexpr (Q8)
+            products_q8(tmem_base);
+        else
+            products_f16(tmem_base);
+    }
+    // Products in flight read shared memory and TMEM: let them end, whichever role gave up.
+    __device__ __forceinline__ void drain(uint32_t leader, uint32_t bar) const {
+        umma_commit(leader, bar + kBarDrain);
+        __syncwarp();
+        (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
+    }
+    // Q8.  S = Qhi K^T + Qlo K^T, e4m3 each; the halves of V by their own barriers.
+    __device__ __forceinline__ void products_q8(uint32_t tmem_base) {
+        const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm), bar = uniform(bars);
+        const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024), k0 = umma_desc(smu + Cfg::kOffKeys, 16, 1024);
+        const uint64_t v0 = umma_desc(smu + Cfg::kOffSlots, 8192, 1024);
+        constexpr uint32_t kRaw16 = kRawBytes >> 4;
+        
+        uint32_t ks = 0, kph = 0, hs = 0, hph = 0;   // the next slot of K, and of V's halves
+        uint32_t unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
+        auto scores = [&](int w) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {   // 32 dimensions at a time, first of the high parts, then of the low ones
+                const uint32_t o = (i & 3) * 32 >> 4;
+                umma_ss_f8(leader, tmem + w * 128, q0 + w * kSlot16 + (i >> 2) * kRaw16 + o, k0 + ks * kRaw16 + o, kIdescQ8, i > 0);
+            }
+        };
+        auto values = [&](int w, int half, uint32_t slot, bool accumulate) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                umma_ts(leader, tmem + 256 + w * 128, tmem + w * 128 + (4 * half + i) * 8, v0 + slot * kRaw16 + ((i * 2048) >> 4),
+                        kIdescPV, accumulate || i > 0);
+        };
+        auto all = [&] {
+            Unit u;
+            while (uniform((int)next(u))) {
+                const int tiles = uniform(active(u, 1) ? 2 : 1), steps = uniform(u.steps);
+                if (!wait(bar + kBarFull + 8 * ks, kph)) return;
+                for (int w = 0; w < tiles; ++w) {
+                    uint32_t& n = w ? unit1 : unit0;
+                    if (!wait(bar + kBarQ + 8 * w, n)) return;
+                    n ^= 1;
+                    tc_fence_after();
+                    scores(w);
+                    umma_commit(leader, bar + kBarS + 8 * w);
+                }
+                for (int j = 0; j < steps; ++j) {
+                    const bool more = j + 1 < steps;
+                    umma_commit(leader, bar + kBarEmpty + 8 * ks);   // of the scores issued last
+                    if (++ks == Cfg::kKeys) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                    const uint32_t h0 = hs, ph0 = hph;
+                    if (++hs == Cfg::kHalves) {
+                        hs = 0;
+                        hph ^= 1;
+                    }
+                    const uint32_t h1 = hs, ph1 = hph;
+                    if (++hs == Cfg::kHalves) {
+                        hs = 0;
+                        hph ^= 1;
+                    }
+    #pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (w >= tiles) break;
+                        uint32_t& n = w ? p1 : p0;
+                        if (w == 0 && !wait(bar + kBarVFull + 8 * h0, ph0)) return;
+                        if (!wait(bar + kBarP + 8 * w, n)) return;
+                        tc_fence_after();
+                        values(w, 0, h0, j > 0);
+                        if (w + 1 == tiles) umma_commit(leader, bar + kBarVEmpty + 8 * h0);
+                        if (w == 0 && !wait(bar + kBarVFull + 8 * h1, ph1)) return;
+                        if (!wait(bar + kBarP2 + 8 * w, n)) return;
+                        n ^= 1;
+                        tc_fence_after();
+                        values(w, 1, h1, true);
+                        if (w + 1 == tiles) umma_commit(leader, bar + kBarVEmpty + 8 * h1);
+                        if (more) {
+                            if (w == 0 && !wait(bar + kBarFull + 8 * ks, kph)) return;
+                            scores(w);
+                        }
+                        umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
+                    }
+                }
+            }
+        };
+        all();
+        drain(leader, bar);
+    }
+    __device__ __forceinline__ void products_f16(uint32_t tmem_base) {
         const int lane = threadIdx.x & 31;
         const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm);
         const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024);
@@ -698,13 +867,19 @@ struct Prefix {
                 pos = k;   // after the last step: the next unit's K(0)
             }
         }
-        // products in flight read shared memory and TMEM: let them end, whichever role gave up
-        umma_commit(leader, bar + kBarDrain);
-        __syncwarp();
-        (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
+        drain(leader, bar);
     }
 
     // ---------------------------------------------------------------- softmax
+    // Four values as the sum of e4m3 pairs (packed, the first in the low byte).
+    static __device__ __forceinline__ void split_e4m3(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+        const uint32_t h0 = f32x2_to_e4m3x2(x0, x1), h1 = f32x2_to_e4m3x2(x2, x3);
+        hi = h0 | h1 << 16;
+        uint32_t f0, f1;
+        e4m3x4_to_f16x2x2(hi, f0, f1);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f0)), b = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+        lo = f32x2_to_e4m3x2(x0 - a.x, x1 - a.y) | f32x2_to_e4m3x2(x2 - b.x, x3 - b.y) << 16;
+    }
     // The warp's 32 query rows into its tile's operand, two rows (16 lanes each) per asynchronous copy; returns
     // the factor from S to log2 units of this lane's own row, 32 * (warp % 4) + lane.  The loops stay
     // rolled: a short prefix waits for this code's first fetch longer than for its execution.
@@ -712,7 +887,9 @@ struct Prefix {
         const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, half = lane >> 4, w = lane & 15;
         const uint32_t base = sm + Cfg::kOffQ + tile * kSlotBytes;
         {
-            const uint32_t dst = base + (w >> 3) * 16384;
+            // 16 bytes w of a row; Q8: neighbours 16 KB apart, where the parts of their 16 dimensions will lie
+            const uint32_t dst = base + (Q8 ? w & 1 : w >> 3) * 16384;
+            const int place = Q8 ? w >> 1 : w & 7;
             const int row0 = u.rt * kUnitRows + tile * kTileRows + r0 + half;
             int seq = row0 / a.QG, q = row0 - seq * a.QG;
             const uint16_t* src = a.query + ((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG * kHeadDim + 8 * w;
@@ -721,7 +898,7 @@ struct Prefix {
             for (int i = 0; i < 16; ++i) {
                 const int r = r0 + 2 * i + half;
                 const bool live = row0 + 2 * i < u.rows;   // else: zeros, and no read
-                cp_async16(dst + r * 128 + (((w & 7) ^ (r & 7)) << 4), live ? src + q * kHeadDim : a.query, live ? 16u : 0u);
+                cp_async16(dst + r * 128 + ((place ^ (r & 7)) << 4), live ? src + q * kHeadDim : a.query, live ? 16u : 0u);
                 q += 2;
                 if (q >= a.QG) {   // the group size is above 2
                     q -= a.QG;
@@ -733,7 +910,40 @@ struct Prefix {
         }
         float c = a.qk_scale_log2;
         if constexpr (TQ) c *= __uint_as_float(lds32v(bars + kPowerAt));
-        if constexpr (F16) {
+        if constexpr (Q8) {
+            // This lane's row times a power of two that brings its largest |q| into [2^7, 2^8), as the sum of two e4m3 parts: the
+            // high one has 4 of bf16's 8 bits, and what is left fits 4 more down to 2^-2.  A smaller |q| is off by at most half a
+            // step of e4m3's smallest, 2^-10: 2^-17 of the row's largest.
+            const uint32_t row = base + (r0 + lane) * 128;
+            const int x = lane & 7;
+            uint32_t mx = 0;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                uint32_t v[4];
+                lds128(row + (i >> 3) * 16384 + ((i & 7) << 4), v[0], v[1], v[2], v[3]);   // in any order
+                mx = __vmaxs2(mx, __vmaxs2(__vmaxs2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu),
+                                           __vmaxs2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu)));
+            }
+            const int top = max(mx & 0xFFFFu, mx >> 16);   // bf16 bits
+            int e = top ? 7 - ((top >> 7) - 127) : 0;
+            e = max(-100, min(100, e));
+            const float pw = __uint_as_float((uint32_t)(e + 127) << 23);
+            c *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {   // 16 dimensions
+                const uint32_t at = row + ((i ^ x) << 4);
+                uint32_t v[2][4], hi[4], lo[4];
+                lds128(at, v[0][0], v[0][1], v[0][2], v[0][3]);
+                lds128(at + 16384, v[1][0], v[1][1], v[1][2], v[1][3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a0 = v[k >> 1][2 * (k & 1)], a1 = v[k >> 1][2 * (k & 1) + 1];
+                    split_e4m3(bf16_lo(a0) * pw, bf16_hi(a0) * pw, bf16_lo(a1) * pw, bf16_hi(a1) * pw, hi[k], lo[k]);
+                }
+                sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                sts128(at + 16384, lo[0], lo[1], lo[2], lo[3]);
+            }
+        } else if constexpr (F16) {
             // This lane's row times a power of two that brings its largest |q| into [2^14, 2^15): f16 then
             // keeps every bf16 bit.  The magnitudes of bf16 values order like their bits.
             const uint32_t row = base + (r0 + lane) * 128;
@@ -772,6 +982,7 @@ struct Prefix {
         int q;
         float c;             // from S to log2 units
         int i, lo;           // TREE: drafted token; the first token of its window
+        uint32_t m0, m1;     // the first words of its mask
     };
     __device__ __forceinline__ Rows start_unit(const Unit& u, int tile, int r) const {
         Rows w;
@@ -782,8 +993,14 @@ struct Prefix {
         w.q = row % a.QG;
         w.c = 0.f;
         w.i = w.lo = 0;
+        w.m0 = w.m1 = 0;
         if constexpr (TREE) {
             w.i = row / a.QG;
+            if (a.masks && w.live) {   // asked for now, needed at the unit's last step
+                const uint32_t* m = a.masks + (long long)(u.seq0 + w.i) * a.words;
+                w.m0 = __ldcg(m);
+                w.m1 = __ldcg(m + 1);
+            }
             if (a.window > 0 && w.live) {
                 // its position: behind the cached tokens and the drafted ones that it sees
                 int before = w.i;
@@ -823,7 +1040,7 @@ struct Prefix {
         uint32_t bits = 0;
         if (fresh && w.live) {
             const uint32_t* m = a.masks + (long long)(u.seq0 + w.i) * a.words;
-            auto word = [&](int k) { return k >= 0 && k < a.words ? __ldcg(m + k) : 0u; };
+            auto word = [&](int k) { return k == 0 ? w.m0 : k == 1 ? w.m1 : k >= 0 && k < a.words ? __ldcg(m + k) : 0u; };
             const int k = j0 >> 5, sh = j0 & 31;    // floor and remainder, also below zero
             bits = __funnelshift_r(word(k), sh ? word(k + 1) : 0u, sh);
         }
@@ -866,19 +1083,7 @@ struct Prefix {
                             }
                         }
                     }
-                    if constexpr (TREE) {
-                        // only the steps with drafted tokens and those where some row's window starts are looked at bit by bit
-                        const int t0 = step_of(u, x, j) * kStep;
-                        if (t0 + kStep > x.ctx || (a.window > 0 && t0 < u.len - a.window && t0 + kStep > a.num_first)) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t see = visible(u, w, x, t0 + 32 * k);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!(see >> i & 1u)) s[k][i] = 0xFF800000u;   // -inf
-                            }
-                        }
-                    } else if (valid < kStep) {
+                    if (valid < kStep) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -949,16 +1154,222 @@ struct Prefix {
             if (!w.on) continue;
             if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
             tc_fence_after();
-            store_partial(u, tile, tO, w, m, l, l > 0.f ? F / l : 0.f);
+            store_rows(u, tile, tO, w, m, l, l > 0.f ? F / l : 0.f);
             tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
         }
     }
 
-    // The warp's 32 rows of O, times inv, to the partials.  A thread holds a row, and storing rows from
+    // The same for drafted tokens, whose rows do not see every token.  In few instructions: S is read twice, 64 columns at a time
+    // in rolled loops, once for the maximum and once for the weights, in place of a whole row in registers and straight
+    // code.  The code of all roles of an SM has to fit its instruction cache: with the straight code 21 % of the fp8 kernel's
+    // requests missed it, and a step of few rows took 2.0 us, half of it without an instruction.
+    __device__ __forceinline__ void softmax_tree(uint32_t tmem_base, int tile) {
+        const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+        const uint32_t lanes = (uint32_t)(r & ~31) << 16;
+        const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
+        constexpr float below = F16 ? kBelow : 0.f;
+        unsigned ns = 0, no = 0, step = 0;
+        Unit u;
+        while (next(u)) {
+            const Rows w = start_unit(u, tile, r);
+            // The other tile's warps release the scales for a tile without rows: units of few rows are the rule here.
+            if (!w.on) {
+                step += u.steps;
+                continue;
+            }
+            const int releases = active(u, 1) ? 1 : 2;
+            const bool idle = u.rt * kUnitRows + tile * kTileRows + (r & ~31) >= u.rows;   // no row of the warp's
+            const Sight x = sight(u);
+            float m = 0.f, l = 0.f, F = 1.f;   // m: the reference, which l and O count from
+            for (int j = 0; j < u.steps; ++j, ++step) {
+                const unsigned st = step % Cfg::kScales;
+                const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
+                const int t0 = step_of(u, x, j) * kStep;
+                if (F16 && !wait(bars + kBarScFull + 8 * st, step / Cfg::kScales & 1)) return;
+                if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
+                tc_fence_after();
+                if (!idle) {
+                    // only the steps with drafted tokens and those where some row's window starts are looked at bit by bit
+                    const bool hidden = t0 + kStep > x.ctx || (a.window > 0 && t0 < u.len - a.window && t0 + kStep > a.num_first);
+                    if (hidden) hide(u, w, x, t0, tS, sc);
+                    uint32_t s[2][32];
+                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        read_scores(s, tS + 64 * k, sc + 256 * k, hidden);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                t[c] = fmaxf(t[c], fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
+                                t[c + 2] = fmaxf(t[c + 2], fmaxf(__uint_as_float(s[c][i + 2]), __uint_as_float(s[c][i + 3])));
+                            }
+                    }
+                    const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * w.c, -1e30f);
+                    float nF = 1.f;
+                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
+                    if (j == 0) {
+                        m = top - below;
+                    } else {
+                        const bool up = top > m + (kLazy + below);
+                        if (__any_sync(kLanes, up || nF != F)) {
+                            float f = F / nF;
+                            if (nF == F) f = 1.f;
+                            if (up) {
+                                const float e = ex2(m - (top - below));
+                                m = top - below;
+                                l *= e;
+                                f *= e;
+                            }
+                            rescale(tO, f);
+                        }
+                    }
+                    F = nF;
+                    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        read_scores(s, tS + 64 * k, sc + 256 * k, hidden);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                fma2(s[c][i], s[c][i + 1], w.c, -m);
+                                fma2(s[c][i + 2], s[c][i + 3], w.c, -m);
+                                float2 y, z;
+                                y.x = ex2(__uint_as_float(s[c][i]));
+                                y.y = ex2(__uint_as_float(s[c][i + 1]));
+                                z.x = ex2(__uint_as_float(s[c][i + 2]));
+                                z.y = ex2(__uint_as_float(s[c][i + 3]));
+                                add2(la, y);
+                                add2(lb, z);
+                                p[i / 2] = F16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                                p[i / 2 + 1] = F16 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
+                            }
+                            tmem_st16(tS + 32 * k + 16 * c, p);   // over S that has been read
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars + (k ? kBarP2 : kBarP) + 8 * tile);
+                    }
+                    l += (la.x + la.y) + (lb.x + lb.y);
+                } else if (lane == 0) {   // its rows of P are whatever S was, and make rows of O that are nobody's
+                    mbar_arrive(bars + kBarP + 8 * tile);
+                    mbar_arrive(bars + kBarP2 + 8 * tile);
+                }
+                if (F16) {
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int k = 0; k < releases; ++k) mbar_arrive(bars + kBarScEmpty + 8 * st);
+                }
+            }
+            if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
+            tc_fence_after();
+            if (!idle) {
+                const float inv = l > 0.f ? F / l : 0.f;
+                if (w.live && u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
+                if (u.pieces > 1 || a.out_f32)
+                    store_rows(u, tile, tO, w, m, l, inv);
+                else
+                    store_out(u, tile, tO, w, inv);
+            }
+            tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
+        }
+    }
+    // 64 columns of S, times their K scales unless they carry them already.
+    __device__ __forceinline__ void read_scores(uint32_t (&s)[2][32], uint32_t at, uint32_t sc, bool scaled) const {
+        tmem_ld32(s[0], at);
+        tmem_ld32(s[1], at + 32);
+        tmem_wait_ld();
+        if (F16 && !scaled) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t f[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) mul2(s[k >> 1][(k & 1) * 16 + i], s[k >> 1][(k & 1) * 16 + i + 1], f[i], f[i + 1]);
+            }
+        }
+    }
+    // A step's S times its K scales, and -inf where the row does not see the token (whatever stands there: the choice comes last).
+    __device__ __forceinline__ void hide(const Unit& u, const Rows& w, const Sight& x, int t0, uint32_t tS, uint32_t sc) const {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t see = visible(u, w, x, t0 + 16 * k);
+            uint32_t s[16];
+            tmem_ld16(s, tS + 16 * k);
+            tmem_wait_ld();
+            if constexpr (F16) {
+                uint32_t f[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) mul2(s[i], s[i + 1], f[i], f[i + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!(see >> i & 1u)) s[i] = 0xFF800000u;
+            tmem_st16(tS + 16 * k, s);
+        }
+        tmem_wait_st();
+    }
+    // TREE: the row of a thread's O in a result of one piece, bf16.
+    __device__ __forceinline__ void store_out(const Unit& u, int tile, uint32_t tO, const Rows& w, float inv) const {
+        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96;
+        const uint32_t stage = sm + Cfg::kOffQ + tile * kSlotBytes + r0 * 128;
+        auto at = [&](int r, int c) { return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+        const int rows = min(32, u.rows - (u.rt * kUnitRows + tile * kTileRows + r0));
+        const long long mine = w.head * a.QG + w.q;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            uint32_t s[2][32];
+            tmem_ld32(s[0], tO + 64 * half);
+            tmem_ld32(s[1], tO + 64 * half + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t* x = &s[c >> 2][(c & 3) * 8];
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = pack_bf16(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+                sts128(at(lane, 8 * half + c), o[0], o[1], o[2], o[3]);
+            }
+        }
+        __syncwarp();
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4);
+            const long long dst = __shfl_sync(kLanes, mine, r);
+            uint32_t v0, v1, v2, v3;
+            lds128(at(r, c), v0, v1, v2, v3);
+            if (r < rows) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 8 * c) = make_uint4(v0, v1, v2, v3);
+        }
+        __syncwarp();   // the next unit's query rows are written by other lanes
+    }
+    // The rows that no unit holds: of a sequence in error zeros, of nobody what is there.  The join leaves rows of one piece alone.
+    __device__ void settle() const {
+        const int lane = threadIdx.x & 31, row = a.Hk * a.QG;
+        const int first = __ldcg(a.group_starts), last = __ldcg(a.group_starts + a.NG);
+        for (long long i = (long long)blockIdx.x * 32 + lane; i < (long long)(first + a.B - last) * row; i += gridDim.x * 32)
+            a.pieces[i < (long long)first * row ? i : i + (long long)(last - first) * row] = 1;
+        for (int g = blockIdx.x; g < a.NG; g += gridDim.x) {
+            const int s0 = __ldcg(a.group_starts + g), s1 = __ldcg(a.group_starts + g + 1), ctx = __ldcg(a.prefix_lens + g);
+            if (ctx >= 0 && ctx <= a.MP * a.BS && s1 - s0 <= a.MP * a.BS - ctx) continue;
+            const long long r0 = (long long)s0 * row, n = (long long)(s1 - s0) * row;
+            for (long long i = lane; i < n; i += 32) a.pieces[r0 + i] = 1;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + r0 * kHeadDim * (a.out_f32 ? 4 : 2));
+            for (long long i = lane; i < n * (a.out_f32 ? 32 : 16); i += 32) out[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    // The warp's 32 rows of O, times inv, to the partials (TREE: or to a result of one piece, fp32).  A thread holds a row, and storing rows from
     // there would touch 32 lines per instruction; each half (64 columns) goes through the warp's own rows of
     // its tile's query operand, which no product reads any more, and out two rows per instruction.
-    __device__ __forceinline__ void store_partial(const Unit& u, int tile, uint32_t tO, const Rows& w, float m, float l,
-                                                  float inv) const {
+    __device__ __forceinline__ void store_rows(const Unit& u, int tile, uint32_t tO, const Rows& w, float m, float l,
+                                               float inv) const {
         const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96;
         const uint32_t stage = sm + Cfg::kOffQ + tile * kSlotBytes + r0 * 128;
         auto at = [&](int r, int c) {   // 16 bytes c of the half row r
@@ -966,11 +1377,13 @@ struct Prefix {
         };
         const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
         const int rows = min(32, u.rows - row0);   // may be negative
-        const long long mine = (w.head * a.slots + u.slot) * a.QG + w.q;
-        if (w.live) {
+        const bool whole = TREE && u.pieces == 1;
+        const long long mine = whole ? w.head * a.QG + w.q : (w.head * a.slots + u.slot) * a.QG + w.q;
+        float* const to = whole ? out_rows() : a.part_o;
+        if (w.live && !whole) {
             a.part_l[mine] = l;
             a.part_m[mine] = m * kLn2S;
-            if (u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
+            if (!TREE && u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -995,10 +1408,16 @@ struct Prefix {
                 uint32_t v0, v1, v2, v3;
                 lds128(at(r, c), v0, v1, v2, v3);
                 if (r < rows)
-                    *reinterpret_cast<uint4*>(a.part_o + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
+                    *reinterpret_cast<uint4*>(to + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
             }
         }
         __syncwarp();   // the next unit's query rows are written by other lanes
+    }
+    __device__ __forceinline__ float* out_rows() const {
+        if constexpr (TREE)
+            return static_cast<float*>(a.out);
+        else
+            return nullptr;
     }
     // O *= f, one row per thread (rare; few registers, since S is held meanwhile).
     static __device__ __forceinline__ void rescale(uint32_t tO, float f) {
@@ -1016,17 +1435,17 @@ struct Prefix {
 };
 
 template <int KV, class Args>
-__global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
+__global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
     pda_prefix_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
                       const Args a) {
-    using Cfg = SharedCfg<KV>;
+    using Cfg = SharedCfg<KV, Args>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sm = smem_addr(smem);
     const uint32_t bars = sm + Cfg::kOffBars;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::kSlots; ++i) {
-            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 ? kConvertWarps : 1);
+            mbar_init(bars + kBarFull + 8 * i, Cfg::kF16 && !Cfg::kQ8 ? kConvertWarps : 1);
             mbar_init(bars + kBarEmpty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1042,6 +1461,10 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
             mbar_init(bars + kBarScRaw + 8 * i, 1);
             mbar_init(bars + kBarScFull + 8 * i, 1);
             mbar_init(bars + kBarScEmpty + 8 * i, 8);
+            if (Cfg::kQ8) {
+                mbar_init(bars + kBarVFull + 8 * i, kConvertWarps);
+                mbar_init(bars + kBarVEmpty + 8 * i, 1);
+            }
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + kBarUnitFull + 8 * i, 1);
@@ -1087,7 +1510,12 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if (fine) p.softmax(tmem, warp >> 2);
+        if (fine) {
+            if constexpr (Cfg::kTree)
+                p.softmax_tree(tmem, warp >> 2);
+            else
+                p.softmax(tmem, warp >> 2);
+        }
     } else {
         if constexpr (Cfg::kF16)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -1098,8 +1526,11 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
                 p.copies(&kv_map, &sc_map);
             else if (warp == 9)
                 p.products(tmem);
-            else if (warp == 11)
+            else if (warp == 11) {
                 p.give(split, first, at, end);
+                if constexpr (Cfg::kTree)
+                    if (!split.refused) p.settle();
+            }
             else if (Cfg::kF16 && warp == 10)
                 p.scales();
             else if (Cfg::kF16 && warp >= 12)
@@ -1118,7 +1549,7 @@ __global__ void __launch_bounds__(SharedCfg<KV>::kThreads, 1)
 template <int KV, class Args>
 static int launch_prefix(const Args& a, const CUtensorMap& kv_map, const CUtensorMap& sc_map, int ctas,
                          cudaStream_t stream) {
-    using Cfg = SharedCfg<KV>;
+    using Cfg = SharedCfg<KV, Args>;
     static bool attr_set[64] = {false};
     static std::mutex mu;
     int dev = 0;

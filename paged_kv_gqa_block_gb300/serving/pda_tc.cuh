@@ -68,6 +68,8 @@ constexpr uint32_t umma_idesc(bool bf16, bool b_mn_major, int M, int N) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// kind::f8f6f4 with e4m3 A and B, K-major, 32 of K per instruction.
+constexpr uint32_t umma_idesc_e4m3(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 // The instructions below take effect in the one thread whose `leader` is set, and are executed by the whole
 // (convergent) warp: tcgen05 reads its operands from uniform registers, and inside a branch of one lane
 // every operand of every instruction would first be moved there one by one (80 cycles per product instead
@@ -78,6 +80,15 @@ __device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a,
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+        : "memory");
+}
+// The same of e4m3 operands.
+__device__ __forceinline__ void umma_ss_f8(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
         : "memory");
 }

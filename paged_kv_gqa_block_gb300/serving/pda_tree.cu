@@ -20,99 +20,91 @@
 namespace pda {
 
 struct TreeJoinArgs {
-    const int* token_starts;
-    const int* context_lens;
     const int* refused;
     const float* part_o;   // [N][Hk][slots][QG][D]
     const float* part_l;   // [N][Hk][slots][QG]
     const float* part_m;
     const int* pieces;     // [N][Hk][QG]
     void* out;
-    int N, B, Hk, QG, room, slots, out_f32;
+    long long rows;        // N * Hk * QG
+    int QG, slots, out_f32;
 };
 
-// One CTA per (drafted token, KV head), one warp per query row; lane i holds (m, l) of pieces i, i + 32, ..; each lane sums four
-// dimensions over the pieces in order.  Rows of tokens that no sequence has stay as they are.
-__global__ void __launch_bounds__(512) pda_tree_join_kernel(const TreeJoinArgs a) {
+// One warp per row of more than one piece; the rows of a warp lie as far apart as there are warps, and their numbers of pieces
+// are read 32 at a time, so that rows of one piece, which are whole already, cost next to nothing.  Lane i holds (m, l) of
+// pieces i, i + 32, ..; each lane sums four dimensions over the pieces in order.
+__global__ void __launch_bounds__(256) pda_tree_join_kernel(const TreeJoinArgs a) {
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const long long unit = blockIdx.x;
-    const int token = (int)(unit / a.Hk);
-    const int pieces = __ldcg(a.pieces + unit * a.QG + q);   // not written for a sequence in error; not used then
-    if (__ldcg(a.refused)) return;
-    // the sequence: the last start that is not above the token, 32 starts at a time
-    int lo = 0, n = a.B + 1;   // starts lo .. lo+n-1 hold the first that is above it, or none does
-    while (n > 0) {
-        const int step = (n + 31) / 32, at = lo + lane * step;
-        const bool below = lane * step < n && __ldg(a.token_starts + at) <= token;
-        const int k = __popc(__ballot_sync(kLanes, below));
-        if (k == 0) break;                       // the first of them is above
-        const int base = lo + (k - 1) * step;    // not above
-        const int end = min(lo + n, base + step);
-        lo = base + 1;
-        n = step == 1 ? 0 : end - lo;
-    }
-    const int b = lo - 1;
-    if (b < 0 || b >= a.B) return;
-    const int drafted = __ldg(a.token_starts + b + 1) - __ldg(a.token_starts + b), ctx = __ldg(a.context_lens + b);
-    const bool fine = ctx >= 0 && ctx <= a.room && drafted <= a.room - ctx;
-    const int total = fine ? max(0, min(a.slots, pieces)) : 0;
-    const long long row0 = unit * a.slots * a.QG + q;
-    auto stats = [&](int i, float& m, float& l) {
-        m = -INFINITY;
-        l = 0.f;
-        if (i < total) {
-            m = __ldcg(a.part_m + row0 + (long long)i * a.QG);
-            l = __ldcg(a.part_l + row0 + (long long)i * a.QG);
-            if (l == 0.f) m = -INFINITY;   // a piece of which the row sees nothing
-        }
-    };
-    float m0, l0;
-    stats(lane, m0, l0);
-    float M = m0;
-    for (int i = lane + 32; i < total; i += 32) {
-        float m, l;
-        stats(i, m, l);
-        M = fmaxf(M, m);
-    }
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * 8, first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int refused = __ldcg(a.refused);
+    for (long long k0 = 0; first + k0 * warps < a.rows; k0 += 32) {
+        const long long mine = first + (k0 + lane) * warps;
+        const int pieces = mine < a.rows ? __ldcg(a.pieces + mine) : 1;
+        if (refused) return;
+        unsigned todo = __ballot_sync(kLanes, pieces > 1);
+        while (todo) {
+            const int src = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const long long row = first + (k0 + src) * warps, unit = row / a.QG;
+            const int total = min(a.slots, __shfl_sync(kLanes, pieces, src));
+            const long long row0 = unit * a.slots * a.QG + (row - unit * a.QG);
+            auto stats = [&](int i, float& m, float& l) {
+                m = -INFINITY;
+                l = 0.f;
+                if (i < total) {
+                    m = __ldcg(a.part_m + row0 + (long long)i * a.QG);
+                    l = __ldcg(a.part_l + row0 + (long long)i * a.QG);
+                    if (l == 0.f) m = -INFINITY;   // a piece of which the row sees nothing
+                }
+            };
+            float m0, l0;
+            stats(lane, m0, l0);
+            float M = m0;
+            for (int i = lane + 32; i < total; i += 32) {
+                float m, l;
+                stats(i, m, l);
+                M = fmaxf(M, m);
+            }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kLanes, M, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    for (int i0 = 0; i0 < total; i0 += 32) {
-        if (i0 > 0) stats(i0 + lane, m0, l0);
-        const float w = l0 != 0.f ? partition_weight(l0, m0, M) : 0.f;
-        sum += w;
-        const int n = min(32, total - i0);
-        for (int j0 = 0; j0 < n; j0 += 8) {
-            float4 o[8];
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kLanes, M, o));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+            for (int i0 = 0; i0 < total; i0 += 32) {
+                if (i0 > 0) stats(i0 + lane, m0, l0);
+                const float w = l0 != 0.f ? partition_weight(l0, m0, M) : 0.f;
+                sum += w;
+                const int n = min(32, total - i0);
+                for (int j0 = 0; j0 < n; j0 += 8) {
+                    float4 o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                o[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row0 + (long long)(i0 + min(j0 + j, n - 1)) * a.QG) * kHeadDim) + lane);
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row0 + (long long)(i0 + min(j0 + j, n - 1)) * a.QG) * kHeadDim) + lane);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = __shfl_sync(kLanes, w, (j0 + j) & 31);
-                if (j0 + j < n) {
-                    acc.x = fmaf(f, o[j].x, acc.x);
-                    acc.y = fmaf(f, o[j].y, acc.y);
-                    acc.z = fmaf(f, o[j].z, acc.z);
-                    acc.w = fmaf(f, o[j].w, acc.w);
+                    for (int j = 0; j < 8; ++j) {
+                        const float f = __shfl_sync(kLanes, w, (j0 + j) & 31);
+                        if (j0 + j < n) {
+                            acc.x = fmaf(f, o[j].x, acc.x);
+                            acc.y = fmaf(f, o[j].y, acc.y);
+                            acc.z = fmaf(f, o[j].z, acc.z);
+                            acc.w = fmaf(f, o[j].w, acc.w);
+                        }
+                    }
                 }
             }
-        }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kLanes, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing gives zeros
-    const long long row = unit * a.QG + q;
-    if (a.out_f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + 4 * lane) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    } else {
-        uint2 v;
-        v.x = pack_bf16(acc.x * inv, acc.y * inv);
-        v.y = pack_bf16(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kHeadDim + 4 * lane) = v;
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kLanes, sum, o);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees nothing gives zeros
+            if (a.out_f32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + 4 * lane) =
+                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            } else {
+                uint2 v;
+                v.x = pack_bf16(acc.x * inv, acc.y * inv);
+                v.y = pack_bf16(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kHeadDim + 4 * lane) = v;
+            }
+        }
     }
 }
 
@@ -219,6 +211,8 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
     a.words = 2 * mask_words;
     a.window = window;
     a.num_first = num_first;
+    a.out = out;
+    a.out_f32 = out_dtype == PDA_OUT_F32;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap kv_map, sc_map;
     if (!encode_tokens_map(&kv_map, kv_cache, plan, num_cache_blocks, a.BS, 1)) return PDA_ERR_LAUNCH;
@@ -235,24 +229,20 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
         rc = launch_prefix<PDA_KV_TQ4>(a, kv_map, sc_map, ctas, s);
     if (rc != PDA_OK) return rc;
     TreeJoinArgs j = {};
-    j.token_starts = token_starts;
-    j.context_lens = context_lens;
     j.refused = a.refused;
     j.part_o = a.part_o;
     j.part_l = a.part_l;
     j.part_m = a.part_m;
     j.pieces = a.pieces;
     j.out = out;
-    j.N = a.B;
-    j.B = a.NG;
-    j.Hk = a.Hk;
+    j.rows = num_tokens * a.Hk * a.QG;
     j.QG = a.QG;
-    j.room = a.MP * a.BS;
     j.slots = a.slots;
-    j.out_f32 = out_dtype == PDA_OUT_F32;
+    j.out_f32 = a.out_f32;
+    const long long join = (j.rows + 7) / 8;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hk));
-    cfg.blockDim = dim3(a.QG * 32);
+    cfg.gridDim = dim3((unsigned)(join < 4ll * sms ? join : 4ll * sms));
+    cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

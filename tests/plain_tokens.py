@@ -3,8 +3,12 @@
 With p_t the weight of token t (their sum is 1) and V_t its value, a row's result is sum p_t V_t over the tokens that it sees.  What
 the kernels may do to it:
   logits   128 products of q and k are summed in fp32, each addition off by at most a step 2^-23 of |q| |k| (the tensor cores may
-           truncate), two more for the scale: 130 of them.  TQ4: centroids are rounded to f16, 2^-11 of every product.  A logit
-           off by d moves a weight by a factor e^d, and the weights' sum by as much
+           truncate), two more for the scale: 130 of them.  TQ4: centroids are rounded to f16, 2^-11 of every product.  Drafted
+           trees, fp8: q, times the power of two that brings its row's largest into [2^7, 2^8), is the sum of two e4m3 parts: the
+           high one is off by at most half a step, 2^(e-4) for |q| in [2^e, 2^(e+1)), and that rest is a multiple of q's own
+           last bit 2^(e-7), so 4 bits, exact where 2^(e-7) is no less than e4m3's smallest step 2^-9; below, it is off by at
+           most 2^-10, 2^-17 of the row's largest; and 256 fp32 additions in place of 128.  A logit off by d moves a weight by
+           a factor e^d, and the weights' sum by as much
   P        drafted trees: bf16 KV 2^-8 of the weight; else f16, 2^-11 of it, or 2^-32 of the row's largest where that is more, but
            no more than itself (the reference is 7 below the maximum, half a step of f16's smallest is 2^-25)
            windows (the partition pass): bf16 KV 2^-16 (two bf16 terms); else its product with V's scale to f16, 2^-11, or
@@ -44,6 +48,9 @@ def attend(q, k, v, see, kv, *, tree, vscale=None, vzero=None, step=None, used=N
     a = np.abs(v)
     reach = np.where(see, scale * np.abs(q) @ np.abs(k).T, 0.0).max(-1, keepdims=True)
     ds = reach * (130 * 2.0 ** -23 + (2.0 ** -11 * 1.001 if kv == TQ4 else 0.0))
+    if kv == FP8 and tree:
+        size = np.where(see, np.abs(k).sum(-1), 0.0).max(-1, keepdims=True)
+        ds = ds + reach * 1.1 * 128 * 2.0 ** -23 + 2.0 ** -17 * scale * np.abs(q).max(-1, keepdims=True) * size
     e = (np.expm1(2 * ds) + (T + 64) * 2.0 ** -23) * (p @ a)
     big = p.max(-1, keepdims=True)
     eps = 2.0 ** -11
