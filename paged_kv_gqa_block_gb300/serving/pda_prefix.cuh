@@ -355,8 +355,9 @@ struct Prefix {
                 const unsigned q = (raws - 1 - s) / kNS;   // the slot's last use
                 (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
             }
-        for (int s = 0; s < Cfg::kKeys; ++s)
-            if (keys > (unsigned)s) (void)mbar_wait(bars + kBarFull + 8 * s, (keys - 1 - s) / Cfg::kKeys & 1, kDefaultTimeoutNs);
+        if constexpr (Q8)
+            for (int s = 0; s < Cfg::kKeys; ++s)
+                if (keys > (unsigned)s) (void)mbar_wait(bars + kBarFull + 8 * s, (keys - 1 - s) / Cfg::kKeys & 1, kDefaultTimeoutNs);
         if (F16) {
             const unsigned issued = (seq + kTiles - 1) / kTiles;   // steps whose scales were asked for
             for (int s = 0; s < Cfg::kScales; ++s)

@@ -22,7 +22,8 @@ namespace pda {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kTokThreads = 256;
 constexpr int kTokWarps = kTokThreads / 32;
-constexpr int kMaxTokensPerCta = 16;
+constexpr int kMaxTokensPerCta = 64;
+constexpr int kHeadsAhead = 4;            // KV heads of one token that a warp takes together, at most, loads first
 
 struct TokenArgs {
     uint8_t* cache;              // read_kv does not write it
@@ -38,15 +39,17 @@ struct TokenArgs {
     long long k_stride, v_stride;
     long long num_cache_blocks, cache_block_bytes, meta_offset_bytes;
     int num_tokens, B, Hk, MB, BS, bs_shift, per_cta;
+    int ahead, groups;           // KV heads of an item, and items of a token
+    unsigned long long by_groups; // 2^32 / groups, rounded up (0 where a CTA has one token)
 };
 
-// Where the CTA's tokens lie: byte offset of the block in the pool and slot, or a negative offset for a token that is no
-// sequence's or has no place.  False (in every thread) where token_starts do not ascend within [0, num_tokens].
+// Where the CTA's tokens lie in the pool: byte offset of the token's row (head 0) and of its first field, or a negative
+// offset for a token that is no sequence's or has no place.  False (in every thread) where token_starts do not ascend within [0, num_tokens].
 struct Places {
-    long long block[kMaxTokensPerCta];
-    int slot[kMaxTokensPerCta];
+    long long row[kMaxTokensPerCta], field[kMaxTokensPerCta];
 };
-__device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int first, int n) {
+__device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int first, int n, int row_bytes,
+                                            int field_bytes) {
     bool bad = false;
     for (int b = threadIdx.x; b <= a.B; b += kTokThreads) {
         const int s = __ldg(a.token_starts + b);
@@ -67,8 +70,7 @@ __device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int 
                 hi = mid;
         }
         const int b = lo - 1;
-        long long block = -1;
-        int slot = 0;
+        long long row = -1, field = 0;
         if (b >= 0 && b < a.B) {
             const int p0 = __ldg(a.positions + b);
             const long long pos = (long long)p0 + (i - __ldg(a.token_starts + b));
@@ -80,29 +82,49 @@ __device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int 
                     if (id < 0 || id >= a.num_cache_blocks) {
                         if (a.err_word) atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
                     } else {
-                        block = id * a.cache_block_bytes;
-                        slot = (int)pos & (a.BS - 1);
+                        const int slot = (int)pos & (a.BS - 1);
+                        row = id * a.cache_block_bytes + (long long)slot * a.Hk * row_bytes;
+                        field = id * a.cache_block_bytes + a.meta_offset_bytes + slot * field_bytes;
                     }
                 }
             }
         }
-        at.block[threadIdx.x] = block;
-        at.slot[threadIdx.x] = slot;
+        at.row[threadIdx.x] = row;
+        at.field[threadIdx.x] = field;
     }
     __syncthreads();
     return true;
 }
 
+// What a warp takes at a time: up to kHeadsAhead KV heads of one token.  Their rows lie a fixed number of bytes apart, so that one
+// address serves all; item x of a CTA is group x % groups of its token x / groups (x < 64 groups, and groups <= 4096 where a CTA has
+// more than one token, so the rounded-up inverse is exact).
+struct Item {
+    int t, h, n;   // token of the CTA, first KV head, KV heads
+    __device__ __forceinline__ Item(const TokenArgs& a, int x)
+        : t((int)(x * a.by_groups >> 32)), h((x - t * a.groups) * a.ahead), n(min(a.ahead, a.Hk - h)) {}
+};
+
 // ------------------------------------------------------------------------- writing
+// x / b rounded to the nearest fp32 value, for many x: r is 1 / b rounded.  Each step adds the remainder over b, which an fma
+// gives exactly; with r correctly rounded and a quotient within one unit in its last place the result is correctly rounded
+// (Markstein), and the first step takes x * r, off by two half units, there.  Holds while no remainder underflows; where
+// the quotient is too small for that, what it is used for does not depend on its last place (see the callers).
+__device__ __forceinline__ float quotient(float x, float b, float r) {
+    float q = __fmul_rn(x, r);
+    q = __fmaf_rn(__fmaf_rn(-q, b, x), r, q);
+    return __fmaf_rn(__fmaf_rn(-q, b, x), r, q);
+}
 // The sorted codebook: midpoints of neighbours (15, then +inf) and the code of each rank.
-struct Codebook {
+struct __align__(16) Codebook {
     float mid[16];
     uint32_t code[16];
+    int plain;   // no midpoint but 0 is below 2^-60
 };
 __device__ __forceinline__ void sort_codebook(const float* centroids, Codebook& book, float* sorted) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const float c = __ldg(centroids + (lane & 15));
+        const float c = __ldg(centroids + (lane & 15));   // lanes 16 .. 31: not looked at
         int rank = 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -114,52 +136,86 @@ __device__ __forceinline__ void sort_codebook(const float* centroids, Codebook& 
             book.code[rank] = lane;
         }
         __syncwarp();
-        if (lane < 16) book.mid[lane] = lane < 15 ? __fmul_rn(__fadd_rn(sorted[lane], sorted[lane + 1]), 0.5f) : INFINITY;
+        const float mid = lane < 15 ? __fmul_rn(__fadd_rn(sorted[lane], sorted[lane + 1]), 0.5f) : INFINITY;
+        if (lane < 16) book.mid[lane] = mid;
+        const bool plain = __all_sync(kAll, lane >= 15 || mid == 0.f || fabsf(mid) >= 8.6736174e-19f);
+        if (lane == 0) book.plain = plain;
     }
 }
 
-__device__ __forceinline__ float half_warp_max(float x) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
-    return x;
+// Integers that are ordered like the floats.
+__device__ __forceinline__ int ordered(float x) {
+    const int b = __float_as_int(x);
+    return b ^ (b >> 31 & 0x7FFFFFFF);
 }
+__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ (b >> 31 & 0x7FFFFFFF)); }
 __device__ __forceinline__ float f16_saturated(float x) {
     return __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
 }
 
-// fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.
-__device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS, int slot) {
-    float x[8];
+__device__ __forceinline__ uint32_t cut_f16(float x, float y) {   // towards zero
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+
+// fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.  Bound by instructions (HBM would take half of the time):
+// a division and the conversion to e4m3 per value are the larger part of them, so both are done only where they decide.  A value
+// times 2^-8 has e4m3's exponent field in f16's bits 13 .. 10 and its mantissa behind it; f16 cut towards zero, plus half of
+// e4m3's last place, cut again, is the code of every value that is no tie.  The correctly rounded quotient lies between x times
+// 1 / scale a little too small and a little too large (2^-21 either way: the approximate inverse is off by 2^-23, four products
+// and the quotient's own rounding by 2^-24 each), and where both have one code that is the quotient's.  Else, in about one row of 500, and
+// in rows that are tiny or hold infinities or NaN, every value is divided.
+__device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float top = 0.f;
+    // magnitudes of bf16 values are ordered like their bits
+    const uint32_t mx = __vmaxs2(__vmaxs2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxs2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    int top = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+    const float most = __uint_as_float((uint32_t)top << 16);
+    float scale = top > 0 ? quotient(most, 448.f, 1.f / 448.f) : 1.f;   // of a normal number that counts
+    const float r = rcp_approx(scale) * 0.00390625f, lo = r * (1.f - 4.76837158e-7f), hi = r * (1.f + 4.76837158e-7f);
+    uint32_t c[4], differ = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-        top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+        const float x = bf16_lo(w[i]), y = bf16_hi(w[i]);
+        c[i] = cut_f16(x * lo, y * lo) + 0x00400040u;
+        differ |= c[i] ^ (cut_f16(x * hi, y * hi) + 0x00400040u);
     }
-    top = half_warp_max(top);
-    const float scale = top > 0.f ? __fdiv_rn(top, 448.f) : 1.f;
-    uint32_t c[4];
+    // the upper byte of each value shifted by one: exponent and mantissa; the signs are those of the bf16 values
+    uint32_t a = (__byte_perm(c[0] << 1, c[1] << 1, 0x7531) & 0x7F7F7F7Fu) | (__byte_perm(w[0], w[1], 0x7531) & 0x80808080u);
+    uint32_t b = (__byte_perm(c[2] << 1, c[3] << 1, 0x7531) & 0x7F7F7F7Fu) | (__byte_perm(w[2], w[3], 0x7531) & 0x80808080u);
+    const bool odd = !(most > 1e-25f && top < 0x7F80);   // the same in the half warp
+    if ((differ & 0xFF80FF80u) || odd) {
+        if (odd) {   // pda_append_kv's maximum and division; fmaxf passes NaN by
+            const uint32_t mine = 0xFFFFu << (lane & 16);
+            float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
-    *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    if ((lane & 15) == 0) scales[(lane >> 4) * BS + slot] = scale;
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mine, m, o));
+            scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+        }
+        auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(v), scale), __fdiv_rn(bf16_hi(v), scale)); };
+        a = code(w[0]) | code(w[1]) << 16;
+        b = code(w[2]) | code(w[3]) << 16;
+    }
+    *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(a, b);
+    if ((lane & 15) == 0) scales[(lane >> 4) * BS] = scale;
 }
 
 // TQ4: every lane holds four dimensions of K and of V, 4l .. 4l+3.
 __device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, uint2 kraw, uint2 vraw, const Codebook& book, int lane,
-                                          int BS, int slot) {
+                                          int BS) {
     const float k[4] = {bf16_lo(kraw.x), bf16_hi(kraw.x), bf16_lo(kraw.y), bf16_hi(kraw.y)};
     const float v[4] = {bf16_lo(vraw.x), bf16_hi(vraw.x), bf16_lo(vraw.y), bf16_hi(vraw.y)};
     float sum = fmaf(k[0], k[0], fmaf(k[1], k[1], fmaf(k[2], k[2], k[3] * k[3])));
     float lo = fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), hi = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(kAll, sum, o);
-        lo = fminf(lo, __shfl_xor_sync(kAll, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kAll, hi, o));
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    lo = from_ordered(__reduce_min_sync(kAll, ordered(lo)));
+    hi = from_ordered(__reduce_max_sync(kAll, ordered(hi)));
     // |k| is rounded to f16 once: nine fp32 roundings of positive terms and the root are off by less than 2^-20, and where
     // that does not decide the f16 value (one row in a thousand) the sum is taken again in 64 bits.  The sum is the same in
     // every lane (a butterfly adds the same pairs), so the warp stays together.
@@ -180,24 +236,28 @@ __device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, uint2 
         norm_bits = __half_as_ushort(__float2half_rn(cut));
     }
     const float norm = __half2float(__ushort_as_half(norm_bits));
-    const float by = norm > 0.f ? norm : 1.f;
+    const float by = norm > 0.f ? norm : 1.f, rk = __frcp_rn(by);
     uint32_t kc = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float x = __fdiv_rn(k[i], by);
-        int r = book.mid[7] < x ? 8 : 0;
-        r += book.mid[r + 3] < x ? 4 : 0;
-        r += book.mid[r + 1] < x ? 2 : 0;
-        r += book.mid[r] < x ? 1 : 0;
-        kc |= book.code[r] << (4 * i);
+        // |k| is at most the norm, or the norm is 65504: nothing overflows; a quotient below 2^-61 lies between the same midpoints
+        // whatever its last places
+        const float x = book.plain ? quotient(k[i], by, rk) : __fdiv_rn(k[i], by);
+        // midpoints 7, then 3 or 11, then the three of one quarter at once
+        const bool upper = book.mid[7] < x;
+        const int q = (upper ? 2 : 0) + ((upper ? book.mid[11] : book.mid[3]) < x ? 1 : 0);
+        const float4 m = *reinterpret_cast<const float4*>(book.mid + 4 * q);
+        const int rank = 4 * q + (m.x < x ? 1 : 0) + (m.y < x ? 1 : 0) + (m.z < x ? 1 : 0);
+        kc |= book.code[rank] << (4 * i);
     }
     const float zero = f16_saturated(lo), step = f16_saturated(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    const float vby = step > 0.f ? step : 1.f;
+    const float vby = step > 0.f ? step : 1.f, rv = __frcp_rn(vby);   // at least f16's smallest, 2^-24
     uint32_t vc = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v[i], zero), vby)), 0.f), 15.f);
-        vc |= (uint32_t)c << (4 * i);
+        // brought into 0 .. 15, then rounded by the sum with 1.5 * 2^23, whose last bits are the integer
+        const float c = fminf(fmaxf(quotient(__fsub_rn(v[i], zero), vby, rv), 0.f), 15.f);
+        vc |= (__float_as_uint(__fadd_rn(c, 12582912.f)) & 15u) << (4 * i);
     }
     // even lanes store eight codes of K, odd lanes of V
     const uint32_t give = lane & 1 ? kc : vc, got = __shfl_xor_sync(kAll, give, 1);
@@ -205,41 +265,50 @@ __device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, uint2 
     *reinterpret_cast<uint32_t*>(row + (lane & 1) * 64 + (lane >> 1) * 4) = word;
     if (lane < 3) {
         const uint16_t f = lane == 0 ? norm_bits : __half_as_ushort(__float2half_rn(lane == 1 ? step : zero));
-        fields[lane * BS + slot] = f;
+        fields[lane * BS] = f;
     }
 }
 
-// One warp per (token, KV head) at a time.
 template <int KV>
 __global__ void __launch_bounds__(kTokThreads) pda_write_kernel(const TokenArgs a) {
     __shared__ Places at;
     __shared__ Codebook book;
     __shared__ float sorted[16];
+    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;   // K and V of one head
     const int first = blockIdx.x * a.per_cta, n = min(a.per_cta, a.num_tokens - first);
     if constexpr (KV == PDA_KV_TQ4) sort_codebook(a.centroids, book, sorted);
-    if (!find_places(a, at, first, n)) return;
+    if (!find_places(a, at, first, n, kRow, KV == PDA_KV_FP8_E4M3 ? 4 : 2)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;   // K and V of one head
-    for (int r = warp; r < n * a.Hk; r += kTokWarps) {
-        const int t = r / a.Hk, h = r - t * a.Hk;
-        if (at.block[t] < 0) continue;
-        const long long i = first + t;
-        const uint16_t* k = a.k_new + i * a.k_stride + h * kHeadDim;
-        const uint16_t* v = a.v_new + i * a.v_stride + h * kHeadDim;
-        uint8_t* block = a.cache + at.block[t];
-        const int slot = at.slot[t];
-        uint8_t* row = block + ((long long)slot * a.Hk + h) * kRow;
-        uint8_t* meta = block + a.meta_offset_bytes;
-        if constexpr (KV == PDA_KV_TQ4) {
-            write_tq4(row, reinterpret_cast<uint16_t*>(meta) + (long long)h * 3 * a.BS, __ldg(reinterpret_cast<const uint2*>(k) + lane),
-                      __ldg(reinterpret_cast<const uint2*>(v) + lane), book, lane, a.BS, slot);
-        } else {
-            const uint4 raw = __ldg(reinterpret_cast<const uint4*>(lane < 16 ? k : v) + (lane & 15));
-            if constexpr (KV == PDA_KV_BF16)
-                *reinterpret_cast<uint4*>(row + 16 * lane) = raw;
-            else
-                write_fp8(row, reinterpret_cast<float*>(meta) + (long long)h * 2 * a.BS, raw, lane, a.BS, slot);
-        }
+    for (int item = warp; item < n * a.groups; item += kTokWarps) {
+        const Item x(a, item);
+        if (at.row[x.t] < 0) continue;
+        const uint16_t* k = a.k_new + (first + x.t) * a.k_stride + x.h * kHeadDim;
+        const uint16_t* v = a.v_new + (first + x.t) * a.v_stride + x.h * kHeadDim;
+        uint4 raw[kHeadsAhead];   // TQ4: four dimensions of K, four of V; else eight of one of them
+#pragma unroll
+        for (int i = 0; i < kHeadsAhead; ++i)
+            if (i < x.n) {
+                if constexpr (KV == PDA_KV_TQ4) {
+                    const uint2 kw = __ldg(reinterpret_cast<const uint2*>(k + i * kHeadDim) + lane);
+                    const uint2 vw = __ldg(reinterpret_cast<const uint2*>(v + i * kHeadDim) + lane);
+                    raw[i] = make_uint4(kw.x, kw.y, vw.x, vw.y);
+                } else {
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>((lane < 16 ? k : v) + i * kHeadDim) + (lane & 15));
+                }
+            }
+        uint8_t* row = a.cache + at.row[x.t] + (long long)x.h * kRow;
+        uint8_t* field = a.cache + at.field[x.t];
+#pragma unroll
+        for (int i = 0; i < kHeadsAhead; ++i)
+            if (i < x.n) {
+                if constexpr (KV == PDA_KV_TQ4)
+                    write_tq4(row + i * kRow, reinterpret_cast<uint16_t*>(field) + (x.h + i) * 3 * a.BS, make_uint2(raw[i].x, raw[i].y),
+                              make_uint2(raw[i].z, raw[i].w), book, lane, a.BS);
+                else if constexpr (KV == PDA_KV_BF16)
+                    *reinterpret_cast<uint4*>(row + i * kRow + 16 * lane) = raw[i];
+                else
+                    write_fp8(row + i * kRow, reinterpret_cast<float*>(field) + (x.h + i) * 2 * a.BS, raw[i], lane, a.BS);
+            }
     }
 }
 
@@ -249,63 +318,76 @@ template <int KV, bool F32>
 __global__ void __launch_bounds__(kTokThreads) pda_read_kernel(const TokenArgs a) {
     __shared__ Places at;
     __shared__ float book[16];
+    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;
     const int first = blockIdx.x * a.per_cta, n = min(a.per_cta, a.num_tokens - first);
     if (KV == PDA_KV_TQ4 && threadIdx.x < 16) book[threadIdx.x] = __ldg(a.centroids + threadIdx.x);
-    if (!find_places(a, at, first, n)) return;
+    if (!find_places(a, at, first, n, kRow, KV == PDA_KV_FP8_E4M3 ? 4 : 2)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-    constexpr int kRow = KV == PDA_KV_BF16 ? 512 : KV == PDA_KV_FP8_E4M3 ? 256 : 128;
-    for (int r = warp; r < n * a.Hk; r += kTokWarps) {
-        const int t = r / a.Hk, h = r - t * a.Hk;
-        if (at.block[t] < 0) continue;
-        const uint8_t* block = a.cache + at.block[t];
-        const int slot = at.slot[t];
-        const uint8_t* row = block + ((long long)slot * a.Hk + h) * kRow;
-        const uint8_t* meta = block + a.meta_offset_bytes;
-        float x[8];
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if constexpr (KV == PDA_KV_BF16) {
-            raw = __ldg(reinterpret_cast<const uint4*>(row) + lane);
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    void* const out = half ? a.v_out : a.k_out;
+    for (int item = warp; item < n * a.groups; item += kTokWarps) {
+        const Item at_heads(a, item);
+        if (at.row[at_heads.t] < 0 || !out) continue;
+        const uint8_t* row = a.cache + at.row[at_heads.t] + (long long)at_heads.h * kRow;
+        const uint8_t* field = a.cache + at.field[at_heads.t];
+        uint4 raw[kHeadsAhead];                // fp8: x, y, TQ4: x
+        float m[kHeadsAhead], z[kHeadsAhead];  // fp8: the scale; TQ4: k_norm, or v_scale and v_zero
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16_lo(w[i]);
-                x[2 * i + 1] = bf16_hi(w[i]);
+        for (int i = 0; i < kHeadsAhead; ++i)
+            if (i < at_heads.n) {
+                if constexpr (KV == PDA_KV_BF16) {
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>(row + i * kRow) + lane);
+                } else if constexpr (KV == PDA_KV_FP8_E4M3) {
+                    const uint2 c = __ldg(reinterpret_cast<const uint2*>(row + i * kRow) + lane);
+                    raw[i].x = c.x;
+                    raw[i].y = c.y;
+                    m[i] = __ldg(reinterpret_cast<const float*>(field) + ((at_heads.h + i) * 2 + half) * a.BS);
+                } else {
+                    const __half* f = reinterpret_cast<const __half*>(field) + (at_heads.h + i) * 3 * a.BS;
+                    raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(row + i * kRow) + lane);
+                    m[i] = __half2float(__ldg(f + half * a.BS));
+                    z[i] = half ? __half2float(__ldg(f + 2 * a.BS)) : 0.f;
+                }
             }
-        } else if constexpr (KV == PDA_KV_FP8_E4M3) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-            const float scale = __ldg(reinterpret_cast<const float*>(meta) + ((long long)h * 2 + half) * a.BS + slot);
-            uint32_t p[4];
-            e4m3x4_to_f16x2x2(c.x, p[0], p[1]);
-            e4m3x4_to_f16x2x2(c.y, p[2], p[3]);
+        const long long o = ((long long)(first + at_heads.t) * a.Hk + at_heads.h) * kHeadDim + 8 * l;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-                x[2 * i] = f.x * scale;
-                x[2 * i + 1] = f.y * scale;
-            }
-        } else {
-            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(row) + lane);
-            const __half* f = reinterpret_cast<const __half*>(meta) + (long long)h * 3 * a.BS + slot;
-            const float m = __half2float(__ldg(f + half * a.BS));              // k_norm or v_scale
-            const float z = half ? __half2float(__ldg(f + 2 * a.BS)) : 0.f;
+        for (int i = 0; i < kHeadsAhead; ++i)
+            if (i < at_heads.n) {
+                float x[8];
+                if constexpr (KV == PDA_KV_BF16) {
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t code = c >> (4 * i) & 15u;
-                x[i] = half ? fmaf((float)code, m, z) : book[code] * m;        // code * v_scale is exact
+                    for (int k = 0; k < 4; ++k) {
+                        x[2 * k] = bf16_lo(w[k]);
+                        x[2 * k + 1] = bf16_hi(w[k]);
+                    }
+                } else if constexpr (KV == PDA_KV_FP8_E4M3) {
+                    uint32_t p[4];
+                    e4m3x4_to_f16x2x2(raw[i].x, p[0], p[1]);
+                    e4m3x4_to_f16x2x2(raw[i].y, p[2], p[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
+                        x[2 * k] = f.x * m[i];
+                        x[2 * k + 1] = f.y * m[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t code = raw[i].x >> (4 * k) & 15u;
+                        x[k] = half ? fmaf((float)code, m[i], z[i]) : book[code] * m[i];   // code * v_scale is exact
+                    }
+                }
+                if constexpr (F32) {
+                    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o + i * kHeadDim);
+                    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+                } else {
+                    uint4 w = raw[i];
+                    if constexpr (KV != PDA_KV_BF16)
+                        w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o + i * kHeadDim) = w;
+                }
             }
-        }
-        void* out = half ? a.v_out : a.k_out;
-        if (!out) continue;
-        const long long o = ((long long)(first + t) * a.Hk + h) * kHeadDim + 8 * l;
-        if constexpr (F32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-            p[0] = make_float4(x[0], x[1], x[2], x[3]);
-            p[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            if constexpr (KV != PDA_KV_BF16)
-                raw = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = raw;
-        }
     }
 }
 
@@ -434,8 +516,15 @@ static int token_args(const pda_plan_t* plan, const void* kv_cache, long long nu
     a.MB = plan->max_blocks_per_seq;
     a.BS = plan->kv_block_size;
     a.bs_shift = a.BS == 32 ? 5 : 4;
-    const long long even = num_tokens / (4 * 152);
-    a.per_cta = (int)(even < 1 ? 1 : even > kMaxTokensPerCta ? kMaxTokensPerCta : even);
+    // Few rows: one per warp, for the sake of the latency (35 tokens of 8 heads 4.2 -> 2.8 us).  Else four CTAs per SM where that
+    // is one wave, in whole rounds of a CTA's warps.
+    a.ahead = num_tokens * a.Hk <= 4 * 152 * kTokWarps ? 1 : kHeadsAhead;
+    a.groups = (a.Hk + a.ahead - 1) / a.ahead;
+    const long long even = (num_tokens + 4 * 152 - 1) / (4 * 152), most = a.groups > 4096 ? 1 : kMaxTokensPerCta;
+    const long long step = a.groups % 8 == 0 ? 1 : a.groups % 4 == 0 ? 2 : a.groups % 2 == 0 ? 4 : 8;   // tokens of whole rounds
+    const long long round = a.ahead == 1 ? even : (even + step - 1) / step * step;
+    a.per_cta = (int)(round > most ? most : round);
+    a.by_groups = a.per_cta == 1 ? 0 : ((1ull << 32) + a.groups - 1) / a.groups;
     grid = (unsigned)((num_tokens + a.per_cta - 1) / a.per_cta);
     return PDA_OK;
 }

@@ -397,3 +397,33 @@ def test_graphs_and_other_streams(pda):
         assert torch.equal(cache, got) and lens == out.tolist() == [13 - shift, 42 - shift]
         assert want is None or not torch.equal(got, want)
         want = got
+
+
+def test_every_quotient_of_e4m3(pda):
+    """Rows of scale 1, 3/7, 2^-40, .. and of every bf16 value up to their largest: next to every border of the codes, the smallest
+    ones and both zeros among them; rows with infinities, NaN and of the smallest values have the bytes of the single-token call."""
+    bits = np.arange(0x10000, dtype=np.uint32)
+    finite = bits[(bits & 0x7F80) != 0x7F80].astype(np.uint16)
+    rows_ = []
+    for top in (448.0, 192.0, 3.0, 1.0, 0.4921875, 2.0 ** -40, 2.0 ** -90, 2.0 ** -100, 2.0 ** -126, 2.0 ** 120):
+        big = wl.round_bf16(np.float32([top]))[0]
+        vals = finite[(finite & 0x7FFF) <= big]
+        near = vals[(vals & 0x7FFF) >= max(0, int(big) - 128 * 22)]       # the others' codes are 0
+        near = near[: len(near) // 127 * 127].reshape(-1, 127)
+        rows_.append(np.concatenate([np.full((len(near), 1), big, np.uint16), near], 1))
+    odd = np.zeros((4, 128), np.uint16)
+    odd[0, 3], odd[0, 5] = 0x7F80, 0x3F80          # +inf
+    odd[1, 3], odd[1, 5] = 0xFFC1, 0xBF80          # a negative NaN
+    odd[2, 7], odd[2, 9] = 0xFF80, 0x7FC0
+    odd[3, 1], odd[3, 2] = 0x0001, 0x8000          # the smallest value, and -0
+    x = np.concatenate(rows_ + [odd])
+    n = len(x)
+    c = setup(pda, FP8, 1, 16, [0], [n], seed=1)
+    c.bits = np.stack([x.reshape(n, 1, 128), x[::-1].reshape(n, 1, 128)])
+    one, many = (torch.from_numpy(c.cache).cuda() for _ in range(2))
+    assert write(pda, c, many) == 0
+    p = pda.plan(n, 1, 8, 16, c.MB, kv_dtype=FP8)
+    table = i32(np.repeat(c.table, n, 0))
+    pda.append_kv(p, bf16(c.bits[0]), bf16(c.bits[1]), one, c.NB, table, i32(np.arange(n)))
+    torch.cuda.synchronize()
+    assert torch.equal(one, many)
