@@ -65,10 +65,53 @@ __device__ __forceinline__ void store_joined(const DecodeArgs& a, long long row,
     }
 }
 
+// The sequence that stands at place `pos` when those of many tiles come first: by eighths of the most tiles that a window has,
+// and by index in some order that is every CTA's.  Called by all threads of a CTA; `counts` [warps][8].
+__device__ __forceinline__ int longest_first(const int* lens, int B, int max_ctx, int window, int num_first, int most, int pos,
+                                             int (*counts)[8]) {
+    const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float eighth = 7.999f / (float)most;
+    auto kind = [&](int b) {   // 0: the most tiles; 8: none there
+        if (b >= B) return 8;
+        return 7 - min(7, (int)((float)WindowTiles(sanitize_ctx(__ldg(lens + b), max_ctx), window, num_first).tiles * eighth));
+    };
+    int mine = 0;   // of kind `lane`
+    for (int b = 32 * warp; b < B; b += 32 * nw) {
+        const int k = kind(b + lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = __popc(__ballot_sync(kFull, k == i));
+            if (lane == i) mine += n;
+        }
+    }
+    if (lane < 8) counts[warp][lane] = mine;
+    __syncthreads();
+    int of_kind = 0;
+    if (lane < 8)
+        for (int w = 0; w < nw; ++w) of_kind += counts[w][lane];
+    int before = of_kind;   // of kinds 0 .. lane, then of those before
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, before, o);
+        if (lane >= o) before += x;
+    }
+    before -= of_kind;
+    const int k = 31 - __clz((int)__ballot_sync(kFull, lane < 8 && before <= pos));   // the last kind that starts no later
+    int r = pos - __shfl_sync(kFull, before, k), w = 0;
+    while (w + 1 < nw && r >= counts[w][k]) r -= counts[w++][k];
+    for (int b = 32 * w; b < B; b += 32 * nw) {
+        const unsigned all = __ballot_sync(kFull, kind(b + lane) == k);
+        const int n = __popc(all);
+        if (r < n) return b + (int)__fns(all, 0, r + 1);
+        r -= n;
+    }
+    return 0;   // not reached
+}
+
 template <int KV, int NT, int S, int NWMAX, int MINB, int LIST>
 __global__ void __launch_bounds__(32 * NWMAX, MINB)
     pda_selected_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap sc_map,
-                        const DecodeArgs a, const int C, const int behind, const int window, const int num_first) {
+                        const DecodeArgs a, const int C, const int behind, const int window, const int num_first, const int most) {
     constexpr bool OWN = LIST == kListOwn, WINDOW = LIST == kListWindow;
     using D = Decode<KV, NT, S, false>;
     using Cfg = DecodeCfg<KV, S>;
@@ -105,8 +148,15 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     };
 
     const int unit = blockIdx.x / C, rank = blockIdx.x - unit * C;
-    const int head = unit % a.sel_heads, list = OWN || WINDOW ? unit / a.sel_heads : unit;   // the table row and length
+    const int head = unit % a.sel_heads;
+    int list = OWN || WINDOW ? unit / a.sel_heads : unit;   // the table row and length
     const int max_ctx = a.MB * a.BS;
+    if constexpr (WINDOW) {
+        // more clusters than fit at once: the long ones start first, and the short ones fill the end
+        __shared__ int counts[NWMAX][8];
+        if (most > 0) list = longest_first(a.context_lens, a.B / a.sel_heads, max_ctx, window, num_first, most, list, counts);
+    }
+    const int rows_of = WINDOW ? list * a.sel_heads + head : unit;   // the query rows and the result's
     // What a warp needs first is asked for at once: the length, its part of the table as if the list were full (a
     // selected list mostly is, and the first warp's part does not depend on it), and the query rows.
     const int ts = a.bs_shift - 4, n = C * nw, wi = rank * nw + warp;
@@ -123,7 +173,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
     const int raw = load_input<OWN>(a.context_lens + list);
     uint32_t qn[NT][16];
     {
-        UnitIt u = {unit, 0, 0, 0, 0, 0};
+        UnitIt u = {rows_of, 0, 0, 0, 0, 0};
         D::template load_q<OWN>(a, u, qn, lane);
     }
     if ((raw < 0 || raw > max_ctx) && rank == 0 && threadIdx.x == 0 && (!(OWN || WINDOW) || head == 0) && a.err_word)
@@ -374,7 +424,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             o.w = fmaf(f, v.w, o.w);
         }
         if (C == 1) {
-            store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
+            store_joined<OWN>(a, (long long)rows_of * a.QG + q, c, o, M, L);
         } else {
             *reinterpret_cast<float4*>(joined + place(q, c)) = o;
             if (c == 0) {
@@ -403,7 +453,7 @@ __global__ void __launch_bounds__(32 * NWMAX, MINB)
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
-        store_joined<OWN>(a, (long long)unit * a.QG + q, c, o, M, L);
+        store_joined<OWN>(a, (long long)rows_of * a.QG + q, c, o, M, L);
     }
     cl.sync();   // nobody leaves while its rows are read
     leave();
