@@ -546,11 +546,12 @@ PDA_API int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long 
  *                 t < num_first.  p is context_lens[b] + the number of drafted tokens other than itself that it sees.  Masks
  *                 alone say which drafted tokens are seen; in a chain they count as cached ones.
  *   workspace     device, pda_tree_workspace_size bytes, 32-byte aligned
- *   out           [num_tokens][Hk*QG][128], as for pda_reduce; a row that sees nothing is 0
+ *   out           [num_tokens][Hk*QG][128], as for pda_reduce but 16-byte aligned in either type; a row that sees nothing is 0
  * K and V of the tokens that any of the sequence's rows sees must be finite: a row that does not see one of them still has it in
  * its products, with weight 0.  What no row sees (before the window, behind the drafted tokens) is not read, or not used,
  * whatever it holds; block ids of blocks wholly before the window are not looked at.
- * The roundings are those of the prefix in pda_decode_shared; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11
+ * The roundings are those of the prefix in pda_decode_shared; fp8: also the query's, the sum of two e4m3 parts, by at most 2^-17 of
+ * the row's largest |q|; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11
  * of its value, or 2^-24 of 1/256 of the step's largest 15 |v_scale| + |v_zero|), centroids to f16.
  * Data errors: a context length out of range (PDA_ERRW_BAD_CONTEXT_LEN) or drafted tokens that do not fit behind it
  * (PDA_ERRW_BAD_POSITION) give zeros for the sequence's rows; block ids as for pda_decode.

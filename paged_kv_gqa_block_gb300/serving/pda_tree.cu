@@ -175,7 +175,7 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
     if (!query || !kv_cache || !block_table || !context_lens || !token_starts || !workspace || !out) return PDA_ERR_INVALID_ARG;
     if (odd(query, 16) || odd(kv_cache, 16) || odd(centroids, 4) || odd(block_table, 4) || odd(context_lens, 4) ||
         odd(token_starts, 4) || odd(tree_masks, 8) || odd(workspace, 32) || odd(err_word, 4) ||
-        odd(out, out_dtype == PDA_OUT_F32 ? 16 : 8))
+        odd(out, 16))
         return PDA_ERR_INVALID_ARG;
     const TreeLayout w = tree_layout(plan, num_tokens);
     if (workspace_bytes < w.bytes) return PDA_ERR_WORKSPACE_TOO_SMALL;

@@ -82,7 +82,7 @@ def test_decode_tree(pda):
               ({13: need - 1}, SMALL), ({13: 0}, SMALL)]
     cases += [({0: at(0, 8)}, INVALID), ({2: at(1, 8)}, INVALID), ({5: at(2, 2)}, INVALID), ({6: at(3, 2)}, INVALID), ({7: at(4, 2)}, INVALID),
               ({8: at(5, 4)}, INVALID), ({12: at(6, 16)}, INVALID), ({14: at(8, 4)}, INVALID), ({14: at(8, 8), 15: 1}, INVALID),
-              ({16: at(9, 2)}, INVALID), ({1: 0}, OK)]
+              ({14: at(8, 8)}, INVALID), ({16: at(9, 2)}, INVALID), ({1: 0}, OK)]
     refused(L.pda_decode_tree, p, good, cases)
     all_plans(pda, L.pda_decode_tree, p, good)
     refused(L.pda_decode_tree, pda.plan(3, 2, 8, 16, 4, kv_dtype=pda.KV_TQ4), good, [({}, INVALID), ({4: at(9, 2)}, INVALID)])
