@@ -18,9 +18,9 @@
 // made of).  Warps take one role each:
 //   0-3, 4-7  softmax of tile 0, tile 1: one query row per thread, so a row's maximum and sum need
 //             no shuffles; S is read from TMEM, P written back
-//   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each)
+//   8         copies: K and V blocks by TMA into a ring of shared-memory slots (32 KB each); drafted tokens: K's (TQ4: both)
 //   9         the matrix products (one thread issues)
-//   10        fp8 and TQ4: the scales of a step
+//   10        fp8 and TQ4: the scales of a step; drafted tokens, bf16 and fp8: the copies of V, with the scales
 //   11        the split: which rows and which tokens this CTA takes
 //   12-15     fp8 and TQ4: codes to f16 between the copy and the product
 // The softmax warps hold a whole row of S (128 registers); the other warps give registers up for them.
@@ -29,6 +29,7 @@
 // row's maximum passes it by 2^8 (log2 units 8), so the rescale of O, the one read-modify-write of
 // TMEM, is rare; a reference below the true maximum leaves the quotient as it is.
 // P is announced in halves, so that PV starts while the second half is computed.
+// Drafted tokens have few rows as a rule, and many short units: see products_tree and halves.
 // P is rounded to bf16 (bf16 KV: by at most 2^-8 of each weight) or f16 (fp8 KV: 2^-11; V carries two more such
 // roundings, see the conversion); m, l, S and O are fp32.  f16 has few exponents: below 2^-14 a value loses bits, and
 // below 2^-25 it is zero, while l counts it; a long even prefix behind one large weight would lose a share of the
@@ -73,7 +74,10 @@ constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bi
 constexpr int kRawBytes = 16384;           // the same in 8 bits
 constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
 constexpr float kLazy = 8.f;               // log2 units that a row's maximum may rise before its reference follows
+constexpr int kHalvesSteps = 3;
 constexpr float kBelow = 7.f;              // f16 P: the reference below the maximum
+
+constexpr int kBarBytes = 720;             // barriers and scalars
 
 // What a KV format and a kind of call take of shared memory, barriers and threads.  Q8 (drafted tokens over fp8 KV): the score
 // product takes K's codes as they are, so that only V is converted, in halves of 64 tokens.
@@ -84,19 +88,21 @@ struct SharedCfg {
     static constexpr int kScaleBytes = kTq ? 1536 : 1024;        // 128 tokens x {K scale, V scale (, V zero)}
     static constexpr int kTiles = kTq ? 1 : 2;                   // copies of a step: a TQ4 row holds K and V
     static constexpr int kSlots = kF16 ? 3 : 5;
-    static constexpr int kRaw = 3, kScales = 3;                  // fp8, TQ4: raw slots, scale stages
+    static constexpr int kRaw = 3, kScales = kQ8 ? 4 : 3;                  // fp8, TQ4: raw slots, scale stages
     static constexpr int kThreads = kF16 ? 512 : 384;
     static constexpr int kOffQ = 0;                               // 2 tiles x 32 KB
-    static constexpr int kKeys = kQ8 ? 3 : 0, kHalves = 3;        // Q8: slots of K's codes, and of converted halves of V
+    static constexpr int kKeys = 3, kHalves = 3;                  // Q8: slots of K's codes, and of converted halves of V; bf16 trees:
+    static constexpr int kValues = kSlots - kKeys;                // the first three slots are K's, the others V's
     static constexpr int kOffKeys = 2 * kSlotBytes;
-    static constexpr int kOffSlots = kOffKeys + kKeys * kRawBytes;
+    static constexpr int kOffSlots = kOffKeys + (kQ8 ? kKeys * kRawBytes : 0);
     static constexpr int kOffRaw = kOffSlots + (kQ8 ? kHalves * kRawBytes : kSlots * kSlotBytes);
     static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
     static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
-    static constexpr int kOffTable = kOffBars + 512;              // TQ4: the centroids of a byte's two codes, f16
-    static constexpr int kSmem = kTq ? kOffTable + 1024 : kOffBars + (kQ8 ? 512 : 448);
+    static constexpr int kOffTable = kOffBars + kBarBytes;        // TQ4: the centroids of a byte's two codes, f16
+    static constexpr int kOffPair = kOffBars + kBarBytes + (kTq ? 1024 : 0);   // drafted tokens: (m, l) of rows' second halves
+    static constexpr int kSmem = kTree ? kOffPair + 1024 : kTq ? kOffTable + 1024 : kOffBars + 448;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
-    static constexpr int kReaders = kF16 ? 15 : 10;               // warps that take units
+    static constexpr int kReaders = kF16 ? 15 : kTree ? 11 : 10;  // warps that take units
 };
 // barriers and scalars after kOffBars
 enum {
@@ -113,13 +119,21 @@ enum {
     kBarDrain = 240,
     kTmemAt = 248,       // TMEM address
     kAbortAt = 252,      // a wait gave up
-    kFAt = 256,          // [3] what a step's V scales are divided by
+    kFAt = 256,          // [3] (Q8: 4) what a step's V scales are divided by
     kBarP2 = 272,        // [2] the second half of P is in TMEM
     kBarScRaw = 288,     // [3] scales as copied
     kBarUnitFull = 312,  // [2] the next unit is in shared memory
     kBarUnitEmpty = 328, // [2]
     kUnitAt = 352,       // [2] units, 48 bytes each
     kPowerAt = 448,      // TQ4: 1 over the power of two that the table's centroids carry
+    kBarHalf = 504,      // [2] drafted tokens: the product of the first half of P is done
+    kBarScFull8 = 520,   // [4] Q8: the scales' barriers and F, of four stages
+    kBarScEmpty8 = 552,
+    kBarScRaw8 = 584,
+    kBarWhole = 616,     // [2] that of the second half too
+    kBarPairFull = 648,  // [2][2] drafted tokens: a warp has handed its second halves over
+    kBarPairEmpty = 680, // [2][2] they have been taken
+    kBarS2 = 632,        // [2] drafted tokens: a tile's S is in the second place (kBarS: in the first)
     kBarVFull = 456,     // [3] Q8: a half of V is converted
     kBarVEmpty = 480     // [3] the products that read it are done
 };
@@ -136,6 +150,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // 16 bytes global -> shared, of which `bytes` (16 or 0) are read and the rest are zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// One arrival on `bar` when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds32v(uint32_t addr) {
@@ -175,6 +193,8 @@ template <int KV, class Args>
 struct Prefix {
     using Cfg = SharedCfg<KV, Args>;
     static constexpr bool F16 = Cfg::kF16, TQ = Cfg::kTq, TREE = Cfg::kTree, Q8 = Cfg::kQ8;
+    static constexpr uint32_t kScFull = Q8 ? kBarScFull8 : kBarScFull, kScEmpty = Q8 ? kBarScEmpty8 : kBarScEmpty,
+                              kScRaw = Q8 ? kBarScRaw8 : kBarScRaw;
     static constexpr uint32_t kIdescQ8 = umma_idesc_e4m3(128, 128);
     static constexpr uint32_t kIdescQK = umma_idesc(!F16, false, 128, 128), kIdescPV = umma_idesc(!F16, true, 128, 128);
 
@@ -268,6 +288,14 @@ struct Prefix {
     }
     // Whether token t of the sequence, below its length, is one that all rows miss.
     __device__ __forceinline__ static bool missed(const Sight& x, int t) { return TREE && t >= x.hole0 && t < x.hole1; }
+    // Row of the group that a tile starts with.  TREE: a row tile of at most 128 rows is either tile's.
+    __device__ __forceinline__ static int first_row(const Unit& u, int tile) {
+        return u.rt * kUnitRows + (!TREE || active(u, 1) ? tile * kTileRows : 0);
+    }
+    // TREE: of at most 64 rows every one is there twice, 64 rows apart: the first half of each step's tokens is one's, the second the
+    // other's, so that a step's softmax takes a warp half as long (fp8, steps of 36 rows: 1.7 -> 1.3 us with everything); the two
+    // are joined at the end, which costs more than it gives in units of one step or two.
+    __device__ __forceinline__ static bool halves(const Unit& u) { return TREE && u.rows - u.rt * kUnitRows <= 64 && u.steps >= kHalvesSteps; }
     __device__ __forceinline__ static bool active(const Unit& u, int tile) {
         return u.rt * kUnitRows + tile * kTileRows < u.rows;
     }
@@ -279,8 +307,7 @@ struct Prefix {
     // raw slots with the step's scales.
     __device__ void copies(const CUtensorMap* kv_map, const CUtensorMap* sc_map) {
         const int lane = threadIdx.x & 31;
-        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? Cfg::kRaw : Cfg::kSlots, kTiles = Cfg::kTiles;
-        constexpr uint32_t kField = TQ ? 6u : 8u;   // bytes of a token's scales
+        constexpr int kHalves = F16 ? 1 : 2, kNS = F16 ? Cfg::kRaw : Cfg::kSlots;
         constexpr uint32_t kFull0 = F16 ? kBarRawFull : kBarFull, kEmpty0 = F16 ? kBarRawEmpty : kBarEmpty;
         constexpr int kBytes = F16 ? kRawBytes : kSlotBytes;
         const uint32_t base = sm + (F16 ? Cfg::kOffRaw : Cfg::kOffSlots);
@@ -299,12 +326,8 @@ struct Prefix {
             int b0 = step_of(u, x, 0) * nblk;
             if (blk < nblk && b0 + blk < last) id = __ldcg(table + b0 + blk);
             for (int j = 0; ok && j < u.steps; ++j, ++step) {
-                int n = min(nblk, last - b0);
-                bool mine = blk < n;
-                if constexpr (TREE) {   // a block that all rows miss may be another's by now, or none: it is not looked at
-                    if ((b0 + blk) * a.BS >= x.hole0 && (b0 + blk + 1) * a.BS <= x.hole1) mine = false;
-                    n = __popc(__ballot_sync(kLanes, mine && half == 0));
-                }
+                const int n = min(nblk, last - b0);
+                const bool mine = blk < n;
                 int nid = 0, b1 = 0;
                 if (j + 1 < u.steps) {
                     b1 = step_of(u, x, j + 1) * nblk;
@@ -313,34 +336,31 @@ struct Prefix {
                 if (mine && half == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
                     atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
                 const unsigned st = step % Cfg::kScales;
-                if (F16 && step >= Cfg::kScales && !wait(bars + kBarScEmpty + 8 * st, (step / Cfg::kScales - 1) & 1)) {
+                if (F16 && step >= Cfg::kScales && !wait(bars + kScEmpty + 8 * st, (step / Cfg::kScales - 1) & 1)) {
                     ok = false;
                     break;
                 }
 #pragma unroll
-                for (int v = 0; v < kTiles; ++v, ++seq) {   // K, then V
-                    // Q8: a ring of its own for each
-                    const bool keys = Q8 && v == 0;
-                    const unsigned at = Q8 ? step : seq, ring = keys ? Cfg::kKeys : kNS;
-                    const unsigned s = at % ring;
-                    if (at >= ring && !wait(bars + (keys ? kBarEmpty : kEmpty0) + 8 * s, (at / ring - 1) & 1)) {
+                for (int v = 0; v < 2; ++v, ++seq) {   // K, then V
+                    const int s = seq % kNS;
+                    if (seq >= kNS && !wait(bars + kEmpty0 + 8 * s, (seq / kNS - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = bars + (keys ? kBarFull : kFull0) + 8 * s;
+                    const uint32_t bar = bars + kFull0 + 8 * s;
                     const uint32_t row_bytes = (uint32_t)n * a.BS * 128u * kHalves;
                     const bool scales = F16 && v == 0;
                     if (lane == 0) {
-                        if (scales) mbar_arrive_expect_tx(bars + kBarScRaw + 8 * st, (uint32_t)n * a.BS * kField);
+                        if (scales) mbar_arrive_expect_tx(bars + kScRaw + 8 * st, (uint32_t)n * a.BS * 8u);
                         mbar_arrive_expect_tx(bar, row_bytes);
                     }
                     __syncwarp();
                     if (mine) {
-                        tma_load_5d((keys ? sm + Cfg::kOffKeys : base) + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
+                        tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, bar, 0, 0,
                                     v * kHalves + half, u.h, id, policy);
                         if (scales)
                             tma_load_4d(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + blk * a.BS * 8, sc_map,
-                                        bars + kBarScRaw + 8 * st, 0, 0, u.h, id, policy);
+                                        bars + kScRaw + 8 * st, 0, 0, u.h, id, policy);
                     }
                     __syncwarp();
                 }
@@ -349,20 +369,109 @@ struct Prefix {
             }
         }
         // no copy may land in this CTA's memory after it leaves, whichever role gave up
-        const unsigned raws = Q8 ? seq / 2 : seq, keys = Q8 ? (seq + 1) / 2 : 0;   // slots filled of each ring
         for (int s = 0; s < kNS; ++s)
-            if (raws > (unsigned)s) {
-                const unsigned q = (raws - 1 - s) / kNS;   // the slot's last use
+            if (seq > (unsigned)s) {
+                const unsigned q = (seq - 1 - s) / kNS;   // the slot's last use
                 (void)mbar_wait(bars + kFull0 + 8 * s, q & 1, kDefaultTimeoutNs);
             }
-        if constexpr (Q8)
-            for (int s = 0; s < Cfg::kKeys; ++s)
-                if (keys > (unsigned)s) (void)mbar_wait(bars + kBarFull + 8 * s, (keys - 1 - s) / Cfg::kKeys & 1, kDefaultTimeoutNs);
         if (F16) {
-            const unsigned issued = (seq + kTiles - 1) / kTiles;   // steps whose scales were asked for
+            const unsigned issued = (seq + 1) / 2;   // steps whose scales were asked for
             for (int s = 0; s < Cfg::kScales; ++s)
                 if (issued > (unsigned)s)
-                    (void)mbar_wait(bars + kBarScRaw + 8 * s, (issued - 1 - s) / Cfg::kScales & 1, kDefaultTimeoutNs);
+                    (void)mbar_wait(bars + kScRaw + 8 * s, (issued - 1 - s) / Cfg::kScales & 1, kDefaultTimeoutNs);
+        }
+    }
+
+    // The same for drafted tokens, one warp for K (TQ4: for all) and one for V (Q8: with the scales, which are plain asynchronous
+    // copies of 16 bytes): a tensor copy takes its warp 26 ns (50
+    // cycles), and 32 of them, of 16 tokens and 64 dimensions each, more than the products of a step of few rows.
+    __device__ __forceinline__ void copies_tree(const CUtensorMap* kv_map, const CUtensorMap* sc_map, int v) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kHalves = F16 ? 1 : 2;
+        constexpr uint32_t kBytes = F16 ? kRawBytes : kSlotBytes, kField = TQ ? 6u : 8u;   // of a token's scales
+        // a ring for each; TQ4: one for both
+        const bool keys = Q8 && v == 0;
+        const uint32_t ring = !F16 ? (v ? Cfg::kValues : Cfg::kKeys) : keys ? Cfg::kKeys : Cfg::kRaw, at = !F16 && v ? Cfg::kKeys : 0;
+        const uint32_t full = bars + (F16 && !keys ? kBarRawFull : kBarFull) + 8 * at, empty = bars + (F16 && !keys ? kBarRawEmpty : kBarEmpty) + 8 * at;
+        const uint32_t base = sm + (keys ? Cfg::kOffKeys : F16 ? Cfg::kOffRaw : Cfg::kOffSlots) + at * kBytes;
+        const int nblk = kStep / a.BS, blk = lane / kHalves, half = lane % kHalves;
+        const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+        unsigned filled = 0, step = 0;   // copies of this warp, in slots; steps whose scales were asked for
+        uint32_t s = 0, ph = 1, st = 0, st_ph = 1;
+        bool ok = true;
+        Unit u;
+        while (ok && next(u)) {
+            const Sight x = sight(u);
+            const uint64_t policy = u.rows > kUnitRows ? again : once;   // other row tiles read it too
+            const int* table = a.prefix_table + (long long)u.g * a.MP;
+            const int last = (u.len + a.BS - 1) / a.BS;   // blocks of the sequence
+            int id = 0, b0 = step_of(u, x, 0) * nblk;
+            if (blk < nblk && b0 + blk < last) id = __ldcg(table + b0 + blk);
+            for (int j = 0; j < u.steps; ++j) {
+                // a block that all rows miss may be another's by now, or none: it is not looked at
+                const bool mine = blk < min(nblk, last - b0) && !((b0 + blk) * a.BS >= x.hole0 && (b0 + blk + 1) * a.BS <= x.hole1);
+                const int n = __popc(__ballot_sync(kLanes, mine && half == 0));
+                int nid = 0, b1 = 0;
+                if (j + 1 < u.steps) {
+                    b1 = step_of(u, x, j + 1) * nblk;
+                    if (blk < nblk && b1 + blk < last) nid = __ldcg(table + b1 + blk);
+                }
+                const bool scales = Q8 ? v == 1 : F16;
+                if (mine && half == 0 && v == 0 && (id < 0 || id >= a.num_cache_blocks) && a.err_word)
+                    atomicOr(a.err_word, PDA_ERRW_BAD_BLOCK_ID);
+                ok = (!scales || wait(bars + kScEmpty + 8 * st, st_ph)) && wait(empty + 8 * s, ph);   // both start free
+                if (!ok) break;
+                if (lane == 0) {
+                    if (!Q8 && scales) mbar_arrive_expect_tx(bars + kScRaw + 8 * st, (uint32_t)n * a.BS * kField);
+                    mbar_arrive_expect_tx(full + 8 * s, (uint32_t)n * a.BS * 128u * kHalves);
+                }
+                __syncwarp();
+                if (mine) {
+                    tma_load_5d(base + s * kBytes + half * 16384 + blk * a.BS * 128, kv_map, full + 8 * s, 0, 0, v * kHalves + half, u.h, id,
+                                policy);
+                    if (!Q8 && scales)
+                        tma_load_4d(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + blk * a.BS * 8, sc_map, bars + kScRaw + 8 * st, 0, 0, u.h,
+                                    id, policy);
+                }
+                __syncwarp();
+                if constexpr (Q8) if (scales) {
+                    const int mask = (int)__ballot_sync(kLanes, mine && id >= 0 && id < a.num_cache_blocks);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {   // 16 bytes c of the step's 1024; a block's are BS * 8
+                        const int c = lane + 32 * i, b = a.BS == 32 ? c >> 4 : c >> 3;
+                        const long long from = __shfl_sync(kLanes, id, b) * a.block_bytes + a.meta_bytes + (long long)u.h * a.BS * 8 + (c * 16 & (a.BS * 8 - 1));
+                        const bool there = mask >> b & 1;
+                        cp_async16(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + 16 * c, there ? a.cache + from : a.cache, there ? 16u : 0u);
+                    }
+                    cp_async_arrive(bars + kScRaw + 8 * st);
+                }
+                ++filled;
+                if (++s == ring) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (scales) {
+                    ++step;
+                    if (++st == Cfg::kScales) {
+                        st = 0;
+                        st_ph ^= 1;
+                    }
+                }
+                id = nid;
+                b0 = b1;
+            }
+        }
+        // no copy may land in this CTA's memory after it leaves, whichever role gave up: the last use of every slot
+        for (uint32_t i = 0; i < ring && i < filled; ++i) {
+            s = s > 0 ? s - 1 : ring - 1;
+            if (s + 1 == ring) ph ^= 1;
+            (void)mbar_wait(full + 8 * s, ph ^ 1, kDefaultTimeoutNs);
+        }
+        if constexpr (Q8) cp_async_wait_all();
+        for (uint32_t i = 0; !Q8 && i < Cfg::kScales && i < step; ++i) {
+            st = st > 0 ? st - 1 : Cfg::kScales - 1;
+            if (st + 1 == Cfg::kScales) st_ph ^= 1;
+            (void)mbar_wait(bars + kScRaw + 8 * st, st_ph ^ 1, kDefaultTimeoutNs);
         }
     }
 
@@ -382,7 +491,7 @@ struct Prefix {
             const Sight x = sight(u);
             for (int j = 0; j < u.steps; ++j) {
                 const int valid = tokens_of(u, x, j), t0 = step_of(u, x, j) * kStep;
-                if (!wait(bars + kBarScRaw + 8 * st, ph)) return;
+                if (!wait(bars + kScRaw + 8 * st, ph)) return;
                 const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
                 float ks[4], vs[4], vz[4], f = 0.f;
 #pragma unroll
@@ -416,7 +525,7 @@ struct Prefix {
                 if (lane == 0) sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
                 fence_proxy_async_shared();   // the next copy into this stage comes after these stores
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars + kBarScFull + 8 * st);
+                if (lane == 0) mbar_arrive(bars + kScFull + 8 * st);
                 if (++st == Cfg::kScales) {
                     st = 0;
                     ph ^= 1;
@@ -437,56 +546,82 @@ struct Prefix {
         else
             convert_fp8();
     }
-    // Q8: V alone, in halves of 64 tokens.  Thread t takes dimensions 64 (t / 64) .. of token t % 64 of the half: its codes
-    // times the token's scale over F, as in convert_fp8.
+    // Q8: V alone, in halves of 64 tokens, two warps each.  Thread t takes token t's 128 codes times the token's scale over F, as
+    // in convert_fp8.  One warp has its processor's quarter to itself for most of a step, so its time is its longest chain: one
+    // wait of each kind, all reads at once, no division but where F moves.
     __device__ __forceinline__ void convert_values() {
-        const int t = threadIdx.x - 384, lane = t & 31, r = t & 63, side = t >> 6, sw = r & 7;
-        const uint32_t raw0 = sm + Cfg::kOffRaw + r * 128, slot0 = sm + Cfg::kOffSlots + side * 8192 + r * 128;
-        const uint32_t scale0 = sm + Cfg::kOffScales + 512 + r * 4;
-        unsigned s = 0, ph = 0, st = 0, st_ph = 0, h = 0, h_ph = 0;
-        static_assert(!Q8 || Cfg::kRaw == Cfg::kScales, "a raw slot and its scales are counted together");
+        const int t = threadIdx.x - 384, lane = t & 31, sw = t & 7, second = t >> 6;
+        const uint32_t raw0 = sm + Cfg::kOffRaw + t * 128, slot0 = sm + Cfg::kOffSlots + (t & 63) * 128;
+        const uint32_t mine = scale_at(sm + Cfg::kOffScales, t, 1), four = scale_at(sm + Cfg::kOffScales, 4 * lane, 1);
+        unsigned s = 0, ph = 0, h = second, h_ph = 1;   // the slots start free
+        uint32_t st = 0, st_ph = 0;
+        float F = 1.f, rF = 1.f;
         Unit u;
         while (next(u)) {
             const Sight x = sight(u);
             for (int j = 0; j < u.steps; ++j) {
                 const int valid = tokens_of(u, x, j), t0 = step_of(u, x, j) * kStep;
+                const uint32_t sc = st * Cfg::kScaleBytes;
+                // F as in `scales`, by each of the warps for itself; the first tells the softmax
+                if (!wait(bars + kScRaw + 8 * st, st_ph)) return;
+                uint32_t v[4];
+                lds128(four + sc, v[0], v[1], v[2], v[3]);
+                float vs = __uint_as_float(lds32v(mine + sc));
+                bool zero = false;
+                if (valid < kStep || (t0 < x.hole1 && t0 + kStep > x.hole0)) {   // a token that is not there may have any scale and codes
+                    zero = t >= valid || missed(x, t0 + t);
+                    if (zero) vs = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * lane + i >= valid || missed(x, t0 + 4 * lane + i)) v[i] = 0u;
+                }
+                // magnitudes are ordered like their bits; a NaN counts for nothing
+                uint32_t y = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] &= 0x7FFFFFFFu;
+                    y = max(y, v[i] > 0x7F800000u ? 0u : v[i]);
+                }
+                y = __reduce_max_sync(kLanes, y);
+                const float top = y ? __uint_as_float(y) : 1.f;
+                if (j == 0 || top > F * 128.f || top < F * 2.f) {
+                    F = fmaxf(top * 0.0625f, 1e-37f);   // 1 / F is finite
+                    rF = 1.f / F;
+                }
+                if (t == 0) {
+                    sts32v(bars + kFAt + 4 * st, __float_as_uint(F));
+                    mbar_arrive(bars + kScFull + 8 * st);
+                }
+                __syncwarp();
+                vs *= rF;
+                const uint32_t vs2 = pack_f16(vs, vs);
                 if (!wait(bars + kBarRawFull + 8 * s, ph)) return;
-                if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int tok = 64 * half + r;
-                    const uint32_t src = raw0 + s * kRawBytes + half * 8192;
-                    uint32_t w[4][4];
+                const uint32_t src = raw0 + s * kRawBytes, dst = slot0 + h * kRawBytes;
+                if (!wait(bars + kBarVEmpty + 8 * h, h_ph)) return;
+#pragma unroll 2
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t w[4], o[8];
+                    lds128(src + ((c ^ sw) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) lds128(src + (((4 * side + c) ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
-                    const float vs = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes + half * 256));
-                    const uint32_t vs2 = pack_f16(vs, vs);
-                    if (!wait(bars + kBarVEmpty + 8 * h, h_ph ^ 1)) return;   // the slots start free
-                    if (tok >= valid || missed(x, t0 + tok)) {
+                    for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(zero ? 0u : w[i], o[2 * i], o[2 * i + 1]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
-                    }
-                    const uint32_t dst = slot0 + h * kRawBytes;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2x2(w[c][i], o[2 * i], o[2 * i + 1]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
-                        sts128(dst + (((2 * c) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-                        sts128(dst + (((2 * c + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
-                    }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bars + kBarVFull + 8 * h);
-                        if (half) mbar_arrive(bars + kBarRawEmpty + 8 * s);
-                    }
-                    if (++h == Cfg::kHalves) {
-                        h = 0;
-                        h_ph ^= 1;
-                    }
+                    for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], vs2);
+                    const uint32_t d = dst + (c >> 2) * 8192;
+                    const int k = 2 * (c & 3);
+                    sts128(d + ((k ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                    sts128(d + (((k + 1) ^ sw) << 4), o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bars + kBarVFull + 8 * h);
+                    mbar_arrive(bars + kBarRawEmpty + 8 * s);
+                    mbar_arrive(bars + kScEmpty + 8 * st);
+                }
+                h += 2;
+                if (h >= Cfg::kHalves) {
+                    h -= Cfg::kHalves;
+                    h_ph ^= 1;
                 }
                 if (++s == Cfg::kRaw) {
                     s = 0;
@@ -519,7 +654,7 @@ struct Prefix {
                     for (int c = 0; c < 8; ++c) lds128(src + ((c ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
                     float vs = 1.f;
                     if (v) {
-                        if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                        if (!wait(bars + kScFull + 8 * st, st_ph)) return;
                         vs = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes));
                         if (++st == Cfg::kScales) {
                             st = 0;
@@ -572,22 +707,21 @@ struct Prefix {
             for (int j = 0; j < u.steps; ++j) {
                 const bool zero = t >= tokens_of(u, x, j) || missed(x, step_of(u, x, j) * kStep + t);
                 if (!wait(bars + kBarRawFull + 8 * rs, rph)) return;
-                uint32_t w[8][4];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) lds128(raw0 + rs * kRawBytes + ((c ^ sw) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
-                if (zero) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
-                }
+                const uint32_t src = raw0 + rs * kRawBytes;
                 if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;   // the slots start free
                 uint32_t dst = slot0 + s * kSlotBytes;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {   // 32 dimensions, in 16 bytes of codes
+                    uint32_t w[4];
+                    lds128(src + ((q ^ sw) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {   // 16 bytes of f16 from 4 of codes
-                    const uint32_t code = w[c >> 2][c & 3];
-                    uint32_t o[4];
+                    for (int c = 0; c < 4; ++c) {   // 16 bytes of f16 from 4 of codes
+                        const uint32_t code = zero ? 0u : w[c];
+                        uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = lds32v(table + ((code >> (8 * i)) & 0xFFu) * 4);
-                    sts128(dst + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                        for (int i = 0; i < 4; ++i) o[i] = lds32v(table + ((code >> (8 * i)) & 0xFFu) * 4);
+                        sts128(dst + (q >> 1) * 16384 + (((4 * (q & 1) + c) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                    }
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -596,7 +730,7 @@ struct Prefix {
                     s = 0;
                     ph ^= 1;
                 }
-                if (!wait(bars + kBarScFull + 8 * st, st_ph)) return;
+                if (!wait(bars + kScFull + 8 * st, st_ph)) return;
                 // 1 + code / 16 costs one instruction: V = (1 + code / 16) 16 v_scale + (v_zero - 16 v_scale).  A token that is
                 // not there has both 0.
                 const float vs = 16.f * __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes));
@@ -607,17 +741,22 @@ struct Prefix {
                 }
                 if (!wait(bars + kBarEmpty + 8 * s, ph ^ 1)) return;
                 dst = slot0 + s * kSlotBytes;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
+                    lds128(src + (((4 + q) ^ sw) << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint32_t code = w[4 + (c >> 2)][c & 3];
-                    uint32_t o[4];
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t code = zero ? 0u : w[c];
+                        uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float lo = __uint_as_float(((code >> (8 * i)) & 0xFu) << 19 | 0x3F800000u);
-                        const float hi = __uint_as_float(((code >> (8 * i + 4)) & 0xFu) << 19 | 0x3F800000u);
-                        o[i] = pack_f16(fmaf(lo, vs, vz), fmaf(hi, vs, vz));
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = __uint_as_float(((code >> (8 * i)) & 0xFu) << 19 | 0x3F800000u);
+                            const float hi = __uint_as_float(((code >> (8 * i + 4)) & 0xFu) << 19 | 0x3F800000u);
+                            o[i] = pack_f16(fmaf(lo, vs, vz), fmaf(hi, vs, vz));
+                        }
+                        sts128(dst + (q >> 1) * 16384 + (((4 * (q & 1) + c) ^ sw) << 4), o[0], o[1], o[2], o[3]);
                     }
-                    sts128(dst + (c >> 3) * 16384 + (((c & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -683,8 +822,8 @@ struct Prefix {
             umma_ts(leader, d, p + i * 8, v + ((i * 2048) >> 4), kIdescPV, accumulate || i > 0);
     }
     __device__ void products(uint32_t tmem_base) {
-        if constexpr (Q8)
-            products_q8(tmem_base);
+        if constexpr (TREE)
+            products_tree(tmem_base);
         else
             products_f16(tmem_base);
     }
@@ -694,80 +833,185 @@ struct Prefix {
         __syncwarp();
         (void)mbar_wait(bars + kBarDrain, 0, kDefaultTimeoutNs);
     }
-    // Q8.  S = Qhi K^T + Qlo K^T, e4m3 each; the halves of V by their own barriers.
-    __device__ __forceinline__ void products_q8(uint32_t tmem_base) {
+    // Drafted tokens.  The units of two tiles as in the prefix pass.  Those of one, at most 128 rows, go to the tiles by turns, so that
+    // one tile's first rows are fetched and its last ones stored beside the other's steps, and their steps use the two places for
+    // S by turns: S of step g + 2 is computed where S and P of step g were as soon as the product of that P is issued, so that the
+    // softmax of a step finds its S there already.
+    // Q8: S = Qhi K^T + Qlo K^T, e4m3 each, and V comes in halves.
+    // Measured, sequences with 4 drafted tokens of 8 heads and 8 query rows each: 64 of 4096 bf16 tokens 194 -> 176 us (6.1 TB/s), of
+    // 1000 66 -> 59; 64 of 4096 fp8 tokens 217 -> 202, and with the halves (see there) 171.
+    __device__ __forceinline__ void products_tree(uint32_t tmem_base) {
+        const int lane = threadIdx.x & 31;
         const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm), bar = uniform(bars);
-        const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024), k0 = umma_desc(smu + Cfg::kOffKeys, 16, 1024);
-        const uint64_t v0 = umma_desc(smu + Cfg::kOffSlots, 8192, 1024);
-        constexpr uint32_t kRaw16 = kRawBytes >> 4;
-        
-        uint32_t ks = 0, kph = 0, hs = 0, hph = 0;   // the next slot of K, and of V's halves
-        uint32_t unit0 = 0, unit1 = 0, p0 = 0, p1 = 0;
-        auto scores = [&](int w) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {   // 32 dimensions at a time, first of the high parts, then of the low ones
-                const uint32_t o = (i & 3) * 32 >> 4;
-                umma_ss_f8(leader, tmem + w * 128, q0 + w * kSlot16 + (i >> 2) * kRaw16 + o, k0 + ks * kRaw16 + o, kIdescQ8, i > 0);
+        constexpr uint32_t kRaw16 = kRawBytes >> 4, kKey16 = Q8 ? kRaw16 : kSlot16;
+        // TQ4: K and V in turn in one ring
+        constexpr uint32_t kVAt = TQ || Q8 ? 0 : Cfg::kKeys, kStride = TQ ? 2 : 1, kKRing = TQ ? Cfg::kSlots : Cfg::kKeys;
+        constexpr uint32_t kVFull = Q8 ? kBarVFull : kBarFull + 8 * kVAt, kVEmpty = Q8 ? kBarVEmpty : kBarEmpty + 8 * kVAt;
+        constexpr uint32_t kVRing = Q8 ? Cfg::kHalves : TQ ? Cfg::kSlots : Cfg::kValues;
+        const uint64_t q0 = umma_desc(smu + Cfg::kOffQ, 16, 1024), k0 = umma_desc(smu + (Q8 ? Cfg::kOffKeys : Cfg::kOffSlots), 16, 1024);
+        const uint64_t v0 = umma_desc(smu + Cfg::kOffSlots + kVAt * kSlotBytes, Q8 ? 8192 : 16384, 1024);
+        uint32_t ks = 0, kph = 0, vs = TQ ? 1 : 0, vph = 0;   // the next slot of K, and of V
+        uint32_t q_ph = 0, p_ph = 0;                          // a bit per tile, and per place
+        uint32_t place = 0;                                   // of the next step of a unit of one tile
+        auto move = [](uint32_t& slot, uint32_t& ph, uint32_t stride, uint32_t ring) {
+            slot += stride;
+            if (slot >= ring) {
+                slot -= ring;
+                ph ^= 1;
             }
         };
-        auto values = [&](int w, int half, uint32_t slot, bool accumulate) {
+        auto scores = [&](uint32_t tile, uint32_t to) {
+            const uint64_t q = q0 + tile * kSlot16, k = k0 + ks * kKey16;
+            if constexpr (Q8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                umma_ts(leader, tmem + 256 + w * 128, tmem + w * 128 + (4 * half + i) * 8, v0 + slot * kRaw16 + ((i * 2048) >> 4),
-                        kIdescPV, accumulate || i > 0);
+                for (int i = 0; i < 8; ++i) {   // 32 dimensions at a time, first of the high parts, then of the low ones
+                    const uint32_t o = (i & 3) * 32 >> 4;
+                    umma_ss_f8(leader, tmem + to * 128, q + (i >> 2) * kRaw16 + o, k + o, kIdescQ8, i > 0);
+                }
+            } else {
+                qk(leader, tmem + to * 128, q, k);
+            }
+            umma_commit(leader, bar + (to ? kBarS2 : kBarS) + 8 * tile);
         };
+        auto release_keys = [&] {
+            umma_commit(leader, bar + kBarEmpty + 8 * ks);
+            move(ks, kph, kStride, kKRing);
+        };
+        // bf16 rows that nobody sees may hold anything: a weight of zero does not silence a NaN
+        auto clear = [&](int valid, int h0, int h1) -> bool {
+            if (!wait(bar + kVFull + 8 * vs, vph)) return false;
+            const uint32_t s = sm + Cfg::kOffSlots + (kVAt + vs) * kSlotBytes;
+            for (int i = lane; i < kStep * 8; i += 32)
+                if (const int r = i >> 3; r >= valid || (r >= h0 && r < h1)) {
+                    sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                    sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
+                }
+            fence_proxy_async_shared();
+            __syncwarp();
+            return true;
+        };
+        // O += P V of a step for one tile, in halves; opens, closes: the step's first and last tile.
+        auto values = [&](uint32_t tile, uint32_t from, bool accumulate, bool opens, bool closes) -> bool {
+            uint32_t v1 = vs, v1ph = vph;   // of the second half
+            if constexpr (Q8) move(v1, v1ph, 1, kVRing);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t slot = half ? v1 : vs;
+                if (opens && (Q8 || half == 0) && !wait(bar + kVFull + 8 * slot, half ? v1ph : vph)) return false;
+                if (!wait(bar + (half ? kBarP2 : kBarP) + 8 * from, p_ph >> from & 1)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_ts(leader, tmem + 256 + tile * 128, tmem + from * 128 + (4 * half + k) * 8,
+                            v0 + slot * kKey16 + (((Q8 ? k : 4 * half + k) * 2048) >> 4), kIdescPV, accumulate || half > 0 || k > 0);
+                umma_commit(leader, bar + (half ? kBarWhole : kBarHalf) + 8 * tile);
+                if (closes && (Q8 || half == 1)) umma_commit(leader, bar + kVEmpty + 8 * slot);
+            }
+            p_ph ^= 1u << from;
+            return true;
+        };
+        auto next_values = [&] {
+            move(vs, vph, kStride, kVRing);
+            if constexpr (Q8) move(vs, vph, 1, kVRing);
+        };
+        auto two_tiles = [&](const Unit& u, const Sight& x) -> bool {
+            const int steps = uniform(u.steps);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (!wait(bar + kBarQ + 8 * w, q_ph >> w & 1)) return false;
+                if (w == 0 && !wait(bar + kBarFull + 8 * ks, kph)) return false;
+                tc_fence_after();
+                scores(w, w);
+            }
+            q_ph ^= 3;
+            release_keys();
+            for (int j = 0; j < steps; ++j) {
+                const bool more = j + 1 < steps;
+                if constexpr (!F16) {
+                    const int t0 = uniform(step_of(u, x, j) * kStep), valid = min(kStep, u.len - t0);
+                    const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
+                    if ((valid < kStep || h0 < h1) && !clear(valid, h0, h1)) return false;
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!values(w, w, j > 0, w == 0, w == 1)) return false;
+                    if (more) {
+                        if (w == 0 && !wait(bar + kBarFull + 8 * ks, kph)) return false;
+                        scores(w, w);
+                    } else {
+                        umma_commit(leader, bar + kBarO + 8 * w);
+                    }
+                }
+                if (more) release_keys();
+                next_values();
+            }
+            return true;
+        };
+        // A step of a unit of one tile: its tile and place, and whether it is the unit's first or last.
+        enum : uint32_t { kPlace = 2, kFirst = 4, kLast = 8, kClear = 16 };
+        Unit u;
+        Sight x = {};
+        int j = 0, out = 0;
+        u.steps = 0;
+        bool more = true;
+        uint32_t first = 0, second = 0;   // steps whose product with V is to come
         auto all = [&] {
-            Unit u;
-            while (uniform((int)next(u))) {
-                const int tiles = uniform(active(u, 1) ? 2 : 1), steps = uniform(u.steps);
-                if (!wait(bar + kBarFull + 8 * ks, kph)) return;
-                for (int w = 0; w < tiles; ++w) {
-                    uint32_t& n = w ? unit1 : unit0;
-                    if (!wait(bar + kBarQ + 8 * w, n)) return;
-                    n ^= 1;
-                    tc_fence_after();
-                    scores(w);
-                    umma_commit(leader, bar + kBarS + 8 * w);
+            for (;;) {
+                if (more && j == u.steps) {
+                    more = uniform((int)next(u));
+                    x = sight(u);
+                    j = 0;
                 }
-                for (int j = 0; j < steps; ++j) {
-                    const bool more = j + 1 < steps;
-                    umma_commit(leader, bar + kBarEmpty + 8 * ks);   // of the scores issued last
-                    if (++ks == Cfg::kKeys) {
-                        ks = 0;
-                        kph ^= 1;
-                    }
-                    const uint32_t h0 = hs, ph0 = hph;
-                    if (++hs == Cfg::kHalves) {
-                        hs = 0;
-                        hph ^= 1;
-                    }
-                    const uint32_t h1 = hs, ph1 = hph;
-                    if (++hs == Cfg::kHalves) {
-                        hs = 0;
-                        hph ^= 1;
-                    }
-    #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (w >= tiles) break;
-                        uint32_t& n = w ? p1 : p0;
-                        if (w == 0 && !wait(bar + kBarVFull + 8 * h0, ph0)) return;
-                        if (!wait(bar + kBarP + 8 * w, n)) return;
-                        tc_fence_after();
-                        values(w, 0, h0, j > 0);
-                        if (w + 1 == tiles) umma_commit(leader, bar + kBarVEmpty + 8 * h0);
-                        if (w == 0 && !wait(bar + kBarVFull + 8 * h1, ph1)) return;
-                        if (!wait(bar + kBarP2 + 8 * w, n)) return;
-                        n ^= 1;
-                        tc_fence_after();
-                        values(w, 1, h1, true);
-                        if (w + 1 == tiles) umma_commit(leader, bar + kBarVEmpty + 8 * h1);
-                        if (more) {
-                            if (w == 0 && !wait(bar + kBarFull + 8 * ks, kph)) return;
-                            scores(w);
+                if (uniform((int)(more && out < 2))) {
+                    if (uniform((int)active(u, 1))) {
+                        if (out == 0) {
+                            if (!two_tiles(u, x)) return;
+                            j = u.steps;
+                            place = 0;
+                            continue;
                         }
-                        umma_commit(leader, bar + (more ? kBarS : kBarO) + 8 * w);
+                    } else {
+                        // The first S of a unit waits for the tile's rows; not while a product is to come: they may come only after it.
+                        const uint32_t tile = uniform(units & 1);
+                        bool ok = true;
+                        if (j == 0) {
+                            if (out) {
+                                ok = __all_sync(kLanes, mbar_test_wait(bar + kBarQ + 8 * tile, q_ph >> tile & 1));
+                            } else if (!wait(bar + kBarQ + 8 * tile, q_ph >> tile & 1)) {
+                                return;
+                            }
+                        }
+                        if (uniform((int)ok)) {
+                            if (j == 0) q_ph ^= 1u << tile;
+                            if (!wait(bar + kBarFull + 8 * ks, kph)) return;
+                            tc_fence_after();
+                            scores(tile, place);
+                            release_keys();
+                            uint32_t turn = tile | place << 1 | (j == 0 ? kFirst : 0);
+                            if (++j == u.steps) turn |= kLast;
+                            if constexpr (!F16) {
+                                const int t0 = uniform(step_of(u, x, j - 1) * kStep), valid = min(kStep, u.len - t0);
+                                const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
+                                if (valid < kStep || h0 < h1) turn |= kClear | valid << 8 | h0 << 16 | h1 << 24;
+                            }
+                            if (out == 0)
+                                first = turn;
+                            else
+                                second = turn;
+                            place ^= 1;
+                            ++out;
+                            continue;
+                        }
                     }
                 }
+                if (out == 0) return;
+                const uint32_t turn = uniform(first), tile = turn & 1;
+                if (!F16 && (turn & kClear) && !clear(turn >> 8 & 255, turn >> 16 & 255, turn >> 24)) return;
+                if (!values(tile, turn >> 1 & 1, !(turn & kFirst), true, true)) return;
+                next_values();
+                if (turn & kLast) umma_commit(leader, bar + kBarO + 8 * tile);
+                first = second;
+                --out;
             }
         };
         all();
@@ -797,7 +1041,7 @@ struct Prefix {
             const Sight x = sight(u);
             // the step that holds the prefix's last, partly filled tile (-1: none)
             int ragged = -1;
-            if (!F16 && !TREE && u.len % kStep) {
+            if (!F16 && u.len % kStep) {
                 const int i = u.len / kStep - u.step0 - u.rot;
                 if (u.len / kStep < u.step0 + u.steps) ragged = i < 0 ? i + u.steps : i;
             }
@@ -821,21 +1065,7 @@ struct Prefix {
             for (int j = 0; j < steps; ++j) {
                 const bool more = j + 1 < steps;
                 const Pos v = pos.next(), k = v.next();   // V(j), K(j + 1)
-                if constexpr (TREE && !F16) {   // the same for the first tokens' end and the window's start
-                    const int t0 = uniform(step_of(u, x, j) * kStep), valid = min(kStep, u.len - t0);
-                    const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
-                    if (valid < kStep || h0 < h1) {
-                        const uint32_t s = sm + Cfg::kOffSlots + v.slot * kSlotBytes;
-                        for (int i = lane; i < kStep * 8; i += 32)
-                            if (const int r = i >> 3; r >= valid || (r >= h0 && r < h1)) {
-                                sts128(s + i * 16, 0u, 0u, 0u, 0u);
-                                sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
-                            }
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                    }
-                }
-                if (!TREE && j == ragged) {
+                if (j == ragged) {
                     // bf16 rows past the prefix may hold anything: a weight of zero does not silence a NaN
                     const int valid = u.len % kStep;
                     const uint32_t s = sm + Cfg::kOffSlots + v.slot * kSlotBytes;
@@ -891,7 +1121,7 @@ struct Prefix {
             // 16 bytes w of a row; Q8: neighbours 16 KB apart, where the parts of their 16 dimensions will lie
             const uint32_t dst = base + (Q8 ? w & 1 : w >> 3) * 16384;
             const int place = Q8 ? w >> 1 : w & 7;
-            const int row0 = u.rt * kUnitRows + tile * kTileRows + r0 + half;
+            const int row0 = first_row(u, tile) + (halves(u) ? r0 & 63 : r0) + half;
             int seq = row0 / a.QG, q = row0 - seq * a.QG;
             const uint16_t* src = a.query + ((long long)(u.seq0 + seq) * a.Hk + u.h) * a.QG * kHeadDim + 8 * w;
             const long long skip = (long long)a.Hk * a.QG * kHeadDim;
@@ -921,7 +1151,7 @@ struct Prefix {
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
                 uint32_t v[4];
-                lds128(row + (i >> 3) * 16384 + ((i & 7) << 4), v[0], v[1], v[2], v[3]);   // in any order
+                lds128(row + (i >> 3) * 16384 + (((i & 7) ^ x) << 4), v[0], v[1], v[2], v[3]);   // in any order
                 mx = __vmaxs2(mx, __vmaxs2(__vmaxs2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu),
                                            __vmaxs2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu)));
             }
@@ -987,8 +1217,8 @@ struct Prefix {
     };
     __device__ __forceinline__ Rows start_unit(const Unit& u, int tile, int r) const {
         Rows w;
-        w.on = active(u, tile);
-        const int row = u.rt * kUnitRows + tile * kTileRows + r;
+        w.on = TREE || active(u, tile);
+        const int row = first_row(u, tile) + (halves(u) ? r & 63 : r);
         w.live = row < u.rows;
         w.head = (long long)(u.seq0 + row / a.QG) * a.Hk + u.h;
         w.q = row % a.QG;
@@ -1019,7 +1249,7 @@ struct Prefix {
             }
         }
         if (w.on) {   // every product with the last unit's rows has ended: their S was read
-            w.c = load_q(u, tile);
+            if (!TREE || first_row(u, tile) + (r & (halves(u) ? 32 : 96)) < u.rows) w.c = load_q(u, tile);   // rows of nobody: whatever is there
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarQ + 8 * tile);
         }
@@ -1062,7 +1292,7 @@ struct Prefix {
             for (int j = 0; j < u.steps; ++j, ++step) {
                 const int valid = tokens_of(u, x, j);
                 const unsigned st = step % Cfg::kScales;
-                if (F16 && !wait(bars + kBarScFull + 8 * st, step / Cfg::kScales & 1)) return;
+                if (F16 && !wait(bars + kScFull + 8 * st, step / Cfg::kScales & 1)) return;
                 if (w.on) {
                     if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
                     tc_fence_after();
@@ -1149,7 +1379,7 @@ struct Prefix {
                 }
                 if (F16) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + kBarScEmpty + 8 * st);
+                    if (lane == 0) mbar_arrive(bars + kScEmpty + 8 * st);
                 }
             }
             if (!w.on) continue;
@@ -1160,44 +1390,58 @@ struct Prefix {
         }
     }
 
-    // The same for drafted tokens, whose rows do not see every token.  In few instructions: S is read twice, 64 columns at a time
-    // in rolled loops, once for the maximum and once for the weights, in place of a whole row in registers and straight
-    // code.  The code of all roles of an SM has to fit its instruction cache: with the straight code 21 % of the fp8 kernel's
+    // The same for drafted tokens, whose rows do not see every token.  In few instructions: 64 tokens at a time in a rolled loop,
+    // in place of a whole row in registers and straight code.  The reference may move before the second half too, whose weights
+    // then wait for the first half's product, since O counts from it.  The code of all roles of an SM has to fit its instruction cache: with the straight code 21 % of the fp8 kernel's
     // requests missed it, and a step of few rows took 2.0 us, half of it without an instruction.
     __device__ __forceinline__ void softmax_tree(uint32_t tmem_base, int tile) {
         const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
         const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-        const uint32_t tS = tmem_base + tile * 128 + lanes, tO = tmem_base + 256 + tile * 128 + lanes;
+        const uint32_t tO = tmem_base + 256 + tile * 128 + lanes;
         constexpr float below = F16 ? kBelow : 0.f;
-        unsigned ns = 0, no = 0, step = 0;
+        unsigned own = 0, no = 0, np = 0, step = 0, turn = 0;   // this tile's steps, those of units of one tile, its units; steps and turns of both
+        uint32_t s_ph = 0;                              // a bit per place
         Unit u;
         while (next(u)) {
-            const Rows w = start_unit(u, tile, r);
-            // The other tile's warps release the scales for a tile without rows: units of few rows are the rule here.
-            if (!w.on) {
+            const bool both = active(u, 1);
+            if (!both && (units & 1) != tile) {   // the other tile's
                 step += u.steps;
+                turn += u.steps;
                 continue;
             }
-            const int releases = active(u, 1) ? 1 : 2;
-            const bool idle = u.rt * kUnitRows + tile * kTileRows + (r & ~31) >= u.rows;   // no row of the warp's
+            const Rows w = start_unit(u, tile, r);
+            const int releases = both ? 1 : 2;
+            const bool part = halves(u), idle = first_row(u, tile) + (r & (part ? 32 : 96)) >= u.rows;   // no row of the warp's
+            const int k0 = part ? r >> 6 : 0, k1 = part ? k0 + 1 : 2;
             const Sight x = sight(u);
             float m = 0.f, l = 0.f, F = 1.f;   // m: the reference, which l and O count from
-            for (int j = 0; j < u.steps; ++j, ++step) {
-                const unsigned st = step % Cfg::kScales;
-                const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
+            if (both) turn = tile;
+            for (int j = 0; j < u.steps; ++j, ++own) {
+                const unsigned st = step % Cfg::kScales, place = turn & 1;
+                const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes, tS = tmem_base + place * 128 + lanes;
                 const int t0 = step_of(u, x, j) * kStep;
-                if (F16 && !wait(bars + kBarScFull + 8 * st, step / Cfg::kScales & 1)) return;
-                if (!wait(bars + kBarS + 8 * tile, ns++ & 1)) return;
+                // a unit's first comes when all before it are through
+                const uint32_t bar = bars + (place ? kBarS2 : kBarS) + 8 * tile, ph = s_ph >> place & 1;
+                if (!(j == 0 ? wait_unit(bar, ph) : wait(bar, ph))) return;
+                s_ph ^= 1u << place;
+                // only now: the other tile may have had the steps between, and S says that they are through
+                if (F16 && !wait(bars + kScFull + 8 * st, step / Cfg::kScales & 1)) return;
+                ++step;
+                turn += both ? 2 : 1;
                 tc_fence_after();
                 if (!idle) {
                     // only the steps with drafted tokens and those where some row's window starts are looked at bit by bit
                     const bool hidden = t0 + kStep > x.ctx || (a.window > 0 && t0 < u.len - a.window && t0 + kStep > a.num_first);
-                    if (hidden) hide(u, w, x, t0, tS, sc);
-                    uint32_t s[2][32];
-                    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (hidden) hide(u, w, x, t0, tS, sc, 4 * k0, 4 * k1);
+                    float nF = 1.f;
+                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
+                    float f = nF == F ? 1.f : F / nF;   // what O is to be multiplied by
+                    F = nF;
 #pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        read_scores(s, tS + 64 * k, sc + 256 * k, hidden);
+                    for (int k = k0; k < k1; ++k) {   // 64 tokens
+                        uint32_t s[2][32];
+                        read_scores(s, tS, 64 * k, sc, hidden);
+                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
 #pragma unroll
@@ -1205,31 +1449,28 @@ struct Prefix {
                                 t[c] = fmaxf(t[c], fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
                                 t[c + 2] = fmaxf(t[c + 2], fmaxf(__uint_as_float(s[c][i + 2]), __uint_as_float(s[c][i + 3])));
                             }
-                    }
-                    const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * w.c, -1e30f);
-                    float nF = 1.f;
-                    if constexpr (F16) nF = __uint_as_float(lds32v(bars + kFAt + 4 * st));
-                    if (j == 0) {
-                        m = top - below;
-                    } else {
+                        const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * w.c, -1e30f);
+                        if (j == 0 && k == k0) {
+                            m = top - below;
+                            f = 1.f;
+                        }
                         const bool up = top > m + (kLazy + below);
-                        if (__any_sync(kLanes, up || nF != F)) {
-                            float f = F / nF;
-                            if (nF == F) f = 1.f;
+                        if (__any_sync(kLanes, up || f != 1.f)) {
                             if (up) {
                                 const float e = ex2(m - (top - below));
                                 m = top - below;
                                 l *= e;
                                 f *= e;
                             }
-                            rescale(tO, f);
+                            if (j > 0 || k > k0) {   // the last step's product may be under way, and that of this one's first half
+                                if (j > 0 && !wait(bars + kBarWhole + 8 * tile, own - 1 & 1)) return;
+                                if (k > k0 && !wait(bars + kBarHalf + 8 * tile, own & 1)) return;
+                                tc_fence_after();
+                                rescale(tO, f);
+                            }
+                            f = 1.f;
                         }
-                    }
-                    F = nF;
-                    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        read_scores(s, tS + 64 * k, sc + 256 * k, hidden);
+                        float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t p[16];
@@ -1247,57 +1488,130 @@ struct Prefix {
                                 p[i / 2] = F16 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
                                 p[i / 2 + 1] = F16 ? pack_f16(z.x, z.y) : pack_bf16(z.x, z.y);
                             }
-                            tmem_st16(tS + 32 * k + 16 * c, p);   // over S that has been read
+                            tmem_st16(tS + 32 * k + 16 * c, p);   // over S of the first 64 tokens, which has been read
+                        }
+                        if (part) {   // no weights for the other half
+                            uint32_t p[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) p[i] = 0u;
+                            tmem_st16(tS + 32 * (1 - k), p);
+                            tmem_st16(tS + 32 * (1 - k) + 16, p);
                         }
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bars + (k ? kBarP2 : kBarP) + 8 * tile);
+                        if (lane == 0) {
+                            if (part || k == 0) mbar_arrive(bars + kBarP + 8 * place);
+                            if (part || k == 1) mbar_arrive(bars + kBarP2 + 8 * place);
+                        }
+                        l += (la.x + la.y) + (lb.x + lb.y);
                     }
-                    l += (la.x + la.y) + (lb.x + lb.y);
                 } else if (lane == 0) {   // its rows of P are whatever S was, and make rows of O that are nobody's
-                    mbar_arrive(bars + kBarP + 8 * tile);
-                    mbar_arrive(bars + kBarP2 + 8 * tile);
+                    mbar_arrive(bars + kBarP + 8 * place);
+                    mbar_arrive(bars + kBarP2 + 8 * place);
                 }
                 if (F16) {
                     __syncwarp();
                     if (lane == 0)
-                        for (int k = 0; k < releases; ++k) mbar_arrive(bars + kBarScEmpty + 8 * st);
+                        for (int k = 0; k < releases; ++k) mbar_arrive(bars + kScEmpty + 8 * st);
                 }
             }
+            if (both) turn = 0;
             if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
             tc_fence_after();
-            if (!idle) {
+            if (part && !idle) {
+                const uint32_t pair = 8 * (2 * tile + (r >> 5 & 1));
+                if (k0) {
+                    hand_over(tile, tO, m, l, F);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + kBarPairFull + pair);
+                    if (!wait(bars + kBarPairEmpty + pair, np++ & 1)) return;   // before the next unit's rows come there
+                } else {
+                    if (!wait(bars + kBarPairFull + pair, np++ & 1)) return;
+                    take_over(tile, tO, m, l, F);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars + kBarPairEmpty + pair);
+                }
+            }
+            if (!idle && !(part && k0)) {
                 const float inv = l > 0.f ? F / l : 0.f;
                 if (w.live && u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
-                if (u.pieces > 1 || a.out_f32)
-                    store_rows(u, tile, tO, w, m, l, inv);
-                else
-                    store_out(u, tile, tO, w, inv);
+                store_rows(u, tile, tO, w, m, l, inv);
             }
             tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
         }
     }
+    // Rows that are there twice: the second's warp gives its rows of O, counted from its reference and in units of its F, and (m, l)
+    // to the first's through the rows' places of both in the query operand (no product reads them any more).  A row that has
+    // seen nothing gives zeros.
+    __device__ __forceinline__ uint32_t pair_row(int tile, int c) const {   // 16 bytes c of this lane's row of 512
+        const int r = threadIdx.x & 63;
+        return sm + Cfg::kOffQ + tile * kSlotBytes + (c >> 4) * 8192 + (c >> 3 & 1) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    }
+    __device__ __forceinline__ void hand_over(int tile, uint32_t tO, float m, float l, float F) const {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o, tO + 16 * k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? __float_as_uint(__uint_as_float(o[i]) * F) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sts128(pair_row(tile, 4 * k + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        const uint32_t at = sm + Cfg::kOffPair + (tile * 64 + (threadIdx.x & 63)) * 8;
+        sts32v(at, __float_as_uint(m));
+        sts32v(at + 4, __float_as_uint(l));
+    }
+    __device__ __forceinline__ void take_over(int tile, uint32_t tO, float& m, float& l, float& F) const {
+        const uint32_t at = sm + Cfg::kOffPair + (tile * 64 + (threadIdx.x & 63)) * 8;
+        const float m1 = __uint_as_float(lds32v(at)), l1 = __uint_as_float(lds32v(at + 4));
+        const float M = l > 0.f && !(l1 > 0.f && m1 > m) ? m : m1;   // the larger of those that count
+        const float e0 = l > 0.f ? ex2(m - M) : 0.f, e1 = l1 > 0.f ? ex2(m1 - M) : 0.f, f0 = F * e0;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o, tO + 16 * k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[4];
+                lds128(pair_row(tile, 4 * k + i), v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float own = l > 0.f ? __uint_as_float(o[4 * i + q]) * f0 : 0.f;
+                    o[4 * i + q] = __float_as_uint(fmaf(__uint_as_float(v[q]), e1, own));
+                }
+            }
+            tmem_st16(tO + 16 * k, o);
+        }
+        tmem_wait_st();
+        l = l * e0 + l1 * e1;
+        m = M;
+        F = 1.f;
+    }
+    // The K scales of 16 tokens from `first` on (a multiple of 16): Q8: where the copies put them.
+    __device__ __forceinline__ uint32_t key_scales(uint32_t sc, int first) const { return Q8 ? scale_at(sc, first, 0) : sc + first * 4; }
     // 64 columns of S, times their K scales unless they carry them already.
-    __device__ __forceinline__ void read_scores(uint32_t (&s)[2][32], uint32_t at, uint32_t sc, bool scaled) const {
-        tmem_ld32(s[0], at);
-        tmem_ld32(s[1], at + 32);
+    __device__ __forceinline__ void read_scores(uint32_t (&s)[2][32], uint32_t tS, int first, uint32_t sc, bool scaled) const {
+        tmem_ld32(s[0], tS + first);
+        tmem_ld32(s[1], tS + first + 32);
         tmem_wait_ld();
         if (F16 && !scaled) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t f[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+                for (int i = 0; i < 16; i += 4) lds128(key_scales(sc, first + 16 * k) + 4 * i, f[i], f[i + 1], f[i + 2], f[i + 3]);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) mul2(s[k >> 1][(k & 1) * 16 + i], s[k >> 1][(k & 1) * 16 + i + 1], f[i], f[i + 1]);
             }
         }
     }
     // A step's S times its K scales, and -inf where the row does not see the token (whatever stands there: the choice comes last).
-    __device__ __forceinline__ void hide(const Unit& u, const Rows& w, const Sight& x, int t0, uint32_t tS, uint32_t sc) const {
+    __device__ __forceinline__ void hide(const Unit& u, const Rows& w, const Sight& x, int t0, uint32_t tS, uint32_t sc, int k0, int k1) const {
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
+        for (int k = k0; k < k1; ++k) {   // 16 tokens
             const uint32_t see = visible(u, w, x, t0 + 16 * k);
             uint32_t s[16];
             tmem_ld16(s, tS + 16 * k);
@@ -1305,7 +1619,7 @@ struct Prefix {
             if constexpr (F16) {
                 uint32_t f[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) lds128(sc + (16 * k + i) * 4, f[i], f[i + 1], f[i + 2], f[i + 3]);
+                for (int i = 0; i < 16; i += 4) lds128(key_scales(sc, 16 * k) + 4 * i, f[i], f[i + 1], f[i + 2], f[i + 3]);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) mul2(s[i], s[i + 1], f[i], f[i + 1]);
             }
@@ -1315,40 +1629,6 @@ struct Prefix {
             tmem_st16(tS + 16 * k, s);
         }
         tmem_wait_st();
-    }
-    // TREE: the row of a thread's O in a result of one piece, bf16.
-    __device__ __forceinline__ void store_out(const Unit& u, int tile, uint32_t tO, const Rows& w, float inv) const {
-        const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96;
-        const uint32_t stage = sm + Cfg::kOffQ + tile * kSlotBytes + r0 * 128;
-        auto at = [&](int r, int c) { return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-        const int rows = min(32, u.rows - (u.rt * kUnitRows + tile * kTileRows + r0));
-        const long long mine = w.head * a.QG + w.q;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            uint32_t s[2][32];
-            tmem_ld32(s[0], tO + 64 * half);
-            tmem_ld32(s[1], tO + 64 * half + 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t* x = &s[c >> 2][(c & 3) * 8];
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = pack_bf16(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
-                sts128(at(lane, 8 * half + c), o[0], o[1], o[2], o[3]);
-            }
-        }
-        __syncwarp();
-        const int c = lane & 15;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4);
-            const long long dst = __shfl_sync(kLanes, mine, r);
-            uint32_t v0, v1, v2, v3;
-            lds128(at(r, c), v0, v1, v2, v3);
-            if (r < rows) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 8 * c) = make_uint4(v0, v1, v2, v3);
-        }
-        __syncwarp();   // the next unit's query rows are written by other lanes
     }
     // The rows that no unit holds: of a sequence in error zeros, of nobody what is there.  The join leaves rows of one piece alone.
     __device__ void settle() const {
@@ -1376,7 +1656,7 @@ struct Prefix {
         auto at = [&](int r, int c) {   // 16 bytes c of the half row r
             return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
         };
-        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
+        const int row0 = first_row(u, tile) + r0;
         const int rows = min(32, u.rows - row0);   // may be negative
         const bool whole = TREE && u.pieces == 1;
         const long long mine = whole ? w.head * a.QG + w.q : (w.head * a.slots + u.slot) * a.QG + w.q;
@@ -1401,6 +1681,23 @@ struct Prefix {
                        __float_as_uint(__uint_as_float(x[3]) * inv));
             }
             __syncwarp();
+            if constexpr (TREE)
+                if (whole && !a.out_f32) {
+                    const int c = lane & 7;   // four rows, 16 bytes per lane
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const long long dst = __shfl_sync(kLanes, mine, r);
+                        uint32_t v[8];
+                        lds128(at(r, 2 * c), v[0], v[1], v[2], v[3]);
+                        lds128(at(r, 2 * c + 1), v[4], v[5], v[6], v[7]);
+                        if (r >= rows) continue;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = pack_bf16(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 64 * half + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    continue;
+                }
             const int c = lane & 15;
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
@@ -1455,6 +1752,15 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             mbar_init(bars + kBarP + 8 * i, 4);
             mbar_init(bars + kBarP2 + 8 * i, 4);
             mbar_init(bars + kBarO + 8 * i, 1);
+            if (Cfg::kTree) {
+                mbar_init(bars + kBarHalf + 8 * i, 1);
+                mbar_init(bars + kBarWhole + 8 * i, 1);
+                mbar_init(bars + kBarS2 + 8 * i, 1);
+                for (int k = 0; k < 2; ++k) {
+                    mbar_init(bars + kBarPairFull + 16 * i + 8 * k, 1);
+                    mbar_init(bars + kBarPairEmpty + 16 * i + 8 * k, 1);
+                }
+            }
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(bars + kBarRawFull + 8 * i, 1);
@@ -1463,7 +1769,7 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             mbar_init(bars + kBarScFull + 8 * i, 1);
             mbar_init(bars + kBarScEmpty + 8 * i, 8);
             if (Cfg::kQ8) {
-                mbar_init(bars + kBarVFull + 8 * i, kConvertWarps);
+                mbar_init(bars + kBarVFull + 8 * i, kConvertWarps / 2);   // of 64 tokens
                 mbar_init(bars + kBarVEmpty + 8 * i, 1);
             }
         }
@@ -1471,6 +1777,12 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             mbar_init(bars + kBarUnitFull + 8 * i, 1);
             mbar_init(bars + kBarUnitEmpty + 8 * i, Cfg::kReaders);
         }
+        if (Cfg::kQ8)
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(bars + kBarScRaw8 + 8 * i, 32);
+                mbar_init(bars + kBarScFull8 + 8 * i, 1);
+                mbar_init(bars + kBarScEmpty8 + 8 * i, 8 + kConvertWarps);
+            }
         mbar_init(bars + kBarDrain, 1);
         sts32v(bars + kAbortAt, (sm & 1023u) ? 1u : 0u);   // the operands' swizzle needs the alignment
         fence_mbar_init();
@@ -1507,7 +1819,9 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
     // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
-        if constexpr (Cfg::kF16)
+        if constexpr (Cfg::kTree && Cfg::kF16)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        else if constexpr (Cfg::kF16)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -1518,13 +1832,19 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
                 p.softmax(tmem, warp >> 2);
         }
     } else {
-        if constexpr (Cfg::kF16)
+        if constexpr (Cfg::kTree && Cfg::kF16)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        else if constexpr (Cfg::kF16)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (fine) {
-            if (warp == 8)
-                p.copies(&kv_map, &sc_map);
+            if (warp == 8 || (Cfg::kTree && !Cfg::kTq && warp == 10)) {
+                if constexpr (Cfg::kTree)
+                    p.copies_tree(&kv_map, &sc_map, warp == 10);
+                else
+                    p.copies(&kv_map, &sc_map);
+            }
             else if (warp == 9)
                 p.products(tmem);
             else if (warp == 11) {
@@ -1532,7 +1852,7 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
                 if constexpr (Cfg::kTree)
                     if (!split.refused) p.settle();
             }
-            else if (Cfg::kF16 && warp == 10)
+            else if (Cfg::kF16 && !Cfg::kQ8 && warp == 10)
                 p.scales();
             else if (Cfg::kF16 && warp >= 12)
                 p.convert();

@@ -41,6 +41,8 @@ struct TreeArgs : SharedArgs {
     int* refused;                // set to 1 by a call whose token_starts do not ascend, else to 0
     int words;                   // 32-bit words of a mask
     int window, num_first;       // window 0: none
+    const uint8_t* cache;        // the pool, for what is not copied by tensor map
+    long long block_bytes, meta_bytes;   // of a block; where its metadata start
     void* out;                   // [B][Hk*QG][D]
     int out_f32;
     static constexpr int kBadStarts = PDA_ERRW_BAD_TOKENS;

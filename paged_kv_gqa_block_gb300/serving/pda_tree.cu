@@ -211,6 +211,9 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
     a.words = 2 * mask_words;
     a.window = window;
     a.num_first = num_first;
+    a.cache = static_cast<const uint8_t*>(kv_cache);
+    a.block_bytes = plan->cache_block_bytes;
+    a.meta_bytes = plan->meta_offset_bytes;
     a.out = out;
     a.out_f32 = out_dtype == PDA_OUT_F32;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

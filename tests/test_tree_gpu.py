@@ -99,6 +99,16 @@ def test_many_sequences(pda, kv):
 
 
 @pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("window,first", [(0, 0), (200, 3)])
+def test_unlike_trees(pda, kv, window, first):
+    """Several units per SM, of one row, of a tile's 128, one more, two tiles' 256 and one more, in every order."""
+    rng = np.random.default_rng(11)
+    counts = [int(x) for x in rng.choice([1, 3, 15, 16, 17, 31, 32, 33, 40], 90)]
+    lens = [int(x) for x in rng.integers(0, 520, 90)]
+    TreeCase(kv, 8, 8, 16, lens, counts, "tree", window, first, seed=12).check(pda)
+
+
+@pytest.mark.parametrize("kv", KVS)
 def test_many_pieces(pda, kv):
     """One long sequence over every SM: more than 32 pieces for the join."""
     TreeCase(kv, 1, 8, 32, [20000], [3], "tree", seed=6).check(pda)
