@@ -74,10 +74,9 @@ constexpr int kSlotBytes = 32768;          // 128 tokens x 128 dimensions, 16 bi
 constexpr int kRawBytes = 16384;           // the same in 8 bits
 constexpr float kLog2eS = 1.4426950408889634f, kLn2S = 0.6931471805599453f;
 constexpr float kLazy = 8.f;               // log2 units that a row's maximum may rise before its reference follows
-constexpr int kHalvesSteps = 3;
 constexpr float kBelow = 7.f;              // f16 P: the reference below the maximum
 
-constexpr int kBarBytes = 720;             // barriers and scalars
+constexpr int kBarBytes = 784;             // barriers and scalars
 
 // What a KV format and a kind of call take of shared memory, barriers and threads.  Q8 (drafted tokens over fp8 KV): the score
 // product takes K's codes as they are, so that only V is converted, in halves of 64 tokens.
@@ -99,8 +98,8 @@ struct SharedCfg {
     static constexpr int kOffScales = kOffRaw + (kF16 ? kRaw * kRawBytes : 0);
     static constexpr int kOffBars = kOffScales + (kF16 ? kScales * kScaleBytes : 0);
     static constexpr int kOffTable = kOffBars + kBarBytes;        // TQ4: the centroids of a byte's two codes, f16
-    static constexpr int kOffPair = kOffBars + kBarBytes + (kTq ? 1024 : 0);   // drafted tokens: (m, l) of rows' second halves
-    static constexpr int kSmem = kTree ? kOffPair + 1024 : kTq ? kOffTable + 1024 : kOffBars + 448;
+    static constexpr int kOffPair = kOffBars + kBarBytes + (kTq ? 1024 : 0);   // drafted tokens: (m, l) of rows' halves
+    static constexpr int kSmem = kTree ? kOffPair + 2048 : kTq ? kOffTable + 1024 : kOffBars + 448;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     static constexpr int kReaders = kF16 ? 15 : kTree ? 11 : 10;  // warps that take units
 };
@@ -131,8 +130,8 @@ enum {
     kBarScEmpty8 = 552,
     kBarScRaw8 = 584,
     kBarWhole = 616,     // [2] that of the second half too
-    kBarPairFull = 648,  // [2][2] drafted tokens: a warp has handed its second halves over
-    kBarPairEmpty = 680, // [2][2] they have been taken
+    kBarPairFull = 648,  // [8] drafted tokens: a softmax warp has handed a part of its rows over
+    kBarPairEmpty = 712, // [8] it has taken what it was handed
     kBarS2 = 632,        // [2] drafted tokens: a tile's S is in the second place (kBarS: in the first)
     kBarVFull = 456,     // [3] Q8: a half of V is converted
     kBarVEmpty = 480     // [3] the products that read it are done
@@ -294,8 +293,8 @@ struct Prefix {
     }
     // TREE: of at most 64 rows every one is there twice, 64 rows apart: the first half of each step's tokens is one's, the second the
     // other's, so that a step's softmax takes a warp half as long (fp8, steps of 36 rows: 1.7 -> 1.3 us with everything); the two
-    // are joined at the end, which costs more than it gives in units of one step or two.
-    __device__ __forceinline__ static bool halves(const Unit& u) { return TREE && u.rows - u.rt * kUnitRows <= 64 && u.steps >= kHalvesSteps; }
+    // are joined at the end.
+    __device__ __forceinline__ static bool halves(const Unit& u) { return TREE && u.rows - u.rt * kUnitRows <= 64; }
     __device__ __forceinline__ static bool active(const Unit& u, int tile) {
         return u.rt * kUnitRows + tile * kTileRows < u.rows;
     }
@@ -1519,76 +1518,47 @@ struct Prefix {
             if (both) turn = 0;
             if (!wait(bars + kBarO + 8 * tile, no++ & 1)) return;
             tc_fence_after();
-            if (part && !idle) {
-                const uint32_t pair = 8 * (2 * tile + (r >> 5 & 1));
-                if (k0) {
-                    hand_over(tile, tO, m, l, F);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + kBarPairFull + pair);
-                    if (!wait(bars + kBarPairEmpty + pair, np++ & 1)) return;   // before the next unit's rows come there
-                } else {
-                    if (!wait(bars + kBarPairFull + pair, np++ & 1)) return;
-                    take_over(tile, tO, m, l, F);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars + kBarPairEmpty + pair);
+            if (!idle) {
+                const uint32_t mine = 8 * (4 * tile + (r >> 5)), other = mine ^ 16;
+                if (part) {
+                    hand_over(tile, k0, tO, m, l, F);
+                    if (lane == 0) mbar_arrive(bars + kBarPairFull + mine);
+                    if (!wait(bars + kBarPairFull + other, np & 1)) return;
                 }
-            }
-            if (!idle && !(part && k0)) {
-                const float inv = l > 0.f ? F / l : 0.f;
-                if (w.live && u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
-                store_rows(u, tile, tO, w, m, l, inv);
+                store_tree(u, tile, part, k0, tO, w, m, l, F);
+                if (part) {   // the other's next rows come to where this warp's were handed over
+                    if (lane == 0) mbar_arrive(bars + kBarPairEmpty + mine);
+                    if (!wait(bars + kBarPairEmpty + other, np++ & 1)) return;
+                }
             }
             tc_fence_before();   // the next unit's products overwrite O once this warp's next P is announced
         }
     }
-    // Rows that are there twice: the second's warp gives its rows of O, counted from its reference and in units of its F, and (m, l)
-    // to the first's through the rows' places of both in the query operand (no product reads them any more).  A row that has
-    // seen nothing gives zeros.
-    __device__ __forceinline__ uint32_t pair_row(int tile, int c) const {   // 16 bytes c of this lane's row of 512
-        const int r = threadIdx.x & 63;
-        return sm + Cfg::kOffQ + tile * kSlotBytes + (c >> 4) * 8192 + (c >> 3 & 1) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    // Rows that are there twice: each of the two warps stores one half of the columns.  A warp gives the other's half of its rows of
+    // O, counted from its reference and in units of its F, and (m, l), through its own rows' places in the query operand (no product
+    // reads them any more).
+    __device__ __forceinline__ uint32_t place(int tile, int r, int c) const {   // 16 bytes c of the 256 of row r
+        return sm + Cfg::kOffQ + tile * kSlotBytes + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     }
-    __device__ __forceinline__ void hand_over(int tile, uint32_t tO, float m, float l, float F) const {
+    __device__ __forceinline__ void hand_over(int tile, int k0, uint32_t tO, float m, float l, float F) const {
+        const int r = threadIdx.x & 127;
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            uint32_t o[16];
-            tmem_ld16(o, tO + 16 * k);
+        for (int k = 0; k < 2; ++k) {
+            uint32_t o[32];
+            tmem_ld32(o, tO + 64 * (1 - k0) + 32 * k);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = l > 0.f ? __float_as_uint(__uint_as_float(o[i]) * F) : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sts128(pair_row(tile, 4 * k + i), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) {
+                const float f = l > 0.f ? F : 0.f;
+                const uint32_t* x = o + 4 * i;
+                sts128(place(tile, r, 8 * k + i), __float_as_uint(__uint_as_float(x[0]) * f), __float_as_uint(__uint_as_float(x[1]) * f),
+                       __float_as_uint(__uint_as_float(x[2]) * f), __float_as_uint(__uint_as_float(x[3]) * f));
+            }
         }
-        const uint32_t at = sm + Cfg::kOffPair + (tile * 64 + (threadIdx.x & 63)) * 8;
+        const uint32_t at = sm + Cfg::kOffPair + (tile * 128 + r) * 8;
         sts32v(at, __float_as_uint(m));
         sts32v(at + 4, __float_as_uint(l));
-    }
-    __device__ __forceinline__ void take_over(int tile, uint32_t tO, float& m, float& l, float& F) const {
-        const uint32_t at = sm + Cfg::kOffPair + (tile * 64 + (threadIdx.x & 63)) * 8;
-        const float m1 = __uint_as_float(lds32v(at)), l1 = __uint_as_float(lds32v(at + 4));
-        const float M = l > 0.f && !(l1 > 0.f && m1 > m) ? m : m1;   // the larger of those that count
-        const float e0 = l > 0.f ? ex2(m - M) : 0.f, e1 = l1 > 0.f ? ex2(m1 - M) : 0.f, f0 = F * e0;
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            uint32_t o[16];
-            tmem_ld16(o, tO + 16 * k);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t v[4];
-                lds128(pair_row(tile, 4 * k + i), v[0], v[1], v[2], v[3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float own = l > 0.f ? __uint_as_float(o[4 * i + q]) * f0 : 0.f;
-                    o[4 * i + q] = __float_as_uint(fmaf(__uint_as_float(v[q]), e1, own));
-                }
-            }
-            tmem_st16(tO + 16 * k, o);
-        }
-        tmem_wait_st();
-        l = l * e0 + l1 * e1;
-        m = M;
-        F = 1.f;
+        __syncwarp();
     }
     // The K scales of 16 tokens from `first` on (a multiple of 16): Q8: where the copies put them.
     __device__ __forceinline__ uint32_t key_scales(uint32_t sc, int first) const { return Q8 ? scale_at(sc, first, 0) : sc + first * 4; }
@@ -1646,7 +1616,7 @@ struct Prefix {
         }
     }
 
-    // The warp's 32 rows of O, times inv, to the partials (TREE: or to a result of one piece, fp32).  A thread holds a row, and storing rows from
+    // The warp's 32 rows of O, times inv, to the partials.  A thread holds a row, and storing rows from
     // there would touch 32 lines per instruction; each half (64 columns) goes through the warp's own rows of
     // its tile's query operand, which no product reads any more, and out two rows per instruction.
     __device__ __forceinline__ void store_rows(const Unit& u, int tile, uint32_t tO, const Rows& w, float m, float l,
@@ -1656,15 +1626,13 @@ struct Prefix {
         auto at = [&](int r, int c) {   // 16 bytes c of the half row r
             return stage + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
         };
-        const int row0 = first_row(u, tile) + r0;
+        const int row0 = u.rt * kUnitRows + tile * kTileRows + r0;
         const int rows = min(32, u.rows - row0);   // may be negative
-        const bool whole = TREE && u.pieces == 1;
-        const long long mine = whole ? w.head * a.QG + w.q : (w.head * a.slots + u.slot) * a.QG + w.q;
-        float* const to = whole ? out_rows() : a.part_o;
-        if (w.live && !whole) {
+        const long long mine = (w.head * a.slots + u.slot) * a.QG + w.q;
+        if (w.live) {
             a.part_l[mine] = l;
             a.part_m[mine] = m * kLn2S;
-            if (!TREE && u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
+            if (u.slot == 0) a.pieces[w.head * a.QG + w.q] = u.pieces;
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -1681,23 +1649,6 @@ struct Prefix {
                        __float_as_uint(__uint_as_float(x[3]) * inv));
             }
             __syncwarp();
-            if constexpr (TREE)
-                if (whole && !a.out_f32) {
-                    const int c = lane & 7;   // four rows, 16 bytes per lane
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const long long dst = __shfl_sync(kLanes, mine, r);
-                        uint32_t v[8];
-                        lds128(at(r, 2 * c), v[0], v[1], v[2], v[3]);
-                        lds128(at(r, 2 * c + 1), v[4], v[5], v[6], v[7]);
-                        if (r >= rows) continue;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = pack_bf16(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 64 * half + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    continue;
-                }
             const int c = lane & 15;
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
@@ -1706,16 +1657,93 @@ struct Prefix {
                 uint32_t v0, v1, v2, v3;
                 lds128(at(r, c), v0, v1, v2, v3);
                 if (r < rows)
-                    *reinterpret_cast<uint4*>(to + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
+                    *reinterpret_cast<uint4*>(a.part_o + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v0, v1, v2, v3);
             }
         }
         __syncwarp();   // the next unit's query rows are written by other lanes
     }
-    __device__ __forceinline__ float* out_rows() const {
-        if constexpr (TREE)
-            return static_cast<float*>(a.out);
-        else
-            return nullptr;
+    // TREE: the same, over l, to the partials or to a result of one piece; of rows that are there twice one half of the columns,
+    // with what the other warp has handed over.
+    __device__ __forceinline__ void store_tree(const Unit& u, int tile, bool part, int k0, uint32_t tO, const Rows& w, float m, float l,
+                                               float F) const {
+        const int lane = threadIdx.x & 31, r0 = part ? threadIdx.x & 32 : threadIdx.x & 96;
+        const int from = (threadIdx.x & 96) ^ (part ? 64 : 0);   // rows whose places are used
+        const int rows = min(32, u.rows - (first_row(u, tile) + r0));
+        const bool whole = u.pieces == 1, bf16 = whole && !a.out_f32;
+        const long long row = w.head * a.QG + w.q, mine = whole ? row : (w.head * a.slots + u.slot) * a.QG + w.q;
+        float* const to = whole ? static_cast<float*>(a.out) : a.part_o;
+        float f0 = l > 0.f ? F : 0.f, f1 = 0.f;
+        if (part) {
+            const uint32_t at = sm + Cfg::kOffPair + (tile * 128 + from + lane) * 8;
+            const float m1 = __uint_as_float(lds32v(at)), l1 = __uint_as_float(lds32v(at + 4));
+            const float M = l > 0.f && !(l1 > 0.f && m1 > m) ? m : m1;   // the larger of those that count
+            const float e = l > 0.f ? ex2(m - M) : 0.f;
+            f1 = l1 > 0.f ? ex2(m1 - M) : 0.f;
+            f0 *= e;
+            l = k0 ? l1 * f1 + l * e : l * e + l1 * f1;
+            m = M;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that sees nothing gives zeros
+        f0 *= inv;
+        f1 *= inv;
+        if (w.live && !k0) {
+            if (u.slot == 0) a.pieces[row] = u.pieces;
+            if (!whole) {
+                a.part_l[mine] = l;
+                a.part_m[mine] = m * kLn2S;
+            }
+        }
+#pragma unroll 1
+        for (int half = part ? k0 : 0; half < (part ? k0 + 1 : 2); ++half) {
+            uint32_t s[2][32];
+            tmem_ld32(s[0], tO + 64 * half);
+            tmem_ld32(s[1], tO + 64 * half + 32);
+            tmem_wait_ld();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = __float_as_uint(__uint_as_float(s[i >> 5][i & 31]) * f0);
+            if (part) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    uint32_t v[4], *x = &s[c >> 3][(c & 7) * 4];
+                    lds128(place(tile, from + lane, c), v[0], v[1], v[2], v[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), f1, __uint_as_float(x[i])));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t* x = &s[c >> 3][(c & 7) * 4];
+                sts128(place(tile, from + lane, c), x[0], x[1], x[2], x[3]);
+            }
+            __syncwarp();
+            if (bf16) {
+                const int c = lane & 7;   // four rows, 16 bytes per lane
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    const long long dst = __shfl_sync(kLanes, mine, r);
+                    uint32_t v[8];
+                    lds128(place(tile, from + r, 2 * c), v[0], v[1], v[2], v[3]);
+                    lds128(place(tile, from + r, 2 * c + 1), v[4], v[5], v[6], v[7]);
+                    if (r >= rows) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = pack_bf16(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 64 * half + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                const int c = lane & 15;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int r = 2 * i + (lane >> 4);
+                    const long long dst = __shfl_sync(kLanes, mine, r);
+                    uint32_t v[4];
+                    lds128(place(tile, from + r, c), v[0], v[1], v[2], v[3]);
+                    if (r < rows) *reinterpret_cast<uint4*>(to + dst * kHeadDim + 64 * half + 4 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+        __syncwarp();   // the next unit's query rows are written by other lanes
     }
     // O *= f, one row per thread (rare; few registers, since S is held meanwhile).
     static __device__ __forceinline__ void rescale(uint32_t tO, float f) {
@@ -1756,9 +1784,9 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
                 mbar_init(bars + kBarHalf + 8 * i, 1);
                 mbar_init(bars + kBarWhole + 8 * i, 1);
                 mbar_init(bars + kBarS2 + 8 * i, 1);
-                for (int k = 0; k < 2; ++k) {
-                    mbar_init(bars + kBarPairFull + 16 * i + 8 * k, 1);
-                    mbar_init(bars + kBarPairEmpty + 16 * i + 8 * k, 1);
+                for (int k = 0; k < 4; ++k) {
+                    mbar_init(bars + kBarPairFull + 32 * i + 8 * k, 1);
+                    mbar_init(bars + kBarPairEmpty + 32 * i + 8 * k, 1);
                 }
             }
         }
