@@ -120,6 +120,7 @@ struct __align__(16) Codebook {
     float mid[16];
     uint32_t code[16];
     int plain;   // no midpoint but 0 is below 2^-60
+    int ascending;   // the codes are the ranks
 };
 __device__ __forceinline__ void sort_codebook(const float* centroids, Codebook& book, float* sorted) {
     if (threadIdx.x < 32) {
@@ -139,16 +140,20 @@ __device__ __forceinline__ void sort_codebook(const float* centroids, Codebook& 
         const float mid = lane < 15 ? __fmul_rn(__fadd_rn(sorted[lane], sorted[lane + 1]), 0.5f) : INFINITY;
         if (lane < 16) book.mid[lane] = mid;
         const bool plain = __all_sync(kAll, lane >= 15 || mid == 0.f || fabsf(mid) >= 8.6736174e-19f);
-        if (lane == 0) book.plain = plain;
+        const bool ascending = __all_sync(kAll, lane >= 16 || rank == lane);
+        if (lane == 0) {
+            book.plain = plain;
+            book.ascending = ascending;
+        }
     }
 }
 
-// Integers that are ordered like the floats.
-__device__ __forceinline__ int ordered(float x) {
-    const int b = __float_as_int(x);
-    return b ^ (b >> 31 & 0x7FFFFFFF);
+// The smaller of two bf16 values each, of zeros the negative one.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ (b >> 31 & 0x7FFFFFFF)); }
 __device__ __forceinline__ float f16_saturated(float x) {
     return __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
 }
@@ -205,67 +210,76 @@ __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw
     if ((lane & 15) == 0) scales[(lane >> 4) * BS] = scale;
 }
 
-// TQ4: every lane holds four dimensions of K and of V, 4l .. 4l+3.
-__device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, uint2 kraw, uint2 vraw, const Codebook& book, int lane,
+// TQ4: a half warp writes a row, lane l of it dimensions 8l .. 8l+7 of K and of V; the other half another row, so that what is done
+// once per row (reductions, roots, inverses) is shared by two.  Bound by instructions.
+__device__ __forceinline__ void write_tq4(uint8_t* row, uint16_t* fields, bool live, uint4 kraw, uint4 vraw, const Codebook& book, int l,
                                           int BS) {
-    const float k[4] = {bf16_lo(kraw.x), bf16_hi(kraw.x), bf16_lo(kraw.y), bf16_hi(kraw.y)};
-    const float v[4] = {bf16_lo(vraw.x), bf16_hi(vraw.x), bf16_lo(vraw.y), bf16_hi(vraw.y)};
-    float sum = fmaf(k[0], k[0], fmaf(k[1], k[1], fmaf(k[2], k[2], k[3] * k[3])));
-    float lo = fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), hi = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    const uint32_t kw[4] = {kraw.x, kraw.y, kraw.z, kraw.w}, vw[4] = {vraw.x, vraw.y, vraw.z, vraw.w};
+    float sum, part[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    lo = from_ordered(__reduce_min_sync(kAll, ordered(lo)));
-    hi = from_ordered(__reduce_max_sync(kAll, ordered(hi)));
-    // |k| is rounded to f16 once: nine fp32 roundings of positive terms and the root are off by less than 2^-20, and where
+    for (int i = 0; i < 4; ++i) part[i] = fmaf(bf16_hi(kw[i]), bf16_hi(kw[i]), bf16_lo(kw[i]) * bf16_lo(kw[i]));
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+    // the smallest V, and the smallest of -V, as bf16 pairs: both exact
+    uint32_t low = min_bf16x2(min_bf16x2(vw[0], vw[1]), min_bf16x2(vw[2], vw[3]));
+    uint32_t high = min_bf16x2(min_bf16x2(vw[0] ^ 0x80008000u, vw[1] ^ 0x80008000u), min_bf16x2(vw[2] ^ 0x80008000u, vw[3] ^ 0x80008000u));
+    uint32_t both = min_bf16x2(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));   // low halves, high halves
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(kAll, sum, o);
+        both = min_bf16x2(both, __shfl_xor_sync(kAll, both, o));
+    }
+    const float lo = bf16_lo(both), hi = -bf16_hi(both);
+    // |k| is rounded to f16 once: eight fp32 roundings of positive terms and the root are off by less than 2^-20, and where
     // that does not decide the f16 value (one row in a thousand) the sum is taken again in 64 bits.  The sum is the same in
-    // every lane (a butterfly adds the same pairs), so the warp stays together.
+    // every lane of the row (a butterfly adds the same pairs).
     const float root = sqrtf(sum);
     uint16_t norm_bits = __half_as_ushort(__float2half_rn(fminf(root, 65504.f)));
     const float up = fminf(__fmul_rn(root, 1.f + 9.5367431640625e-7f), 65504.f);
     const float down = fminf(__fmul_rn(root, 1.f - 9.5367431640625e-7f), 65504.f);
-    if (__half_as_ushort(__float2half_rn(up)) != __half_as_ushort(__float2half_rn(down))) {
+    const bool open = __half_as_ushort(__float2half_rn(up)) != __half_as_ushort(__float2half_rn(down));
+    if (__any_sync(kAll, open)) {
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s += (double)k[i] * (double)k[i];
+        for (int i = 0; i < 4; ++i) s += (double)bf16_lo(kw[i]) * (double)bf16_lo(kw[i]) + (double)bf16_hi(kw[i]) * (double)bf16_hi(kw[i]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
         // by way of fp32 without rounding twice: cut, and odd where something was cut off
         const double exact = fmin(sqrt(s), 65504.0);
         float cut = __double2float_rz(exact);
         if ((double)cut != exact) cut = __uint_as_float(__float_as_uint(cut) | 1u);
-        norm_bits = __half_as_ushort(__float2half_rn(cut));
+        if (open) norm_bits = __half_as_ushort(__float2half_rn(cut));
     }
     const float norm = __half2float(__ushort_as_half(norm_bits));
     const float by = norm > 0.f ? norm : 1.f, rk = __frcp_rn(by);
     uint32_t kc = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         // |k| is at most the norm, or the norm is 65504: nothing overflows; a quotient below 2^-61 lies between the same midpoints
         // whatever its last places
-        const float x = book.plain ? quotient(k[i], by, rk) : __fdiv_rn(k[i], by);
+        const float k = i & 1 ? bf16_hi(kw[i >> 1]) : bf16_lo(kw[i >> 1]), x = book.plain ? quotient(k, by, rk) : __fdiv_rn(k, by);
         // midpoints 7, then 3 or 11, then the three of one quarter at once
         const bool upper = book.mid[7] < x;
         const int q = (upper ? 2 : 0) + ((upper ? book.mid[11] : book.mid[3]) < x ? 1 : 0);
         const float4 m = *reinterpret_cast<const float4*>(book.mid + 4 * q);
         const int rank = 4 * q + (m.x < x ? 1 : 0) + (m.y < x ? 1 : 0) + (m.z < x ? 1 : 0);
-        kc |= book.code[rank] << (4 * i);
+        kc |= (book.ascending ? (uint32_t)rank : book.code[rank]) << (4 * i);
     }
     const float zero = f16_saturated(lo), step = f16_saturated(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     const float vby = step > 0.f ? step : 1.f, rv = __frcp_rn(vby);   // at least f16's smallest, 2^-24
     uint32_t vc = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         // brought into 0 .. 15, then rounded by the sum with 1.5 * 2^23, whose last bits are the integer
-        const float c = fminf(fmaxf(quotient(__fsub_rn(v[i], zero), vby, rv), 0.f), 15.f);
+        const float v = i & 1 ? bf16_hi(vw[i >> 1]) : bf16_lo(vw[i >> 1]);
+        const float c = fminf(fmaxf(quotient(__fsub_rn(v, zero), vby, rv), 0.f), 15.f);
         vc |= (__float_as_uint(__fadd_rn(c, 12582912.f)) & 15u) << (4 * i);
     }
-    // even lanes store eight codes of K, odd lanes of V
-    const uint32_t give = lane & 1 ? kc : vc, got = __shfl_xor_sync(kAll, give, 1);
-    const uint32_t word = lane & 1 ? got | vc << 16 : kc | got << 16;
-    *reinterpret_cast<uint32_t*>(row + (lane & 1) * 64 + (lane >> 1) * 4) = word;
-    if (lane < 3) {
-        const uint16_t f = lane == 0 ? norm_bits : __half_as_ushort(__float2half_rn(lane == 1 ? step : zero));
-        fields[lane * BS] = f;
+    if (!live) return;
+    *reinterpret_cast<uint32_t*>(row + 4 * l) = kc;
+    *reinterpret_cast<uint32_t*>(row + 64 + 4 * l) = vc;
+    if (l < 3) {
+        const uint16_t f = l == 0 ? norm_bits : __half_as_ushort(__float2half_rn(l == 1 ? step : zero));
+        fields[l * BS] = f;
     }
 }
 
@@ -284,27 +298,28 @@ __global__ void __launch_bounds__(kTokThreads) pda_write_kernel(const TokenArgs 
         if (at.row[x.t] < 0) continue;
         const uint16_t* k = a.k_new + (first + x.t) * a.k_stride + x.h * kHeadDim;
         const uint16_t* v = a.v_new + (first + x.t) * a.v_stride + x.h * kHeadDim;
-        uint4 raw[kHeadsAhead];   // TQ4: four dimensions of K, four of V; else eight of one of them
+        uint4 raw[kHeadsAhead];   // eight dimensions of K or V; TQ4: of K and V of every other head
+        const int half = lane >> 4, l = lane & 15;
 #pragma unroll
-        for (int i = 0; i < kHeadsAhead; ++i)
-            if (i < x.n) {
-                if constexpr (KV == PDA_KV_TQ4) {
-                    const uint2 kw = __ldg(reinterpret_cast<const uint2*>(k + i * kHeadDim) + lane);
-                    const uint2 vw = __ldg(reinterpret_cast<const uint2*>(v + i * kHeadDim) + lane);
-                    raw[i] = make_uint4(kw.x, kw.y, vw.x, vw.y);
-                } else {
-                    raw[i] = __ldg(reinterpret_cast<const uint4*>((lane < 16 ? k : v) + i * kHeadDim) + (lane & 15));
-                }
+        for (int i = 0; i < kHeadsAhead; ++i) {
+            if constexpr (KV == PDA_KV_TQ4) {
+                const int head = min((i & ~1) + half, x.n - 1);   // an odd last one is taken twice, and written once
+                if ((i & ~1) < x.n) raw[i] = __ldg(reinterpret_cast<const uint4*>((i & 1 ? v : k) + head * kHeadDim) + l);
+            } else if (i < x.n) {
+                raw[i] = __ldg(reinterpret_cast<const uint4*>((lane < 16 ? k : v) + i * kHeadDim) + l);
             }
+        }
         uint8_t* row = a.cache + at.row[x.t] + (long long)x.h * kRow;
         uint8_t* field = a.cache + at.field[x.t];
 #pragma unroll
         for (int i = 0; i < kHeadsAhead; ++i)
             if (i < x.n) {
-                if constexpr (KV == PDA_KV_TQ4)
-                    write_tq4(row + i * kRow, reinterpret_cast<uint16_t*>(field) + (x.h + i) * 3 * a.BS, make_uint2(raw[i].x, raw[i].y),
-                              make_uint2(raw[i].z, raw[i].w), book, lane, a.BS);
-                else if constexpr (KV == PDA_KV_BF16)
+                if constexpr (KV == PDA_KV_TQ4) {
+                    if (i & 1) continue;
+                    const int head = i + half;
+                    write_tq4(row + head * kRow, reinterpret_cast<uint16_t*>(field) + (x.h + head) * 3 * a.BS, head < x.n, raw[i], raw[i + 1],
+                              book, l, a.BS);
+                } else if constexpr (KV == PDA_KV_BF16)
                     *reinterpret_cast<uint4*>(row + i * kRow + 16 * lane) = raw[i];
                 else
                     write_fp8(row + i * kRow, reinterpret_cast<float*>(field) + (x.h + i) * 2 * a.BS, raw[i], lane, a.BS);
