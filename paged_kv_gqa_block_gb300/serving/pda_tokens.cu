@@ -169,8 +169,9 @@ __device__ __forceinline__ uint32_t cut_f16(float x, float y) {   // towards zer
 // times 2^-8 has e4m3's exponent field in f16's bits 13 .. 10 and its mantissa behind it; f16 cut towards zero, plus half of
 // e4m3's last place, cut again, is the code of every value that is no tie.  The correctly rounded quotient lies between x times
 // 1 / scale a little too small and a little too large (2^-21 either way: the approximate inverse is off by 2^-23, four products
-// and the quotient's own rounding by 2^-24 each), and where both have one code that is the quotient's.  Else, in about one row of 500, and
-// in rows that are tiny or hold infinities or NaN, every value is divided.
+// and the quotient's own rounding by 2^-24 each), and where both have one code that is the quotient's.  Else, in one row of
+// four (bf16 values have few mantissas, so their quotients meet e4m3's ties often), the lane's quotients are computed; in rows that are
+// tiny or hold infinities or NaN every value is divided.
 __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     // magnitudes of bf16 values are ordered like their bits
@@ -201,10 +202,15 @@ __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mine, m, o));
             scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+            auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(v), scale), __fdiv_rn(bf16_hi(v), scale)); };
+            a = code(w[0]) | code(w[1]) << 16;
+            b = code(w[2]) | code(w[3]) << 16;
+        } else {   // a quotient whose remainder underflows is far below e4m3's smallest
+            const float by = __frcp_rn(scale);
+            auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(quotient(bf16_lo(v), scale, by), quotient(bf16_hi(v), scale, by)); };
+            a = code(w[0]) | code(w[1]) << 16;
+            b = code(w[2]) | code(w[3]) << 16;
         }
-        auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(v), scale), __fdiv_rn(bf16_hi(v), scale)); };
-        a = code(w[0]) | code(w[1]) << 16;
-        b = code(w[2]) | code(w[3]) << 16;
     }
     *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(a, b);
     if ((lane & 15) == 0) scales[(lane >> 4) * BS] = scale;
