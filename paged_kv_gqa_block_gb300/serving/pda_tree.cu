@@ -19,6 +19,10 @@
 
 namespace pda {
 
+// CTAs per SM of the join: its rows wait for their loads.  With eight pieces at a time in place of four (and three CTAs) 32 sequences of up
+// to 33 drafted tokens took 140 us and not 130; six CTAs spill.
+constexpr int kJoinCtas = 4;
+
 struct TreeJoinArgs {
     const int* refused;
     const float* part_o;   // [N][Hk][slots][QG][D]
@@ -33,7 +37,7 @@ struct TreeJoinArgs {
 // One warp per row of more than one piece; the rows of a warp lie as far apart as there are warps, and their numbers of pieces
 // are read 32 at a time, so that rows of one piece, which are whole already, cost next to nothing.  Lane i holds (m, l) of
 // pieces i, i + 32, ..; each lane sums four dimensions over the pieces in order.
-__global__ void __launch_bounds__(256) pda_tree_join_kernel(const TreeJoinArgs a) {
+__global__ void __launch_bounds__(256, kJoinCtas) pda_tree_join_kernel(const TreeJoinArgs a) {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * 8, first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -58,6 +62,13 @@ __global__ void __launch_bounds__(256) pda_tree_join_kernel(const TreeJoinArgs a
                     if (l == 0.f) m = -INFINITY;   // a piece of which the row sees nothing
                 }
             };
+            float4 o[4];   // four pieces at a time, the first asked for with the statistics
+            auto ask = [&](int i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row0 + (long long)min(i + j, total - 1) * a.QG) * kHeadDim) + lane);
+            };
+            ask(0);
             float m0, l0;
             stats(lane, m0, l0);
             float M = m0;
@@ -72,18 +83,14 @@ __global__ void __launch_bounds__(256) pda_tree_join_kernel(const TreeJoinArgs a
             float sum = 0.f;
             for (int i0 = 0; i0 < total; i0 += 32) {
                 if (i0 > 0) stats(i0 + lane, m0, l0);
-                const float w = l0 != 0.f ? partition_weight(l0, m0, M) : 0.f;
+                const float w = l0 != 0.f ? partition_weight(l0, m0, M) : 0.f;   // 0 past the last piece
                 sum += w;
-                const int n = min(32, total - i0);
-                for (int j0 = 0; j0 < n; j0 += 8) {
-                    float4 o[8];
+                for (int j0 = i0; j0 < min(total, i0 + 32); j0 += 4) {
+                    if (j0 > 0) ask(j0);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row0 + (long long)(i0 + min(j0 + j, n - 1)) * a.QG) * kHeadDim) + lane);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const float f = __shfl_sync(kLanes, w, (j0 + j) & 31);
-                        if (j0 + j < n) {
+                        if (j0 + j < total) {
                             acc.x = fmaf(f, o[j].x, acc.x);
                             acc.y = fmaf(f, o[j].y, acc.y);
                             acc.z = fmaf(f, o[j].z, acc.z);
@@ -244,7 +251,7 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
     j.out_f32 = a.out_f32;
     const long long join = (j.rows + 7) / 8;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(join < 4ll * sms ? join : 4ll * sms));
+    cfg.gridDim = dim3((unsigned)(join < (long long)kJoinCtas * sms ? join : (long long)kJoinCtas * sms));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
