@@ -127,6 +127,14 @@ def test_peaked_weights(pda, kv):
     TreeCase(kv, 2, 8, 16, [900, 60], [12, 3], "tree", seed=8, q_scale=8.0, v_spread=2.0).check(pda)
 
 
+@pytest.mark.parametrize("kv", KVS)
+def test_peaked_weights_in_units_of_every_size(pda, kv):
+    """References that move, in the first and the second half of a step, in rows held twice (up to 64), in one tile and in two."""
+    lens, counts = [900, 60, 1300, 700, 1024, 411, 1500, 640], [12, 8, 16, 17, 1, 33, 9, 40]
+    TreeCase(kv, 4, 8, 16, lens, counts, "tree", seed=13, q_scale=8.0, v_spread=2.0).check(pda)
+    TreeCase(kv, 4, 8, 32, lens, counts, "anything", 500, 4, seed=14, q_scale=8.0, v_spread=2.0).check(pda)
+
+
 def test_one_token_is_the_plain_step(pda):
     """Chains of one token over n cached ones are a plain step over n + 1."""
     for kv in KVS:
@@ -281,3 +289,33 @@ def test_a_round_of_speculative_decoding(pda, kv, window, first):
         for pool, o in zip((cache, plain), back):
             pda.read_kv(p, pool, NB, table, i32(starts), i32([0, 0, 0]), *o, centroids=book)
         assert torch.equal(back[0][0], back[1][0]) and torch.equal(back[0][1], back[1][1])
+
+
+def test_pinned_query_and_out(pda):
+    for kv in KVS:
+        t = TreeCase(kv, 2, 8, 16, [300, 40, 0], [5, 33, 9], "tree", seed=15)
+        for dtype in (torch.float32, torch.bfloat16):
+            d = t.device()
+            want, err = t.run(pda, d, dtype)
+            assert err == 0
+            d["query"] = d["query"].cpu().pin_memory()
+            out = torch.full(want.shape, 7.0, dtype=dtype).pin_memory()
+            pda.decode_tree(t.plan(pda), **d, out=out)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want.cpu())
+
+
+def test_two_calls_at_once(pda):
+    """On two streams, each with a workspace of its own."""
+    cases = [TreeCase(kv, 8, 8, 16, [2000] * 20, [4, 33] * 10, "tree", seed=16 + kv) for kv in (BF16, FP8)]
+    ds, plans = [t.device() for t in cases], [t.plan(pda) for t in cases]
+    want = [t.run(pda, d)[0] for t, d in zip(cases, ds)]
+    wss = [pda.tree_workspace(p, t.N, "cuda") for p, t in zip(plans, cases)]
+    outs = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, d, ws, out, s in zip(plans, ds, wss, outs, streams):
+            pda.decode_tree(p, **d, ws=ws, out=out, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
