@@ -202,12 +202,31 @@ struct Prefix {
     const uint32_t bars;
     unsigned units = 0;        // units taken (or given) by this warp
     unsigned busy = 0;         // their steps
+    const bool poll;           // TREE: a short limit; and the limit in 1024 ns, half an hour at most
+    const uint32_t patience;
 
     __device__ __forceinline__ Prefix(const Args& args, uint32_t base)
-        : a(args), sm(base), bars(base + Cfg::kOffBars) {}
+        : a(args), sm(base), bars(base + Cfg::kOffBars), poll(args.timeout_ns < 1000000ull),
+          patience((uint32_t)min(args.timeout_ns >> 10, 0x7FFFFFFFull)) {}
 
     // A whole warp waits (bounded).  False once any wait of the CTA has given up.
+    // TREE: in less code, since there is a wait in every other line (fp8 steps 2 to 4 % shorter): the first test does not sleep, and
+    // time is counted in 1024 ns and 32 bits.
+    __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, uint32_t limit) const {
+        if (__all_sync(kLanes, mbar_test_wait(bar, parity))) return true;
+        const uint32_t t0 = (uint32_t)(global_timer_ns() >> 10);
+        for (;;) {
+            const bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+            if (__all_sync(kLanes, ok)) return true;
+            const bool late = (uint32_t)(global_timer_ns() >> 10) - t0 > limit;
+            if (__any_sync(kLanes, late || lds32v(bars + kAbortAt) != 0u)) {
+                sts32v(bars + kAbortAt, 1u);
+                return false;
+            }
+        }
+    }
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        if constexpr (TREE) return wait_short(bar, parity, patience);
         const bool poll = a.timeout_ns < 1000000ull;   // try_wait may sleep past a short limit
         bool ok = poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
         if (__all_sync(kLanes, ok)) return true;
@@ -231,6 +250,8 @@ struct Prefix {
     // A unit, or its place, may come only when warps that are behind have finished one that was taken before: the
     // limit is that of their waits, a few per step (long limits, from 0.27 s on, do for any unit).
     __device__ __forceinline__ bool wait_unit(uint32_t bar, uint32_t parity) const {
+        if constexpr (TREE)
+            return wait_short(bar, parity, patience >> 18 ? patience : (uint32_t)min((patience + 1) * (64 + 8ull * busy), 0x7FFFFFFFull));
         const uint64_t limit = a.timeout_ns >> 28 ? a.timeout_ns : a.timeout_ns * (64 + 8ull * busy);
         const bool poll = a.timeout_ns < 1000000ull;
         if (__all_sync(kLanes, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) return true;
