@@ -277,6 +277,19 @@ struct Prefix {
             put(u);
         }
     }
+    // TREE: the same, with the first one looked up here too.
+    __device__ void give_all(const Split& split, int at, int end) {
+        for (;;) {
+            const Unit u = find_unit(a, split, at, end);
+            if (units > 1 && !wait_unit(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
+            put(u);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitFull + 8 * (units & 1));
+            ++units;
+            if (u.steps == 0) return;
+            busy += u.steps;
+        }
+    }
     __device__ __forceinline__ bool next(Unit& u) {
         const uint32_t slot = units & 1, at = bars + kUnitAt + slot * 48;
         if (!wait_unit(bars + kBarUnitFull + 8 * slot, units >> 1 & 1)) return false;
@@ -1716,26 +1729,24 @@ struct Prefix {
         }
 #pragma unroll 1
         for (int half = part ? k0 : 0; half < (part ? k0 + 1 : 2); ++half) {
-            uint32_t s[2][32];
-            tmem_ld32(s[0], tO + 64 * half);
-            tmem_ld32(s[1], tO + 64 * half + 32);
-            tmem_wait_ld();
-            __syncwarp();
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {   // 32 columns
+                uint32_t s[32];
+                tmem_ld32(s, tO + 64 * half + 32 * q);
+                tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = __float_as_uint(__uint_as_float(s[i >> 5][i & 31]) * f0);
-            if (part) {
+                for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f0);
+                if (part) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    uint32_t v[4], *x = &s[c >> 3][(c & 7) * 4];
-                    lds128(place(tile, from + lane, c), v[0], v[1], v[2], v[3]);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t v[4];
+                        lds128(place(tile, from + lane, 8 * q + c), v[0], v[1], v[2], v[3]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), f1, __uint_as_float(x[i])));
+                        for (int i = 0; i < 4; ++i) s[4 * c + i] = __float_as_uint(fmaf(__uint_as_float(v[i]), f1, __uint_as_float(s[4 * c + i])));
+                    }
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t* x = &s[c >> 3][(c & 7) * 4];
-                sts128(place(tile, from + lane, c), x[0], x[1], x[2], x[3]);
+                for (int c = 0; c < 8; ++c) sts128(place(tile, from + lane, 8 * q + c), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
             }
             __syncwarp();
             if (bf16) {
@@ -1853,8 +1864,10 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             if (blockIdx.x == 0 && (threadIdx.x & 31) == 0) *a.refused = split.refused;
         at = (int)min((long long)blockIdx.x * split.per, (long long)split.total);
         end = at + min(split.per, split.total - at);
-        first = find_unit(a, split, at, end);
-        p.put(first);
+        if constexpr (!Cfg::kTree) {
+            first = find_unit(a, split, at, end);
+            p.put(first);
+        }
     }
     if constexpr (Cfg::kTq) {
         if (warp == 12) p.make_table();
@@ -1897,7 +1910,10 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             else if (warp == 9)
                 p.products(tmem);
             else if (warp == 11) {
-                p.give(split, first, at, end);
+                if constexpr (Cfg::kTree)
+                    p.give_all(split, at, end);
+                else
+                    p.give(split, first, at, end);
                 if constexpr (Cfg::kTree)
                     if (!split.refused) p.settle();
             }
