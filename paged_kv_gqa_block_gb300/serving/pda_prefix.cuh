@@ -191,6 +191,7 @@ __device__ __forceinline__ void add2(float2& x, const float2& y) {
 template <int KV, class Args>
 struct Prefix {
     using Cfg = SharedCfg<KV, Args>;
+    using Split = SplitBy<Args::kSwitchSteps>;
     static constexpr bool F16 = Cfg::kF16, TQ = Cfg::kTq, TREE = Cfg::kTree, Q8 = Cfg::kQ8;
     static constexpr uint32_t kScFull = Q8 ? kBarScFull8 : kBarScFull, kScEmpty = Q8 ? kBarScEmpty8 : kBarScEmpty,
                               kScRaw = Q8 ? kBarScRaw8 : kBarScRaw;
@@ -1855,7 +1856,7 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
     // that an earlier grid left in this SM's L1 is not looked at.
     if (a.first) grid_dependency_wait();
     Prefix<KV, Args> p(a, sm);
-    Split split;
+    SplitBy<Args::kSwitchSteps> split;
     Unit first;
     int at, end;
     if (warp == 11) {

@@ -12,7 +12,7 @@ namespace pda {
 constexpr uint32_t kLanes = 0xFFFFFFFFu;
 constexpr int kStep = 128;                 // tokens per step
 constexpr int kUnitRows = 256;             // query rows of a row tile
-constexpr int kSwitch = 3;                 // what a change of row tiles costs a CTA, in steps
+constexpr int kSwitch = 3;                 // what a change of row tiles costs a CTA, in steps: of prefixes
 
 struct SharedArgs {
     const uint16_t* query;       // bf16 [B][Hk*QG][D]
@@ -30,6 +30,7 @@ struct SharedArgs {
     float qk_scale_log2;
     unsigned long long timeout_ns;
     static constexpr int kBadStarts = PDA_ERRW_BAD_GROUP;
+    static constexpr int kSwitchSteps = kSwitch, kUncut = 0;
 };
 
 // pda_decode_tree: a group is a sequence, its rows are those of its drafted tokens, and its tokens are the cached ones and,
@@ -46,6 +47,10 @@ struct TreeArgs : SharedArgs {
     void* out;                   // [B][Hk*QG][D]
     int out_f32;
     static constexpr int kBadStarts = PDA_ERRW_BAD_TOKENS;
+    // 64 sequences of up to 6 tokens in a window of 4096 fp8 tokens 101 -> 97 us with 4 in place of 3 for a change of row tiles, of 4
+    // over 1000 79 -> 76 (5: 75, but 16 over 4096 48 -> 53); 16 of 32 tokens over 4096 bf16 tokens 82 -> 64 us with runs of their own
+    // where those end up to 3 steps later, and fp8 96 -> 86 (6: the same).
+    static constexpr int kSwitchSteps = 4, kUncut = 3;
 };
 
 // What a sequence's drafted tokens see of it: every one of them misses tokens hole0 .. hole1-1, and the steps at, ..,
@@ -130,25 +135,27 @@ __device__ __forceinline__ int quotient(int x, int d) { return (int)((unsigned)x
 
 // How one warp sees the split: lane i holds group i (and re-reads the others where there are more
 // than 32).  The host has made sure that the places of all steps of ascending groups fit an int.
-struct Split {
+template <int SWITCH>
+struct SplitBy {
     Group mine;
     int before, total;     // places of the groups before lane i's (of the first 32), and of all
     int per;               // places of a CTA's run
     int whole;             // if not 0: places of every row tile
     bool refused;          // starts that do not ascend: there are no steps
     // Places of a row tile: its steps, and unused ones after them.  A CTA whose run goes on into another row tile
-    // pays for it (store the rows, load others, refill the pipeline: kSwitch steps); either that is counted
+    // pays for it (store the rows, load others, refill the pipeline: SWITCH steps); either that is counted
     // as places between two tiles, or every tile has whole runs of its own.
-    __device__ __forceinline__ int span(int steps) const { return steps == 0 ? 0 : whole ? whole : steps + kSwitch; }
+    __device__ __forceinline__ int span(int steps) const { return steps == 0 ? 0 : whole ? whole : steps + SWITCH; }
 };
+using Split = SplitBy<kSwitch>;
 
 // `per`: an even share of all places, or, where that is no longer, the longest tile's share of the runs that every
 // tile can have; and at least 1/P of the longest prefix, so that a row tile is cut into at most P + 1 pieces
 // (the workspace's slots).
 template <class Args>
-__device__ __forceinline__ Split make_split(const Args& a, int ctas, bool report) {
+__device__ __forceinline__ SplitBy<Args::kSwitchSteps> make_split(const Args& a, int ctas, bool report) {
     const int lane = threadIdx.x & 31;
-    Split s;
+    SplitBy<Args::kSwitchSteps> s;
     int bad = 0;
     s.mine = group_shape(a, lane, bad);
     int tiles = s.mine.steps > 0 ? s.mine.tiles * a.Hk : 0, steps = tiles * s.mine.steps;
@@ -164,13 +171,15 @@ __device__ __forceinline__ Split make_split(const Args& a, int ctas, bool report
     tiles = __reduce_add_sync(kLanes, tiles);
     steps = __reduce_add_sync(kLanes, steps);
     longest = __reduce_max_sync(kLanes, longest);
-    const int q = quotient(lane == 0 ? longest + a.P - 1 : lane == 1 ? steps + kSwitch * tiles + ctas - 1 : ctas,
+    const int q = quotient(lane == 0 ? longest + a.P - 1 : lane == 1 ? steps + Args::kSwitchSteps * tiles + ctas - 1 : ctas,
                            lane == 0 ? a.P : lane == 1 ? ctas : max(tiles, 1));
     const int least = max(__shfl_sync(kLanes, q, 0), 1), even = max(__shfl_sync(kLanes, q, 1), least);
     const int runs = __shfl_sync(kLanes, q, 2);
     const int own = runs > 0 ? max(quotient(longest + runs - 1, runs), least) : even + 1;
-    s.per = min(own, even);
-    s.whole = own <= even ? quotient(longest + own - 1, own) * own : 0;   // the first CTAs work: they start first
+    // Runs of their own also where they end up to Args::kUncut steps later: what is not cut needs no partials and no join.
+    const bool whole = own <= even || (runs > 0 && own <= even + Args::kUncut);
+    s.per = whole ? own : even;
+    s.whole = whole ? quotient(longest + own - 1, own) * own : 0;   // the first CTAs work: they start first
     const int mine = s.mine.tiles * a.Hk * s.span(s.mine.steps);
     int incl = mine;
 #pragma unroll
@@ -199,7 +208,7 @@ __device__ __forceinline__ Split make_split(const Args& a, int ctas, bool report
 // One warp: the piece that starts at place `at` of the run of all places, or after the unused ones there, and ends
 // with its row tile or at `end`; `at` moves past it.  Without steps: there is none.
 template <class Args>
-__device__ __forceinline__ Unit find_unit(const Args& a, const Split& s, int& at, int end) {
+__device__ __forceinline__ Unit find_unit(const Args& a, const SplitBy<Args::kSwitchSteps>& s, int& at, int end) {
     const int lane = threadIdx.x & 31;
     Unit u = {};
 #pragma unroll 1

@@ -143,7 +143,7 @@ static int tree_pieces(const pda_plan_t* p, long long tokens) {
 }
 static bool tree_fits(const pda_plan_t* p, long long tokens) {
     return tokens >= 0 && tokens * p->query_group_size <= 1ll << 30 &&
-           most_tree_tiles(p, tokens) * (steps_of(p) + kSwitch) <= 2000000000ll;   // places are ints
+           most_tree_tiles(p, tokens) * (steps_of(p) + TreeArgs::kSwitchSteps) <= 2000000000ll;   // places are ints
 }
 struct TreeLayout {
     long long o, l, m, pieces, refused, bytes;

@@ -23,7 +23,7 @@ int tree_pieces_of(int NG, const int* starts, const int* lens, int tokens, int Q
     for (int cta = 0; cta < ctas && n >= 0; ++cta)
         host_warp::run([&] {
             const bool lead = threadIdx.x == 0;
-            const pda::Split split = pda::make_split(a, ctas, cta == 0);
+            const auto split = pda::make_split(a, ctas, cta == 0);
             int at = (int)std::min((long long)cta * split.per, (long long)split.total);
             const int end = at + std::min(split.per, split.total - at);
             if (lead) scalars[1] = split.per, scalars[2] = split.total, scalars[3] = split.whole, scalars[4] = split.refused;
