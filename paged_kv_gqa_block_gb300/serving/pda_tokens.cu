@@ -12,9 +12,9 @@
 //
 // A warp takes up to four KV heads of one token at a time, whose loads are asked for together: addresses are computed once per token
 // (a search of token_starts and the block table's entry, by one thread), and a whole row leaves in one or two store instructions.
-// Measured, 131072 tokens of 8 heads: written in bf16 162 us (6.6 TB/s: HBM), fp8 184 us (4.4 TB/s), TQ4 298 us (2.3 TB/s: 276
+// Measured, 131072 tokens of 8 heads: written in bf16 162 us (6.6 TB/s: HBM), fp8 169 us (4.8 TB/s), TQ4 298 us (2.3 TB/s: 276
 // instructions per row, 71 % of the issue slots used); read back from bf16 165 us, fp8 128 us (6.3 TB/s), TQ4 139 us (4.9 TB/s).
-// 16 prompts of up to 2048 tokens into fp8 26 us, 16 contexts of up to 8192 fp8 tokens back 45 us (5.6 TB/s), up to six tokens of
+// 16 prompts of up to 2048 tokens into fp8 22 us, 16 contexts of up to 8192 fp8 tokens back 45 us (5.6 TB/s), up to six tokens of
 // 8 sequences 2.9 us.
 #include <cuda_runtime.h>
 
@@ -165,20 +165,11 @@ __device__ __forceinline__ float f16_saturated(float x) {
     return __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
 }
 
-__device__ __forceinline__ uint32_t cut_f16(float x, float y) {   // towards zero
-    uint32_t r;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-    return r;
-}
-
-// fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.  Bound by instructions (HBM would take half of the time):
-// a division and the conversion to e4m3 per value are the larger part of them, so both are done only where they decide.  A value
-// times 2^-8 has e4m3's exponent field in f16's bits 13 .. 10 and its mantissa behind it; f16 cut towards zero, plus half of
-// e4m3's last place, cut again, is the code of every value that is no tie.  The correctly rounded quotient lies between x times
-// 1 / scale a little too small and a little too large (2^-21 either way: the approximate inverse is off by 2^-23, four products
-// and the quotient's own rounding by 2^-24 each), and where both have one code that is the quotient's.  Else, in one row of
-// four (bf16 values have few mantissas, so their quotients meet e4m3's ties often), the lane's quotients are computed; in rows that are
-// tiny or hold infinities or NaN every value is divided.
+// fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.  Bound by instructions (HBM would take two thirds of the time),
+// so a value is divided by its row's inverse and two exact remainders, five instructions: a quotient whose remainder underflows is far
+// below e4m3's smallest.  (Codes from products a little too small and a little too large, and quotients only where the two differ, were
+// slower: bf16 values have few mantissas, their quotients meet e4m3's ties often, and a row of four was left open; 16 prompts of up to 2048
+// tokens 26 us and not 22.)  Rows that are tiny or hold infinities or NaN are divided.
 __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     // magnitudes of bf16 values are ordered like their bits
@@ -188,36 +179,25 @@ __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
     const float most = __uint_as_float((uint32_t)top << 16);
     float scale = top > 0 ? quotient(most, 448.f, 1.f / 448.f) : 1.f;   // of a normal number that counts
-    const float r = rcp_approx(scale) * 0.00390625f, lo = r * (1.f - 4.76837158e-7f), hi = r * (1.f + 4.76837158e-7f);
-    uint32_t c[4], differ = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x = bf16_lo(w[i]), y = bf16_hi(w[i]);
-        c[i] = cut_f16(x * lo, y * lo) + 0x00400040u;
-        differ |= c[i] ^ (cut_f16(x * hi, y * hi) + 0x00400040u);
-    }
-    // the upper byte of each value shifted by one: exponent and mantissa; the signs are those of the bf16 values
-    uint32_t a = (__byte_perm(c[0] << 1, c[1] << 1, 0x7531) & 0x7F7F7F7Fu) | (__byte_perm(w[0], w[1], 0x7531) & 0x80808080u);
-    uint32_t b = (__byte_perm(c[2] << 1, c[3] << 1, 0x7531) & 0x7F7F7F7Fu) | (__byte_perm(w[2], w[3], 0x7531) & 0x80808080u);
+    uint32_t a, b;
     const bool odd = !(most > 1e-25f && top < 0x7F80);   // the same in the half warp
-    if ((differ & 0xFF80FF80u) || odd) {
-        if (odd) {   // pda_append_kv's maximum and division; fmaxf passes NaN by
-            const uint32_t mine = 0xFFFFu << (lane & 16);
-            float m = 0.f;
+    if (odd) {   // pda_append_kv's maximum and division; fmaxf passes NaN by
+        const uint32_t mine = 0xFFFFu << (lane & 16);
+        float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mine, m, o));
-            scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
-            auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(v), scale), __fdiv_rn(bf16_hi(v), scale)); };
-            a = code(w[0]) | code(w[1]) << 16;
-            b = code(w[2]) | code(w[3]) << 16;
-        } else {   // a quotient whose remainder underflows is far below e4m3's smallest
-            const float by = __frcp_rn(scale);
-            auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(quotient(bf16_lo(v), scale, by), quotient(bf16_hi(v), scale, by)); };
-            a = code(w[0]) | code(w[1]) << 16;
-            b = code(w[2]) | code(w[3]) << 16;
-        }
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mine, m, o));
+        scale = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+        auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(__fdiv_rn(bf16_lo(v), scale), __fdiv_rn(bf16_hi(v), scale)); };
+        a = code(w[0]) | code(w[1]) << 16;
+        b = code(w[2]) | code(w[3]) << 16;
+    } else {
+        const float by = __frcp_rn(scale);
+        auto code = [&](uint32_t v) { return f32x2_to_e4m3x2(quotient(bf16_lo(v), scale, by), quotient(bf16_hi(v), scale, by)); };
+        // the sign of a zero does not outlive its remainder, so signs are those of the values
+        a = code(w[0]) | code(w[1]) << 16 | (__byte_perm(w[0], w[1], 0x7531) & 0x80808080u);
+        b = code(w[2]) | code(w[3]) << 16 | (__byte_perm(w[2], w[3], 0x7531) & 0x80808080u);
     }
     *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(a, b);
     if ((lane & 15) == 0) scales[(lane >> 4) * BS] = scale;

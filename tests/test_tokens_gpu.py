@@ -427,3 +427,20 @@ def test_every_quotient_of_e4m3(pda):
     pda.append_kv(p, bf16(c.bits[0]), bf16(c.bits[1]), one, c.NB, table, i32(np.arange(n)))
     torch.cuda.synchronize()
     assert torch.equal(one, many)
+
+
+def test_zeros_keep_their_sign(pda):
+    """Zeros of either sign, and values whose code is a zero, among ordinary ones: the bytes of the single-token call."""
+    c = setup(pda, FP8, 8, 16, [3, 0], [40, 21], seed=2)
+    kind = c.rng.integers(0, 6, c.bits.shape)
+    for k, v in ((0, 0x8000), (1, 0x0000), (2, 0x8001), (3, 0xA000)):     # the last: -2^-63
+        c.bits[kind == k] = v
+    one, many = (torch.from_numpy(c.cache).cuda() for _ in range(2))
+    assert write(pda, c, many) == 0
+    n = int(c.starts[-1])
+    p = pda.plan(n, 8, 8, 16, c.MB, kv_dtype=FP8)
+    owner = np.repeat([0, 1], [40, 21])
+    pos = np.concatenate([3 + np.arange(40), np.arange(21)])
+    pda.append_kv(p, bf16(c.bits[0]), bf16(c.bits[1]), one, c.NB, i32(c.table[owner]), i32(pos))
+    torch.cuda.synchronize()
+    assert torch.equal(one, many)
