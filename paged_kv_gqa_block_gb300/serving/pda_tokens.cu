@@ -12,10 +12,10 @@
 //
 // A warp takes up to four KV heads of one token at a time, whose loads are asked for together: addresses are computed once per token
 // (a search of token_starts and the block table's entry, by one thread), and a whole row leaves in one or two store instructions.
-// Measured, 131072 tokens of 8 heads: written in bf16 162 us (6.6 TB/s: HBM), fp8 169 us (4.8 TB/s), TQ4 298 us (2.3 TB/s: 276
-// instructions per row, 71 % of the issue slots used); read back from bf16 165 us, fp8 128 us (6.3 TB/s), TQ4 139 us (4.9 TB/s).
-// 16 prompts of up to 2048 tokens into fp8 22 us, 16 contexts of up to 8192 fp8 tokens back 45 us (5.6 TB/s), up to six tokens of
-// 8 sequences 2.9 us.
+// Measured, 131072 tokens of 8 heads: written in bf16 160 us (6.7 TB/s: HBM), fp8 164 us (5.0 TB/s), TQ4 288 us (2.4 TB/s: 276
+// instructions per row, 71 % of the issue slots used); read back from bf16 159 us, fp8 124 us (6.6 TB/s), TQ4 138 us (4.9 TB/s).
+// 16 prompts of up to 2048 tokens into fp8 22 us, 16 contexts of up to 8192 fp8 tokens back 42 us (6.1 TB/s), up to six tokens of
+// 8 sequences 2.8 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,7 +29,7 @@ namespace pda {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kTokThreads = 256;
 constexpr int kTokWarps = kTokThreads / 32;
-constexpr int kMaxTokensPerCta = 64;
+constexpr int kMaxTokensPerCta = 32, kManyReads = 16;
 constexpr int kHeadsAhead = 4;            // KV heads of one token that a warp takes together, at most, loads first
 
 struct TokenArgs {
@@ -104,7 +104,7 @@ __device__ __forceinline__ bool find_places(const TokenArgs& a, Places& at, int 
 }
 
 // What a warp takes at a time: up to kHeadsAhead KV heads of one token.  Their rows lie a fixed number of bytes apart, so that one
-// address serves all; item x of a CTA is group x % groups of its token x / groups (x < 64 groups, and groups <= 4096 where a CTA has
+// address serves all; item x of a CTA is group x % groups of its token x / groups (x < 32 groups, and groups <= 4096 where a CTA has
 // more than one token, so the rounded-up inverse is exact).
 struct Item {
     int t, h, n;   // token of the CTA, first KV head, KV heads
@@ -501,7 +501,7 @@ static bool bad_pool(long long nb) { return nb < 1 || nb > (1ll << 31) - 1; }
 // What both directions check and fill in.  A status other than OK ends the call; *nothing: there is no token to move.
 static int token_args(const pda_plan_t* plan, const void* kv_cache, long long num_cache_blocks, const float* centroids,
                       const int* block_table, const int* token_starts, const int* positions, long long num_tokens,
-                      int* err_word, TokenArgs& a, unsigned& grid) {
+                      int* err_word, bool reading, TokenArgs& a, unsigned& grid) {
     if (!plan || pda_workspace_size(plan) < 0) return PDA_ERR_INVALID_ARG;
     if ((plan->kv_dtype == PDA_KV_TQ4) != (centroids != nullptr)) return PDA_ERR_INVALID_ARG;
     if (num_tokens < 0 || num_tokens > (1ll << 31) - 1 - kMaxTokensPerCta || bad_pool(num_cache_blocks)) return PDA_ERR_INVALID_ARG;
@@ -529,7 +529,10 @@ static int token_args(const pda_plan_t* plan, const void* kv_cache, long long nu
     // is one wave, in whole rounds of a CTA's warps.
     a.ahead = num_tokens * a.Hk <= 4 * 152 * kTokWarps ? 1 : kHeadsAhead;
     a.groups = (a.Hk + a.ahead - 1) / a.ahead;
-    const long long even = (num_tokens + 4 * 152 - 1) / (4 * 152), most = a.groups > 4096 ? 1 : kMaxTokensPerCta;
+    // More than one wave: 32 tokens per CTA (64 left the last wave uneven: 60000 fp8 tokens of 8 heads back 70 -> 62 us, into TQ4 157 -> 145;
+    // 24 and 16 are slower in writes of one wave), and 16 in reads, whose CTAs are twice as many per SM (62 -> 60 us).
+    const long long even = (num_tokens + 4 * 152 - 1) / (4 * 152);
+    const long long most = a.groups > 4096 ? 1 : reading && even > kMaxTokensPerCta ? kManyReads : kMaxTokensPerCta;
     const long long step = a.groups % 8 == 0 ? 1 : a.groups % 4 == 0 ? 2 : a.groups % 2 == 0 ? 4 : 8;   // tokens of whole rounds
     const long long round = a.ahead == 1 ? even : (even + step - 1) / step * step;
     a.per_cta = (int)(round > most ? most : round);
@@ -550,7 +553,7 @@ int pda_write_kv(const pda_plan_t* plan, const void* k_new, const void* v_new, l
     TokenArgs a = {};
     unsigned grid;
     const int rc = token_args(plan, kv_cache, num_cache_blocks, centroids, block_table, token_starts, positions, num_tokens,
-                              err_word, a, grid);
+                              err_word, false, a, grid);
     if (rc != PDA_OK) return rc;
     const long long row = (long long)plan->num_kv_heads * kHeadDim;
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return PDA_ERR_INVALID_ARG;
@@ -577,7 +580,7 @@ int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long num_cach
     TokenArgs a = {};
     unsigned grid;
     const int rc = token_args(plan, kv_cache, num_cache_blocks, centroids, block_table, token_starts, positions, num_tokens,
-                              err_word, a, grid);
+                              err_word, true, a, grid);
     if (rc != PDA_OK || grid == 0) return rc;
     if ((!k_out && !v_out) || off(k_out, 16) || off(v_out, 16)) return PDA_ERR_INVALID_ARG;
     a.k_out = k_out;

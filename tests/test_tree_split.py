@@ -123,3 +123,13 @@ def test_window_tiles(lib):
                     got += range(a, a + k)
                 assert got == [t for t in range(ctx) if t < first or ctx - 1 - t < window]
                 assert n <= -(-min(first, ctx) // 16) + -(-(min(window, ctx) + 15) // 16)
+
+
+def test_row_tiles_stay_whole_where_that_costs_little(lib):
+    """128 row tiles of 33 steps on 152 CTAs: cut evenly they would end two steps earlier, and every one would be in pieces."""
+    starts, lens = np.arange(17) * 32, [4096] * 16
+    check(lib, starts, lens, 8, 8, 260, 16, 40, 0, 0, 152)
+    units, (_, per, total, whole, _) = pieces(lib, starts, lens, 8, 8, 260, 16, 40, 0, 0, 152)
+    assert len(units) == 128 and whole == per == 33 and all(u["pieces"] == 1 and u["steps"] == 33 for u in units)
+    units, (_, per, _, whole, _) = pieces(lib, starts, [12288] * 16, 8, 8, 1000, 16, 40, 0, 0, 152)   # here 15 steps earlier
+    assert not whole and per < 97 and max(u["pieces"] for u in units) > 1
