@@ -873,7 +873,7 @@ struct Prefix {
     // softmax of a step finds its S there already.
     // Q8: S = Qhi K^T + Qlo K^T, e4m3 each, and V comes in halves.
     // Measured, sequences with 4 drafted tokens of 8 heads and 8 query rows each: 64 of 4096 bf16 tokens 194 -> 176 us (6.1 TB/s), of
-    // 1000 66 -> 59; 64 of 4096 fp8 tokens 217 -> 202, and with the halves (see there) 171.
+    // 1000 66 -> 59; 64 of 4096 fp8 tokens 217 -> 202, and with the halves (see there) 166.
     __device__ __forceinline__ void products_tree(uint32_t tmem_base) {
         const int lane = threadIdx.x & 31;
         const uint32_t leader = elect_one(), tmem = uniform(tmem_base), smu = uniform(sm), bar = uniform(bars);

@@ -10,11 +10,11 @@
 // 256 rows and not once per drafted token: pda_prefix.cuh, where a sequence takes the place of a group.  Its pieces are joined
 // here.
 //
-// Measured, calls from a graph: 4 trees of 64 tokens over 32768 bf16 tokens 194 us (1.42 PFLOP/s: the tensor cores); 32 trees of up
-// to 33 over contexts of up to 8192 129 us (rows of the second row tile read K and V again: 484 MB of 352; the join 15); 64 trees of
-// up to 6 in a window of 4096 fp8 tokens 107 us (1.9 TB/s: 1.1 us per step and CTA, and 5 us where a CTA goes on to the next
-// sequence and head, most of it the first fetch of the code); 64 of 4 over 4096 bf16 tokens 174 us (6.2 TB/s: HBM), fp8 165 us, TQ4
-// 253 us (its conversion); one of 4 over 250 10.2 us (latency of two launches).
+// Measured, calls from a graph: 4 trees of 64 tokens over 32768 bf16 tokens 192 us (1.43 PFLOP/s: the tensor cores); 32 trees of 9 to
+// 33 over contexts of 2048 to 8192 128 us (sequences of more than 256 rows have further row tiles, which read K and V again: 487 MB of
+// 352; the join 12); 64 trees of up to 6 in a window of 4096 fp8 tokens 98 us (2.0 TB/s: 1.1 to 1.3 us per step and CTA, and some 5 us
+// where a CTA goes on to the next sequence and head, most of it the first fetch of the code); 64 of 4 over 4096 bf16 tokens 174 us (6.2
+// TB/s: HBM), fp8 155 us, TQ4 250 us (its conversion); one of 4 over 250 10.1 us (latency of two launches).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
