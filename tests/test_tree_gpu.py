@@ -319,3 +319,20 @@ def test_two_calls_at_once(pda):
             pda.decode_tree(p, **d, ws=ws, out=out, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("kv", KVS)
+def test_pools_past_4_gb(pda, kv):
+    """Block offsets past 32 bits: the same blocks at a large pool's end."""
+    t = TreeCase(kv, 8, 8, 32, [300, 40, 0], [5, 33, 9], "tree", seed=17)
+    d, p = t.device(), t.plan(pda)
+    want, err = t.run(pda, d)
+    assert err == 0
+    size, n = p.cache_block_bytes, d["num_cache_blocks"]
+    far = 5 * 10 ** 9 // size
+    big = torch.empty((far + n) * size, dtype=torch.uint8, device="cuda")
+    big[far * size:] = d["kv_cache"].view(-1)[:n * size]
+    table = d["block_table"]
+    d.update(kv_cache=big, num_cache_blocks=far + n, block_table=torch.where(table >= 0, table + far, table))
+    out, err = t.run(pda, d)
+    assert err == 0 and torch.equal(out, want)
