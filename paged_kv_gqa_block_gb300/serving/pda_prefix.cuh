@@ -426,7 +426,8 @@ struct Prefix {
         // a ring for each; TQ4: one for both
         const bool keys = Q8 && v == 0;
         const uint32_t ring = !F16 ? (v ? Cfg::kValues : Cfg::kKeys) : keys ? Cfg::kKeys : Cfg::kRaw, at = !F16 && v ? Cfg::kKeys : 0;
-        const uint32_t full = bars + (F16 && !keys ? kBarRawFull : kBarFull) + 8 * at, empty = bars + (F16 && !keys ? kBarRawEmpty : kBarEmpty) + 8 * at;
+        const uint32_t full = bars + (F16 && !keys ? kBarRawFull : kBarFull) + 8 * at;
+        const uint32_t empty = bars + (F16 && !keys ? kBarRawEmpty : kBarEmpty) + 8 * at;
         const uint32_t base = sm + (keys ? Cfg::kOffKeys : F16 ? Cfg::kOffRaw : Cfg::kOffSlots) + at * kBytes;
         const int nblk = kStep / a.BS, blk = lane / kHalves, half = lane % kHalves;
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
@@ -473,7 +474,8 @@ struct Prefix {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {   // 16 bytes c of the step's 1024; a block's are BS * 8
                         const int c = lane + 32 * i, b = a.BS == 32 ? c >> 4 : c >> 3;
-                        const long long from = __shfl_sync(kLanes, id, b) * a.block_bytes + a.meta_bytes + (long long)u.h * a.BS * 8 + (c * 16 & (a.BS * 8 - 1));
+                        const long long from = __shfl_sync(kLanes, id, b) * a.block_bytes + a.meta_bytes +
+                                               (long long)u.h * a.BS * 8 + (c * 16 & (a.BS * 8 - 1));
                         const bool there = mask >> b & 1;
                         cp_async16(sm + Cfg::kOffScales + st * Cfg::kScaleBytes + 16 * c, there ? a.cache + from : a.cache, there ? 16u : 0u);
                     }
@@ -1283,7 +1285,8 @@ struct Prefix {
             }
         }
         if (w.on) {   // every product with the last unit's rows has ended: their S was read
-            if (!TREE || first_row(u, tile) + (r & (halves(u) ? 32 : 96)) < u.rows) w.c = load_q(u, tile);   // rows of nobody: whatever is there
+            // TREE: a warp whose rows are nobody's leaves what is there
+            if (!TREE || first_row(u, tile) + (r & (halves(u) ? 32 : 96)) < u.rows) w.c = load_q(u, tile);
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarQ + 8 * tile);
         }
@@ -1426,14 +1429,16 @@ struct Prefix {
 
     // The same for drafted tokens, whose rows do not see every token.  In few instructions: 64 tokens at a time in a rolled loop,
     // in place of a whole row in registers and straight code.  The reference may move before the second half too, whose weights
-    // then wait for the first half's product, since O counts from it.  The code of all roles of an SM has to fit its instruction cache: with the straight code 21 % of the fp8 kernel's
-    // requests missed it, and a step of few rows took 2.0 us, half of it without an instruction.
+    // then wait for the first half's product, since O counts from it.  The code of all roles of an SM has to fit its instruction
+    // cache: with the straight code 21 % of the fp8 kernel's requests missed it, and a step of few rows took 2.0 us, half of it
+    // without an instruction.
     __device__ __forceinline__ void softmax_tree(uint32_t tmem_base, int tile) {
         const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
         const uint32_t lanes = (uint32_t)(r & ~31) << 16;
         const uint32_t tO = tmem_base + 256 + tile * 128 + lanes;
         constexpr float below = F16 ? kBelow : 0.f;
-        unsigned own = 0, no = 0, np = 0, step = 0, turn = 0;   // this tile's steps, those of units of one tile, its units; steps and turns of both
+        unsigned own = 0, no = 0, np = 0;   // this tile's steps and units, and those of them with rows held twice
+        unsigned step = 0, turn = 0;        // steps and turns of both tiles
         uint32_t s_ph = 0;                              // a bit per place
         Unit u;
         while (next(u)) {
@@ -1762,7 +1767,8 @@ struct Prefix {
                     if (r >= rows) continue;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = pack_bf16(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * kHeadDim + 64 * half + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                    uint16_t* const p = static_cast<uint16_t*>(a.out) + dst * kHeadDim + 64 * half + 8 * c;
+                    *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
             } else {
                 const int c = lane & 15;

@@ -98,7 +98,8 @@ static int launch_clusters(bool behind, const DecodeArgs& a, const CUtensorMap& 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C, (int)behind, window, num_first, most) == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, kv_map, sc_map, a, shape.C, (int)behind, window, num_first, most);
+    return e == cudaSuccess ? PDA_OK : PDA_ERR_LAUNCH;
 }
 
 template <int LIST, int KV, int NT, int S, int NWMAX, int WPS>
@@ -158,10 +159,13 @@ int launch_window_clusters(int kv_dtype, const DecodeArgs& a, const CUtensorMap&
     auto of = [&](auto launch) { return launch(false, a, kv_map, sc_map, stream, window, num_first); };
     const bool narrow = a.QG <= 8;
     if (kv_dtype == PDA_KV_BF16)
-        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_BF16, 1, 3, 8, 8>) : of(launch_clusters_of<kListWindow, PDA_KV_BF16, 2, 3, 8, 8>);
+        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_BF16, 1, 3, 8, 8>)
+                      : of(launch_clusters_of<kListWindow, PDA_KV_BF16, 2, 3, 8, 8>);
     if (kv_dtype == PDA_KV_TQ4)
-        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 1, 6, 6, 12>) : of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 2, 6, 4, 8>);
-    return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 1, 3, 6, 12>) : of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 2, 4, 4, 8>);
+        return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 1, 6, 6, 12>)
+                      : of(launch_clusters_of<kListWindow, PDA_KV_TQ4, 2, 6, 4, 8>);
+    return narrow ? of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 1, 3, 6, 12>)
+                  : of(launch_clusters_of<kListWindow, PDA_KV_FP8_E4M3, 2, 4, 4, 8>);
 }
 
 }  // namespace pda
