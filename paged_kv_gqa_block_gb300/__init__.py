@@ -635,6 +635,14 @@ def decode_shared(prefix_plan: Plan, p: Plan, query, kv_cache, num_cache_blocks:
 # arrays are sequence b's.
 def _rows(c: _Call, t, name: str, p: Plan):
     """Pointer and row stride (elements) of bf16 [N][Hk][128] whose rows may lie apart."""
+    try:   # the common case first and short, as in _Call.ptr
+        n, heads, dims = t.shape
+        stride, between, step = t.stride()
+        if (t.get_device() == c.index and t.dtype in _BF16 and heads == p.num_kv_heads and dims == p.head_dim == between
+                and step == 1 and stride >= heads * dims and n > 1):
+            return t.data_ptr(), stride
+    except (AttributeError, ValueError):   # no tensor, or not of three dimensions
+        pass
     if not isinstance(t, torch.Tensor) or t.get_device() != c.index:
         raise ValueError(f"{name} must be on cuda:{c.index}")
     if t.dtype not in _BF16:
