@@ -738,10 +738,12 @@ def decode_tree(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, co
 def accept_tokens(p: Plan, kv_cache, num_cache_blocks: int, block_table, context_lens, path, path_lens, out_lens,
                   err_word=None, stream=None) -> None:
     """pda_accept_tokens: the accepted drafted tokens move to consecutive positions (see include/pda.h).
-    path: int32 [B][max_path], ascending; path_lens, out_lens: int32 [B]."""
+    path: int32 [B][max_path], ascending, rows past the B sequences' not looked at; path_lens, out_lens: int32 [B]."""
     c = _Call(kv_cache, "kv_cache")
     B = p.num_seqs
-    A = path.numel() // B if B else 0
+    if path.dim() != 2 or path.shape[0] < B:
+        raise ValueError("path must be [sequences][max_path]")
+    A = path.shape[1]
     args = (c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
             c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
             c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(path, "path", _I32, B * A * 4),
