@@ -659,6 +659,14 @@ def _rows(c: _Call, t, name: str, p: Plan):
     return t.data_ptr(), stride
 
 
+def _tokens(t, name: str, heads: int, dims: int) -> int:
+    """How many tokens of [heads][dims] a packed tensor holds: nothing else may be left, and rows of other heads are refused."""
+    n = t.numel() // (heads * dims)
+    if t.numel() != n * heads * dims or (t.dim() > 2 and t.shape[-1] != dims) or (t.dim() == 3 and t.shape[0] != n):
+        raise ValueError(f"{name} must be [tokens][{heads}][{dims}]")
+    return n
+
+
 def write_kv(p: Plan, k_new, v_new, kv_cache, num_cache_blocks: int, block_table, token_starts, positions, centroids=None,
              err_word=None, stream=None) -> None:
     """pda_write_kv: K and V of any number of new tokens per sequence, in the cache's format (see include/pda.h).
@@ -682,14 +690,14 @@ def read_kv(p: Plan, kv_cache, num_cache_blocks: int, block_table, token_starts,
     include/pda.h).  One of the two may be None."""
     c = _Call(kv_cache, "kv_cache")
     B, row = p.num_seqs, p.num_kv_heads * p.head_dim
-    given = [t for t in (k_out, v_out) if t is not None]
+    given = [(t, n) for t, n in ((k_out, "k_out"), (v_out, "v_out")) if t is not None]
     if not given:
         raise ValueError("k_out or v_out must be given")
-    dtype = given[0].dtype
+    dtype = given[0][0].dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"k_out and v_out have dtype {dtype}")
-    N = given[0].numel() // row
-    outs = tuple(c.opt(t, n, (dtype,), N * row * given[0].element_size()) for t, n in ((k_out, "k_out"), (v_out, "v_out")))
+    N = [_tokens(t, n, p.num_kv_heads, p.head_dim) for t, n in given][0]
+    outs = tuple(c.opt(t, n, (dtype,), N * row * dtype.itemsize) for t, n in ((k_out, "k_out"), (v_out, "v_out")))
     args = (c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
             c.opt(centroids, "centroids", _F32, 64), c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
             c.ptr(token_starts, "token_starts", _I32, (B + 1) * 4), c.ptr(positions, "positions", _I32, B * 4), N, *outs,
@@ -712,7 +720,7 @@ def decode_tree(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, co
     [N][Hk*QG][128], tree_masks: int64 [N][words]; returns out [N][Hk*QG][128]."""
     c = _Call(kv_cache, "kv_cache")
     B, rows, D = p.num_seqs, p.num_kv_heads * p.query_group_size, p.head_dim
-    N = query.numel() // (rows * D)
+    N = _tokens(query, "query", rows, D)
     words = 0
     if tree_masks is not None:
         if tree_masks.dim() != 2 or tree_masks.shape[0] < N or tree_masks.shape[1] < 1:

@@ -51,3 +51,44 @@ def test_paths_of_other_shapes_are_refused(calls, shape):
     with pytest.raises(ValueError, match="path"):
         pda.accept_tokens(p, pool(p), 40, i32(4, 8), i32(4), i32(*shape), i32(4), i32(4))
     assert not made
+
+
+def half(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("shape,tokens", [((7, 2, 128), 7), ((0, 2, 128), 0), ((7, 256), 7), ((7 * 256,), 7), ((1, 7, 2, 128), 7)])
+def test_read_kv_takes_whole_tokens(calls, shape, tokens):
+    pda, made = calls
+    p = pda.plan(3, 2, 8, 16, 8)
+    for outs in ((half(*shape), half(*shape)), (half(*shape), None), (None, half(*shape))):
+        pda.read_kv(p, pool(p), 40, i32(3, 8), i32(4), i32(3), *outs)
+        assert made[-1][1][6] == tokens
+
+
+@pytest.mark.parametrize("shape", [(7, 2, 127), (1000,), (7, 4, 128), (14, 1, 128), (7, 128, 2, 3)])
+def test_read_kv_refuses_parts_of_tokens_and_other_heads(calls, shape):
+    """Not the whole tokens in front of a remainder, and not 14 tokens of one head as 7 of two."""
+    pda, made = calls
+    p = pda.plan(3, 2, 8, 16, 8)
+    for outs in ((half(*shape), None), (None, half(*shape))):
+        with pytest.raises(ValueError, match="tokens"):
+            pda.read_kv(p, pool(p), 40, i32(3, 8), i32(4), i32(3), *outs)
+    assert not made
+
+
+@pytest.mark.parametrize("shape,tokens", [((5, 16, 128), 5), ((5, 2, 8, 128), 5), ((0, 16, 128), 0), ((5 * 2048,), 5)])
+def test_decode_tree_takes_whole_tokens(calls, shape, tokens):
+    pda, made = calls
+    p = pda.plan(3, 2, 8, 16, 8)
+    pda.decode_tree(p, half(*shape), pool(p), 40, i32(3, 8), i32(3), i32(4))
+    assert made[-1][1][1] == tokens and made[-1][1][13] == pda.lib().pda_tree_workspace_size(p, tokens)
+
+
+@pytest.mark.parametrize("shape", [(5, 16, 127), (5000,), (5, 32, 128), (10, 8, 128)])
+def test_decode_tree_refuses_other_queries(calls, shape):
+    pda, made = calls
+    p = pda.plan(3, 2, 8, 16, 8)
+    with pytest.raises(ValueError, match="query"):
+        pda.decode_tree(p, half(*shape), pool(p), 40, i32(3, 8), i32(3), i32(4))
+    assert not made
