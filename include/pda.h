@@ -548,8 +548,9 @@ PDA_API int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long 
  *   workspace     device, pda_tree_workspace_size bytes, 32-byte aligned
  *   out           [num_tokens][Hk*QG][128], as for pda_reduce but 16-byte aligned in either type; a row that sees nothing is 0
  * K and V of the tokens that any of the sequence's rows sees must be finite: a row that does not see one of them still has it in
- * its products, with weight 0.  What no row sees (before the window, behind the drafted tokens) is not read, or not used,
- * whatever it holds; block ids of blocks wholly before the window are not looked at.
+ * its products, with weight 0.  What no row sees (cached tokens before the window of a drafted token at position context_lens[b],
+ * drafted tokens that no mask names, what lies behind them) is not read, or not used, whatever it holds; block ids of blocks
+ * wholly before that window and behind the first num_first tokens are not looked at.
  * The roundings are those of the prefix in pda_decode_shared; fp8: also the query's, the sum of two e4m3 parts, by at most 2^-17 of
  * the row's largest |q|; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11
  * of its value, or 2^-24 of 1/256 of the step's largest 15 |v_scale| + |v_zero|), centroids to f16.

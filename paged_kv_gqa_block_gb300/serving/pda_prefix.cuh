@@ -263,7 +263,7 @@ struct Prefix {
         if ((threadIdx.x & 31) == 0) {
             sts128(at, u.g, u.h, u.rt, u.seq0);
             sts128(at + 16, u.rows, u.len, u.step0, u.steps);
-            sts128(at + 32, u.rot, u.slot, u.pieces, 0);
+            sts128(at + 32, u.rot, u.slot, u.pieces, TREE ? u.hidden : 0);
         }
     }
     __device__ void give(const Split& split, Unit u, int at, int end) {   // the first one is there already
@@ -280,8 +280,14 @@ struct Prefix {
     }
     // TREE: the same, with the first one looked up here too.
     __device__ void give_all(const Split& split, int at, int end) {
+        int noted = -1, hidden = 0;   // of the last sequence looked at
         for (;;) {
-            const Unit u = find_unit(a, split, at, end);
+            Unit u = find_unit(a, split, at, end);
+            if (a.masks && u.steps > 0) {
+                if (u.g != noted) hidden = note_hidden(u);
+                noted = u.g;
+                u.hidden = hidden;
+            }
             if (units > 1 && !wait_unit(bars + kBarUnitEmpty + 8 * (units & 1), (units >> 1) - 1 & 1)) return;
             put(u);
             __syncwarp();
@@ -299,6 +305,7 @@ struct Prefix {
         for (int i = 0; i < 12; i += 4) lds128(at + 4 * i, x[i], x[i + 1], x[i + 2], x[i + 3]);
         u.g = x[0], u.h = x[1], u.rt = x[2], u.seq0 = x[3], u.rows = x[4], u.len = x[5], u.step0 = x[6], u.steps = x[7];
         u.rot = x[8], u.slot = x[9], u.pieces = x[10];
+        u.hidden = TREE ? x[11] : 0;
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarUnitEmpty + 8 * slot);
         ++units;
@@ -332,6 +339,35 @@ struct Prefix {
     __device__ __forceinline__ static bool halves(const Unit& u) { return TREE && u.rows - u.rt * kUnitRows <= 64; }
     __device__ __forceinline__ static bool active(const Unit& u, int tile) {
         return u.rt * kUnitRows + tile * kTileRows < u.rows;
+    }
+    // Drafted tokens that no row sees may hold anything, and a weight of zero silences neither a NaN nor a scale that the others
+    // vanish beside, so their values and fields count as zeros.  In a chain every token is seen, and in a tree by itself as a rule.
+    // Where one is not, the warp that looks the units up notes for each whether some row sees it, and says so with the unit.
+    __device__ __forceinline__ bool note_hidden(const Unit& u) const {
+        const int lane = threadIdx.x & 31, drafted = u.rows / a.QG;
+        const uint32_t* m = a.masks + (long long)u.seq0 * a.words;
+        bool own = true;
+#pragma unroll 1
+        for (int j = lane; j < drafted; j += 32) own = own && j >> 5 < a.words && (__ldcg(m + (long long)j * a.words + (j >> 5)) >> lane & 1);
+        if (__all_sync(kLanes, own)) return false;
+#pragma unroll 1
+        for (int j = 0; j < drafted; j += 32, ++m) {   // a word of every row
+            uint32_t any = 0;
+            if (j >> 5 < a.words) {
+#pragma unroll 1
+                for (int i = lane; i < drafted; i += 32) any |= __ldcg(m + (long long)i * a.words);
+            }
+            any = __reduce_or_sync(kLanes, any);
+            if (j + lane < drafted) a.seen[u.seq0 + j + lane] = any >> lane & 1;
+        }
+        return true;
+    }
+    // Whether token t of the sequence, below its length, is such a one.
+    __device__ __forceinline__ bool hidden(const Unit& u, const Sight& x, int t) const {
+        if constexpr (TREE)
+            return u.hidden && t >= x.ctx && !a.seen[u.seq0 + (t - x.ctx)];
+        else
+            return false;
     }
 
     // ---------------------------------------------------------------- copies
@@ -527,13 +563,17 @@ struct Prefix {
             const Sight x = sight(u);
             for (int j = 0; j < u.steps; ++j) {
                 const int valid = tokens_of(u, x, j), t0 = step_of(u, x, j) * kStep;
+                uint32_t gone = 0;
+                if (u.hidden && t0 + kStep > x.ctx)
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) gone |= (uint32_t)(lane + 32 * i < valid && hidden(u, x, t0 + lane + 32 * i)) << i;
                 if (!wait(bars + kScRaw + 8 * st, ph)) return;
                 const uint32_t sc = sm + Cfg::kOffScales + st * Cfg::kScaleBytes;
                 float ks[4], vs[4], vz[4], f = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = lane + 32 * i;
-                    const bool there = tok < valid && !missed(x, t0 + tok);
+                    const bool there = tok < valid && !missed(x, t0 + tok) && !(gone >> i & 1);
                     if constexpr (TQ) {
                         ks[i] = there ? field_at(sc, tok, 0) : 0.f;
                         vs[i] = there ? field_at(sc, tok, 1) : 0.f;
@@ -610,6 +650,13 @@ struct Prefix {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (4 * lane + i >= valid || missed(x, t0 + 4 * lane + i)) v[i] = 0u;
+                }
+                if (u.hidden && t0 + kStep > x.ctx) {
+                    zero = zero || hidden(u, x, t0 + t);   // not past the sequence's end
+                    if (zero) vs = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * lane + i < valid && hidden(u, x, t0 + 4 * lane + i)) v[i] = 0u;
                 }
                 // magnitudes are ordered like their bits; a NaN counts for nothing
                 uint32_t y = 0;
@@ -914,11 +961,11 @@ struct Prefix {
             move(ks, kph, kStride, kKRing);
         };
         // bf16 rows that nobody sees may hold anything: a weight of zero does not silence a NaN
-        auto clear = [&](int valid, int h0, int h1) -> bool {
+        auto clear = [&](int valid, int h0, int h1, uint32_t unseen) -> bool {   // unseen: see unseen_of
             if (!wait(bar + kVFull + 8 * vs, vph)) return false;
             const uint32_t s = sm + Cfg::kOffSlots + (kVAt + vs) * kSlotBytes;
-            for (int i = lane; i < kStep * 8; i += 32)
-                if (const int r = i >> 3; r >= valid || (r >= h0 && r < h1)) {
+            for (int i = lane; i < kStep * 8; i += 32)   // r / 32 is the warp's
+                if (const int r = i >> 3; (__shfl_sync(kLanes, unseen, r >> 5) >> (r & 31) & 1) || r >= valid || (r >= h0 && r < h1)) {
                     sts128(s + i * 16, 0u, 0u, 0u, 0u);
                     sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
                 }
@@ -950,6 +997,18 @@ struct Prefix {
             move(vs, vph, kStride, kVRing);
             if constexpr (Q8) move(vs, vph, 1, kVRing);
         };
+        // Hidden tokens of a step, a bit each: the words of tokens 32 i .. 32 i + 31 in lane i.
+        auto unseen_of = [&](const Unit& u, const Sight& x, int t0) -> uint32_t {
+            uint32_t unseen = 0;
+            if (u.hidden && t0 + kStep > x.ctx)
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int t = t0 + 32 * i + lane;
+                    const uint32_t w = __ballot_sync(kLanes, t < u.len && hidden(u, x, t));
+                    if (lane == i) unseen = w;
+                }
+            return unseen;
+        };
         auto two_tiles = [&](const Unit& u, const Sight& x) -> bool {
             const int steps = uniform(u.steps);
 #pragma unroll
@@ -966,7 +1025,8 @@ struct Prefix {
                 if constexpr (!F16) {
                     const int t0 = uniform(step_of(u, x, j) * kStep), valid = min(kStep, u.len - t0);
                     const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
-                    if ((valid < kStep || h0 < h1) && !clear(valid, h0, h1)) return false;
+                    const uint32_t unseen = unseen_of(u, x, t0);
+                    if ((valid < kStep || h0 < h1 || (u.hidden && t0 + kStep > x.ctx)) && !clear(valid, h0, h1, unseen)) return false;
                 }
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
@@ -991,6 +1051,7 @@ struct Prefix {
         u.steps = 0;
         bool more = true;
         uint32_t first = 0, second = 0;   // steps whose product with V is to come
+        uint32_t first_unseen = 0, second_unseen = 0;
         auto all = [&] {
             for (;;) {
                 if (more && j == u.steps) {
@@ -1028,7 +1089,8 @@ struct Prefix {
                             if constexpr (!F16) {
                                 const int t0 = uniform(step_of(u, x, j - 1) * kStep), valid = min(kStep, u.len - t0);
                                 const int h0 = min(max(x.hole0 - t0, 0), kStep), h1 = min(max(x.hole1 - t0, 0), kStep);
-                                if (valid < kStep || h0 < h1) turn |= kClear | valid << 8 | h0 << 16 | h1 << 24;
+                                if (valid < kStep || h0 < h1 || (u.hidden && t0 + kStep > x.ctx)) turn |= kClear | valid << 8 | h0 << 16 | h1 << 24;
+                                (out == 0 ? first_unseen : second_unseen) = unseen_of(u, x, t0);
                             }
                             if (out == 0)
                                 first = turn;
@@ -1042,11 +1104,12 @@ struct Prefix {
                 }
                 if (out == 0) return;
                 const uint32_t turn = uniform(first), tile = turn & 1;
-                if (!F16 && (turn & kClear) && !clear(turn >> 8 & 255, turn >> 16 & 255, turn >> 24)) return;
+                if (!F16 && (turn & kClear) && !clear(turn >> 8 & 255, turn >> 16 & 255, turn >> 24, first_unseen)) return;
                 if (!values(tile, turn >> 1 & 1, !(turn & kFirst), true, true)) return;
                 next_values();
                 if (turn & kLast) umma_commit(leader, bar + kBarO + 8 * tile);
                 first = second;
+                first_unseen = second_unseen;
                 --out;
             }
         };
@@ -1908,7 +1971,11 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (fine) {
-            if (warp == 8 || (Cfg::kTree && !Cfg::kTq && warp == 10)) {
+            // The conversion first: where its code lies decides over a tenth of an fp8 step (64 sequences of 4 drafted tokens over 4096
+            // tokens 156 us, in the warps' order 174; TQ4 258 and 273), since the code is larger than the instruction cache.
+            if (Cfg::kF16 && warp >= 12)
+                p.convert();
+            else if (warp == 8 || (Cfg::kTree && !Cfg::kTq && warp == 10)) {
                 if constexpr (Cfg::kTree)
                     p.copies_tree(&kv_map, &sc_map, warp == 10);
                 else
@@ -1926,8 +1993,6 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
             }
             else if (Cfg::kF16 && !Cfg::kQ8 && warp == 10)
                 p.scales();
-            else if (Cfg::kF16 && warp >= 12)
-                p.convert();
         }
     }
     __syncwarp();

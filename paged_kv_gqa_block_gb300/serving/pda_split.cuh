@@ -40,6 +40,7 @@ struct TreeArgs : SharedArgs {
     const uint32_t* masks;       // [B][words], or null: token i sees the drafted tokens 0 .. i
     const float* centroids;      // TQ4: [16]
     int* refused;                // set to 1 by a call whose token_starts do not ascend, else to 0
+    uint8_t* seen;               // [B]: some row sees the drafted token; of sequences of which one does not see itself
     int words;                   // 32-bit words of a mask
     int window, num_first;       // window 0: none
     const uint8_t* cache;        // the pool, for what is not copied by tensor map
@@ -82,6 +83,7 @@ struct Unit {
     int step0, steps;      // this piece
     int rot;               // the piece's steps are taken from step0 + rot on, then from step0
     int slot, pieces;      // its number, and how many the row tile has
+    int hidden;            // drafted tokens: one of them does not see itself (set by the kernel)
 };
 
 struct Group {

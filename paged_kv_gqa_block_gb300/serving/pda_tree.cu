@@ -146,7 +146,7 @@ static bool tree_fits(const pda_plan_t* p, long long tokens) {
            most_tree_tiles(p, tokens) * (steps_of(p) + TreeArgs::kSwitchSteps) <= 2000000000ll;   // places are ints
 }
 struct TreeLayout {
-    long long o, l, m, pieces, refused, bytes;
+    long long o, l, m, pieces, seen, refused, bytes;
     int slots;
 };
 static TreeLayout tree_layout(const pda_plan_t* p, long long tokens) {
@@ -157,7 +157,8 @@ static TreeLayout tree_layout(const pda_plan_t* p, long long tokens) {
     w.l = w.o + up256(rows * w.slots * kHeadDim * 4);
     w.m = w.l + up256(rows * w.slots * 4);
     w.pieces = w.m + up256(rows * w.slots * 4);
-    w.refused = w.pieces + up256(rows * 4);
+    w.seen = w.pieces + up256(rows * 4);
+    w.refused = w.seen + up256(tokens);
     w.bytes = w.refused + 256;
     return w;
 }
@@ -221,6 +222,7 @@ int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tok
     a.masks = reinterpret_cast<const uint32_t*>(tree_masks);
     a.centroids = centroids;
     a.refused = reinterpret_cast<int*>(ws + w.refused);
+    a.seen = ws + w.seen;
     a.words = 2 * mask_words;
     a.window = window;
     a.num_first = num_first;
