@@ -142,8 +142,10 @@ static int tree_pieces(const pda_plan_t* p, long long tokens) {
     return (int)(want < most ? want : most);
 }
 static bool tree_fits(const pda_plan_t* p, long long tokens) {
-    return tokens >= 0 && tokens * p->query_group_size <= 1ll << 30 &&
-           most_tree_tiles(p, tokens) * (steps_of(p) + TreeArgs::kSwitchSteps) <= 2000000000ll;   // places are ints
+    constexpr long long kPlaces = 2000000000ll;   // places are ints
+    if (tokens < 0 || tokens > (1ll << 30) / p->query_group_size) return false;
+    const long long tiles = most_tree_tiles(p, tokens);
+    return tiles <= kPlaces && tiles * (steps_of(p) + TreeArgs::kSwitchSteps) <= kPlaces;
 }
 struct TreeLayout {
     long long o, l, m, pieces, seen, refused, bytes;
