@@ -545,7 +545,7 @@ PDA_API int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long 
  *   window        0: every cached token is seen.  Else a token at position p sees the cached tokens t with p - t < window, and
  *                 t < num_first.  p is context_lens[b] + the number of drafted tokens other than itself that it sees.  Masks
  *                 alone say which drafted tokens are seen; in a chain they count as cached ones.
- *   workspace     device, pda_tree_workspace_size bytes, 32-byte aligned
+ *   workspace     device, 32-byte aligned, pda_tree_workspace_size bytes; one made under the same plan for more tokens will do
  *   out           [num_tokens][Hk*QG][128], as for pda_reduce but 16-byte aligned in either type; a row that sees nothing is 0
  * K and V of the tokens that any of the sequence's rows sees must be finite: a row that does not see one of them still has it in
  * its products, with weight 0.  What no row sees (cached tokens before the window of a drafted token at position context_lens[b],

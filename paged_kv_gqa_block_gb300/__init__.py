@@ -706,7 +706,7 @@ def read_kv(p: Plan, kv_cache, num_cache_blocks: int, block_table, token_starts,
 
 
 def tree_workspace(p: Plan, num_tokens: int, device):
-    """The workspace of decode_tree with num_tokens drafted tokens in all (one made for more tokens may be too small)."""
+    """The workspace of decode_tree with up to num_tokens drafted tokens in all."""
     n = lib().pda_tree_workspace_size(p, num_tokens)
     if n < 0:
         raise PdaError(-1, "pda_tree_workspace_size")

@@ -132,13 +132,15 @@ static long long most_tree_tiles(const pda_plan_t* p, long long tokens) {
     return (tokens * p->query_group_size / kUnitRows + seqs) * p->num_kv_heads;
 }
 // Pieces of the longest sequence: four times as many as give every SM one, since lengths differ, and of two steps at least.
+static long long wanted_tiles() {
+    const int sms = device_sm_count();
+    return 4ll * (sms > 0 ? sms : 152);
+}
 static int tree_pieces(const pda_plan_t* p, long long tokens) {
-    int sms = device_sm_count();
-    if (sms <= 0) sms = 152;
     const long long rows = (tokens * p->query_group_size + kUnitRows - 1) / kUnitRows;
     const long long seqs = p->num_seqs < tokens ? p->num_seqs : tokens;
     const long long tiles = (rows > seqs ? rows : seqs) * p->num_kv_heads;
-    const long long want = (4ll * sms + tiles - 1) / tiles, most = (steps_of(p) + 1) / 2;
+    const long long want = (wanted_tiles() + tiles - 1) / tiles, most = (steps_of(p) + 1) / 2;
     return (int)(want < most ? want : most);
 }
 static bool tree_fits(const pda_plan_t* p, long long tokens) {
@@ -174,7 +176,16 @@ extern "C" {
 long long pda_tree_workspace_size(const pda_plan_t* plan, long long num_tokens) {
     if (!plan || pda_workspace_size(plan) < 0 || !tree_fits(plan, num_tokens)) return -1;
     if (num_tokens == 0 || plan->num_seqs == 0) return 0;
-    return tree_layout(plan, num_tokens).bytes;
+    // Fewer tokens may be cut into more pieces, and take more.  A workspace serves those too: the largest of the calls with so few
+    // tiles that they are cut into `pieces` or more are the ones with the most tokens.
+    long long bytes = tree_layout(plan, num_tokens).bytes;
+    for (int pieces = tree_pieces(plan, num_tokens) + 1, last = tree_pieces(plan, 1); pieces <= last; ++pieces) {
+        const long long x = (wanted_tiles() - 1) / ((pieces - 1ll) * plan->num_kv_heads);   // row tiles of a head
+        const long long fewer = plan->num_seqs <= x ? x * kUnitRows / plan->query_group_size : x;
+        const long long b = tree_layout(plan, fewer < num_tokens ? fewer : num_tokens).bytes;
+        if (b > bytes) bytes = b;
+    }
+    return bytes;
 }
 
 int pda_decode_tree(const pda_plan_t* plan, const void* query, long long num_tokens, const void* kv_cache,
