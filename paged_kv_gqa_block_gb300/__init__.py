@@ -659,6 +659,13 @@ def _rows(c: _Call, t, name: str, p: Plan):
     return t.data_ptr(), stride
 
 
+def _int32(x: int, name: str) -> int:
+    """ctypes would take a larger number modulo 2^32."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return x
+
+
 def _tokens(t, name: str, heads: int, dims: int) -> int:
     """How many tokens of [heads][dims] a packed tensor holds: nothing else may be left, and rows of other heads are refused."""
     n = t.numel() // (heads * dims)
@@ -736,7 +743,8 @@ def decode_tree(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, co
             c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
             c.opt(centroids, "centroids", _F32, 64), c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4),
             c.ptr(context_lens, "context_lens", _I32, B * 4), c.ptr(token_starts, "token_starts", _I32, (B + 1) * 4),
-            c.opt(tree_masks, "tree_masks", (torch.int64, torch.uint64), N * words * 8), words, window, num_first,
+            c.opt(tree_masks, "tree_masks", (torch.int64, torch.uint64), N * words * 8), words,
+            _int32(window, "window"), _int32(num_first, "num_first"),
             c.ptr(ws, "ws", _U8, 0), ws.nbytes, c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_tree", lib().pda_decode_tree, p, args, err_word, stream)
@@ -773,7 +781,8 @@ def decode_window(p: Plan, query, kv_cache, num_cache_blocks: int, block_table, 
             c.ptr(kv_cache, "kv_cache", None, num_cache_blocks * p.cache_block_bytes), num_cache_blocks,
             c.opt(centroids, "centroids", _F32, 64),
             c.ptr(block_table, "block_table", _I32, B * p.max_blocks_per_seq * 4, host_ok=True),
-            c.ptr(context_lens, "context_lens", _I32, B * 4, host_ok=True), window, num_first,
+            c.ptr(context_lens, "context_lens", _I32, B * 4, host_ok=True), _int32(window, "window"),
+            _int32(num_first, "num_first"),
             c.ptr(out, "out", (torch.float32, torch.bfloat16), n * (4 if f32 else 2), host_ok=True),
             OUT_F32 if f32 else OUT_BF16)
     c.run("pda_decode_window", lib().pda_decode_window, p, args, err_word, stream)

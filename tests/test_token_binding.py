@@ -92,3 +92,20 @@ def test_decode_tree_refuses_other_queries(calls, shape):
     with pytest.raises(ValueError, match="query"):
         pda.decode_tree(p, half(*shape), pool(p), 40, i32(3, 8), i32(3), i32(4))
     assert not made
+
+
+@pytest.mark.parametrize("name", ["window", "num_first"])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 16, 1 << 63, -(1 << 31) - 1, -(1 << 32) + 16])
+def test_windows_past_32_bits_are_refused(calls, name, value):
+    """Not taken modulo 2^32, as a window of 16."""
+    pda, made = calls
+    p = pda.plan(3, 2, 8, 16, 8)
+    kw = dict(window=100, num_first=4)
+    kw[name] = value
+    with pytest.raises(ValueError, match=name):
+        pda.decode_tree(p, half(5, 16, 128), pool(p), 40, i32(3, 8), i32(3), i32(4), **kw)
+    with pytest.raises(ValueError, match=name):
+        pda.decode_window(p, half(3, 16, 128), pool(p), 40, i32(3, 8), i32(3), **kw)
+    assert not made
+    pda.decode_tree(p, half(5, 16, 128), pool(p), 40, i32(3, 8), i32(3), i32(4), window=(1 << 31) - 1, num_first=(1 << 31) - 1)
+    assert made[-1][1][10:12] == ((1 << 31) - 1, (1 << 31) - 1)
