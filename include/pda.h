@@ -570,7 +570,7 @@ PDA_API int pda_decode_tree(const pda_plan_t* plan, const void* query, long long
  * free to be overwritten.
  *   path       device, int32 [num_seqs][max_path]: ascending indices of drafted tokens (an ancestor before its descendants)
  *   path_lens  device, int32 [num_seqs], each in [0, max_path]
- *   out_lens   device, int32 [num_seqs]; must not overlap context_lens or path_lens
+ *   out_lens   device, int32 [num_seqs]; must overlap none of context_lens, path, path_lens and block_table
  * The call works within the pool it is given; the pools of a model's other layers need the same call each.  Sequences must not
  * share the blocks that hold drafted tokens.
  * Data errors: a context length out of range (PDA_ERRW_BAD_CONTEXT_LEN), a path that does not ascend or is too long

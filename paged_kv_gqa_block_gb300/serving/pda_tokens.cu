@@ -607,11 +607,14 @@ int pda_accept_tokens(const pda_plan_t* plan, void* kv_cache, long long num_cach
     if (off(kv_cache, 16) || off(block_table, 4) || off(context_lens, 4) || off(path, 4) || off(path_lens, 4) ||
         off(out_lens, 4) || off(err_word, 4))
         return PDA_ERR_INVALID_ARG;
-    auto overlap = [&](const int* p) {   // CTAs of a sequence read what one of them would have written
-        const uintptr_t x = (uintptr_t)p, y = (uintptr_t)out_lens, n = 4ull * plan->num_seqs;
-        return x < y + n && y < x + n;
+    auto overlap = [&](const int* p, long long n) {   // CTAs of a sequence read what one of them would have written
+        const uintptr_t x = (uintptr_t)p, y = (uintptr_t)out_lens;
+        return x < y + 4ull * plan->num_seqs && y < x + 4ull * n;
     };
-    if (overlap(context_lens) || overlap(path_lens)) return PDA_ERR_INVALID_ARG;
+    const long long seqs = plan->num_seqs;
+    if (overlap(context_lens, seqs) || overlap(path_lens, seqs) || overlap(path, seqs * max_path) ||
+        overlap(block_table, seqs * plan->max_blocks_per_seq))
+        return PDA_ERR_INVALID_ARG;
     AcceptArgs a = {};
     a.cache = static_cast<uint8_t*>(kv_cache);
     a.block_table = block_table;
