@@ -964,11 +964,18 @@ struct Prefix {
         auto clear = [&](int valid, int h0, int h1, uint32_t unseen) -> bool {   // unseen: see unseen_of
             if (!wait(bar + kVFull + 8 * vs, vph)) return false;
             const uint32_t s = sm + Cfg::kOffSlots + (kVAt + vs) * kSlotBytes;
-            for (int i = lane; i < kStep * 8; i += 32)   // r / 32 is the warp's
-                if (const int r = i >> 3; (__shfl_sync(kLanes, unseen, r >> 5) >> (r & 31) & 1) || r >= valid || (r >= h0 && r < h1)) {
+            for (int i = lane; i < kStep * 8; i += 32)
+                if (const int r = i >> 3; r >= valid || (r >= h0 && r < h1)) {
                     sts128(s + i * 16, 0u, 0u, 0u, 0u);
                     sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
                 }
+            if (__any_sync(kLanes, unseen))   // rare, and apart: in the loop above its test cost every last step 0.3 us
+#pragma unroll 1
+                for (int i = lane; i < kStep * 8; i += 32)
+                    if (__shfl_sync(kLanes, unseen, i >> 5) >> (i >> 3 & 3) & 1) {
+                        sts128(s + i * 16, 0u, 0u, 0u, 0u);
+                        sts128(s + 16384 + i * 16, 0u, 0u, 0u, 0u);
+                    }
             fence_proxy_async_shared();
             __syncwarp();
             return true;
@@ -997,16 +1004,12 @@ struct Prefix {
             move(vs, vph, kStride, kVRing);
             if constexpr (Q8) move(vs, vph, 1, kVRing);
         };
-        // Hidden tokens of a step, a bit each: the words of tokens 32 i .. 32 i + 31 in lane i.
+        // Hidden tokens of a step, a bit each: of tokens 4 i .. 4 i + 3 in lane i.
         auto unseen_of = [&](const Unit& u, const Sight& x, int t0) -> uint32_t {
             uint32_t unseen = 0;
             if (u.hidden && t0 + kStep > x.ctx)
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int t = t0 + 32 * i + lane;
-                    const uint32_t w = __ballot_sync(kLanes, t < u.len && hidden(u, x, t));
-                    if (lane == i) unseen = w;
-                }
+                for (int t = t0 + 4 * lane + 3, i = 0; i < 4; --t, ++i) unseen = 2 * unseen + (t < u.len && hidden(u, x, t));
             return unseen;
         };
         auto two_tiles = [&](const Unit& u, const Sight& x) -> bool {
@@ -1948,7 +1951,8 @@ __global__ void __launch_bounds__(SharedCfg<KV, Args>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = lds32v(bars + kTmemAt);
     allow_dependent_launch();
-    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64
+    // registers at launch: 384 x 168 = 64512 = 256 x 200 + 128 x 104; 512 x 128 = 65536 = 256 x 192 + 256 x 64, of drafted tokens
+    // 256 x 160 + 256 x 96
     const bool fine = lds32v(bars + kAbortAt) == 0u;
     if (warp < 8) {
         if constexpr (Cfg::kTree && Cfg::kF16)
