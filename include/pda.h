@@ -504,9 +504,10 @@ PDA_API int pda_decode_shared(const pda_plan_t* prefix_plan, const pda_plan_t* p
  *   positions      device, int32 [num_seqs]; negative: none of the sequence's rows is written
  *   centroids      device, fp32 [16], finite, in any order, for a TQ4 plan, else NULL
  * bf16 and fp8 caches get the bytes that pda_append_kv would give them.  TQ4 (keys already in the basis of the codebook, as the
- * query; K and V finite): K: k_norm = the norm of the row rounded to fp16 (from the exact sum of squares, at most 65504),
+ * query; K and V finite): K: k_norm = the norm of the row, taken in 64 bits and rounded once to fp16 (at most 65504),
  * code = how many midpoints of neighbouring centroids, (c + c') / 2 in fp32, lie below k_d / k_norm in fp32 (of the sorted
- * codebook; a row of norm 0 is divided by 1); V: v_zero = fp16(min v), v_scale = fp16((max v - min v) / 15), code =
+ * codebook; a row of norm 0 is divided by 1); V: v_zero = fp16(min v), v_scale = fp16((max v - min v) / 15), both kept within
+ * +-65504, code =
  * (v_d - v_zero) / v_scale (by 1 where v_scale is 0), rounded to the nearest even integer and brought into 0 .. 15; all
  * quotients and differences correctly rounded in fp32.
  * Data errors: a row past max_blocks_per_seq*kv_block_size (PDA_ERRW_BAD_POSITION) or whose block id is outside the pool
@@ -552,8 +553,9 @@ PDA_API int pda_read_kv(const pda_plan_t* plan, const void* kv_cache, long long 
  * drafted tokens that no mask names, what lies behind them) is not read, or not used, whatever it holds; block ids of blocks
  * wholly before that window and behind the first num_first tokens are not looked at.
  * The roundings are those of the prefix in pda_decode_shared; fp8: also the query's, the sum of two e4m3 parts, by at most 2^-17 of
- * the row's largest |q|; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11
- * of its value, or 2^-24 of 1/256 of the step's largest 15 |v_scale| + |v_zero|), centroids to f16.
+ * the row's largest |q|; TQ4: the weights to f16 as there, V rounded once to f16 (2^-11 of its value, or 2^-33 of the step's
+ * largest 15 |v_scale| + |v_zero|) from a sum in fp32 (2^-18 |v_scale| + 2^-21 |v_zero|, which shows where the two cancel),
+ * centroids to f16.
  * Data errors: a context length out of range (PDA_ERRW_BAD_CONTEXT_LEN) or drafted tokens that do not fit behind it
  * (PDA_ERRW_BAD_POSITION) give zeros for the sequence's rows; block ids as for pda_decode.
  */

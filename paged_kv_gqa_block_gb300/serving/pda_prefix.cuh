@@ -815,7 +815,8 @@ struct Prefix {
                 }
                 if (!wait(bars + kScFull + 8 * st, st_ph)) return;
                 // 1 + code / 16 costs one instruction: V = (1 + code / 16) 16 v_scale + (v_zero - 16 v_scale).  A token that is
-                // not there has both 0.
+                // not there has both 0.  Off, in units of 2^-24, by 2 v_scale code + 2 v_zero for 1 / F and the products with it, by
+                // 16 v_scale + v_zero for the difference and by the value for the sum: below 2^-18 |v_scale| + 2^-21 |v_zero|.
                 const float vs = 16.f * __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes));
                 const float vz = __uint_as_float(lds32v(scale0 + st * Cfg::kScaleBytes + 512)) - vs;
                 if (++st == Cfg::kScales) {

@@ -7,14 +7,14 @@
 //          division, so that a token has the same bytes whichever call wrote it
 //   TQ4    K: k_norm = f16(|k|), code = the number of midpoints of neighbouring centroids below fp32(k_d / k_norm)
 //          V: v_zero = f16(min v), v_scale = f16((max v - min v) / 15), code = rint((v_d - v_zero) / v_scale) in 0 .. 15
-// Every quotient is an IEEE division and |k| is rounded once, from 64 bits where 32 cannot tell to which f16 value, so that the
-// codes are a function of the values alone: two writes of one token, on any grid, give the same bytes.
+// Every quotient is that of an IEEE division and |k| is rounded once, from 64 bits where 32 cannot tell to which f16 value, so
+// that the codes are a function of the values alone: two writes of one token, on any grid, give the same bytes.
 //
 // A warp takes up to four KV heads of one token at a time, whose loads are asked for together: addresses are computed once per token
 // (a search of token_starts and the block table's entry, by one thread), and a whole row leaves in one or two store instructions.
 // Measured, 131072 tokens of 8 heads: written in bf16 160 us (6.7 TB/s: HBM), fp8 164 us (5.0 TB/s), TQ4 288 us (2.4 TB/s: 276
-// instructions per row, 71 % of the issue slots used); read back from bf16 159 us, fp8 124 us (6.6 TB/s), TQ4 138 us (4.9 TB/s).
-// 16 prompts of up to 2048 tokens into fp8 22 us, 16 contexts of up to 8192 fp8 tokens back 42 us (6.1 TB/s), up to six tokens of
+// instructions per row, 71 % of the issue slots used); read back from bf16 159 us, fp8 124 us (6.6 TB/s), TQ4 138 us (4.9 TB/s: a conversion per code).
+// 16 prompts of up to 4096 tokens into fp8 22 us, 16 contexts of up to 8192 fp8 tokens back 42 us (6.1 TB/s), up to nine tokens of
 // 8 sequences 2.8 us.
 #include <cuda_runtime.h>
 
@@ -168,7 +168,7 @@ __device__ __forceinline__ float f16_saturated(float x) {
 // fp8: lane l < 16 holds K's dimensions 8l .. 8l+7, lane 16 + l V's.  Bound by instructions (HBM would take two thirds of the time),
 // so a value is divided by its row's inverse and two exact remainders, five instructions: a quotient whose remainder underflows is far
 // below e4m3's smallest.  (Codes from products a little too small and a little too large, and quotients only where the two differ, were
-// slower: bf16 values have few mantissas, their quotients meet e4m3's ties often, and a row of four was left open; 16 prompts of up to 2048
+// slower: bf16 values have few mantissas, their quotients meet e4m3's ties often, and a row of four was left open; 16 prompts of up to 4096
 // tokens 26 us and not 22.)  Rows that are tiny or hold infinities or NaN are divided.
 __device__ __forceinline__ void write_fp8(uint8_t* row, float* scales, uint4 raw, int lane, int BS) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};

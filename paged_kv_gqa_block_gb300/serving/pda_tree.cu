@@ -10,11 +10,14 @@
 // 256 rows and not once per drafted token: pda_prefix.cuh, where a sequence takes the place of a group.  Its pieces are joined
 // here.
 //
-// Measured, calls from a graph: 4 trees of 64 tokens over 32768 bf16 tokens 192 us (1.43 PFLOP/s: the tensor cores); 32 trees of 9 to
-// 33 over contexts of 2048 to 8192 128 us (sequences of more than 256 rows have further row tiles, which read K and V again: 487 MB of
-// 352; the join 12); 64 trees of up to 6 in a window of 4096 fp8 tokens 98 us (2.0 TB/s: 1.1 to 1.3 us per step and CTA, and some 5 us
-// where a CTA goes on to the next sequence and head, most of it the first fetch of the code); 64 of 4 over 4096 bf16 tokens 174 us (6.2
-// TB/s: HBM), fp8 155 us, TQ4 250 us (its conversion); one of 4 over 250 10.1 us (latency of two launches).
+// Measured, replays of a graph (a call from Python by itself is longer, see the table of cases): 4 trees of 64 tokens over 32768
+// bf16 tokens 192 us (1.43 PFLOP/s: the tensor cores); 32 trees of 9 to 33 over contexts of 2048 to 8192 128 us (sequences of
+// more than 256 rows have further row tiles, which read K and V again: 487 MB of 352; the join 12); 64 trees of up to 6 in a
+// window of 4096 fp8 tokens 98 us (2.0 TB/s: 1.1 to 1.3 us per step and CTA, and some 5 us where a CTA goes on to the next
+// sequence and head, most of it the first fetch of the code); 64 of 4 over 4096 bf16 tokens 175 us (6.2 TB/s: HBM), fp8 156 us,
+// TQ4 258 us (four warps convert K, then V, in short loops: 2.3 us per step); one of 4 over 250 10.3 us (latency of two launches).
+// Chains: every row tile walks all steps of its sequence, also those behind its own tokens; 512 tokens of 64 heads behind nothing
+// 23 us (bf16), 2048 196 us, in a window of 128 210 us (16 steps per row tile where its tokens see 3).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -4,8 +4,9 @@
 // t < num_first.  What it does not see is not read: the kernel is the cluster kernel over short lists (pda_selected.cuh),
 // whose list here is a run of tiles computed from the length (WindowTiles).
 //
-// Measured: 64 sequences of 500 to 16384 fp8 tokens in a window of 4096 68 us (5.3 TB/s: HBM, and the uneven end), 4 of 32768 bf16
-// tokens in one of 1024 8.9 us (latency: table, copies, joins in the cluster).
+// Measured: 64 sequences of 500 to 16384 fp8 tokens in a window of 4096 68 us (5.3 TB/s: HBM, and the uneven end), bf16 109 us, TQ4
+// 74 us (2.5 TB/s: the decoding of its codes); 4 of 32768 bf16 tokens in one of 1024 9.0 us (latency: table, copies, joins in
+// the cluster).
 #include <cuda_runtime.h>
 
 #include <cstdint>
